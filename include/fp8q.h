@@ -73,8 +73,10 @@ extern "C" {
 #define FP8Q_API
 #endif
 
-/* 8-bit target formats */
-enum { FP8Q_E4M3 = 0, FP8Q_E5M2 = 1 };
+/* 8-bit target formats, and the 4-bit format of the key/value cache (OCP
+ * E2M1: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6; accepted by the mx_kv_*
+ * calls alone) */
+enum { FP8Q_E4M3 = 0, FP8Q_E5M2 = 1, FP8Q_E2M1 = 2 };
 /* input element types */
 enum { FP8Q_F32 = 0, FP8Q_BF16 = 1 };
 /* status codes */
@@ -87,7 +89,8 @@ enum {
   FP8Q_EHANDLE = -5,  /* null or destroyed handle                           */
   FP8Q_ENOMEM = -6,   /* device or host allocation failed                   */
   FP8Q_EDEVICE = -7,  /* handle used with another device current            */
-  FP8Q_ESIZE = -8     /* size above the limit of a fixed-size scratch area  */
+  FP8Q_ESIZE = -8     /* size above the limit of a fixed-size scratch area, or
+                         a workspace below the size its query gives         */
 };
 
 /* Largest history window a handle may keep. */
@@ -364,6 +367,95 @@ FP8Q_API int mx_error_stats(const void* x, int dtype, int64_t rows, int64_t cols
 FP8Q_API int fp8q_error_stats_noalloc(const void* x, int dtype, int64_t n, const uint8_t* q,
                                       int format, const float* d_scale_inv, double* d_out,
                                       void* stream);
+
+/* ---- key/value cache held in MX blocks --------------------------------------
+ *
+ * A paged cache of attention keys and values, quantised as it is written.  A
+ * cached row is one token of one head: head_dim codes in blocks of 32, each
+ * block with one E8M0 byte (E + 127), under the same rules as mx_cast_ex.
+ * Codes are E2M1 (two per byte, the even element in the low four bits), E4M3
+ * or E5M2.  A block holding NaN or Inf gets E8M0 0xFF and every code
+ * sign|largest (E2M1: sign|7); it reads back as NaN.
+ *
+ * The four arrays are caller-owned device memory, 16-byte aligned and
+ * contiguous:
+ *   k_q, v_q          [num_pages, kv_heads, page_size, row bytes]
+ *                     (row bytes: head_dim / 2 for E2M1, head_dim otherwise)
+ *   k_e8m0, v_e8m0    [num_pages, kv_heads, page_size, head_dim / 32]
+ * Slot s is token s % page_size of page s / page_size.  page_size is a power
+ * of two (1 .. 2^20), kv_heads 1 .. MX_KV_MAX_HEADS, head_dim a multiple of
+ * 32 up to 256.  The struct itself is host memory, read during the call. */
+#define MX_KV_MAX_HEADS 4096
+typedef struct mx_kv_cache {
+  uint8_t* k_q;
+  uint8_t* k_e8m0;
+  uint8_t* v_q;
+  uint8_t* v_e8m0;
+  int64_t num_pages;
+  int32_t page_size, kv_heads, head_dim;
+  int32_t format;               /* FP8Q_E2M1, FP8Q_E4M3 or FP8Q_E5M2 */
+} mx_kv_cache;
+
+/* Quantise keys and values into the cache: row (token t, head h) of k lies at
+ * k + t * k_token_stride + h * k_head_stride (elements of dtype; the head_dim
+ * elements of a row are consecutive), likewise v, and goes to slot slots[t].
+ *   dtype    FP8Q_BF16 or FP8Q_F32; bases and strides multiples of 16 bytes
+ *            (else FP8Q_EALIGN)
+ *   slots    device int64 [tokens]; a slot below 0 or past the cache is not
+ *            written (padding tokens).  Slots of one call must be distinct.
+ *   rule     FP8Q_MX_FLOOR, FP8Q_MX_CEIL or FP8Q_MX_NEAREST
+ * One launch; each input element is read once. */
+FP8Q_API int mx_kv_write(const mx_kv_cache* c, const void* k, const void* v, int dtype, int64_t tokens,
+                         int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                         int64_t v_head_stride, const int64_t* slots, int rule, void* stream);
+
+/* The reverse: the values that slots[t] holds, code * 2^E, rounded to nearest
+ * even where dtype is bf16 (exact there unless subnormal).  A slot below 0 or
+ * past the cache gives zeros.  One launch. */
+FP8Q_API int mx_kv_read(const mx_kv_cache* c, const int64_t* slots, int64_t tokens, void* k, void* v, int dtype,
+                        int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                        int64_t v_head_stride, void* stream);
+
+/* Attention of query tokens over a 4-bit cache, without a 16-bit copy of it:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j
+ * for each query token and query head; head h reads key/value head
+ * h / (q_heads / kv_heads).  The queries of sequence b are rows cu_q[b] ..
+ * cu_q[b + 1) of q and are its last tokens: query i of n sits at position
+ * kv_lens[b] - n + i and sees the keys j <= its position and, with window
+ * W > 0, j > its position - W.  A query that sees no key gets zeros.
+ *   c            format FP8Q_E2M1 (else FP8Q_EDTYPE), head_dim 64 or 128
+ *   q, out       FP8Q_BF16 rows [total_q, q_heads, head_dim] with the given
+ *                element strides (multiples of 8), bases 16-byte aligned; they may not overlap
+ *   lse          device float [total_q, q_heads]: log of the softmax sum
+ *                (-inf where no key is seen), or NULL
+ *   cu_q         device int32 [batch + 1], non-decreasing, cu_q[batch] <=
+ *                total_q; NULL: one query per sequence (total_q == batch)
+ *   kv_lens      device int32 [batch]: tokens in each sequence's cache, its
+ *                queries included (values below 0 or past the table are
+ *                clamped)
+ *   page_table   device int32 [batch, table_width], rows table_stride apart:
+ *                the pages of a sequence in order; entries past its length
+ *                are not used, a page outside the cache hides its tokens
+ *   max_q        at least the largest number of queries of a sequence (rows
+ *                past it are left unwritten)
+ *   scale        > 0;  window >= 0 (0: no window)
+ *   workspace    device memory of mx_kv_attention_workspace(...) bytes,
+ *                16-byte aligned, zeroed before its first use; every call
+ *                leaves it ready for the next one.  Calls that may overlap on
+ *                the GPU need one each.  FP8Q_ESIZE if it is too small.
+ * Scores, softmax statistics and sums are fp32.  Capturable into CUDA graphs;
+ * the lengths and the table are read by the kernel, so replays see their
+ * current contents. */
+FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int64_t total_q, int q_heads,
+                             int64_t q_token_stride, int64_t q_head_stride, void* out, int64_t out_token_stride,
+                             int64_t out_head_stride, float* lse, const int32_t* cu_q, const int32_t* kv_lens,
+                             const int32_t* page_table, int64_t table_stride, int table_width, int batch, int max_q,
+                             float scale, int window, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes that mx_kv_attention needs for these sizes on the current
+ * device (possibly 0), or a negative status. */
+FP8Q_API int64_t mx_kv_attention_workspace(const mx_kv_cache* c, int64_t total_q, int q_heads, int batch, int max_q,
+                                           int table_width);
 
 /* Number of pipeline waits on the current device that ran out of time since
  * the last call (and reset it).  Kernels that stage tiles through TMA

@@ -1,0 +1,231 @@
+// Quantising keys and values into cache slots, and reading slots back.
+//
+// Both are streaming codecs bound by HBM: a write moves 2 or 4 bytes in and
+// 0.53 (E2M1) or 1.03 bytes out per element, a read the reverse.  The unit of
+// work is eight elements of a row: 16 bytes of bf16, 4 of E2M1, so that a
+// warp's accesses cover whole 128-byte lines of the plain tensor and 64-byte
+// runs of a cached row; four neighbouring lanes hold one block and share its
+// maximum by two shuffles.  Each thread has kKvUnroll units in flight.
+#include "kv_device.cuh"
+
+namespace fp8q {
+
+constexpr int kKvThreads = 256;
+constexpr int kKvUnroll = 4;
+
+struct KvCopy {
+  KvShape s;
+  KvPool pool[2];           // keys, values
+  char* x[2];               // plain rows
+  int64_t tok[2], head[2];  // strides in elements
+  const int64_t* slots;
+  int64_t tokens;
+  FastDiv row_units, dim_units;   // units per token (heads * dim / 8) and per row (dim / 8)
+  int32_t tokens_per_cta, rule;
+};
+
+// Where unit i of the CTA's tokens lives.
+struct KvUnit {
+  int64_t slot, x, q;   // cache slot (< 0: none), element offsets into the plain tensor and the cache
+};
+
+__device__ __forceinline__ KvUnit kv_unit(const KvCopy& p, int which, int64_t token0, uint32_t i) {
+  KvUnit u;
+  const uint32_t t = p.row_units.div(i), r = i - t * p.row_units.d;
+  const uint32_t h = p.dim_units.div(r), c = r - h * p.dim_units.d;
+  const int64_t token = token0 + t;
+  u.slot = __ldg(p.slots + token);
+  if (u.slot >= p.s.slots) u.slot = -1;
+  u.x = token * p.tok[which] + h * p.head[which] + c * 8;
+  u.q = u.slot < 0 ? 0 : kv_row(p.s, u.slot, (int)h) * p.s.dim + c * 8;
+  return u;
+}
+
+template <int FMT, int DT>
+__global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_constant__ KvCopy p) {
+  constexpr int W = DT == FP8Q_BF16 ? 1 : 2;        // 16-byte loads per unit
+  const int which = blockIdx.y;
+  const int64_t token0 = (int64_t)blockIdx.x * p.tokens_per_cta;
+  const uint32_t n = (uint32_t)min((int64_t)p.tokens_per_cta, p.tokens - token0) * p.row_units.d;
+  const KvPool pool = p.pool[which];
+  for (uint32_t base = 0; base < n; base += kKvThreads * kKvUnroll) {
+    KvUnit u[kKvUnroll];
+    uint4 v[kKvUnroll][W];
+#pragma unroll
+    for (int j = 0; j < kKvUnroll; ++j) {
+      const uint32_t i = base + j * kKvThreads + threadIdx.x;
+      u[j].slot = -1;
+#pragma unroll
+      for (int w = 0; w < W; ++w) v[j][w] = make_uint4(0, 0, 0, 0);
+      if (i < n) {
+        u[j] = kv_unit(p, which, token0, i);
+        const uint4* src = reinterpret_cast<const uint4*>(p.x[which] + u[j].x * (DT == FP8Q_BF16 ? 2 : 4));
+#pragma unroll
+        for (int w = 0; w < W; ++w) v[j][w] = __ldcs(src + w);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kKvUnroll; ++j) {
+      // n and the strides between units are multiples of 4: a block's four
+      // lanes are all in range or none is
+      uint32_t m = absmax_load<DT>(v[j][0]);
+      if (W == 2) m = absmax_merge<DT>(m, absmax_load<DT>(v[j][W - 1]));
+      m = unpack_max<DT>(m);
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      if (u[j].slot < 0) continue;
+      const bool finite = m < 0x7F800000u;
+      const int E = !finite ? 0 : FMT == FP8Q_E2M1 ? block_exp_e2m1(m, p.rule) : block_exp<FMT == FP8Q_E2M1 ? FP8Q_E4M3 : FMT>(m, p.rule, 0);
+      const float s = pow2f(-E);
+      float f[8];
+      uint32_t sign = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t b = elem_bits<DT>(v[j][W == 1 ? 0 : k >> 2], W == 1 ? k : k & 3);
+        f[k] = __uint_as_float(b) * s;
+        sign |= (b >> 31) << k;
+      }
+      if (FMT == FP8Q_E2M1) {
+        uint32_t o = cvt_e2m1x8(f);
+        if (!finite) {
+          o = 0x77777777u;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o |= ((sign >> k) & 1u) << (4 * k + 3);
+        }
+        *reinterpret_cast<uint32_t*>(pool.q + (u[j].q >> 1)) = o;
+      } else {
+        constexpr int F8 = FMT == FP8Q_E2M1 ? FP8Q_E4M3 : FMT;
+        uint2 o;
+        o.x = cvt_pair<F8>(f[0], f[1]) | (cvt_pair<F8>(f[2], f[3]) << 16);
+        o.y = cvt_pair<F8>(f[4], f[5]) | (cvt_pair<F8>(f[6], f[7]) << 16);
+        if (!finite) {
+          o.x = o.y = 0x7F7F7F7Fu;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o.x |= ((sign >> k) & 1u) << (8 * k + 7);
+            o.y |= ((sign >> (k + 4)) & 1u) << (8 * k + 7);
+          }
+        }
+        *reinterpret_cast<uint2*>(pool.q + u[j].q) = o;
+      }
+      if ((threadIdx.x & 3) == 0) pool.e8m0[u[j].q >> 5] = (uint8_t)(finite ? E + 127 : 255);
+    }
+  }
+}
+
+template <int FMT, int DT>
+__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_constant__ KvCopy p) {
+  const int which = blockIdx.y;
+  const int64_t token0 = (int64_t)blockIdx.x * p.tokens_per_cta;
+  const uint32_t n = (uint32_t)min((int64_t)p.tokens_per_cta, p.tokens - token0) * p.row_units.d;
+  const KvPool pool = p.pool[which];
+  for (uint32_t base = 0; base < n; base += kKvThreads * kKvUnroll) {
+    KvUnit u[kKvUnroll];
+    uint2 v[kKvUnroll];
+    uint32_t e[kKvUnroll];
+#pragma unroll
+    for (int j = 0; j < kKvUnroll; ++j) {
+      const uint32_t i = base + j * kKvThreads + threadIdx.x;
+      u[j].slot = -1;
+      v[j] = make_uint2(0, 0);
+      e[j] = 127;
+      if (i < n) {
+        u[j] = kv_unit(p, which, token0, i);
+        if (u[j].slot >= 0) {
+          if (FMT == FP8Q_E2M1) v[j].x = __ldcs(reinterpret_cast<const uint32_t*>(pool.q + (u[j].q >> 1)));
+          else v[j] = __ldcs(reinterpret_cast<const uint2*>(pool.q + u[j].q));
+          e[j] = pool.e8m0[u[j].q >> 5];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kKvUnroll; ++j) {
+      const uint32_t i = base + j * kKvThreads + threadIdx.x;
+      if (i >= n) continue;
+      uint32_t h[4];
+      if (FMT == FP8Q_E2M1) {
+        e2m1x8_f16(v[j].x, h);
+      } else {
+        constexpr int F8 = FMT == FP8Q_E2M1 ? FP8Q_E4M3 : FMT;
+        fp8x4_f16<F8>(v[j].x, h[0], h[1]);
+        fp8x4_f16<F8>(v[j].y, h[2], h[3]);
+      }
+      const float s = e8m0_value(e[j]);
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 a = f16x2_f32(h[k]);
+        f[2 * k] = a.x * s;
+        f[2 * k + 1] = a.y * s;
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.x[which] + u[j].x * (DT == FP8Q_BF16 ? 2 : 4));
+      if (DT == FP8Q_BF16) {
+        __stcs(dst, make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
+                               cvt_bf16x2(f[6], f[7])));
+      } else {
+        const uint32_t* b = reinterpret_cast<const uint32_t*>(f);
+        __stcs(dst, make_uint4(b[0], b[1], b[2], b[3]));
+        __stcs(dst + 1, make_uint4(b[4], b[5], b[6], b[7]));
+      }
+    }
+  }
+}
+
+template <int FMT, int DT>
+static cudaError_t launch_copy(bool write, const KvCopy& p, dim3 grid, cudaStream_t st) {
+  if (write) kv_write_kernel<FMT, DT><<<grid, kKvThreads, 0, st>>>(p);
+  else kv_read_kernel<FMT, DT><<<grid, kKvThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+static cudaError_t launch_any(bool write, const KvShape& s, int format, KvPool k, KvPool v, void* kx, void* vx,
+                              int dtype, int64_t tokens, const int64_t* strides, const int64_t* slots, int rule,
+                              cudaStream_t st, int* launches) {
+  KvCopy p;
+  p.s = s;
+  p.pool[0] = k;
+  p.pool[1] = v;
+  p.x[0] = static_cast<char*>(kx);
+  p.x[1] = static_cast<char*>(vx);
+  p.tok[0] = strides[0];
+  p.head[0] = strides[1];
+  p.tok[1] = strides[2];
+  p.head[1] = strides[3];
+  p.slots = slots;
+  p.tokens = tokens;
+  p.rule = rule;
+  const uint32_t row = (uint32_t)s.heads * (s.dim / 8);
+  p.row_units = FastDiv(row);
+  p.dim_units = FastDiv((uint32_t)s.dim / 8);
+  // one pass of a CTA over its units, or more where the grid would pass 2^31
+  int64_t per = (kKvThreads * kKvUnroll + row - 1) / row;
+  per = per < 1 ? 1 : per;
+  while ((tokens + per - 1) / per > 0x7FFFFFFF) per *= 2;
+  p.tokens_per_cta = (int32_t)per;
+  const dim3 grid((unsigned)((tokens + per - 1) / per), 2);
+  cudaError_t e;
+  const bool b = dtype == FP8Q_BF16;
+  if (format == FP8Q_E2M1)
+    e = b ? launch_copy<FP8Q_E2M1, FP8Q_BF16>(write, p, grid, st) : launch_copy<FP8Q_E2M1, FP8Q_F32>(write, p, grid, st);
+  else if (format == FP8Q_E4M3)
+    e = b ? launch_copy<FP8Q_E4M3, FP8Q_BF16>(write, p, grid, st) : launch_copy<FP8Q_E4M3, FP8Q_F32>(write, p, grid, st);
+  else
+    e = b ? launch_copy<FP8Q_E5M2, FP8Q_BF16>(write, p, grid, st) : launch_copy<FP8Q_E5M2, FP8Q_F32>(write, p, grid, st);
+  *launches += 1;
+  return e;
+}
+
+cudaError_t launch_kv_write(const KvShape& s, int format, KvPool k, KvPool v, const void* kx, const void* vx,
+                            int dtype, int64_t tokens, const int64_t* strides, const int64_t* slots, int rule,
+                            cudaStream_t st, int* launches) {
+  return launch_any(true, s, format, k, v, const_cast<void*>(kx), const_cast<void*>(vx), dtype, tokens, strides,
+                    slots, rule, st, launches);
+}
+
+cudaError_t launch_kv_read(const KvShape& s, int format, KvPool k, KvPool v, void* kx, void* vx, int dtype,
+                           int64_t tokens, const int64_t* strides, const int64_t* slots, cudaStream_t st,
+                           int* launches) {
+  return launch_any(false, s, format, k, v, kx, vx, dtype, tokens, strides, slots, 0, st, launches);
+}
+
+}  // namespace fp8q

@@ -1,0 +1,154 @@
+// The quantised key/value cache: its layout, the 4-bit format and the small
+// device helpers that the write, read and attention kernels share.
+//
+// A cached row (one token of one head, D elements) is D / 32 MX blocks: codes
+// in E2M1 (two per byte, the even element in the low half), E4M3 or E5M2, and
+// one E8M0 byte (E + 127) per block.  Rows of one head and page are
+// consecutive, so a page of a head is one contiguous run of codes and one of
+// E8M0 bytes.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "fp8q_device.cuh"
+#include "mx_device.cuh"
+
+namespace fp8q {
+
+// Exact division of n < 2^31 by a fixed d >= 1: q = (hi(n * mul) + n) >> shift
+// (round-up reciprocal of the invariant divisor).
+struct FastDiv {
+  uint32_t mul, shift, d;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t v) : d(v) {
+    shift = 0;
+    while ((1ull << shift) < v) ++shift;
+    mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - v)) / v + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
+// One kind (keys or values) of the cache as the kernels see it.
+struct KvPool {
+  uint8_t* q;
+  uint8_t* e8m0;
+};
+
+struct KvShape {
+  int64_t slots;        // num_pages * page_size
+  int32_t page_shift;   // log2(page_size)
+  int32_t heads, dim;
+};
+
+// Row index of (slot, head): the codes of a row start at row * row bytes, its
+// E8M0 bytes at row * (dim / 32).
+__device__ __forceinline__ int64_t kv_row(const KvShape& s, int64_t slot, int head) {
+  const int64_t page = slot >> s.page_shift, off = slot & ((1ll << s.page_shift) - 1);
+  return (((page * s.heads + head) << s.page_shift) + off);
+}
+
+// 2^(byte - 127) of an E8M0 byte as fp32; 0xFF is NaN.
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+  return __uint_as_float(b == 255u ? 0x7FFFFFFFu : b == 0u ? 0x00400000u : b << 23);
+}
+
+// Shared exponent of an E2M1 block from its amax bits m (finite); the rules
+// of block_exp for fmax = 6 = 1.5 * 2^2: ceil adds one above the significand
+// 1.5, nearest takes one off below 1.5 / sqrt 2, i.e. M^2 < 9 * 2^43 on the
+// 24-bit significand, M <= isqrt(9 * 2^43 - 1).
+__device__ __forceinline__ int block_exp_e2m1(uint32_t m, int rule) {
+  if (m == 0u) return -127;
+  int k;
+  uint32_t M;
+  if (m >> 23) {
+    k = (int)(m >> 23) - 127;
+    M = 0x800000u | (m & 0x7FFFFFu);
+  } else {
+    const int lb = 31 - __clz((int)m);
+    k = lb - 149;
+    M = m << (23 - lb);
+  }
+  int E = k - 2;
+  if (rule == FP8Q_MX_CEIL) E += (M > 0xC00000u) ? 1 : 0;
+  else if (rule == FP8Q_MX_NEAREST) E -= (M <= 8897462u) ? 1 : 0;
+  return min(127, max(-127, E));
+}
+
+// Eight fp32 values -> eight E2M1 codes in a word (element i in bits 4i..),
+// round to nearest even, saturating to +-6.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float* v) {
+  uint32_t r;
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// The eight codes of a word -> four f16 pairs (exact).
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// Four 8-bit codes of a word -> two f16 pairs (exact for both formats).
+template <int FMT>
+__device__ __forceinline__ void fp8x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (FMT == FP8Q_E4M3)
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n"
+        " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(w));
+  else
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n"
+        " cvt.rn.f16x2.e5m2x2 %0, a;\n cvt.rn.f16x2.e5m2x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+__device__ __forceinline__ float2 f16x2_f32(uint32_t h) {
+  float2 f;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}"
+      : "=f"(f.x), "=f"(f.y) : "r"(h));
+  return f;
+}
+
+// Two fp32 -> a bf16 pair, round to nearest even (`lo` in the low half).
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ---- launches (kv_cache.cu, kv_attention.cu) --------------------------------
+cudaError_t launch_kv_write(const KvShape& s, int format, KvPool k, KvPool v, const void* kx, const void* vx,
+                            int dtype, int64_t tokens, const int64_t* strides, const int64_t* slots, int rule,
+                            cudaStream_t st, int* launches);
+cudaError_t launch_kv_read(const KvShape& s, int format, KvPool k, KvPool v, void* kx, void* vx, int dtype,
+                           int64_t tokens, const int64_t* strides, const int64_t* slots, cudaStream_t st,
+                           int* launches);
+
+// Arguments of one attention call, checked on the host.
+struct KvAttn {
+  KvShape shape;
+  KvPool k, v;
+  const void* q;
+  void* out;
+  float* lse;
+  const int32_t* cu_q;
+  const int32_t* kv_lens;
+  const int32_t* table;
+  int64_t q_tok, q_head, out_tok, out_head;   // strides in elements
+  int64_t table_stride;
+  int32_t table_width, batch, total_q, max_q, q_heads, group, window;
+  float scale;
+};
+int64_t kv_attention_workspace(const KvShape& s, int q_heads, int64_t total_q, int batch, int max_q,
+                               int table_width, int sms);
+cudaError_t launch_kv_attention(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches);
+
+}  // namespace fp8q

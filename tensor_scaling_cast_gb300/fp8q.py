@@ -16,7 +16,7 @@ import torch
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libfp8q.so")
 
-E4M3, E5M2 = 0, 1
+E4M3, E5M2, E2M1 = 0, 1, 2
 MX_FLOOR, MX_CEIL, MX_NEAREST = 0, 1, 2
 MX_ROWWISE, MX_COLWISE = 0, 1
 EST_MAX_WINDOW, EST_SMOOTHED = 0, 1
@@ -72,6 +72,12 @@ def load() -> ctypes.CDLL:
     L.fp8q_error_stats.argtypes = [p, i, i64, p, i, p, p, p]
     L.mx_error_stats.argtypes = [p, i, i64, i64, p, p, i, p, p]
     L.fp8q_error_stats_noalloc.argtypes = [p, i, i64, p, i, p, p, p]
+    L.mx_kv_write.argtypes = [p, p, p, i, i64, i64, i64, i64, i64, p, i, p]
+    L.mx_kv_read.argtypes = [p, p, i64, p, p, i, i64, i64, i64, i64, p]
+    L.mx_kv_attention.argtypes = [p, p, i, i64, i, i64, i64, p, i64, i64, p, p, p, p, i64, i, i, i, f, i, p,
+                                  i64, p]
+    L.mx_kv_attention_workspace.argtypes = [p, i64, i, i, i, i]
+    L.mx_kv_attention_workspace.restype = i64
     L.fp8q_pipeline_status.argtypes = [ctypes.POINTER(ctypes.c_uint)]
     L.fp8q_pipeline_status.restype = i
     L.fp8q_pipeline_selftest.argtypes = [p]
@@ -85,7 +91,8 @@ def load() -> ctypes.CDLL:
                  "fp8q_create", "fp8q_create_ex", "fp8q_get_estimator_state",
                  "fp8q_set_estimator_state", "fp8q_destroy", "fp8q_cast", "fp8q_cast_multi", "mx_cast", "mx_cast_ex",
                  "fp8q_amax_history", "fp8q_scale_state", "fp8q_set_history", "fp8q_reset",
-                 "fp8q_error_stats", "mx_error_stats", "fp8q_error_stats_noalloc"):
+                 "fp8q_error_stats", "mx_error_stats", "fp8q_error_stats_noalloc",
+                 "mx_kv_write", "mx_kv_read", "mx_kv_attention"):
         getattr(L, name).restype = i
     _lib = L
     return L
@@ -325,6 +332,115 @@ def mx_error_stats(x: torch.Tensor, q: torch.Tensor, e8m0: torch.Tensor, fmt: in
     rows, cols = x.shape
     _check(load().mx_error_stats(_ptr(x), _dtype(x), rows, cols, _ptr(q), _ptr(e8m0), fmt,
                                  _ptr(out), _stream(stream)), "mx_error_stats")
+
+
+# ---- key/value cache ---------------------------------------------------------
+
+class _KVCacheStruct(ctypes.Structure):
+    _fields_ = [("k_q", ctypes.c_void_p), ("k_e8m0", ctypes.c_void_p), ("v_q", ctypes.c_void_p),
+                ("v_e8m0", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class MXKVCache:
+    """The four arrays of a paged key/value cache and their description for
+    the C calls: codes uint8 [pages, kv_heads, page_size, head_dim / 2 (E2M1)
+    or head_dim] and E8M0 bytes uint8 [pages, kv_heads, page_size,
+    head_dim / 32], for keys and for values."""
+
+    def __init__(self, k_q: torch.Tensor, k_e8m0: torch.Tensor, v_q: torch.Tensor, v_e8m0: torch.Tensor,
+                 fmt: int = E2M1):
+        pages, heads, page, blocks = k_e8m0.shape
+        dim = 32 * blocks
+        row = (pages, heads, page, dim // 2 if fmt == E2M1 else dim)
+        for t, shape in ((k_q, row), (v_q, row), (k_e8m0, k_e8m0.shape), (v_e8m0, k_e8m0.shape)):
+            if t.dtype != torch.uint8 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+                raise TypeError(f"cache arrays are contiguous uint8 of shape {tuple(shape)}: "
+                                f"got {t.dtype} {tuple(t.shape)}")
+        self.k_q, self.k_e8m0, self.v_q, self.v_e8m0 = k_q, k_e8m0, v_q, v_e8m0
+        self.fmt, self.num_pages, self.kv_heads, self.page_size, self.head_dim = fmt, pages, heads, page, dim
+        self._struct = _KVCacheStruct(k_q.data_ptr(), k_e8m0.data_ptr(), v_q.data_ptr(), v_e8m0.data_ptr(),
+                                      pages, page, heads, dim, fmt)
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def allocate(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int = E2M1,
+                 device="cuda") -> "MXKVCache":
+        """A cache of zeroed arrays."""
+        row = head_dim // 2 if fmt == E2M1 else head_dim
+        q, e = (num_pages, kv_heads, page_size, row), (num_pages, kv_heads, page_size, head_dim // 32)
+        return cls(*(torch.zeros(s, dtype=torch.uint8, device=device) for s in (q, e, q, e)), fmt=fmt)
+
+
+def _kv_rows(x: torch.Tensor, cache: MXKVCache, heads: int, what: str):
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != cache.head_dim or (x.stride(2) != 1 and x.numel()):
+        raise TypeError(f"{what}: rows [tokens, {heads}, {cache.head_dim}] with consecutive elements expected, "
+                        f"got {tuple(x.shape)} with strides {x.stride()}")
+
+
+def _kv_pair(k, v, slots, cache, what):
+    _kv_rows(k, cache, cache.kv_heads, what)
+    _kv_rows(v, cache, cache.kv_heads, what)
+    if slots.dtype != torch.int64 or not slots.is_contiguous() or slots.numel() != k.shape[0] or \
+            v.shape[0] != k.shape[0] or v.dtype != k.dtype:
+        raise TypeError(f"{what}: slots are contiguous int64, one per token, and k and v alike")
+
+
+def mx_kv_write(cache: MXKVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, rule: int = MX_FLOOR,
+                stream=None):
+    """Quantise k and v [tokens, kv_heads, head_dim] (bf16 or fp32, any token and
+    head stride) into the cache slots `slots` (int64; negative: not written)."""
+    _kv_pair(k, v, slots, cache, "mx_kv_write")
+    _check(load().mx_kv_write(cache._ref, _ptr(k), _ptr(v), _dtype(k), k.shape[0], k.stride(0), k.stride(1),
+                              v.stride(0), v.stride(1), _ptr(slots), rule, _stream(stream)), "mx_kv_write")
+
+
+def mx_kv_read(cache: MXKVCache, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None):
+    """Read the slots back into k and v [tokens, kv_heads, head_dim] (bf16 or
+    fp32); a negative slot gives zeros."""
+    _kv_pair(k, v, slots, cache, "mx_kv_read")
+    _check(load().mx_kv_read(cache._ref, _ptr(slots), k.shape[0], _ptr(k), _ptr(v), _dtype(k), k.stride(0),
+                             k.stride(1), v.stride(0), v.stride(1), _stream(stream)), "mx_kv_read")
+
+
+def mx_kv_attention_workspace(cache: MXKVCache, q: torch.Tensor, page_table: torch.Tensor, max_q: int = 1):
+    """A zeroed workspace for mx_kv_attention calls of these shapes, or None
+    where they need none.  One per stream; reusable by every call of the same
+    or smaller shapes whose own query asks for no more."""
+    n = load().mx_kv_attention_workspace(cache._ref, q.shape[0], q.shape[1], page_table.shape[0], max_q,
+                                         page_table.shape[1])
+    if n < 0:
+        _check(n, "mx_kv_attention_workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def mx_kv_attention(cache: MXKVCache, q: torch.Tensor, out: torch.Tensor, page_table: torch.Tensor,
+                    kv_lens: torch.Tensor, cu_q=None, max_q: int = 1, scale=None, window: int = 0, lse=None,
+                    workspace=None, stream=None):
+    """Attention of q [total_q, q_heads, head_dim] (bf16) over the 4-bit cache,
+    into out of the same shape.  page_table int32 [batch, pages], kv_lens int32
+    [batch], cu_q int32 [batch + 1] (None: one query per sequence), max_q >= the
+    queries of any sequence, scale (None: head_dim ** -0.5), lse float32
+    [total_q, q_heads] or None, workspace of mx_kv_attention_workspace."""
+    heads = q.shape[1] if q.dim() == 3 else 0
+    _kv_rows(q, cache, heads, "mx_kv_attention q")
+    _kv_rows(out, cache, heads, "mx_kv_attention out")
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or out.shape != q.shape:
+        raise TypeError("mx_kv_attention: q and out are bf16 of one shape")
+    batch = page_table.shape[0]
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or (page_table.stride(1) != 1 and page_table.shape[1] > 1) or \
+            kv_lens.dtype != torch.int32 or kv_lens.numel() != batch or not kv_lens.is_contiguous() or \
+            (cu_q is not None and (cu_q.dtype != torch.int32 or cu_q.numel() != batch + 1 or
+                                   not cu_q.is_contiguous())) or \
+            (lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or
+                                  not lse.is_contiguous())):
+        raise TypeError("mx_kv_attention: page_table int32 [batch, pages], kv_lens int32 [batch], "
+                        "cu_q int32 [batch + 1], lse float32 [total_q, q_heads]")
+    _check(load().mx_kv_attention(
+        cache._ref, _ptr(q), BF16, q.shape[0], heads, q.stride(0), q.stride(1), _ptr(out), out.stride(0),
+        out.stride(1), _ptr(lse), _ptr(cu_q), _ptr(kv_lens), _ptr(page_table), page_table.stride(0),
+        page_table.shape[1], batch, max_q, cache.head_dim ** -0.5 if scale is None else scale, window,
+        _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)), "mx_kv_attention")
 
 
 # ---- convenience wrapper ---------------------------------------------------

@@ -1,0 +1,392 @@
+"""The quantised key/value cache on a GPU against the plain 64-bit reference
+(oracle/kv.py): written bytes and values read back bit for bit, attention
+within bounds derived from its roundings."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from canary import Guards
+from oracle import kv
+from tensor_scaling_cast_gb300 import fp8q as F
+
+pytestmark = pytest.mark.gpu
+
+G = Guards(seed=0x4B)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.fail("a CUDA GPU is required for the gpu tests")
+    from tensor_scaling_cast_gb300 import build
+    build.build()
+    F.load()
+    torch.cuda.set_device(0)
+
+
+@pytest.fixture(autouse=True)
+def _guards():
+    G.release()
+    yield
+    G.check_and_release("at the end of the test")
+    assert F.fp8q_pipeline_status() == 0
+
+
+def new_cache(pages, page, heads, dim, fmt, fill=None):
+    """A cache in guarded arrays, of random bytes (fill None) or of one value."""
+    row = dim // 2 if fmt == kv.E2M1 else dim
+    arrays = []
+    for last in (row, dim // 32, row, dim // 32):
+        t = G.empty((pages, heads, page, last))
+        if fill is None:
+            t.copy_(torch.randint(0, 256, t.shape, dtype=torch.uint8))
+        else:
+            t.fill_(fill)
+        arrays.append(t)
+    return F.MXKVCache(*arrays, fmt=fmt)
+
+
+def same(a, b):
+    """Equal values, NaN for NaN, zeros by sign."""
+    a, b = np.asarray(a), np.asarray(b)
+    return np.array_equal(a, b, equal_nan=True) and np.array_equal(np.signbit(a)[~np.isnan(a)], np.signbit(b)[~np.isnan(b)])
+
+
+# ---- write and read ----------------------------------------------------------
+
+COPY = [  # tokens, kv_heads, head_dim, page, fmt, rule, dtype, strided
+    (1, 1, 32, 1, kv.E2M1, kv.FLOOR, torch.bfloat16, False),
+    (1, 8, 128, 16, kv.E2M1, kv.CEIL, torch.bfloat16, True),
+    (37, 3, 96, 4, kv.E2M1, kv.NEAREST, torch.float32, True),
+    (515, 5, 64, 16, kv.E2M1, kv.CEIL, torch.float32, False),
+    (129, 2, 256, 64, kv.E2M1, kv.FLOOR, torch.bfloat16, True),
+    (77, 1, 160, 2, kv.E4M3, kv.FLOOR, torch.bfloat16, True),
+    (300, 4, 128, 32, kv.E4M3, kv.CEIL, torch.float32, False),
+    (64, 7, 64, 128, kv.E5M2, kv.NEAREST, torch.bfloat16, True),
+    (33, 2, 224, 8, kv.E5M2, kv.CEIL, torch.float32, True),
+]
+
+
+@pytest.mark.parametrize("tokens,heads,dim,page,fmt,rule,dtype,strided", COPY)
+def test_write_and_read_are_exact(tokens, heads, dim, page, fmt, rule, dtype, strided):
+    g = torch.Generator().manual_seed(tokens * 1000 + dim)
+    pages = -(-tokens // page) + 3
+    cache = new_cache(pages, page, heads, dim, fmt)
+    before = [t.cpu().numpy().copy() for t in (cache.k_q, cache.k_e8m0, cache.v_q, cache.v_e8m0)]
+    x = torch.randn(tokens, 2 * heads + 1, dim, generator=g) * torch.exp2(
+        torch.randint(-30, 30, (tokens, 2 * heads + 1, 1), generator=g).float())
+    flat = x.view(-1, 32)
+    for i, v in enumerate((0.0, -0.0, float("inf"), float("nan"), 1e-40, 3e38, -6.0, 2.0 ** -126)):
+        if 7 * i < flat.shape[0]:
+            flat[7 * i, : 32 if i in (0, 1, 4, 5, 6, 7) else 3] = v * (1 if i != 5 else 1.1)
+    x = x.to(dtype).cuda()
+    k, v = (x[:, :heads], x[:, heads:2 * heads]) if strided else (x[:, :heads].contiguous(), x[:, heads:2 * heads].contiguous())
+    slots = torch.randperm(pages * page, generator=g)[:tokens]
+    if tokens > 3:
+        slots[1], slots[2] = -1, pages * page + 5          # padding, and past the cache
+    F.mx_kv_write(cache, k, v, slots.cuda(), rule=rule)
+    G.check("after mx_kv_write")
+    keep = ((slots >= 0) & (slots < pages * page)).numpy()
+    at, off = slots.numpy()[keep] // page, slots.numpy()[keep] % page
+    for n, (src, q, e) in enumerate(((k, cache.k_q, cache.k_e8m0), (v, cache.v_q, cache.v_e8m0))):
+        code, e8 = kv.encode(src.float().cpu().numpy(), fmt, rule)
+        want_q, want_e = before[2 * n], before[2 * n + 1]
+        want_q[at, :, off] = kv.pack(code, fmt)[keep]
+        want_e[at, :, off] = e8[keep]
+        assert np.array_equal(q.cpu().numpy(), want_q)
+        assert np.array_equal(e.cpu().numpy(), want_e)
+    for kind in (torch.bfloat16, torch.float32):
+        ko, vo = G.empty((tokens, heads, dim), kind), G.empty((tokens, heads, dim), kind)
+        F.mx_kv_read(cache, slots.cuda(), ko, vo)
+        G.check("after mx_kv_read")
+        for got, q, e in ((ko, cache.k_q, cache.k_e8m0), (vo, cache.v_q, cache.v_e8m0)):
+            want = np.zeros((tokens, heads, dim))
+            want[keep] = kv.decode(q.cpu().numpy()[at, :, off], e.cpu().numpy()[at, :, off], fmt)
+            want = torch.from_numpy(want).float().to(kind).float().numpy()
+            assert same(got.float().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("fmt", [kv.E2M1, kv.E4M3, kv.E5M2])
+def test_read_decodes_every_byte_and_scale(fmt):
+    """All 256 code bytes under all 256 E8M0 bytes."""
+    dim = 256
+    row = dim // 2 if fmt == kv.E2M1 else dim
+    cache = new_cache(256, 2, 1, dim, fmt)
+    codes = torch.arange(256, dtype=torch.uint8).view(2, row) if fmt == kv.E2M1 else \
+        torch.arange(256, dtype=torch.uint8).expand(2, row)
+    cache.k_q.copy_(codes.expand(256, 1, 2, row))
+    cache.v_q.copy_(codes.flip(-1).expand(256, 1, 2, row))
+    e = torch.arange(256, dtype=torch.uint8).view(256, 1, 1, 1).expand(256, 1, 2, 8)
+    cache.k_e8m0.copy_(e)
+    cache.v_e8m0.copy_(e)
+    slots = torch.arange(512, device="cuda")
+    for kind in (torch.bfloat16, torch.float32):
+        k, v = G.empty((512, 1, dim), kind), G.empty((512, 1, dim), kind)
+        F.mx_kv_read(cache, slots, k, v)
+        for got, q in ((k, cache.k_q), (v, cache.v_q)):
+            want = kv.decode(q.cpu().numpy(), cache.k_e8m0.cpu().numpy(), fmt).reshape(512, 1, dim)
+            with np.errstate(over="ignore"):
+                want = torch.from_numpy(want.astype(np.float32)).to(kind).float().numpy()
+            assert same(got.float().cpu().numpy(), want)
+
+
+# ---- attention ---------------------------------------------------------------
+
+def attend_case(lens, nqs, heads, group, dim, page, window=0, seed=0, spread=2, scale=None, q=None, hide=(), extra=0,
+                lse=True):
+    """Runs mx_kv_attention on random codes and checks it against the
+    reference; returns the output.  Everything a query must not see holds
+    0xFF bytes.  hide: (sequence, page number) entries sent out of the cache."""
+    rng = np.random.default_rng(seed)
+    per = [-(-n // page) for n in lens]
+    pages = sum(per) + 2
+    cache = new_cache(pages, page, heads, dim, kv.E2M1, fill=255)
+    width = max(1, max(per)) + extra
+    table = np.full((len(lens), width), -7, dtype=np.int32)
+    order, at = rng.permutation(pages), 0
+    rows = []
+    arrays = [t.cpu().numpy() for t in (cache.k_q, cache.k_e8m0, cache.v_q, cache.v_e8m0)]
+    for b, n in enumerate(lens):
+        table[b, :per[b]] = order[at:at + per[b]]
+        at += per[b]
+        one = []
+        for a in range(2):
+            codes = rng.integers(0, 256, (n, heads, dim // 2), dtype=np.uint8)
+            e8 = (127 - 2 + rng.integers(-spread, spread + 1, (n, heads, dim // 32))).astype(np.uint8)
+            t = np.arange(n)
+            arrays[2 * a][table[b, t // page], :, t % page] = codes
+            arrays[2 * a + 1][table[b, t // page], :, t % page] = e8
+            one.append(kv.decode(codes, e8, kv.E2M1))
+        rows.append(one)
+    for t, a in zip((cache.k_q, cache.k_e8m0, cache.v_q, cache.v_e8m0), arrays):
+        t.copy_(torch.from_numpy(a))
+    for n, (b, p) in enumerate(hide):
+        table[b, p] = (-1, pages, 2 ** 31 - 1)[n % 3]
+    total, q_heads = sum(nqs), heads * group
+    cu = np.concatenate([[0], np.cumsum(nqs)]).astype(np.int32)
+    if q is None:
+        q = torch.from_numpy(rng.standard_normal((total, q_heads, dim)).astype(np.float32)).bfloat16()
+    wide = torch.zeros(total, q_heads + 1, dim + 8, dtype=torch.bfloat16)
+    wide[:, :q_heads, :dim] = q
+    qd = wide.cuda()[:, :q_heads, :dim]
+    out = G.empty((total, q_heads, dim), torch.bfloat16)
+    out_lse = G.full((total, q_heads), 77.0, torch.float32) if lse else None
+    scale = dim ** -0.5 if scale is None else scale
+    tt = torch.from_numpy(table).cuda()
+    max_q = max(1, max(nqs))
+    ws = F.mx_kv_attention_workspace(cache, qd, tt, max_q=max_q)
+    one_each = max(nqs) == min(nqs) == 1
+    args = dict(cu_q=None if one_each else torch.from_numpy(cu).cuda(), max_q=max_q, scale=scale, window=window,
+                workspace=ws)
+    ld = torch.tensor(lens, dtype=torch.int32).cuda()
+    F.mx_kv_attention(cache, qd, out, tt, ld, lse=out_lse, **args)
+    G.check("after mx_kv_attention")
+    first = out.clone()
+    out.zero_()
+    F.mx_kv_attention(cache, qd, out, tt, ld, **args)      # the workspace is ready again, and bits repeat
+    assert torch.equal(first.view(torch.int16), out.view(torch.int16))
+    got = first.float().cpu().numpy().astype(np.float64)
+    qn = q.float().numpy().astype(np.float64)
+    for b, (k, v) in enumerate(rows):
+        r = slice(cu[b], cu[b + 1])
+        gone = np.zeros(lens[b], dtype=bool)
+        for hb, p in hide:
+            if hb == b:
+                gone[p * page:(p + 1) * page] = True
+        for h in range(heads):
+            hs = slice(h * group, (h + 1) * group)
+            want, want_lse = kv.attention(qn[r, hs], k[:, h], v[:, h], scale, window, gone)
+            size, _ = kv.attention(qn[r, hs], k[:, h], np.abs(v[:, h]), scale, window, gone)
+            # the output's rounding (half a bf16 step, 2^-9), and weights of 8 bits or more (2^-9 of
+            # sum p |v|); scores and sums are fp32, far below that.  Weights are held in 16 bits relative
+            # to a query's largest, so what is below 2^-25 of it may be dropped: at most 2^-25 of the
+            # largest value for each key
+            top = np.abs(np.where(np.isfinite(v[:, h]), v[:, h], 0)).max() if lens[b] else 0
+            tol = 2 ** -9 * 1.01 * np.abs(want) + (2 ** -9 + 2 ** -11) * size + lens[b] * 2 ** -25 * top
+            assert np.array_equal(np.isnan(got[r, hs]), np.isnan(want))
+            bad = np.abs(got[r, hs] - want) > tol
+            assert not bad.any(), (b, h, np.argwhere(bad)[:4], got[r, hs][bad][:4], want[bad][:4])
+            if lse and lens[b]:
+                # D fp32 additions of products q k, and a sum of exponentials
+                most = scale * (np.abs(qn[r, hs]).reshape(-1, dim) @ np.abs(k[:, h]).T).max() if nqs[b] else 0
+                lt = 2 ** -22 * dim * most + 2 ** -16
+                gl = out_lse.cpu().numpy()[r, hs]
+                assert np.array_equal(np.isinf(gl), np.isinf(want_lse))
+                fin = np.isfinite(want_lse)
+                assert (np.abs(gl[fin] - want_lse[fin]) <= lt + 2 ** -22 * np.abs(want_lse[fin])).all()
+    return first
+
+
+ATTEND = [  # lens, queries, kv_heads, group, head_dim, page, window
+    ([1], [1], 1, 1, 64, 16, 0),
+    ([2], [1], 1, 1, 128, 1, 0),
+    ([31], [1], 2, 8, 128, 16, 0),
+    ([32, 33, 0, 1], [1, 1, 1, 1], 2, 4, 64, 16, 0),
+    ([1000], [1], 4, 4, 64, 16, 0),
+    ([515, 64, 63, 65, 7], [1] * 5, 3, 5, 128, 4, 0),
+    ([700, 129], [1, 1], 1, 16, 128, 64, 0),
+    ([300], [1], 1, 24, 64, 32, 0),
+    ([2100, 40], [1, 1], 1, 8, 128, 128, 100),
+    ([600, 10], [1, 1], 2, 7, 64, 2, 1),
+    ([100, 5, 0, 3], [4, 4, 4, 0], 2, 4, 128, 16, 0),          # more queries than keys, none at all
+    ([260, 77], [5, 3], 2, 3, 64, 32, 33),
+    ([90], [8], 1, 1, 128, 8, 0),
+    ([128, 200], [128, 30], 2, 4, 128, 16, 0),
+    ([257], [257], 1, 1, 64, 64, 0),
+    ([300, 20, 41], [129, 20, 1], 1, 5, 128, 1, 0),
+    ([400, 150], [100, 150], 2, 2, 64, 16, 50),
+    ([700], [40], 1, 8, 128, 32, 0),
+    ([333], [333], 1, 8, 128, 16, 7),
+    ([10], [50], 1, 4, 128, 16, 0),                            # most queries sit before the first key
+]
+
+
+@pytest.mark.parametrize("lens,nqs,heads,group,dim,page,window", ATTEND)
+def test_attention(lens, nqs, heads, group, dim, page, window):
+    attend_case(lens, nqs, heads, group, dim, page, window, seed=sum(lens) + dim, extra=len(lens) % 3)
+
+
+@pytest.mark.parametrize("nq", [1, 3, 70])
+def test_attention_wide_scales(nq):
+    """Block scales 2^-12 .. 2^8 apart from one another, large scores."""
+    attend_case([500, 90], [nq, nq], 2, 4, 128, 16, seed=nq, spread=8, scale=0.02)
+    attend_case([220], [nq], 1, 2, 64, 16, seed=nq + 1, spread=3, scale=2.0)
+
+
+@pytest.mark.parametrize("nq", [1, 6, 80])
+def test_attention_pages_outside_the_cache_hide_their_tokens(nq):
+    attend_case([300, 64], [nq, nq], 1, 4, 64, 16, seed=3, hide=[(0, 0), (0, 7), (0, 11), (1, 2)])
+    attend_case([90], [nq], 1, 2, 128, 32, seed=4, hide=[(0, 0), (0, 1), (0, 2)])      # nothing left
+
+
+@pytest.mark.parametrize("nq", [1, 4, 66])
+def test_attention_nan_stays_where_it_is_seen(nq):
+    """NaN blocks: a key's reaches every query that sees the token, a value's
+    its 32 columns; a NaN query spoils its own row."""
+    heads, group, dim, page, n = 2, 4, 64, 16, 200
+    g = torch.Generator().manual_seed(nq)
+    cache = new_cache(14, page, heads, dim, kv.E2M1, fill=255)
+    k = torch.randn(n, heads, dim, generator=g)
+    v = torch.randn(n, heads, dim, generator=g)
+    k[n - 2, 0, 40] = float("nan")                             # head 0, seen from position n - 2 on
+    v[50, 1, 3] = float("inf")                                 # head 1, columns 0 .. 31
+    F.mx_kv_write(cache, k.cuda(), v.cuda(), torch.arange(n, device="cuda"), rule=F.MX_CEIL)
+    table = torch.arange(14, dtype=torch.int32, device="cuda")[None]
+    q = torch.randn(nq, heads * group, dim, generator=g).bfloat16()
+    q[0, 7, 5] = float("nan")
+    out = G.empty((nq, heads * group, dim), torch.bfloat16)
+    ws = F.mx_kv_attention_workspace(cache, q.cuda(), table, max_q=nq)
+    F.mx_kv_attention(cache, q.cuda(), out, table, torch.tensor([n], dtype=torch.int32).cuda(),
+                      cu_q=torch.tensor([0, nq], dtype=torch.int32).cuda(), max_q=nq, workspace=ws)
+    want = torch.zeros(nq, heads * group, dim, dtype=torch.bool)
+    pos = torch.arange(n - nq, n)
+    want[pos >= n - 2, :group] = True
+    want[:, group:, :32] = (pos >= 50)[:, None, None]
+    want[0, 7] = True
+    assert torch.equal(torch.isnan(out).cpu(), want)
+
+
+def test_attention_large_queries_and_zero_values():
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(1))
+    attend_case([100, 30], [1, 1], 1, 4, 64, 16, q=(q * 1e20).bfloat16(), scale=1e-20, seed=8)
+    attend_case([100, 30], [1, 1], 1, 4, 64, 16, q=(q * 1e-20).bfloat16(), scale=1e19, seed=9)
+    attend_case([100, 30], [1, 1], 1, 4, 64, 16, q=(q * 0).bfloat16(), seed=10)
+
+
+def test_zero_values_keep_their_share_of_the_weights():
+    """Tokens whose values are all zero (E8M0 byte 0) still count in the sum."""
+    for nq in (1, 70):
+        n = 128
+        cache = new_cache(8, 16, 1, 64, kv.E2M1, fill=0)
+        v = torch.ones(n, 1, 64)
+        v[: n - nq] = 0
+        k = torch.zeros(n, 1, 64)
+        F.mx_kv_write(cache, k.cuda(), v.cuda(), torch.arange(n, device="cuda"))
+        table = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+        q = torch.randn(nq, 2, 64, generator=torch.Generator().manual_seed(nq)).bfloat16().cuda()
+        out = G.empty((nq, 2, 64), torch.bfloat16)
+        ws = F.mx_kv_attention_workspace(cache, q, table, max_q=nq)
+        F.mx_kv_attention(cache, q, out, table, torch.tensor([n], dtype=torch.int32).cuda(),
+                          cu_q=torch.tensor([0, nq], dtype=torch.int32).cuda(), max_q=nq, workspace=ws)
+        want = torch.arange(1, nq + 1) / torch.arange(n - nq + 1, n + 1)     # ones seen / keys seen
+        assert torch.allclose(out.float().cpu(), want[:, None, None].expand(nq, 2, 64), rtol=2 ** -8, atol=0)
+
+
+def test_attention_in_a_graph_sees_new_lengths_on_another_stream():
+    cache = new_cache(40, 16, 2, 128, kv.E2M1, fill=255)
+    n = 600
+    g = torch.Generator().manual_seed(0)
+    k, v = (torch.randn(n, 2, 128, generator=g).cuda() for _ in range(2))
+    F.mx_kv_write(cache, k, v, torch.arange(n, device="cuda"), rule=F.MX_CEIL)
+    table = torch.arange(40, dtype=torch.int32, device="cuda")[None]
+    q = torch.randn(1, 8, 128, generator=g).bfloat16().cuda()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = G.empty((1, 8, 128), torch.bfloat16)
+    ws = F.mx_kv_attention_workspace(cache, q, table)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        F.mx_kv_attention(cache, q, out, table, lens, workspace=ws)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        F.mx_kv_attention(cache, q, out, table, lens, workspace=ws)
+    eager = torch.empty_like(out)
+    for length in (600, 1, 0, 33, 599):
+        lens.fill_(length)
+        graph.replay()
+        torch.cuda.synchronize()
+        F.mx_kv_attention(cache, q, eager, table, lens, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), eager.view(torch.int16))
+
+
+def test_offsets_past_32_bits():
+    """Pages whose codes lie more than 2^32 bytes into the arrays."""
+    heads, dim, page = 8, 128, 64
+    pages = (1 << 32) // (heads * page * dim // 2) + 8
+    q_shape, e_shape = (pages, heads, page, dim // 2), (pages, heads, page, dim // 32)
+    arrays = [torch.empty(s, dtype=torch.uint8, device="cuda") for s in (q_shape, e_shape, q_shape, e_shape)]
+    cache = F.MXKVCache(*arrays, fmt=F.E2M1)
+    n = 150
+    g = torch.Generator().manual_seed(2)
+    k, v = torch.randn(n, heads, dim, generator=g).cuda(), torch.randn(n, heads, dim, generator=g).cuda()
+    slots = torch.arange((pages - 3) * page, (pages - 3) * page + n, device="cuda")
+    F.mx_kv_write(cache, k, v, slots)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    F.mx_kv_read(cache, slots, ko, vo)
+    for src, got in ((k, ko), (v, vo)):
+        code, e8 = kv.encode(src.cpu().numpy(), kv.E2M1)
+        assert same(got.cpu().numpy(), kv.decode(kv.pack(code, kv.E2M1), e8, kv.E2M1))
+    table = torch.arange(pages - 3, pages, dtype=torch.int32, device="cuda")[None]
+    for nq in (1, 100):
+        q = torch.randn(nq, 2 * heads, dim, generator=g).bfloat16()
+        out = G.empty((nq, 2 * heads, dim), torch.bfloat16)
+        ws = F.mx_kv_attention_workspace(cache, q.cuda(), table, max_q=nq)
+        F.mx_kv_attention(cache, q.cuda(), out, table, torch.tensor([n], dtype=torch.int32).cuda(),
+                          cu_q=torch.tensor([0, nq], dtype=torch.int32).cuda(), max_q=nq, workspace=ws)
+        for h in (0, 7):
+            hs = slice(2 * h, 2 * h + 2)
+            a = [t.double().cpu().numpy()[:, h] for t in (ko, vo)]
+            qn = q[:, hs].double().numpy()
+            want, _ = kv.attention(qn, a[0], a[1], dim ** -0.5)
+            size, _ = kv.attention(qn, a[0], np.abs(a[1]), dim ** -0.5)
+            err = np.abs(out[:, hs].double().cpu().numpy() - want)
+            assert (err <= 2 ** -9 * 1.01 * np.abs(want) + (2 ** -9 + 2 ** -11) * size).all()
+
+
+def test_workspace_too_small_is_refused():
+    cache = new_cache(64, 128, 1, 128, kv.E2M1, fill=0)
+    table = torch.arange(64, dtype=torch.int32, device="cuda")[None]
+    q = torch.zeros(1, 8, 128, dtype=torch.bfloat16, device="cuda")
+    ws = F.mx_kv_attention_workspace(cache, q, table)
+    if ws is None:
+        pytest.skip("these sizes need no workspace")
+    lens = torch.tensor([8192], dtype=torch.int32, device="cuda")
+    with pytest.raises(F.Fp8qError) as e:
+        F.mx_kv_attention(cache, q, torch.empty_like(q), table, lens, workspace=ws[:-1])
+    assert e.value.status == -8
+    with pytest.raises(F.Fp8qError):
+        F.mx_kv_attention(cache, q, torch.empty_like(q), table, lens)
