@@ -109,7 +109,12 @@ FP8Q_API int64_t mx_kv_attention_workspace(const mx_kv_cache* c, int64_t total_q
   KvShape s;
   int st = check_attention(c, total_q, q_heads, batch, max_q, table_width, &s);
   if (st != FP8Q_OK) return st;
-  return kv_attention_workspace(s, q_heads, total_q, batch, max_q, table_width, sm_count(device_of_current()));
+  if (total_q == 0 || batch == 0) return 0;
+  if (max_q > total_q) max_q = (int)total_q;
+  int64_t bytes = 0;
+  const cudaError_t e = kv_attention_workspace(s, q_heads, batch, max_q, table_width,
+                                               sm_count(device_of_current()), &bytes);
+  return e == cudaSuccess ? bytes : record_cuda_error(e);
 }
 
 FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int64_t total_q, int q_heads,
@@ -130,7 +135,10 @@ FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int
   if (st == FP8Q_OK) st = check_rows(out, dtype, total_q, q_heads, out_token_stride, out_head_stride);
   if (st != FP8Q_OK) return st;
   const int sms = sm_count(device_of_current());
-  const int64_t need = kv_attention_workspace(a.shape, q_heads, total_q, batch, max_q, table_width, sms);
+  if (max_q > total_q) max_q = (int)total_q;
+  int64_t need = 0;
+  const cudaError_t we = kv_attention_workspace(a.shape, q_heads, batch, max_q, table_width, sms, &need);
+  if (we != cudaSuccess) return record_cuda_error(we);
   if (need > workspace_bytes) return FP8Q_ESIZE;
   if (need > 0 && !workspace) return FP8Q_EINVAL;
   if (need > 0 && !kv_aligned16(workspace)) return FP8Q_EALIGN;
@@ -150,10 +158,10 @@ FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int
   a.table_width = table_width;
   a.batch = batch;
   a.total_q = (int32_t)total_q;
-  a.max_q = max_q < total_q ? max_q : (int32_t)total_q;
+  a.max_q = max_q;
   a.q_heads = q_heads;
   a.group = q_heads / c->kv_heads;
-  a.window = window;
+  a.window = window > 0x3FFFFFFF ? 0 : window;   // no sequence is that long
   a.scale = scale;
   int launches = 0;
   const cudaError_t e = launch_kv_attention(a, workspace, sms, reinterpret_cast<cudaStream_t>(stream), &launches);

@@ -89,9 +89,16 @@ __global__ void __launch_bounds__(32 * kAttnWarps) kv_attention_kernel(const __g
   if (a.lse && lane == 0) a.lse[row * a.q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-int64_t kv_attention_workspace(const KvShape&, int, int64_t, int, int, int, int) { return 0; }
+cudaError_t kv_attention_workspace(const KvShape& s, int q_heads, int batch, int max_q, int table_width, int sms,
+                                   int64_t* bytes) {
+  *bytes = 0;
+  if (kv_decode_takes(max_q, q_heads / s.heads))
+    return kv_decode_workspace(s, q_heads / s.heads, batch, max_q, table_width, sms, bytes);
+  return cudaSuccess;
+}
 
-cudaError_t launch_kv_attention(const KvAttn& a, void*, int, cudaStream_t st, int* launches) {
+cudaError_t launch_kv_attention(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches) {
+  if (kv_decode_takes(a.max_q, a.group)) return launch_kv_decode(a, workspace, sms, st, launches);
   const dim3 grid((a.q_heads + kAttnWarps - 1) / kAttnWarps, a.max_q, a.batch);
   if (a.shape.dim == 64) kv_attention_kernel<64><<<grid, 32 * kAttnWarps, 0, st>>>(a);
   else kv_attention_kernel<128><<<grid, 32 * kAttnWarps, 0, st>>>(a);

@@ -1,0 +1,707 @@
+// Attention of a few query rows per key/value head over the 4-bit cache
+// (decoding one token, or checking a few).
+//
+// Mathematics.  With a row's codes c (E2M1) and block exponents E, a score is
+//   x = scale * log2(e) * sum_blocks 2^E * (q . c)
+// and the output sum_j 2^(x_j - M) v_j over the same factors' sum.  The codes
+// are exact in 16-bit floats, so both products run on them unscaled: the key
+// scales multiply the fp32 sums of each block, the value scales the weights.
+// Values are held relative to the largest block scale 2^R of their 32 tokens,
+// and the running reference M is of x + R, so that the weights p = 2^(x + R -
+// M) stay at or below 2^8 in f16 whatever the scales are; the softmax sum
+// takes p * 2^-R.  M moves only when a tile passes it by 2^8 (one vote per
+// tile), which is when the sums are rescaled.
+//
+// What bounds it: 68 bytes of cache per token and head at D = 128 against 512
+// multiply-adds for each query row, HBM as long as the unpacking keeps up:
+// the codes of 8 tokens cross the SM in 80 instructions.  mma.sync and not
+// tcgen05: with 16 tokens x 8 query rows a product it takes 2 of the 23 issue
+// slots that a token has at the full HBM rate, its operands come straight
+// from the unpacked registers, and nothing waits on a tensor-memory round
+// trip.
+//
+// Layout.  A warp owns tiles of 32 tokens, copied by cp.async into a ring of
+// its own (no CTA barrier while it streams).  Keys are the A operand (16
+// tokens x 16 columns, the columns of a block permuted alike in q so that a
+// lane's 32-bit word of codes is one lane's share of two products); values
+// are the A operand of the transposed product (16 columns x 16 tokens), read
+// by ldmatrix.trans, which pairs a token's codes with its neighbour's.  The
+// scores come out with tokens down and query rows across, so that a weight
+// tile needs one movmatrix per 8 x 8 to become the B operand.
+//
+// Work is split over the tiles of all sequences and heads: CTA i takes tiles
+// [i * per, (i + 1) * per) in (sequence, head) order, so that uneven lengths
+// fill the GPU evenly and the host needs to know none of them.  A (sequence,
+// head) that spans several CTAs is joined by the last of them to arrive, in
+// the order of the tiles (the result does not depend on which that is).
+#include "kv_device.cuh"
+
+namespace fp8q {
+
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecStages = 3;
+constexpr int kTile = 32;                 // tokens of a warp tile
+constexpr int kMinTiles = 16;             // tiles of a CTA, at least
+constexpr float kNoMax = -3.0e38f;        // reference before the first score
+constexpr float kSlack = 8.0f;            // weights reach 2^kSlack before M moves
+constexpr int kMinScale = 127 - 80;       // R stays within [-80, 126] (as E8M0 bytes): p * 2^-R is
+constexpr int kMaxScale = 127 + 126;      // finite and 2^-R normal
+constexpr int kMaxGrid = 4096;            // tickets of a workspace
+
+template <int D>
+struct DecSmem {
+  static constexpr int kRow = D / 2;      // bytes of a row of codes
+  static constexpr int kBlocks = D / 32;
+  struct Stage {
+    uint8_t k[kTile * kRow];
+    uint8_t v[kTile * kRow];
+    uint8_t ke[kTile * kBlocks];
+    uint8_t ve[kTile * kBlocks];
+  };
+  struct Warp {
+    Stage stage[kDecStages];
+    __half factor[kBlocks][kTile];        // value scales of the tile being used
+    uint32_t valid[kDecStages];           // tokens of the stage that exist
+    uint32_t pad[4 - kDecStages % 4];
+  };
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  if (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// d += a (16 x 16, row) * b (16 x 8, column), f16 in, fp32 sums.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two E8M0 bytes (the low half of w) -> 2^(byte - 127), NaN for 0xFF.
+__device__ __forceinline__ float2 e8m0x2_f32(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %1;\n cvt.rn.bf16x2.ue8m0x2 %0, a;\n}" : "=r"(r) : "r"(w));
+  return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
+}
+
+// Chunk c (16 bytes) of row r of a code tile: swizzled so that the eight rows
+// of an 8 x 8 load fall on different banks.
+template <int D>
+__device__ __forceinline__ uint32_t code_offset(int r, int c) {
+  return D == 128 ? r * 64 + ((c ^ (r >> 1)) & 3) * 16 : r * 32 + ((c ^ (r >> 2)) & 1) * 16;
+}
+
+// The part of one sequence that a call has to visit.
+struct DecSeq {
+  int q0, nq, len, tile0, tiles;     // first query row, queries, keys, first tile, tiles
+};
+__device__ __forceinline__ DecSeq dec_seq(const KvAttn& a, int b) {
+  DecSeq s;
+  s.q0 = a.cu_q ? a.cu_q[b] : b;
+  s.nq = a.cu_q ? a.cu_q[b + 1] - s.q0 : 1;
+  s.q0 = max(s.q0, 0);
+  s.nq = max(0, min(min(s.nq, a.max_q), a.total_q - s.q0));
+  const int64_t most = (int64_t)a.table_width << a.shape.page_shift;
+  s.len = (int)min((int64_t)max(a.kv_lens[b], 0), most);
+  const int first = a.window > 0 ? max(0, s.len - s.nq - a.window + 1) : 0;   // oldest key any query sees
+  s.tile0 = first / kTile;
+  // a sequence with queries and no keys still has its zeros to write
+  s.tiles = s.nq == 0 ? 0 : max(1, (s.len + kTile - 1) / kTile - s.tile0);
+  return s;
+}
+
+struct DecPlan {
+  uint32_t* ticket;      // [kMaxGrid], zero between calls
+  float* part;           // [2 * grid][rows * (D + 2)]
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
+kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPlan plan) {
+  constexpr int NB = D / 32, RB = D / 2, ROWS = 8 * NT;
+  using Smem = DecSmem<D>;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int li = lane >> 2, lc = lane & 3;
+  typename Smem::Warp& sm = reinterpret_cast<typename Smem::Warp*>(smem_raw)[warp];
+  __shared__ long long s_scan[kDecThreads / 32 + 1];
+  __shared__ int s_start[2];
+  __shared__ long long s_before;
+  __shared__ uint32_t s_last;
+
+  // ---- this CTA's range of tiles: a scan of the sequences' tile counts
+  const int per_thread = (a.batch + kDecThreads - 1) / kDecThreads;
+  const int b_lo = min(a.batch, (int)threadIdx.x * per_thread), b_hi = min(a.batch, b_lo + per_thread);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += (long long)dec_seq(a, b).tiles * a.shape.heads;
+  long long incl = mine;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, x);
+    if (lane >= x) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  const long long per = max((long long)kMinTiles, (total + gridDim.x - 1) / gridDim.x);
+  const long long begin = (long long)blockIdx.x * per, end = min(total, begin + per);
+  if (begin >= end) return;
+  if (before <= begin && begin < before + mine) {
+    int b = b_lo;
+    for (; b < b_hi; ++b) {
+      const long long n = (long long)dec_seq(a, b).tiles * a.shape.heads;
+      if (begin < before + n) break;
+      before += n;
+    }
+    s_start[0] = b;
+    s_before = before;
+  }
+  __syncthreads();
+  int b = s_start[0];
+  long long seg0 = s_before;                    // global tile of (b, head 0)
+  DecSeq sq = dec_seq(a, b);
+  int head = (int)((begin - seg0) / sq.tiles);
+  seg0 += (long long)head * sq.tiles;
+
+  for (long long at = begin; at < end;) {
+    // ---- one (sequence, head): tiles [t0, t1) of it
+    const int t0 = (int)(at - seg0), t1 = (int)min((long long)sq.tiles, end - seg0);
+    const int rows = sq.nq * a.group;
+    const int n_mine = t1 - t0 > warp ? (t1 - t0 - warp + kDecWarps - 1) / kDecWarps : 0;
+
+    // ---- queries: f16, each row scaled by a power of two to a largest
+    // magnitude in [2^14, 2^15), which keeps bf16 exact down to 2^-29 of it
+    uint32_t qf[NT][NB][4];
+    float fx[NT][2];                             // score factor of query rows 2 lc, 2 lc + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + li;
+      const bool on = r < rows;
+      const int qi = on ? r / a.group : 0, g = on ? r - qi * a.group : 0;
+      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)(sq.q0 + qi) * a.q_tok +
+                               (int64_t)(head * a.group + g) * a.q_head + lc * 8;
+      uint4 w[NB];
+      uint32_t m = 0;
+#pragma unroll
+      for (int x = 0; x < NB; ++x) {
+        w[x] = on ? *reinterpret_cast<const uint4*>(q + x * 32) : make_uint4(0, 0, 0, 0);
+        m = vmax_u16x2(m, absmax_load<FP8Q_BF16>(w[x]));
+      }
+      m = unpack_max<FP8Q_BF16>(m);
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      const int e = m == 0 ? 0 : max(-112, (int)(m >> 23) - 127) - 14;   // q = q' * 2^e, e in [-126, 113]
+      const float s = pow2f(-e);
+      float f = a.scale * 1.4426950408889634f * pow2f(e);
+      if (m >= 0x7F800000u) f = __uint_as_float(0x7FFFFFFFu);            // NaN or Inf: the row is NaN
+#pragma unroll
+      for (int x = 0; x < NB; ++x) {
+        const uint32_t ws[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          qf[nt][x][y] = cvt_f16x2(__uint_as_float(ws[y] << 16) * s, __uint_as_float(ws[y] & 0xFFFF0000u) * s);
+      }
+      fx[nt][0] = __shfl_sync(0xFFFFFFFFu, f, lc * 8);
+      fx[nt][1] = __shfl_sync(0xFFFFFFFFu, f, lc * 8 + 4);
+    }
+
+    float o[NT][NB][2][4];
+    float mref[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) { mref[nt][x] = kNoMax; l[nt][x] = 0.0f; }
+#pragma unroll
+      for (int x = 0; x < NB; ++x)
+#pragma unroll
+        for (int y = 0; y < 8; ++y) o[nt][x][y >> 2][y & 3] = 0.0f;
+    }
+
+    const int pos0 = sq.len - sq.nq;             // position of query 0
+    const int32_t* table = a.table + b * a.table_stride;
+    // token of this lane in the warp's k-th tile, and the page that holds it
+    const int tok0 = (sq.tile0 + t0 + warp) * kTile + lane;
+    auto page_of = [&](int k) {
+      const int tok = tok0 + k * (kDecWarps * kTile);
+      return k < n_mine && tok < sq.len ? table[tok >> a.shape.page_shift] : -1;
+    };
+    const int page_mask = (1 << a.shape.page_shift) - 1;
+    auto issue = [&](int k, int page) {
+      if (k < n_mine) {
+        const int st = k % kDecStages;
+        const int tok = tok0 + k * (kDecWarps * kTile);
+        const int64_t slot = ((int64_t)page << a.shape.page_shift) + (tok & page_mask);
+        const bool ok = page >= 0 && slot < a.shape.slots;
+        const int64_t row = ok ? kv_row(a.shape, slot, head) : 0;
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok);
+        if (lane == 0) sm.valid[st] = valid;
+        constexpr int CH = RB / 16;              // 16-byte chunks of a row
+        const uint32_t kd = smem_u32(sm.stage[st].k), vd = smem_u32(sm.stage[st].v);
+#pragma unroll
+        for (int x = 0; x < CH; ++x) {
+          const int r = x * (32 / CH) + lane / CH, c = lane % CH;
+          const int64_t rr = __shfl_sync(0xFFFFFFFFu, row, r);
+          const bool on = (valid >> r) & 1;
+          const uint32_t off = code_offset<D>(r, c);
+          cp_async16(kd + off, a.k.q + rr * RB + c * 16, on);
+          cp_async16(vd + off, a.v.q + rr * RB + c * 16, on);
+        }
+        if (D == 128) {
+          cp_async4(smem_u32(sm.stage[st].ke) + lane * 4, a.k.e8m0 + row * 4, ok);
+          cp_async4(smem_u32(sm.stage[st].ve) + lane * 4, a.v.e8m0 + row * 4, ok);
+        } else if (a.shape.page_shift > 0) {     // two tokens' scales are one word
+          const bool pair = (valid >> (lane & ~1)) & 1;
+          if (!(lane & 1)) {
+            cp_async4(smem_u32(sm.stage[st].ke) + lane * 2, a.k.e8m0 + row * 2, pair);
+            cp_async4(smem_u32(sm.stage[st].ve) + lane * 2, a.v.e8m0 + row * 2, pair);
+          }
+        } else {
+          const uint16_t ke = ok ? *reinterpret_cast<const uint16_t*>(a.k.e8m0 + row * 2) : 0;
+          const uint16_t ve = ok ? *reinterpret_cast<const uint16_t*>(a.v.e8m0 + row * 2) : 0;
+          reinterpret_cast<uint16_t*>(sm.stage[st].ke)[lane] = ke;
+          reinterpret_cast<uint16_t*>(sm.stage[st].ve)[lane] = ve;
+        }
+      }
+      cp_commit();
+    };
+
+#pragma unroll
+    for (int k = 0; k < kDecStages - 1; ++k) issue(k, page_of(k));
+    int page_next = page_of(kDecStages - 1);
+
+    for (int k = 0; k < n_mine; ++k) {
+      cp_wait<kDecStages - 2>();
+      __syncwarp();
+      const int st = k % kDecStages;
+      const typename Smem::Stage& tile = sm.stage[st];
+      const uint32_t valid = sm.valid[st];
+      const int tok = (sq.tile0 + t0 + warp + k * kDecWarps) * kTile;
+
+      // ---- value scales: one token per lane, relative to the tile's largest
+      float rv;
+      bool v_nan;
+      {
+        const uint32_t w = NB == 4 ? reinterpret_cast<const uint32_t*>(tile.ve)[lane]
+                                   : reinterpret_cast<const uint16_t*>(tile.ve)[lane];
+        const bool ok = (valid >> lane) & 1;
+        uint32_t e[NB], top = 0;
+        bool bad = false;
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+          e[x] = (w >> (8 * x)) & 0xFFu;
+          const bool n = e[x] == 255u;
+          bad |= n;
+          top = max(top, n ? 0u : e[x]);
+        }
+        top = __reduce_max_sync(0xFFFFFFFFu, ok ? top : 0u);
+        v_nan = __any_sync(0xFFFFFFFFu, ok && bad);
+        top = min(max(top, (uint32_t)kMinScale), (uint32_t)kMaxScale);
+        rv = (float)((int)top - 127);
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+          const int d = min(126, (int)(top - e[x]));
+          float f = __uint_as_float((uint32_t)(127 - d) << 23);
+          if (e[x] == 255u) f = __uint_as_float(0x7FFFFFFFu);
+          sm.factor[x][lane] = __float2half_rn(ok ? f : 0.0f);
+        }
+        __syncwarp();
+      }
+
+      // ---- scores: tokens down, query rows across
+      float s[2][NT][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) s[u][nt][y] = 0.0f;
+        uint32_t kw[2][NB];                      // [token half][block]
+        const uint32_t base = smem_u32(tile.k);
+        if (D == 128) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[4];
+            ldmatrix4<false>(r, base + code_offset<D>(u * 16 + h * 8 + (lane & 7), lane >> 3));
+#pragma unroll
+            for (int x = 0; x < NB; ++x) kw[h][x] = r[x & 3];
+          }
+        } else {
+          uint32_t r[4];
+          ldmatrix4<false>(r, base + code_offset<D>(u * 16 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1));
+          kw[0][0] = r[0]; kw[0][1] = r[1]; kw[1][0] = r[2]; kw[1][1] = r[3];
+        }
+        float ks[2][NB];                         // scales of tokens li, li + 8
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int t = u * 16 + h * 8 + li;
+          const uint32_t w = NB == 4 ? reinterpret_cast<const uint32_t*>(tile.ke)[t]
+                                     : reinterpret_cast<const uint16_t*>(tile.ke)[t];
+#pragma unroll
+          for (int x = 0; x < NB; x += 2) {
+            const float2 f = e8m0x2_f32(x ? w >> 16 : w);
+            ks[h][x] = f.x;
+            ks[h][x + 1] = f.y;
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+          uint32_t ka[4], kb[4];
+          e2m1x8_f16(kw[0][x], ka);
+          e2m1x8_f16(kw[1][x], kb);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma(c, ka[0], kb[0], ka[1], kb[1], qf[nt][x][0], qf[nt][x][1]);
+            mma(c, ka[2], kb[2], ka[3], kb[3], qf[nt][x][2], qf[nt][x][3]);
+            s[u][nt][0] += c[0] * ks[0][x];
+            s[u][nt][1] += c[1] * ks[0][x];
+            s[u][nt][2] += c[2] * ks[1][x];
+            s[u][nt][3] += c[3] * ks[1][x];
+          }
+        }
+      }
+
+      // ---- masks, only where the tile has any
+      const bool edge = valid != 0xFFFFFFFFu || tok + kTile - 1 > pos0 ||
+                        (a.window > 0 && tok <= pos0 + sq.nq - 1 - a.window);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) s[u][nt][y] *= fx[nt][y & 1];
+      if (edge) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int pos = pos0 + (nt * 8 + lc * 2 + y) / a.group;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const int t = z * 8 + li, j = tok + t;
+              const bool seen = ((valid >> t) & 1) && j <= pos && (a.window == 0 || j > pos - a.window);
+              float& x = s[z >> 1][nt][(z & 1) * 2 + y];
+              x = seen ? x : -INFINITY;
+            }
+          }
+      }
+
+      // ---- the reference moves when some score passes it by 2^kSlack
+      bool move = false;
+      float top[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          top[nt][y] = fmaxf(fmaxf(s[0][nt][y], s[0][nt][y + 2]), fmaxf(s[1][nt][y], s[1][nt][y + 2])) + rv;
+          move |= top[nt][y] > mref[nt][y] + kSlack;
+        }
+      if (__any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float t = top[nt][y];
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, x));
+            t = fmaxf(t, mref[nt][y]);
+            const float fix = ex2(mref[nt][y] - t);
+            mref[nt][y] = t;
+            l[nt][y] *= fix;
+#pragma unroll
+            for (int x = 0; x < NB; ++x)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                o[nt][x][z][y] *= fix;
+                o[nt][x][z][y + 2] *= fix;
+              }
+          }
+      }
+
+      // ---- weights, their sum, and the second product
+      const float unscale = pow2f(-(int)rv);
+      uint32_t p[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float a0 = ex2(s[u][nt][0] + (rv - mref[nt][0])), a1 = ex2(s[u][nt][1] + (rv - mref[nt][1]));
+          const float a2 = ex2(s[u][nt][2] + (rv - mref[nt][0])), a3 = ex2(s[u][nt][3] + (rv - mref[nt][1]));
+          l[nt][0] += (a0 + a2) * unscale;
+          l[nt][1] += (a1 + a3) * unscale;
+          p[u][nt][0] = movmatrix(cvt_f16x2(a0, a1));
+          p[u][nt][1] = movmatrix(cvt_f16x2(a2, a3));
+        }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t vw[2][NB];                      // [token half][block]: codes 4 li .. 4 li + 3 of tokens 2 lc, 2 lc + 1
+        const uint32_t base = smem_u32(tile.v);
+        if (D == 128) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[4];
+            ldmatrix4<true>(r, base + code_offset<D>(u * 16 + h * 8 + (lane & 7), lane >> 3));
+#pragma unroll
+            for (int x = 0; x < NB; ++x) vw[h][x] = r[x & 3];
+          }
+        } else {
+          uint32_t r[4];
+          ldmatrix4<true>(r, base + code_offset<D>(u * 16 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1));
+          vw[0][0] = r[0]; vw[0][1] = r[1]; vw[1][0] = r[2]; vw[1][1] = r[3];
+        }
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+          // bytes that pair a token's code with its neighbour's
+          const uint32_t even = __byte_perm(vw[0][x], vw[1][x], 0x5410), odd = __byte_perm(vw[0][x], vw[1][x], 0x7632);
+          const uint32_t m = 0x0F0F0F0Fu;
+          uint32_t c02[4], c13[4];               // columns 0, 2 then 1, 3; token halves 0, 1
+          e2m1x8_f16((even & m) | ((odd << 4) & ~m), c02);
+          e2m1x8_f16(((even >> 4) & m) | (odd & ~m), c13);
+          const uint32_t f0 = *reinterpret_cast<const uint32_t*>(&sm.factor[x][u * 16 + lc * 2]);
+          const uint32_t f1 = *reinterpret_cast<const uint32_t*>(&sm.factor[x][u * 16 + 8 + lc * 2]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint32_t b0 = mul_f16x2(p[u][nt][0], f0), b1 = mul_f16x2(p[u][nt][1], f1);
+            if (edge && v_nan) {                 // a hidden token's NaN scale must not reach its zero weight
+              const int pos = pos0 + (nt * 8 + li) / a.group;
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const int j = tok + u * 16 + (z >> 1) * 8 + lc * 2 + (z & 1);
+                if (j > pos || (a.window > 0 && j <= pos - a.window))
+                  (z >> 1 ? b1 : b0) &= (z & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+              }
+            }
+            mma(o[nt][x][0], c02[0], c13[0], c02[2], c13[2], b0, b1);
+            mma(o[nt][x][1], c02[1], c13[1], c02[3], c13[3], b0, b1);
+          }
+        }
+      }
+      __syncwarp();
+      issue(k + kDecStages - 1, page_next);
+      page_next = page_of(k + kDecStages);
+    }
+
+    // ---- join the warps: sums of a row over its lanes, then over the warps
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][y] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][y], x);
+    cp_wait<0>();
+    __syncthreads();                             // the rings are free
+    float* so = reinterpret_cast<float*>(smem_raw) + warp * ROWS * (D + 2);   // [rows][D], then M, then l
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = nt * 8 + lc * 2 + y;
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+          float* d = so + r * D + x * 32 + li * 4;
+          d[0] = o[nt][x][0][y];
+          d[1] = o[nt][x][0][y + 2];
+          d[2] = o[nt][x][1][y];
+          d[3] = o[nt][x][1][y + 2];
+        }
+        if (li == 0) {
+          so[ROWS * D + r] = mref[nt][y];
+          so[ROWS * D + ROWS + r] = l[nt][y];
+        }
+      }
+    __syncthreads();
+
+    const bool whole = t0 == 0 && t1 == sq.tiles;
+    const float* src = reinterpret_cast<const float*>(smem_raw);
+    // parts: [n] of stride `stride`, each [rows][D], M[rows], l[rows]; a NULL
+    // dst gives the output itself
+    auto join = [&](auto part_at, int n, float* dst) {
+      for (int w = threadIdx.x; w < rows * (D / 4); w += kDecThreads) {
+        const int r = w / (D / 4), c = w % (D / 4);
+        float m = kNoMax;
+        for (int i = 0; i < n; ++i) m = fmaxf(m, part_at(i)[ROWS * D + r]);
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float sum = 0.0f;
+        for (int i = 0; i < n; ++i) {
+          const float* q = part_at(i);
+          const float f = ex2(q[ROWS * D + r] - m);
+          const float4 v = *reinterpret_cast<const float4*>(q + r * D + c * 4);
+          s.x += v.x * f;
+          s.y += v.y * f;
+          s.z += v.z * f;
+          s.w += v.w * f;
+          sum += q[ROWS * D + ROWS + r] * f;
+        }
+        if (dst) {
+          *reinterpret_cast<float4*>(dst + r * D + c * 4) = s;
+          if (c == 0) {
+            dst[ROWS * D + r] = m;
+            dst[ROWS * D + ROWS + r] = sum;
+          }
+        } else {
+          const int qi = r / a.group, h = head * a.group + r - qi * a.group;
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)(sq.q0 + qi) * a.out_tok +
+                               (int64_t)h * a.out_head + c * 4;
+          uint2 v;
+          v.x = sum == 0.0f ? 0u : cvt_bf16x2(s.x * inv, s.y * inv);
+          v.y = sum == 0.0f ? 0u : cvt_bf16x2(s.z * inv, s.w * inv);
+          *reinterpret_cast<uint2*>(out) = v;
+          if (a.lse && c == 0)
+            a.lse[(int64_t)(sq.q0 + qi) * a.q_heads + h] =
+                sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+        }
+      }
+    };
+    constexpr int PART = ROWS * (D + 2);
+    if (whole) {
+      join([&](int i) { return src + i * PART; }, kDecWarps, static_cast<float*>(nullptr));
+      __syncthreads();
+    } else {
+      // parts of this (sequence, head): CTAs first .. last; a CTA's slot is 0
+      // where the (sequence, head) covers the start of its range, else 1
+      const long long first = seg0 / per, last = (seg0 + sq.tiles - 1) / per;
+      float* mine_part = plan.part + (2 * (long long)blockIdx.x + (seg0 <= begin ? 0 : 1)) * PART;
+      join([&](int i) { return src + i * PART; }, kDecWarps, mine_part);
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        uint32_t* t = plan.ticket + first;       // a CTA starts at most one that others go on with
+        const uint32_t got = atomicAdd(t, 1u);
+        s_last = got == (uint32_t)(last - first);
+        if (s_last) *t = 0;
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        join([&](int i) {
+          const long long c = first + i;
+          return const_cast<const float*>(plan.part) + (2 * c + (seg0 <= c * per ? 0 : 1)) * PART;
+        }, (int)(last - first) + 1, static_cast<float*>(nullptr));
+      }
+      __syncthreads();
+    }
+
+    // ---- the next (sequence, head)
+    at = seg0 + t1;
+    seg0 += sq.tiles;
+    if (++head == a.shape.heads) {
+      head = 0;
+      if (at < end) {
+        do sq = dec_seq(a, ++b);
+        while (sq.tiles == 0);
+      }
+    }
+  }
+}
+
+// ---- host side ---------------------------------------------------------------
+
+static int dec_nt(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
+
+template <int D, int NT>
+static int dec_smem() {
+  const int ring = kDecWarps * (int)sizeof(typename DecSmem<D>::Warp), join = kDecWarps * 8 * NT * (D + 2) * 4;
+  return ring > join ? ring : join;
+}
+
+struct DecLaunch {
+  const void* kernel;
+  int smem, nt;
+};
+template <int D>
+static DecLaunch dec_pick(int nt) {
+  switch (nt) {
+    case 1: return {reinterpret_cast<const void*>(kv_decode_kernel<D, 1>), dec_smem<D, 1>(), 1};
+    case 2: return {reinterpret_cast<const void*>(kv_decode_kernel<D, 2>), dec_smem<D, 2>(), 2};
+    case 3: return {reinterpret_cast<const void*>(kv_decode_kernel<D, 3>), dec_smem<D, 3>(), 3};
+    default: return {reinterpret_cast<const void*>(kv_decode_kernel<D, 4>), dec_smem<D, 4>(), 4};
+  }
+}
+
+// CTAs of a call: as many as are resident at once, or one per kMinTiles tiles
+// of the longest the sequences can be, if that is fewer.
+static cudaError_t dec_grid(const DecLaunch& k, const KvShape& s, int batch, int table_width, int sms, int* grid) {
+  int occ = 1;
+  const cudaError_t e = kernel_occupancy(k.kernel, kDecThreads, k.smem, &occ);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (((int64_t)table_width << s.page_shift) + kTile - 1) / kTile;
+  const int64_t most = (tiles * batch * s.heads + kMinTiles - 1) / kMinTiles;
+  int64_t n = most < (int64_t)sms * occ ? most : (int64_t)sms * occ;
+  *grid = (int)(n < kMaxGrid ? n : kMaxGrid);
+  return cudaSuccess;
+}
+
+bool kv_decode_takes(int max_q, int group) { return (int64_t)max_q * group <= 32; }
+
+cudaError_t kv_decode_workspace(const KvShape& s, int group, int batch, int max_q, int table_width, int sms,
+                                int64_t* bytes) {
+  const int nt = dec_nt(max_q * group);
+  const DecLaunch k = s.dim == 128 ? dec_pick<128>(nt) : dec_pick<64>(nt);
+  int grid = 0;
+  const cudaError_t e = dec_grid(k, s, batch, table_width, sms, &grid);
+  *bytes = grid < 2 ? 0 : kMaxGrid * 4 + (int64_t)grid * 2 * 8 * nt * (s.dim + 2) * 4;
+  return e;
+}
+
+cudaError_t launch_kv_decode(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches) {
+  const int nt = dec_nt(a.max_q * a.group);
+  const DecLaunch k = a.shape.dim == 128 ? dec_pick<128>(nt) : dec_pick<64>(nt);
+  int grid = 0;
+  cudaError_t e = dec_grid(k, a.shape, a.batch, a.table_width, sms, &grid);
+  if (e != cudaSuccess) return e;
+  DecPlan plan;
+  plan.ticket = static_cast<uint32_t*>(workspace);
+  plan.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMaxGrid * 4);
+  void* args[2] = {const_cast<KvAttn*>(&a), &plan};
+  e = cudaLaunchKernel(k.kernel, dim3(grid), dim3(kDecThreads), args, (size_t)k.smem, st);
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
+}  // namespace fp8q

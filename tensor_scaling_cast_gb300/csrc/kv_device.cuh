@@ -147,8 +147,14 @@ struct KvAttn {
   int32_t table_width, batch, total_q, max_q, q_heads, group, window;
   float scale;
 };
-int64_t kv_attention_workspace(const KvShape& s, int q_heads, int64_t total_q, int batch, int max_q,
-                               int table_width, int sms);
+// Few query rows per key/value head (kv_decode.cu).
+bool kv_decode_takes(int max_q, int group);
+cudaError_t kv_decode_workspace(const KvShape& s, int group, int batch, int max_q, int table_width, int sms,
+                                int64_t* bytes);
+cudaError_t launch_kv_decode(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches);
+// Any call: the kernel that fits it (kv_attention.cu).
+cudaError_t kv_attention_workspace(const KvShape& s, int q_heads, int batch, int max_q, int table_width, int sms,
+                                   int64_t* bytes);
 cudaError_t launch_kv_attention(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches);
 
 }  // namespace fp8q
