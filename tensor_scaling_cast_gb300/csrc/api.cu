@@ -15,6 +15,7 @@
 
 #include "fp8q.h"
 #include "fp8q_internal.cuh"
+#include "kv_device.cuh"
 #include "mx_device.cuh"
 
 namespace fp8q {
@@ -201,10 +202,11 @@ FP8Q_API int fp8q_pipeline_selftest(void* stream) {
 FP8Q_API int fp8q_pipeline_status(unsigned int* timed_out_waits) {
   FP8Q_TRACE_CALL();
   if (!timed_out_waits) return FP8Q_EINVAL;
-  unsigned int a = 0, b = 0;
+  unsigned int a = 0, b = 0, c = 0;
   cudaError_t e = read_wait_timeouts(&a);
   if (e == cudaSuccess) e = read_tp_wait_timeouts(&b);
-  *timed_out_waits = a + b;
+  if (e == cudaSuccess) e = read_kv_wait_timeouts(&c);
+  *timed_out_waits = a + b + c;
   return e == cudaSuccess ? FP8Q_OK : fail_cuda(e);
 }
 

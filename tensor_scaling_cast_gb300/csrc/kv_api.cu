@@ -112,7 +112,7 @@ FP8Q_API int64_t mx_kv_attention_workspace(const mx_kv_cache* c, int64_t total_q
   if (total_q == 0 || batch == 0) return 0;
   if (max_q > total_q) max_q = (int)total_q;
   int64_t bytes = 0;
-  const cudaError_t e = kv_attention_workspace(s, q_heads, batch, max_q, table_width,
+  const cudaError_t e = kv_attention_workspace(s, q_heads, batch, total_q, max_q, table_width,
                                                sm_count(device_of_current()), &bytes);
   return e == cudaSuccess ? bytes : record_cuda_error(e);
 }
@@ -137,7 +137,7 @@ FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int
   const int sms = sm_count(device_of_current());
   if (max_q > total_q) max_q = (int)total_q;
   int64_t need = 0;
-  const cudaError_t we = kv_attention_workspace(a.shape, q_heads, batch, max_q, table_width, sms, &need);
+  const cudaError_t we = kv_attention_workspace(a.shape, q_heads, batch, total_q, max_q, table_width, sms, &need);
   if (we != cudaSuccess) return record_cuda_error(we);
   if (need > workspace_bytes) return FP8Q_ESIZE;
   if (need > 0 && !workspace) return FP8Q_EINVAL;

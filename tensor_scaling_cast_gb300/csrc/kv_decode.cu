@@ -43,11 +43,6 @@ constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecStages = 3;
 constexpr int kTile = 32;                 // tokens of a warp tile
 constexpr int kMinTiles = 16;             // tiles of a CTA, at least
-constexpr float kNoMax = -3.0e38f;        // reference before the first score
-constexpr float kSlack = 8.0f;            // weights reach 2^kSlack before M moves
-constexpr int kMinScale = 127 - 80;       // R stays within [-80, 126] (as E8M0 bytes): p * 2^-R is
-constexpr int kMaxScale = 127 + 126;      // finite and 2^-R normal
-constexpr int kMaxGrid = 4096;            // tickets of a workspace
 
 template <int D>
 struct DecSmem {
@@ -102,21 +97,6 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // Two E8M0 bytes (the low half of w) -> 2^(byte - 127), NaN for 0xFF.
 __device__ __forceinline__ float2 e8m0x2_f32(uint32_t w) {
   uint32_t r;
@@ -131,20 +111,14 @@ __device__ __forceinline__ uint32_t code_offset(int r, int c) {
   return D == 128 ? r * 64 + ((c ^ (r >> 1)) & 3) * 16 : r * 32 + ((c ^ (r >> 2)) & 1) * 16;
 }
 
-// The part of one sequence that a call has to visit.
-struct DecSeq {
-  int q0, nq, len, tile0, tiles;     // first query row, queries, keys, first tile, tiles
+// A sequence's tiles: the ones that hold a key some query sees.
+struct DecSeq : KvSeq {
+  int tile0, tiles;
 };
 __device__ __forceinline__ DecSeq dec_seq(const KvAttn& a, int b) {
   DecSeq s;
-  s.q0 = a.cu_q ? a.cu_q[b] : b;
-  s.nq = a.cu_q ? a.cu_q[b + 1] - s.q0 : 1;
-  s.q0 = max(s.q0, 0);
-  s.nq = max(0, min(min(s.nq, a.max_q), a.total_q - s.q0));
-  const int64_t most = (int64_t)a.table_width << a.shape.page_shift;
-  s.len = (int)min((int64_t)max(a.kv_lens[b], 0), most);
-  const int first = a.window > 0 ? max(0, s.len - s.nq - a.window + 1) : 0;   // oldest key any query sees
-  s.tile0 = first / kTile;
+  static_cast<KvSeq&>(s) = kv_seq(a, b);
+  s.tile0 = (a.window > 0 ? max(0, s.pos0 - a.window + 1) : 0) / kTile;
   // a sequence with queries and no keys still has its zeros to write
   s.tiles = s.nq == 0 ? 0 : max(1, (s.len + kTile - 1) / kTile - s.tile0);
   return s;
@@ -262,7 +236,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
         for (int y = 0; y < 8; ++y) o[nt][x][y >> 2][y & 3] = 0.0f;
     }
 
-    const int pos0 = sq.len - sq.nq;             // position of query 0
+    const int pos0 = sq.pos0;
     const int32_t* table = a.table + b * a.table_stride;
     // token of this lane in the warp's k-th tile, and the page that holds it
     const int tok0 = (sq.tile0 + t0 + warp) * kTile + lane;

@@ -124,6 +124,36 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The online softmax of both attention kernels keeps a reference M per row:
+// weights are 2^(x - M), and M moves only when a score passes it by
+// 2^kSlack.  Value scales are taken relative to a group's largest R, which
+// stays within [-80, 126] (as E8M0 bytes), so that the sum's terms, weights
+// times 2^-R, are finite and 2^-R is a normal number.
+constexpr float kNoMax = -3.0e38f;        // M before the first score
+constexpr float kSlack = 8.0f;
+constexpr int kMinScale = 127 - 80;
+constexpr int kMaxScale = 127 + 126;
+
+// A workspace: tickets (zero between calls), then the parts of rows whose
+// keys several CTAs share.
+constexpr int kMaxGrid = 4096;            // tickets, and CTAs of a call at most
+
 // ---- launches (kv_cache.cu, kv_attention.cu) --------------------------------
 cudaError_t launch_kv_write(const KvShape& s, int format, KvPool k, KvPool v, const void* kx, const void* vx,
                             int dtype, int64_t tokens, const int64_t* strides, const int64_t* slots, int rule,
@@ -147,14 +177,36 @@ struct KvAttn {
   int32_t table_width, batch, total_q, max_q, q_heads, group, window;
   float scale;
 };
+// What a call has to do for sequence b.  Query i of the sequence sits at
+// position pos0 + i; lengths and offsets that point outside are clamped.
+struct KvSeq {
+  int q0, nq, len, pos0;      // first query row, queries, keys, position of query 0
+};
+__device__ __forceinline__ KvSeq kv_seq(const KvAttn& a, int b) {
+  KvSeq s;
+  s.q0 = a.cu_q ? a.cu_q[b] : b;
+  const int n = a.cu_q ? max(0, a.cu_q[b + 1] - s.q0) : 1;
+  s.q0 = max(s.q0, 0);
+  s.nq = max(0, min(min(n, a.max_q), a.total_q - s.q0));
+  const int64_t most = (int64_t)a.table_width << a.shape.page_shift;
+  s.len = (int)min((int64_t)max(a.kv_lens[b], 0), most);
+  s.pos0 = s.len - n;
+  return s;
+}
+
 // Few query rows per key/value head (kv_decode.cu).
 bool kv_decode_takes(int max_q, int group);
 cudaError_t kv_decode_workspace(const KvShape& s, int group, int batch, int max_q, int table_width, int sms,
                                 int64_t* bytes);
 cudaError_t launch_kv_decode(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches);
+// Any number of them (kv_prompt.cu).
+cudaError_t kv_prompt_workspace(const KvShape& s, int group, int batch, int64_t total_q, int max_q, int table_width,
+                                int sms, int64_t* bytes);
+cudaError_t launch_kv_prompt(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches);
+cudaError_t read_kv_wait_timeouts(unsigned int* count);   // and reset to 0
 // Any call: the kernel that fits it (kv_attention.cu).
-cudaError_t kv_attention_workspace(const KvShape& s, int q_heads, int batch, int max_q, int table_width, int sms,
-                                   int64_t* bytes);
+cudaError_t kv_attention_workspace(const KvShape& s, int q_heads, int batch, int64_t total_q, int max_q,
+                                   int table_width, int sms, int64_t* bytes);
 cudaError_t launch_kv_attention(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches);
 
 }  // namespace fp8q
