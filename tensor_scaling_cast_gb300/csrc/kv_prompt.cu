@@ -117,6 +117,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Low n bits.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
 
@@ -225,7 +231,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
 
   if (wg < 2) {
     // ================= softmax of 128 rows, one per thread =================
-    regs_inc<184>();
+    regs_inc<144>();
     [&]() {
       const int rl = threadIdx.x & 127;              // row within the warpgroup, tensor-memory lane
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -276,38 +282,41 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           if (!wait(&sm.s_full[wg], mine_t)) return;
           tmem_fence_after();
           const PrInfo& info = sm.info[kt & 3];
-          uint32_t s[4][32];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) tmem_ld32(s[x], t_s + x * 32);
-          tmem_wait_ld();
-          const bool edge = tok + kPrKeys - 1 > first_pos || (a.window > 0 && tok <= last_pos - a.window) ||
-                            (info.valid[0] & info.valid[1] & info.valid[2] & info.valid[3]) != 0xFFFFFFFFu;
           const bool any_nan = (info.any_nan[0] | info.any_nan[1] | info.any_nan[2] | info.any_nan[3]) != 0;
-          if (edge || any_nan) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int base = tok + x * 32;
-              uint32_t seen = info.valid[x] & low_bits(pos - base + 1);
-              if (a.window > 0) seen &= ~low_bits(pos - a.window + 1 - base);
-#pragma unroll
-              for (int y = 0; y < 32; ++y) s[x][y] = (seen >> y) & 1 ? s[x][y] : 0xFF800000u;
-              if (info.any_nan[x])
-                for (int y = 0; y < NB; ++y) nan_blocks |= (info.vnan[x][y] & seen) ? 1u << y : 0u;
-            }
-          }
+          const bool edge = tok + kPrKeys - 1 > first_pos || (a.window > 0 && tok <= last_pos - a.window) || any_nan ||
+                            (info.valid[0] & info.valid[1] & info.valid[2] & info.valid[3]) != 0xFFFFFFFFu;
+          // bit y: this row sees token y of the x-th 32
+          auto seen = [&](int x) {
+            const int base = tok + x * 32;
+            uint32_t m = info.valid[x] & low_bits(pos - base + 1);
+            if (a.window > 0) m &= ~low_bits(pos - a.window + 1 - base);
+            return m;
+          };
+          // The scores are read twice, 32 at a time, for the largest one and for
+          // the weights: 128 of them in registers would not leave room for the rest.
+          uint32_t s[2][32];
           float top = kNoMax;
-          float fk[4], rv[4];
+          tmem_ld32(s[0], t_s);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            fk[x] = f_row * info.rk[x];
-            rv[x] = info.rv[x];
-            float t0 = __uint_as_float(s[x][0]), t1 = __uint_as_float(s[x][1]);
+            uint32_t(&v)[32] = s[x & 1];
+            tmem_wait_ld(v);
+            tmem_ld32(s[(x + 1) & 1], t_s + ((x + 1) & 3) * 32);    // the last one is the second pass's first
+            if (edge) {
+              const uint32_t m = seen(x);
 #pragma unroll
-            for (int y = 2; y < 32; y += 2) {
-              t0 = fmaxf(t0, __uint_as_float(s[x][y]));
-              t1 = fmaxf(t1, __uint_as_float(s[x][y + 1]));
+              for (int y = 0; y < 32; ++y) v[y] = (m >> y) & 1 ? v[y] : 0xFF800000u;
+              if (info.any_nan[x])
+                for (int y = 0; y < NB; ++y) nan_blocks |= (info.vnan[x][y] & m) ? 1u << y : 0u;
             }
-            top = fmaxf(top, fmaxf(t0, t1) * fk[x] + rv[x]);
+            float t0 = __uint_as_float(v[0]), t1 = __uint_as_float(v[1]);
+#pragma unroll
+            for (int y = 2; y < 30; y += 4) {
+              t0 = max3(t0, __uint_as_float(v[y]), __uint_as_float(v[y + 1]));
+              t1 = max3(t1, __uint_as_float(v[y + 2]), __uint_as_float(v[y + 3]));
+            }
+            t0 = max3(t0, __uint_as_float(v[30]), __uint_as_float(v[31]));
+            top = fmaxf(top, fmaxf(t0, t1) * (f_row * info.rk[x]) + info.rv[x]);
           }
           if (__any_sync(0xFFFFFFFFu, top > m_ref + kSlack)) {
             const float m2 = fmaxf(m_ref, top), fix = ex2(m_ref - m2);
@@ -316,39 +325,47 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
             if (u > u0) {                              // the sums so far, once the product that made them is done
               if (!wait(&sm.o_full[wg], mine_t - 1)) return;
               tmem_fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int x = 0; x < D / 32; ++x) {
+                tmem_wait_ld(s[0]);                    // the first scores stay as they are
                 uint32_t o[32];
                 tmem_ld32(o, t_o + x * 32);
-                tmem_wait_ld();
+                tmem_wait_ld(o);
 #pragma unroll
                 for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * fix);
                 tmem_st32(t_o + x * 32, o);
               }
             }
           }
+          uint32_t p[32];
 #pragma unroll
-          for (int x = 0; x < 4; x += 2) {
-            uint32_t p[32];
+          for (int x = 0; x < 4; ++x) {
+            uint32_t(&v)[32] = s[x & 1];
+            tmem_wait_ld(v);
+            if (x < 3) tmem_ld32(s[(x + 1) & 1], t_s + (x + 1) * 32);
+            if (edge) {
+              const uint32_t m = seen(x);
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const float c = rv[x + z] - m_ref;
-              const uint64_t f2 = pack2(fk[x + z], fk[x + z]), c2 = pack2(c, c);
-              uint64_t sum = 0;
-#pragma unroll
-              for (int y = 0; y < 32; y += 2) {
-                float e0, e1;
-                unpack2(fma2(pack2(__uint_as_float(s[x + z][y]), __uint_as_float(s[x + z][y + 1])), f2, c2), e0, e1);
-                e0 = ex2(e0);
-                e1 = ex2(e1);
-                sum = add2(sum, pack2(e0, e1));
-                p[z * 16 + y / 2] = cvt_f16x2(e0, e1);
-              }
-              float a0, a1;
-              unpack2(sum, a0, a1);
-              l += (a0 + a1) * pow2f(-(int)rv[x + z]);
+              for (int y = 0; y < 32; ++y) v[y] = (m >> y) & 1 ? v[y] : 0xFF800000u;
             }
-            tmem_st32(t_s + x * 16, p);
+            const float rv = info.rv[x], f = f_row * info.rk[x], c = rv - m_ref;
+            const uint64_t f2 = pack2(f, f), c2 = pack2(c, c);
+            uint64_t sum = 0;
+#pragma unroll
+            for (int y = 0; y < 32; y += 2) {
+              float e0, e1;
+              unpack2(fma2(pack2(__uint_as_float(v[y]), __uint_as_float(v[y + 1])), f2, c2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum = add2(sum, pack2(e0, e1));
+              p[(x & 1) * 16 + y / 2] = cvt_f16x2(e0, e1);
+            }
+            float a0, a1;
+            unpack2(sum, a0, a1);
+            l += (a0 + a1) * pow2f(-(int)rv);
+            // the weights of 64 tokens go over scores that both passes are done with
+            if (x == 1) tmem_st32(t_s, p);
+            if (x == 3) tmem_st32(t_s + 32, p);
           }
           tmem_wait_st();
           tmem_fence_before();
@@ -370,7 +387,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           for (int x = 0; x < D / 32; ++x) {
             uint32_t o[32];
             tmem_ld32(o, t_o + x * 32);
-            tmem_wait_ld();
+            tmem_wait_ld(o);
             if ((nan_blocks >> x) & 1)
 #pragma unroll
               for (int y = 0; y < 32; ++y) o[y] = 0x7FFFFFFFu;
@@ -461,7 +478,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     }();
   } else if (wg == 2) {
     // ================= unpacking keys and values =================
-    regs_dec<96>();
+    regs_inc<152>();
     [&]() {
       const int grp = warp & 3;                      // tokens 32 grp .. + 31 of a tile
       const int sub = lane & 7;                      // token of 8 within a step
@@ -472,31 +489,29 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
       auto token_of = [&](int j) { return D == 128 ? j * 8 + sub : j * 16 + (lane >> 4) * 8 + sub; };
       const int page_mask = (1 << a.shape.page_shift) - 1;
       uint4 kc[U], vc[U];
-      uint32_t kw = 0, vw = 0, valid = 0;            // scales of this lane's token
+      uint32_t kw = 0, vw = 0, valid = 0;            // scales of this lane's token; tokens that exist
+      int64_t row = 0;                               // this lane's token in the cache
       auto page_of = [&](const PrItem& x, int u) {
         const int tok = (x.tile0 + u) * kPrKeys + grp * 32 + lane;
         return tok < x.sq.len ? a.table[x.b * a.table_stride + (tok >> a.shape.page_shift)] : -1;
       };
-      auto load = [&](const PrItem& x, int u, int page) {
+      // the unit's rows (row, the mask) and one kind of their codes and scales
+      auto locate = [&](const PrItem& x, int u, int page) {
         const int tok = (x.tile0 + u) * kPrKeys + grp * 32 + lane;
         const int64_t slot = ((int64_t)page << a.shape.page_shift) + (tok & page_mask);
         const bool ok = page >= 0 && slot < a.shape.slots;
-        const int64_t row = ok ? kv_row(a.shape, slot, x.head) : 0;
-        valid = __ballot_sync(0xFFFFFFFFu, ok);
-        if (D == 128) {
-          kw = ok ? reinterpret_cast<const uint32_t*>(a.k.e8m0)[row] : 0;
-          vw = ok ? reinterpret_cast<const uint32_t*>(a.v.e8m0)[row] : 0;
-        } else {
-          kw = ok ? reinterpret_cast<const uint16_t*>(a.k.e8m0)[row] : 0;
-          vw = ok ? reinterpret_cast<const uint16_t*>(a.v.e8m0)[row] : 0;
-        }
+        row = ok ? kv_row(a.shape, slot, x.head) : 0;
+        return __ballot_sync(0xFFFFFFFFu, ok);
+      };
+      auto load = [&](const KvPool& pool, uint32_t there, uint4 (&codes)[U], uint32_t& w) {
+        if (D == 128) w = (there >> lane) & 1 ? reinterpret_cast<const uint32_t*>(pool.e8m0)[row] : 0;
+        else w = (there >> lane) & 1 ? reinterpret_cast<const uint16_t*>(pool.e8m0)[row] : 0;
 #pragma unroll
         for (int j = 0; j < U; ++j) {
           const int t = token_of(j);
           const int64_t rr = __shfl_sync(0xFFFFFFFFu, row, t);
-          const bool there = (valid >> t) & 1;
-          kc[j] = there ? *reinterpret_cast<const uint4*>(a.k.q + rr * (D / 2) + blk * 16) : make_uint4(0, 0, 0, 0);
-          vc[j] = there ? *reinterpret_cast<const uint4*>(a.v.q + rr * (D / 2) + blk * 16) : make_uint4(0, 0, 0, 0);
+          codes[j] = (there >> t) & 1 ? *reinterpret_cast<const uint4*>(pool.q + rr * (D / 2) + blk * 16)
+                                      : make_uint4(0, 0, 0, 0);
         }
       };
       // codes * 2^(E - R) of this warp's 32 tokens into a swizzled tile; gives R
@@ -547,12 +562,10 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
         return top;
       };
 
-      // an item's units in turn; codes of the next unit and the page after
-      // that are in flight while one is unpacked
+      // The items' units in turn.  While one kind of a unit is unpacked, the
+      // other kind's codes are in flight, and the page of the unit after.
       PrItem nx = it;
       long long nseg = seg0, at = begin;
-      int page = page_of(nx, (int)(at - nseg));
-      load(nx, (int)(at - nseg), page);
       auto step = [&]() {                            // nx, nseg, at: one unit on; false at the end
         ++at;
         if (at >= end) return false;
@@ -562,6 +575,10 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
         }
         return true;
       };
+      int page = page_of(nx, (int)(at - nseg));
+      valid = locate(nx, (int)(at - nseg), page);
+      load(a.k, valid, kc, kw);
+      load(a.v, valid, vc, vw);
       bool more = step();
       if (more) page = page_of(nx, (int)(at - nseg));
       const uint32_t units = (uint32_t)(end - begin);
@@ -576,66 +593,95 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
         }
         fence_proxy_async();
         mbar_arrive(&sm.k_full[stg]);
+        uint32_t next = 0;
+        if (more) {
+          next = locate(nx, (int)(at - nseg), page);
+          load(a.k, next, kc, kw);
+        }
         if (kt >= 2 && !wait(&sm.v_empty[stg], (kt >> 1) - 1)) return;
         const uint32_t rv = unpack(sm.v[stg], vc, vw, true, info);
         if (lane == 0) info.rv[grp] = (float)((int)rv - 127);
         fence_proxy_async();
         mbar_arrive(&sm.v_full[stg]);
         if (more) {
-          load(nx, (int)(at - nseg), page);
+          load(a.v, next, vc, vw);
           more = step();
           if (more) page = page_of(nx, (int)(at - nseg));
         }
+        valid = next;
       }
     }();
   } else {
-    // ================= one thread issues the products =================
-    regs_dec<48>();
-    if (warp == 12 && lane == 0) {
+    // ================= one warp issues the products =================
+    // The whole warp goes through the loop, so that addresses and descriptors
+    // stay in uniform registers; one elected lane issues.
+    regs_dec<72>();
+    if (warp == 12) {
       [&]() {
         constexpr uint32_t kQK = f16_idesc(128, kPrKeys, false), kPV = f16_idesc(128, D, true);
-        uint32_t kt = 0, items[2] = {0, 0}, done[2] = {0, 0};
+        constexpr uint32_t kHi = desc_hi(1024);
+        const uint32_t qa = desc_lo(smem_addr(sm.q[0]), 16), ka = desc_lo(smem_addr(sm.k[0]), 16);
+        const uint32_t va = desc_lo(smem_addr(sm.v[0]), Smem::kHalf);
+        const bool lead = elect_one();
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        uint32_t kt = 0, items0 = 0, items1 = 0, done0 = 0, done1 = 0;
         auto scores = [&](int w, int stg) {
-          const uint32_t qa = smem_addr(sm.q[w]), ka = smem_addr(sm.k[stg]);
+          const uint32_t q = qa + w * (Smem::kTileBytes >> 4), k = ka + stg * (Smem::kTileBytes >> 4);
+          if (lead) {
 #pragma unroll
-          for (int x = 0; x < D / 16; ++x) {
-            const uint32_t off = (x >> 2) * Smem::kHalf + (x & 3) * 32;
-            mma_ss(tmem + kS + w * 128, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), kQK, x > 0);
+            for (int x = 0; x < D / 16; ++x) {
+              const uint32_t off = ((x >> 2) * Smem::kHalf + (x & 3) * 32) >> 4;
+              mma_ss(tm + kS + w * 128, q + off, k + off, kHi, kQK, x > 0);
+            }
+            mma_commit(&sm.s_full[w]);
           }
-          mma_commit(&sm.s_full[w]);
+          __syncwarp();
         };
         auto values = [&](int w, int stg, bool first) {
-          const uint32_t va = smem_addr(sm.v[stg]);
+          const uint32_t v = va + stg * (Smem::kTileBytes >> 4);
+          if (lead) {
 #pragma unroll
-          for (int x = 0; x < kPrKeys / 16; ++x)
-            mma_ts(tmem + kO + w * 128, tmem + kS + w * 128 + x * 8, smem_desc(va + x * 2048, Smem::kHalf, 1024), kPV,
-                   !first || x > 0);
-          mma_commit(&sm.o_full[w]);
+            for (int x = 0; x < kPrKeys / 16; ++x)
+              mma_ts(tm + kO + w * 128, tm + kS + w * 128 + x * 8, v + x * (2048 >> 4), kHi, kPV, !first || x > 0);
+            mma_commit(&sm.o_full[w]);
+          }
+          __syncwarp();
         };
         for (long long at = begin; at < end;) {
           const int u0 = (int)(at - seg0), u1 = (int)min((long long)it.n, end - seg0);
-          const int groups = it.rt * kPrRows + 128 < it.rows ? 2 : 1;
-          if (!wait1(&sm.k_full[kt & 1], kt >> 1)) return;
-          for (int w = 0; w < groups; ++w) {
-            if (!wait1(&sm.q_full[w], items[w]++)) return;
+          const bool two = it.rt * kPrRows + 128 < it.rows;
+          if (!wait(&sm.k_full[kt & 1], kt >> 1)) return;
+          if (!wait(&sm.q_full[0], items0++)) return;
+          tmem_fence_after();
+          scores(0, kt & 1);
+          if (two) {
+            if (!wait(&sm.q_full[1], items1++)) return;
             tmem_fence_after();
-            scores(w, kt & 1);
+            scores(1, kt & 1);
           }
-          mma_commit(&sm.k_empty[kt & 1]);
+          if (lead) mma_commit(&sm.k_empty[kt & 1]);
           for (int u = u0; u < u1; ++u, ++kt) {
             const uint32_t nk = kt + 1;
-            if (!wait1(&sm.v_full[kt & 1], kt >> 1)) return;
-            for (int w = 0; w < groups; ++w) {
-              if (!wait1(&sm.p_full[w], done[w]++)) return;
-              tmem_fence_after();
-              values(w, kt & 1, u == u0);
-              if (u + 1 < u1) {
-                if (w == 0 && !wait1(&sm.k_full[nk & 1], nk >> 1)) return;
-                scores(w, nk & 1);
-              }
+            const bool more = u + 1 < u1;
+            if (!wait(&sm.v_full[kt & 1], kt >> 1)) return;
+            if (!wait(&sm.p_full[0], done0++)) return;
+            tmem_fence_after();
+            values(0, kt & 1, u == u0);
+            if (more) {
+              if (!wait(&sm.k_full[nk & 1], nk >> 1)) return;
+              scores(0, nk & 1);
             }
-            mma_commit(&sm.v_empty[kt & 1]);
-            if (u + 1 < u1) mma_commit(&sm.k_empty[nk & 1]);
+            if (two) {
+              if (!wait(&sm.p_full[1], done1++)) return;
+              tmem_fence_after();
+              values(1, kt & 1, u == u0);
+              if (more) scores(1, nk & 1);
+            }
+            if (lead) {
+              mma_commit(&sm.v_empty[kt & 1]);
+              if (more) mma_commit(&sm.k_empty[nk & 1]);
+            }
+            __syncwarp();
           }
           at = seg0 + u1;
           seg0 += it.n;
@@ -643,8 +689,9 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
         }
       }();
       // nothing may still be running when the tensor memory goes back
-      mma_commit(&sm.drain);
-      wait1(&sm.drain, 0);
+      if (elect_one()) mma_commit(&sm.drain);
+      __syncwarp();
+      wait(&sm.drain, 0);
     }
     __syncwarp();
   }
