@@ -62,16 +62,6 @@ struct DecSmem {
   };
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -102,13 +92,6 @@ __device__ __forceinline__ float2 e8m0x2_f32(uint32_t w) {
   uint32_t r;
   asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %1;\n cvt.rn.bf16x2.ue8m0x2 %0, a;\n}" : "=r"(r) : "r"(w));
   return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
-}
-
-// Chunk c (16 bytes) of row r of a code tile: swizzled so that the eight rows
-// of an 8 x 8 load fall on different banks.
-template <int D>
-__device__ __forceinline__ uint32_t code_offset(int r, int c) {
-  return D == 128 ? r * 64 + ((c ^ (r >> 1)) & 3) * 16 : r * 32 + ((c ^ (r >> 2)) & 1) * 16;
 }
 
 // A sequence's tiles: the ones that hold a key some query sees.
@@ -254,32 +237,9 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
         const int64_t row = ok ? kv_row(a.shape, slot, head) : 0;
         const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok);
         if (lane == 0) sm.valid[st] = valid;
-        constexpr int CH = RB / 16;              // 16-byte chunks of a row
-        const uint32_t kd = smem_u32(sm.stage[st].k), vd = smem_u32(sm.stage[st].v);
-#pragma unroll
-        for (int x = 0; x < CH; ++x) {
-          const int r = x * (32 / CH) + lane / CH, c = lane % CH;
-          const int64_t rr = __shfl_sync(0xFFFFFFFFu, row, r);
-          const bool on = (valid >> r) & 1;
-          const uint32_t off = code_offset<D>(r, c);
-          cp_async16(kd + off, a.k.q + rr * RB + c * 16, on);
-          cp_async16(vd + off, a.v.q + rr * RB + c * 16, on);
-        }
-        if (D == 128) {
-          cp_async4(smem_u32(sm.stage[st].ke) + lane * 4, a.k.e8m0 + row * 4, ok);
-          cp_async4(smem_u32(sm.stage[st].ve) + lane * 4, a.v.e8m0 + row * 4, ok);
-        } else if (a.shape.page_shift > 0) {     // two tokens' scales are one word
-          const bool pair = (valid >> (lane & ~1)) & 1;
-          if (!(lane & 1)) {
-            cp_async4(smem_u32(sm.stage[st].ke) + lane * 2, a.k.e8m0 + row * 2, pair);
-            cp_async4(smem_u32(sm.stage[st].ve) + lane * 2, a.v.e8m0 + row * 2, pair);
-          }
-        } else {
-          const uint16_t ke = ok ? *reinterpret_cast<const uint16_t*>(a.k.e8m0 + row * 2) : 0;
-          const uint16_t ve = ok ? *reinterpret_cast<const uint16_t*>(a.v.e8m0 + row * 2) : 0;
-          reinterpret_cast<uint16_t*>(sm.stage[st].ke)[lane] = ke;
-          reinterpret_cast<uint16_t*>(sm.stage[st].ve)[lane] = ve;
-        }
+        const bool pair = a.shape.page_shift > 0;
+        copy_rows<D>(smem_u32(sm.stage[st].k), smem_u32(sm.stage[st].ke), a.k, row, valid, pair);
+        copy_rows<D>(smem_u32(sm.stage[st].v), smem_u32(sm.stage[st].ve), a.v, row, valid, pair);
       }
       cp_commit();
     };

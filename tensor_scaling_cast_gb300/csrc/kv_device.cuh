@@ -140,6 +140,49 @@ __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Chunk c (16 bytes) of row r of a code tile: swizzled so that the eight rows
+// of an 8 x 8 load fall on different banks.
+template <int D>
+__device__ __forceinline__ uint32_t code_offset(int r, int c) {
+  return D == 128 ? r * 64 + ((c ^ (r >> 1)) & 3) * 16 : r * 32 + ((c ^ (r >> 2)) & 1) * 16;
+}
+
+// This warp's copy of the codes and scales of 32 cached rows into shared
+// memory, asynchronously: row is the cache row of the lane's token, bit t of
+// valid says whether token t exists (else zeros are written).  pair_scales:
+// two tokens' rows are neighbours (page size 2 or more).
+template <int D>
+__device__ __forceinline__ void copy_rows(uint32_t codes, uint32_t scales, const KvPool& pool, int64_t row,
+                                          uint32_t valid, bool pair_scales) {
+  constexpr int RB = D / 2, CH = RB / 16;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int x = 0; x < CH; ++x) {
+    const int r = x * (32 / CH) + lane / CH, c = lane % CH;
+    const int64_t rr = __shfl_sync(0xFFFFFFFFu, row, r);
+    cp_async16(codes + code_offset<D>(r, c), pool.q + rr * RB + c * 16, (valid >> r) & 1);
+  }
+  const bool ok = (valid >> lane) & 1;
+  if (D == 128) {
+    cp_async4(scales + lane * 4, pool.e8m0 + row * 4, ok);
+  } else if (pair_scales) {              // two tokens' scales are one word, the even one's row even
+    if (!(lane & 1)) cp_async4(scales + lane * 2, pool.e8m0 + row * 2, ok);
+  } else {
+    const uint16_t e = ok ? *reinterpret_cast<const uint16_t*>(pool.e8m0 + row * 2) : 0;
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(scales + lane * 2), "h"(e) : "memory");
+  }
+}
+
 // The online softmax of both attention kernels keeps a reference M per row:
 // weights are 2^(x - M), and M moves only when a score passes it by
 // 2^kSlack.  Value scales are taken relative to a group's largest R, which

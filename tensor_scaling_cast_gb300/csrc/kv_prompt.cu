@@ -30,33 +30,24 @@
 
 namespace fp8q {
 
-constexpr int kPrThreads = 512;
+constexpr int kPrThreads = 640;
+constexpr int kPrIssuer = 16;             // this warp and the next issue the products; it owns tensor memory
 constexpr int kPrRows = 256;              // query rows of an item: two warpgroups of 128
 constexpr int kPrKeys = 128;              // keys of a unit
+constexpr int kPrHalf = 64;               // and of a half of it: scores are made and used by halves
+constexpr int kPrStages = 2;              // units of unpacked keys, and of values, in shared memory
 constexpr int kPrMinUnits = 4;            // units of a CTA, at least
 
 __device__ unsigned int g_kv_wait_timeouts = 0;
 
-struct PrInfo {                           // per tile, written by the unpacking warps
-  float rk[4];                            // 2^Rk of each 32 tokens
-  float rv[4];                            // Rv
-  uint32_t valid[4];                      // tokens that exist
-  uint32_t any_nan[4];                    // tokens with a NaN block of values,
-  uint32_t vnan[4][4];                    // and with block b NaN (set where any_nan is not 0)
-};
-
-template <int D>
-struct PrSmem {
-  static constexpr int kHalf = 128 * 128;             // 128 rows of 64 f16
-  static constexpr int kTileBytes = kHalf * (D / 64);
-  uint8_t q[2][kTileBytes];
-  uint8_t k[2][kTileBytes];
-  uint8_t v[2][kTileBytes];
-  PrInfo info[4];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];     // per warpgroup of rows
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];   // per stage
-  uint64_t join_all, join_last, drain;
-  uint32_t tmem, last;
+constexpr int kPrInfos = 4;               // more units than the unpacking warps can be ahead
+struct PrInfo {                           // of a unit, written by the unpacking warps
+  struct Group {                          // of 32 tokens
+    float rk, rv, unscale;                // 2^Rk, Rv, 2^-Rv
+    uint32_t valid, any_nan;              // tokens that exist, tokens with a NaN block of values
+    uint32_t pad[3];
+  } g[4];
+  uint32_t vnan[4][4];                    // tokens with block b of the values NaN (set where any_nan is not 0)
 };
 
 // One item: 256 rows of one (sequence, head) and the units of 128 keys that
@@ -67,6 +58,27 @@ struct PrItem {
   int rows, tiles_r;        // rows of the (sequence, head), row tiles
   int tile0, n;             // first 128 keys, units
 };
+template <int D>
+struct PrSmem {
+  static constexpr int kQHalf = 128 * 128, kHalf = kPrKeys * 128;      // 64 columns of f16 rows
+  static constexpr int kQBytes = kQHalf * (D / 64), kTileBytes = kHalf * (D / 64);
+  uint8_t q[2][kQBytes];
+  uint8_t k[kPrStages][kTileBytes];
+  uint8_t v[kPrStages][kTileBytes];
+  struct Raw {                                        // a warp's 32 rows as they lie in the cache
+    uint8_t codes[32 * D / 2];
+    uint8_t scales[32 * D / 32];
+  } raw[8];
+  PrInfo info[kPrInfos];
+  PrItem item[kPrThreads / 32];                       // each warp's place in the CTA's items
+  uint64_t q_full[2];                                 // per warpgroup of rows
+  uint64_t s_full[2][2], p_full[2][2], o_full[2][2];  // and half of a unit (o: the product of its weights)
+  uint64_t k_full[kPrStages], k_empty[kPrStages], v_full[kPrStages], v_empty[kPrStages];
+  uint64_t info_full[kPrInfos];
+  uint64_t join_all, join_last, drain;
+  uint32_t tmem, last;
+};
+
 __device__ __forceinline__ void pr_units(const KvAttn& a, const KvSeq& s, int rt, int* tile0, int* n) {
   const int rows = s.nq * a.group;
   const int first = rt * kPrRows / a.group, last = (min(rows, (rt + 1) * kPrRows) - 1) / a.group;
@@ -92,6 +104,10 @@ __device__ __forceinline__ void pr_next(const KvAttn& a, PrItem& it) {
   }
   pr_units(a, it.sq, it.rt, &it.tile0, &it.n);
 }
+
+// Sums of a half's weights above this move the reference: no weight reaches
+// f16's largest value below it.
+constexpr float kMostSum = 16384.0f;
 
 struct PrPlan {
   uint32_t* ticket;
@@ -139,6 +155,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
   // ---- this CTA's range of units
   __shared__ long long s_scan[kPrThreads / 32];
   __shared__ long long s_first[2];                   // begin's (sequence, its first unit)
+  __shared__ long long s_range[2];                   // begin, units of a CTA
   constexpr int W = kPrThreads / 32;
   const int per_warp = (a.batch + W - 1) / W;
   const int b_lo = min(a.batch, warp * per_warp), b_hi = min(a.batch, b_lo + per_warp);
@@ -166,6 +183,10 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
   const long long per = max((long long)kPrMinUnits, (total + gridDim.x - 1) / gridDim.x);
   const long long begin = (long long)blockIdx.x * per, end = min(total, begin + per);
   if (begin >= end) return;
+  if (threadIdx.x == 0) {
+    s_range[0] = begin;
+    s_range[1] = per;
+  }
   if (before <= begin && begin < before + mine) {
     for (int b = b_lo; b < b_hi; ++b) {
       const long long n = seq_units(kv_seq(a, b)) * a.shape.heads;
@@ -180,53 +201,77 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
   // ---- barriers and tensor memory
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&sm.q_full[x], 128);
-      mbar_init(&sm.s_full[x], 1);
-      mbar_init(&sm.p_full[x], 128);
-      mbar_init(&sm.o_full[x], 1);
-      mbar_init(&sm.k_full[x], 128);
-      mbar_init(&sm.k_empty[x], 1);
-      mbar_init(&sm.v_full[x], 128);
-      mbar_init(&sm.v_empty[x], 1);
+      mbar_init(&sm.q_full[x], 4);
+      for (int y = 0; y < 2; ++y) {
+        mbar_init(&sm.s_full[x][y], 1);
+        mbar_init(&sm.p_full[x][y], 4);
+        mbar_init(&sm.o_full[x][y], 1);
+      }
     }
-    mbar_init(&sm.join_all, 256);
+    for (int x = 0; x < kPrStages; ++x) {
+      mbar_init(&sm.k_full[x], 4);
+      mbar_init(&sm.k_empty[x], 2);
+      mbar_init(&sm.v_full[x], 4);
+      mbar_init(&sm.v_empty[x], 2);
+    }
+    for (int x = 0; x < kPrInfos; ++x) mbar_init(&sm.info_full[x], 8);
+    mbar_init(&sm.join_all, 8);
     mbar_init(&sm.join_last, 1);
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain, 2);
     fence_barrier_init();
   }
-  if (warp == 12) tmem_alloc(&sm.tmem, 512);
+  if (warp == kPrIssuer) tmem_alloc(&sm.tmem, 512);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = sm.tmem;
 
-  PrItem it;
-  it.b = (int)s_first[0];
+  // each warp's item is warp-uniform and used now and then: it lives in shared memory
+  PrItem& it = sm.item[warp];
   long long seg0 = s_first[1];                       // global unit of the item's first one
-  it.sq = kv_seq(a, it.b);
-  pr_set(a, it);
   {
-    const long long u = seq_units(it.sq);
-    it.head = (int)((begin - seg0) / u);
-    seg0 += it.head * u;
-    it.rt = 0;
-    pr_units(a, it.sq, 0, &it.tile0, &it.n);
-    while (begin >= seg0 + it.n) {
-      seg0 += it.n;
-      ++it.rt;
-      pr_units(a, it.sq, it.rt, &it.tile0, &it.n);
+    PrItem x;
+    x.b = (int)s_first[0];
+    x.sq = kv_seq(a, x.b);
+    pr_set(a, x);
+    const long long u = seq_units(x.sq);
+    x.head = (int)((begin - seg0) / u);
+    seg0 += x.head * u;
+    x.rt = 0;
+    pr_units(a, x.sq, 0, &x.tile0, &x.n);
+    while (begin >= seg0 + x.n) {
+      seg0 += x.n;
+      ++x.rt;
+      pr_units(a, x.sq, x.rt, &x.tile0, &x.n);
     }
+    if (lane == 0) it = x;
+    __syncwarp();
   }
+  auto next_item = [&]() {
+    __syncwarp();
+    if (lane == 0) pr_next(a, it);
+    __syncwarp();
+  };
+
+  // From here on units count from `begin`: an item's first one is at rel (not
+  // above 0 for the first item).
+  const int units = (int)(end - begin);
+  int rel = (int)(seg0 - begin);
 
   // Every wait is bounded; a role whose wait runs out counts it and returns,
   // and so do the others in turn, to the common end.
   auto wait1 = [&](uint64_t* bar, uint32_t parity) {             // one thread
-    if (mbar_wait(bar, parity & 1)) return true;
+    if (mbar_sleep(bar, parity & 1)) return true;
     atomicAdd(&g_kv_wait_timeouts, 1u);
     return false;
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) {              // a whole warp: one answer for all its lanes
     return __all_sync(0xFFFFFFFFu, wait1(bar, parity)) != 0;
+  };
+
+  auto arrive = [&](uint64_t* bar) {                             // of a whole warp, as one
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
   };
 
   if (wg < 2) {
@@ -235,10 +280,10 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     [&]() {
       const int rl = threadIdx.x & 127;              // row within the warpgroup, tensor-memory lane
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t t_s = tmem + lanes + kS + wg * 128, t_o = tmem + lanes + kO + wg * 128;
+      const uint32_t t_s0 = tmem + lanes + kS + wg * 128, t_o = tmem + lanes + kO + wg * 128;
       uint32_t kt = 0, mine_t = 0, items = 0, joins = 0;   // tiles of the CTA, tiles and items of this warpgroup
-      for (long long at = begin; at < end;) {
-        const int u0 = (int)(at - seg0), u1 = (int)min((long long)it.n, end - seg0);
+      for (int cur = 0; cur < units;) {
+        const int u0 = cur - rel, u1 = min(it.n, units - rel);
         const int row0 = it.rt * kPrRows + wg * 128, r = row0 + rl;
         const bool active = row0 < it.rows, on = r < it.rows;
         const int qi = on ? r / a.group : 0, g = on ? r - qi * a.group : 0;
@@ -269,119 +314,138 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
             h.y = cvt_f16x2(__uint_as_float(w.y << 16) * s, __uint_as_float(w.y & 0xFFFF0000u) * s);
             h.z = cvt_f16x2(__uint_as_float(w.z << 16) * s, __uint_as_float(w.z & 0xFFFF0000u) * s);
             h.w = cvt_f16x2(__uint_as_float(w.w << 16) * s, __uint_as_float(w.w & 0xFFFF0000u) * s);
-            *reinterpret_cast<uint4*>(sm.q[wg] + (x >> 3) * Smem::kHalf + rl * 128 + (((x & 7) ^ (rl & 7)) * 16)) = h;
+            *reinterpret_cast<uint4*>(sm.q[wg] + (x >> 3) * Smem::kQHalf + rl * 128 + (((x & 7) ^ (rl & 7)) * 16)) = h;
           }
           fence_proxy_async();
-          mbar_arrive(&sm.q_full[wg]);
+          arrive(&sm.q_full[wg]);
           ++items;
         }
         for (int u = u0; u < u1; ++u, ++kt) {
           if (!active) continue;
           const int tok = (it.tile0 + u) * kPrKeys;
-          if (!wait(&sm.v_full[kt & 1], kt >> 1)) return;
-          if (!wait(&sm.s_full[wg], mine_t)) return;
-          tmem_fence_after();
-          const PrInfo& info = sm.info[kt & 3];
-          const bool any_nan = (info.any_nan[0] | info.any_nan[1] | info.any_nan[2] | info.any_nan[3]) != 0;
-          const bool edge = tok + kPrKeys - 1 > first_pos || (a.window > 0 && tok <= last_pos - a.window) || any_nan ||
-                            (info.valid[0] & info.valid[1] & info.valid[2] & info.valid[3]) != 0xFFFFFFFFu;
-          // bit y: this row sees token y of the x-th 32
-          auto seen = [&](int x) {
-            const int base = tok + x * 32;
-            uint32_t m = info.valid[x] & low_bits(pos - base + 1);
+          if (!wait(&sm.info_full[kt % kPrInfos], kt / kPrInfos)) return;
+          const PrInfo& info = sm.info[kt % kPrInfos];
+          bool edge = tok + kPrKeys - 1 > first_pos || (a.window > 0 && tok <= last_pos - a.window);
+          {
+            uint32_t all = 0xFFFFFFFFu, nan = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              all &= info.g[x].valid;
+              nan |= info.g[x].any_nan;
+            }
+            edge |= all != 0xFFFFFFFFu || nan != 0;
+          }
+          // 16 scores from column c on: what this row does not see becomes -inf
+          auto mask = [&](int c, uint32_t (&v)[16]) {
+            const int x = c >> 5, base = tok + x * 32;
+            uint32_t m = info.g[x].valid & low_bits(pos - base + 1);
             if (a.window > 0) m &= ~low_bits(pos - a.window + 1 - base);
-            return m;
+            m = (m >> (c & 16)) & 0xFFFFu;
+#pragma unroll
+            for (int y = 0; y < 16; ++y) v[y] = (m >> y) & 1 ? v[y] : 0xFF800000u;
+            if (info.g[x].any_nan)
+              for (int y = 0; y < NB; ++y) nan_blocks |= ((info.vnan[x][y] >> (c & 16)) & m) ? 1u << y : 0u;
           };
-          // The scores are read twice, 32 at a time, for the largest one and for
-          // the weights: 128 of them in registers would not leave room for the rest.
-          uint32_t s[2][32];
-          float top = kNoMax;
-          tmem_ld32(s[0], t_s);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t(&v)[32] = s[x & 1];
-            tmem_wait_ld(v);
-            tmem_ld32(s[(x + 1) & 1], t_s + ((x + 1) & 3) * 32);    // the last one is the second pass's first
-            if (edge) {
-              const uint32_t m = seen(x);
-#pragma unroll
-              for (int y = 0; y < 32; ++y) v[y] = (m >> y) & 1 ? v[y] : 0xFF800000u;
-              if (info.any_nan[x])
-                for (int y = 0; y < NB; ++y) nan_blocks |= (info.vnan[x][y] & m) ? 1u << y : 0u;
-            }
-            float t0 = __uint_as_float(v[0]), t1 = __uint_as_float(v[1]);
-#pragma unroll
-            for (int y = 2; y < 30; y += 4) {
-              t0 = max3(t0, __uint_as_float(v[y]), __uint_as_float(v[y + 1]));
-              t1 = max3(t1, __uint_as_float(v[y + 2]), __uint_as_float(v[y + 3]));
-            }
-            t0 = max3(t0, __uint_as_float(v[30]), __uint_as_float(v[31]));
-            top = fmaxf(top, fmaxf(t0, t1) * (f_row * info.rk[x]) + info.rv[x]);
-          }
-          if (__any_sync(0xFFFFFFFFu, top > m_ref + kSlack)) {
-            const float m2 = fmaxf(m_ref, top), fix = ex2(m_ref - m2);
-            m_ref = m2;
-            l *= fix;
-            if (u > u0) {                              // the sums so far, once the product that made them is done
-              if (!wait(&sm.o_full[wg], mine_t - 1)) return;
-              tmem_fence_after();
 #pragma unroll 1
-              for (int x = 0; x < D / 32; ++x) {
-                tmem_wait_ld(s[0]);                    // the first scores stay as they are
-                uint32_t o[32];
-                tmem_ld32(o, t_o + x * 32);
-                tmem_wait_ld(o);
+          for (int h = 0; h < 2; ++h) {
+            if (!wait(&sm.s_full[wg][h], mine_t)) return;
+            tmem_fence_after();
+            const uint32_t t_s = t_s0 + h * kPrHalf;
+            // Weights are made against the reference of the tiles before, in one
+            // pass over the scores.  Where their sum passes kMostSum (then some
+            // weight might not fit f16), and on an item's first scores, the
+            // reference moves to the largest score first and the scores, still
+            // in place, are read once more.
+            uint32_t p[kPrHalf / 2];
+            bool again = u == u0 && h == 0;
+            while (true) {
+              if (again) {
+                float top = m_ref;
+#pragma unroll 1
+                for (int x = 0; x < kPrHalf / 16; ++x) {
+                  const int c = h * kPrHalf + x * 16;
+                  uint32_t v[16];
+                  tmem_ld16(v, t_s + x * 16);
+                  tmem_wait_ld(v);
+                  if (edge) mask(c, v);
+                  float t = __uint_as_float(v[0]);
 #pragma unroll
-                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * fix);
-                tmem_st32(t_o + x * 32, o);
+                  for (int y = 1; y < 15; y += 2) t = max3(t, __uint_as_float(v[y]), __uint_as_float(v[y + 1]));
+                  t = fmaxf(t, __uint_as_float(v[15]));
+                  top = fmaxf(top, t * (f_row * info.g[c >> 5].rk) + info.g[c >> 5].rv);
+                }
+                const float fix = ex2(m_ref - top);
+                m_ref = top;
+                l *= fix;
+                if (u > u0 || h > 0) {                 // the sums so far, once the product that made them is done
+                  if (!wait(&sm.o_full[wg][h ^ 1], h ? mine_t : mine_t - 1)) return;
+                  tmem_fence_after();
+#pragma unroll 1
+                  for (int x = 0; x < D / 16; ++x) {
+                    uint32_t o[16];
+                    tmem_ld16(o, t_o + x * 16);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * fix);
+                    tmem_st16(t_o + x * 16, o);
+                  }
+                }
               }
+              uint32_t s[2][16];
+              float sum_p = 0.0f, sum_l = 0.0f;
+              tmem_ld16(s[0], t_s);
+#pragma unroll
+              for (int x = 0; x < kPrHalf / 16; ++x) {
+                uint32_t(&v)[16] = s[x & 1];
+                tmem_wait_ld(v);
+                if (x + 1 < kPrHalf / 16) tmem_ld16(s[(x + 1) & 1], t_s + (x + 1) * 16);
+                const PrInfo::Group& g = info.g[h * 2 + (x >> 1)];
+                if (edge) mask(h * kPrHalf + x * 16, v);
+                const float f = f_row * g.rk, c = g.rv - m_ref;
+                const uint64_t f2 = pack2(f, f), c2 = pack2(c, c);
+                uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+                for (int y = 0; y < 16; y += 4) {
+                  float e0, e1, e2, e3;
+                  unpack2(fma2(pack2(__uint_as_float(v[y]), __uint_as_float(v[y + 1])), f2, c2), e0, e1);
+                  unpack2(fma2(pack2(__uint_as_float(v[y + 2]), __uint_as_float(v[y + 3])), f2, c2), e2, e3);
+                  e0 = ex2(e0);
+                  e1 = ex2(e1);
+                  e2 = ex2(e2);
+                  e3 = ex2(e3);
+                  sum0 = add2(sum0, pack2(e0, e1));
+                  sum1 = add2(sum1, pack2(e2, e3));
+                  p[x * 8 + y / 2] = cvt_f16x2(e0, e1);
+                  p[x * 8 + y / 2 + 1] = cvt_f16x2(e2, e3);
+                }
+                float a0, a1;
+                unpack2(add2(sum0, sum1), a0, a1);
+                sum_p += a0 + a1;
+                sum_l += (a0 + a1) * g.unscale;
+              }
+              if (again || !__any_sync(0xFFFFFFFFu, sum_p > kMostSum)) {
+                l += sum_l;
+                break;
+              }
+              again = true;
             }
+            tmem_st32(t_s, p);                         // over the scores
+            tmem_wait_st();
+            tmem_fence_before();
+            arrive(&sm.p_full[wg][h]);
           }
-          uint32_t p[32];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t(&v)[32] = s[x & 1];
-            tmem_wait_ld(v);
-            if (x < 3) tmem_ld32(s[(x + 1) & 1], t_s + (x + 1) * 32);
-            if (edge) {
-              const uint32_t m = seen(x);
-#pragma unroll
-              for (int y = 0; y < 32; ++y) v[y] = (m >> y) & 1 ? v[y] : 0xFF800000u;
-            }
-            const float rv = info.rv[x], f = f_row * info.rk[x], c = rv - m_ref;
-            const uint64_t f2 = pack2(f, f), c2 = pack2(c, c);
-            uint64_t sum = 0;
-#pragma unroll
-            for (int y = 0; y < 32; y += 2) {
-              float e0, e1;
-              unpack2(fma2(pack2(__uint_as_float(v[y]), __uint_as_float(v[y + 1])), f2, c2), e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              sum = add2(sum, pack2(e0, e1));
-              p[(x & 1) * 16 + y / 2] = cvt_f16x2(e0, e1);
-            }
-            float a0, a1;
-            unpack2(sum, a0, a1);
-            l += (a0 + a1) * pow2f(-(int)rv);
-            // the weights of 64 tokens go over scores that both passes are done with
-            if (x == 1) tmem_st32(t_s, p);
-            if (x == 3) tmem_st32(t_s + 32, p);
-          }
-          tmem_wait_st();
-          tmem_fence_before();
-          mbar_arrive(&sm.p_full[wg]);
           ++mine_t;
         }
 
         // ---- the item's end: output, or a part to be joined
         const bool whole = u0 == 0 && u1 == it.n;
         constexpr int PART = kPrRows * (D + 2);
-        float* part = plan.part + (2 * (long long)blockIdx.x + (seg0 <= begin ? 0 : 1)) * PART;
+        float* part = plan.part + (2 * (long long)blockIdx.x + (rel <= 0 ? 0 : 1)) * PART;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t out_row = it.sq.q0 + qi;
         const int out_head = it.head * a.group + g;
         if (active) {
-          if (!wait(&sm.o_full[wg], mine_t - 1)) return;
+          if (!wait(&sm.o_full[wg][1], mine_t - 1)) return;
           tmem_fence_after();
 #pragma unroll
           for (int x = 0; x < D / 32; ++x) {
@@ -419,9 +483,9 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           tmem_fence_before();
         }
         if (!whole) {
-          const long long first = seg0 / per, last = (seg0 + it.n - 1) / per;
+          const long long per = s_range[1], seg0 = s_range[0] + rel, first = seg0 / per, last = (seg0 + it.n - 1) / per;
           __threadfence();
-          mbar_arrive(&sm.join_all);
+          arrive(&sm.join_all);
           if (warp == 0 && !wait(&sm.join_all, joins)) return;
           if (threadIdx.x == 0) {
             uint32_t* t = plan.ticket + first;       // a CTA starts at most one that others go on with
@@ -471,16 +535,17 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
             }
           }
         }
-        at = seg0 + u1;
-        seg0 += it.n;
-        if (at < end) pr_next(a, it);
+        cur = rel + u1;
+        rel += it.n;
+        if (cur < units) next_item();
       }
     }();
-  } else if (wg == 2) {
+  } else if (wg < 4) {
     // ================= unpacking keys and values =================
-    regs_inc<152>();
+    regs_dec<64>();
     [&]() {
-      const int grp = warp & 3;                      // tokens 32 grp .. + 31 of a tile
+      const bool values = wg == 3;                   // a warpgroup for keys, one for values
+      const int grp = warp & 3;                      // tokens 32 grp .. + 31 of a unit
       const int sub = lane & 7;                      // token of 8 within a step
       // a lane's units are the 16-byte blocks blk of U tokens: eight lanes write
       // the same chunk of eight rows, which the swizzle spreads over all banks
@@ -488,60 +553,99 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
       const int blk = D == 128 ? lane >> 3 : (lane >> 3) & 1;
       auto token_of = [&](int j) { return D == 128 ? j * 8 + sub : j * 16 + (lane >> 4) * 8 + sub; };
       const int page_mask = (1 << a.shape.page_shift) - 1;
-      uint4 kc[U], vc[U];
-      uint32_t kw = 0, vw = 0, valid = 0;            // scales of this lane's token; tokens that exist
-      int64_t row = 0;                               // this lane's token in the cache
-      auto page_of = [&](const PrItem& x, int u) {
-        const int tok = (x.tile0 + u) * kPrKeys + grp * 32 + lane;
-        return tok < x.sq.len ? a.table[x.b * a.table_stride + (tok >> a.shape.page_shift)] : -1;
+      const KvPool pool = values ? a.v : a.k;
+      int cur = 0;
+      typename Smem::Raw& raw = sm.raw[warp - 8];
+      auto page_of = [&]() {
+        const int tok = (it.tile0 + cur - rel) * kPrKeys + grp * 32 + lane;
+        return tok < it.sq.len ? a.table[it.b * a.table_stride + (tok >> a.shape.page_shift)] : -1;
       };
-      // the unit's rows (row, the mask) and one kind of their codes and scales
-      auto locate = [&](const PrItem& x, int u, int page) {
-        const int tok = (x.tile0 + u) * kPrKeys + grp * 32 + lane;
+      // starts the copy of this warp's rows of the unit; gives the mask of those that exist
+      auto fetch = [&](int page) {
+        const int tok = (it.tile0 + cur - rel) * kPrKeys + grp * 32 + lane;
         const int64_t slot = ((int64_t)page << a.shape.page_shift) + (tok & page_mask);
         const bool ok = page >= 0 && slot < a.shape.slots;
-        row = ok ? kv_row(a.shape, slot, x.head) : 0;
-        return __ballot_sync(0xFFFFFFFFu, ok);
+        const uint32_t there = __ballot_sync(0xFFFFFFFFu, ok);
+        copy_rows<D>(smem_addr(raw.codes), smem_addr(raw.scales), pool, ok ? kv_row(a.shape, slot, it.head) : 0, there,
+                     a.shape.page_shift > 0);
+        cp_commit();
+        return there;
       };
-      auto load = [&](const KvPool& pool, uint32_t there, uint4 (&codes)[U], uint32_t& w) {
-        if (D == 128) w = (there >> lane) & 1 ? reinterpret_cast<const uint32_t*>(pool.e8m0)[row] : 0;
-        else w = (there >> lane) & 1 ? reinterpret_cast<const uint16_t*>(pool.e8m0)[row] : 0;
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-          const int t = token_of(j);
-          const int64_t rr = __shfl_sync(0xFFFFFFFFu, row, t);
-          codes[j] = (there >> t) & 1 ? *reinterpret_cast<const uint4*>(pool.q + rr * (D / 2) + blk * 16)
-                                      : make_uint4(0, 0, 0, 0);
+
+      // The items' units in turn.  A unit's codes go to registers as soon as
+      // they have arrived, and the copy of the next one starts at once.
+      auto step = [&]() {                            // it, rel, cur: one unit on; false past the end
+        if (++cur >= units) return false;
+        if (cur == rel + it.n) {
+          rel += it.n;
+          next_item();
         }
+        return true;
       };
-      // codes * 2^(E - R) of this warp's 32 tokens into a swizzled tile; gives R
-      auto unpack = [&](uint8_t* tile, const uint4 (&codes)[U], uint32_t w, bool values, PrInfo& info) {
+      uint32_t next = fetch(page_of());
+      bool more = step();
+      int page = more ? page_of() : -1;
+      uint64_t* full = values ? sm.v_full : sm.k_full;
+      uint64_t* empty = values ? sm.v_empty : sm.k_empty;
+      for (int kt = 0; kt < units; ++kt) {
+        PrInfo& info = sm.info[kt % kPrInfos];
+        const int stg = kt % kPrStages;
+        cp_wait<0>();
+        __syncwarp();
+        const uint32_t valid = next;
+        uint4 codes[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+          codes[j] = *reinterpret_cast<const uint4*>(raw.codes + code_offset<D>(token_of(j), blk));
+        // scales of the lane's token; the pair copy may have brought those of a token that does not exist
+        uint32_t sc = NB == 4 ? reinterpret_cast<const uint32_t*>(raw.scales)[lane]
+                              : reinterpret_cast<const uint16_t*>(raw.scales)[lane];
+        sc = (valid >> lane) & 1 ? sc : 0u;
+        __syncwarp();
+        if (more) {
+          next = fetch(page);
+          more = step();
+          if (more) page = page_of();
+        }
+        if (kt >= kPrStages && !wait(&empty[stg], kt / kPrStages - 1)) return;
+
+        // the group's largest block scale 2^R
         uint32_t top = 0;
         bool bad = false;
 #pragma unroll
         for (int x = 0; x < NB; ++x) {
-          const uint32_t e = (w >> (8 * x)) & 0xFFu;
+          const uint32_t e = (sc >> (8 * x)) & 0xFFu;
           bad |= e == 255u;
           top = max(top, e == 255u ? 0u : e);
         }
-        const bool there = (valid >> lane) & 1;
-        top = __reduce_max_sync(0xFFFFFFFFu, there ? top : 0u);
+        top = __reduce_max_sync(0xFFFFFFFFu, top);   // tokens that do not exist have scale bytes 0
         top = min(max(top, (uint32_t)kMinScale), (uint32_t)kMaxScale);
         if (values) {
-          const uint32_t any = __ballot_sync(0xFFFFFFFFu, there && bad);
+          const uint32_t any = __ballot_sync(0xFFFFFFFFu, bad);
           if (any) {
 #pragma unroll
             for (int x = 0; x < NB; ++x) {
-              const uint32_t m = __ballot_sync(0xFFFFFFFFu, there && ((w >> (8 * x)) & 0xFFu) == 255u);
+              const uint32_t m = __ballot_sync(0xFFFFFFFFu, ((sc >> (8 * x)) & 0xFFu) == 255u);
               if (lane == 0) info.vnan[grp][x] = m;
             }
           }
-          if (lane == 0) info.any_nan[grp] = any;
+          if (lane == 0) {
+            info.g[grp].any_nan = any;
+            info.g[grp].rv = (float)((int)top - 127);
+            info.g[grp].unscale = pow2f(127 - (int)top);
+          }
+        } else if (lane == 0) {
+          info.g[grp].rk = pow2f((int)top - 127);
+          info.g[grp].valid = valid;
         }
+        if (lane == 0) mbar_arrive(&sm.info_full[kt % kPrInfos]);
+
+        // codes * 2^(E - R) into the swizzled tile
+        uint8_t* tile = (values ? sm.v[stg] : sm.k[stg]) + (blk >> 1) * Smem::kHalf + grp * 32 * 128;
 #pragma unroll
         for (int j = 0; j < U; ++j) {
           const int t = token_of(j);
-          const uint32_t e = (__shfl_sync(0xFFFFFFFFu, w, t) >> (8 * blk)) & 0xFFu;
+          const uint32_t e = (__shfl_sync(0xFFFFFFFFu, sc, t) >> (8 * blk)) & 0xFFu;
           const int d = min(126, (int)(top - e));
           float f = __uint_as_float((uint32_t)(127 - d) << 23);
           // a NaN block of keys is NaN to every row that sees the token; one of
@@ -549,143 +653,98 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           if (e == 255u) f = values ? 0.0f : __uint_as_float(0x7FFFFFFFu);
           const uint32_t f2 = cvt_f16x2(f, f);
           const uint32_t ws[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
-          const int row = grp * 32 + t;
-          uint8_t* dst = tile + (blk >> 1) * Smem::kHalf + row * 128;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             uint32_t h[4];
             e2m1x8_f16(ws[x], h);
-            *reinterpret_cast<uint4*>(dst + ((((blk & 1) * 4 + x) ^ (row & 7)) * 16)) =
+            *reinterpret_cast<uint4*>(tile + t * 128 + ((((blk & 1) * 4 + x) ^ sub) * 16)) =
                 make_uint4(mul_f16x2(h[0], f2), mul_f16x2(h[1], f2), mul_f16x2(h[2], f2), mul_f16x2(h[3], f2));
           }
         }
-        return top;
-      };
-
-      // The items' units in turn.  While one kind of a unit is unpacked, the
-      // other kind's codes are in flight, and the page of the unit after.
-      PrItem nx = it;
-      long long nseg = seg0, at = begin;
-      auto step = [&]() {                            // nx, nseg, at: one unit on; false at the end
-        ++at;
-        if (at >= end) return false;
-        if (at == nseg + nx.n) {
-          nseg += nx.n;
-          pr_next(a, nx);
-        }
-        return true;
-      };
-      int page = page_of(nx, (int)(at - nseg));
-      valid = locate(nx, (int)(at - nseg), page);
-      load(a.k, valid, kc, kw);
-      load(a.v, valid, vc, vw);
-      bool more = step();
-      if (more) page = page_of(nx, (int)(at - nseg));
-      const uint32_t units = (uint32_t)(end - begin);
-      for (uint32_t kt = 0; kt < units; ++kt) {
-        PrInfo& info = sm.info[kt & 3];
-        const int stg = kt & 1;
-        if (kt >= 2 && !wait(&sm.k_empty[stg], (kt >> 1) - 1)) return;
-        const uint32_t rk = unpack(sm.k[stg], kc, kw, false, info);
-        if (lane == 0) {
-          info.rk[grp] = pow2f((int)rk - 127);
-          info.valid[grp] = valid;
-        }
         fence_proxy_async();
-        mbar_arrive(&sm.k_full[stg]);
-        uint32_t next = 0;
-        if (more) {
-          next = locate(nx, (int)(at - nseg), page);
-          load(a.k, next, kc, kw);
-        }
-        if (kt >= 2 && !wait(&sm.v_empty[stg], (kt >> 1) - 1)) return;
-        const uint32_t rv = unpack(sm.v[stg], vc, vw, true, info);
-        if (lane == 0) info.rv[grp] = (float)((int)rv - 127);
-        fence_proxy_async();
-        mbar_arrive(&sm.v_full[stg]);
-        if (more) {
-          load(a.v, next, vc, vw);
-          more = step();
-          if (more) page = page_of(nx, (int)(at - nseg));
-        }
-        valid = next;
+        arrive(&full[stg]);
       }
     }();
   } else {
-    // ================= one warp issues the products =================
-    // The whole warp goes through the loop, so that addresses and descriptors
-    // stay in uniform registers; one elected lane issues.
-    regs_dec<72>();
-    if (warp == 12) {
+    // ================= two warps issue the products, one for each 128 rows =================
+    // Issuing blocks while the tensor cores are busy and a wait costs a hundred
+    // clocks even where nothing is waited for; with a warp each, one side's waits
+    // pass while the other's products run.  The whole warp goes through the
+    // loop, so that addresses and descriptors stay in uniform registers; one
+    // elected lane issues.
+    regs_dec<64>();
+    if (warp < kPrIssuer + 2) {
       [&]() {
-        constexpr uint32_t kQK = f16_idesc(128, kPrKeys, false), kPV = f16_idesc(128, D, true);
-        constexpr uint32_t kHi = desc_hi(1024);
-        const uint32_t qa = desc_lo(smem_addr(sm.q[0]), 16), ka = desc_lo(smem_addr(sm.k[0]), 16);
+        constexpr uint32_t kQK = f16_idesc(128, kPrHalf, false), kPV = f16_idesc(128, D, true);
+        constexpr uint32_t kHi = desc_hi(1024), kHalfBytes = kPrHalf * 128;
+        const int w = __shfl_sync(0xFFFFFFFFu, warp - kPrIssuer, 0);
+        const uint32_t qa = desc_lo(smem_addr(sm.q[w]), 16), ka = desc_lo(smem_addr(sm.k[0]), 16);
         const uint32_t va = desc_lo(smem_addr(sm.v[0]), Smem::kHalf);
         const bool lead = elect_one();
-        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-        uint32_t kt = 0, items0 = 0, items1 = 0, done0 = 0, done1 = 0;
-        auto scores = [&](int w, int stg) {
-          const uint32_t q = qa + w * (Smem::kTileBytes >> 4), k = ka + stg * (Smem::kTileBytes >> 4);
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0) + w * 128;
+        uint32_t kt = 0, items = 0, mine_t = 0;       // units of the CTA; this side's items and units
+        auto scores = [&](uint32_t stg, int h) {
+          const uint32_t k = ka + ((stg * Smem::kTileBytes + h * kHalfBytes) >> 4), d = tm + kS + h * kPrHalf;
           if (lead) {
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-              const uint32_t off = ((x >> 2) * Smem::kHalf + (x & 3) * 32) >> 4;
-              mma_ss(tm + kS + w * 128, q + off, k + off, kHi, kQK, x > 0);
-            }
-            mma_commit(&sm.s_full[w]);
+            for (int x = 0; x < D / 16; ++x)
+              mma_ss(d, qa + (((x >> 2) * Smem::kQHalf + (x & 3) * 32) >> 4),
+                     k + (((x >> 2) * Smem::kHalf + (x & 3) * 32) >> 4), kHi, kQK, x > 0);
+            mma_commit(&sm.s_full[w][h]);
+            if (h) mma_commit(&sm.k_empty[stg]);
           }
           __syncwarp();
         };
-        auto values = [&](int w, int stg, bool first) {
-          const uint32_t v = va + stg * (Smem::kTileBytes >> 4);
+        auto values = [&](uint32_t stg, int h, bool first) {
+          const uint32_t v = va + ((stg * Smem::kTileBytes + h * kHalfBytes) >> 4), p = tm + kS + h * kPrHalf;
           if (lead) {
 #pragma unroll
-            for (int x = 0; x < kPrKeys / 16; ++x)
-              mma_ts(tm + kO + w * 128, tm + kS + w * 128 + x * 8, v + x * (2048 >> 4), kHi, kPV, !first || x > 0);
-            mma_commit(&sm.o_full[w]);
+            for (int x = 0; x < kPrHalf / 16; ++x)
+              mma_ts(tm + kO, p + x * 8, v + x * (2048 >> 4), kHi, kPV, !first || x > 0);
+            mma_commit(&sm.o_full[w][h]);
+            if (h) mma_commit(&sm.v_empty[stg]);
           }
           __syncwarp();
         };
-        for (long long at = begin; at < end;) {
-          const int u0 = (int)(at - seg0), u1 = (int)min((long long)it.n, end - seg0);
-          const bool two = it.rt * kPrRows + 128 < it.rows;
-          if (!wait(&sm.k_full[kt & 1], kt >> 1)) return;
-          if (!wait(&sm.q_full[0], items0++)) return;
-          tmem_fence_after();
-          scores(0, kt & 1);
-          if (two) {
-            if (!wait(&sm.q_full[1], items1++)) return;
+        // Each half's scores of the next unit are made as soon as the weights
+        // that lie over them have been used, while the other half is in work.
+        for (int cur = 0; cur < units;) {
+          const int n = min(it.n, units - rel) - (cur - rel);
+          const bool active = it.rt * kPrRows + w * 128 < it.rows;
+          if (active) {
+            if (!wait(&sm.q_full[w], items++)) return;
+            if (!wait(&sm.k_full[kt % kPrStages], kt / kPrStages)) return;
             tmem_fence_after();
-            scores(1, kt & 1);
-          }
-          if (lead) mma_commit(&sm.k_empty[kt & 1]);
-          for (int u = u0; u < u1; ++u, ++kt) {
-            const uint32_t nk = kt + 1;
-            const bool more = u + 1 < u1;
-            if (!wait(&sm.v_full[kt & 1], kt >> 1)) return;
-            if (!wait(&sm.p_full[0], done0++)) return;
-            tmem_fence_after();
-            values(0, kt & 1, u == u0);
-            if (more) {
-              if (!wait(&sm.k_full[nk & 1], nk >> 1)) return;
-              scores(0, nk & 1);
-            }
-            if (two) {
-              if (!wait(&sm.p_full[1], done1++)) return;
+            scores(kt % kPrStages, 0);
+            scores(kt % kPrStages, 1);
+            for (int u = 0; u < n; ++u, ++kt, ++mine_t) {
+              const uint32_t stg = kt % kPrStages, nk = kt + 1, ns = nk % kPrStages;
+              if (!wait(&sm.v_full[stg], kt / kPrStages)) return;
+              if (!wait(&sm.p_full[w][0], mine_t)) return;
               tmem_fence_after();
-              values(1, kt & 1, u == u0);
-              if (more) scores(1, nk & 1);
+              values(stg, 0, u == 0);
+              if (u + 1 < n) {
+                if (!wait(&sm.k_full[ns], nk / kPrStages)) return;
+                scores(ns, 0);
+              }
+              if (!wait(&sm.p_full[w][1], mine_t)) return;
+              tmem_fence_after();
+              values(stg, 1, false);
+              if (u + 1 < n) scores(ns, 1);
             }
-            if (lead) {
-              mma_commit(&sm.v_empty[kt & 1]);
-              if (more) mma_commit(&sm.k_empty[nk & 1]);
+          } else {                                   // no such rows: the stages still need this side's word
+            for (int u = 0; u < n; ++u, ++kt) {
+              const uint32_t stg = kt % kPrStages;
+              if (!wait(&sm.k_full[stg], kt / kPrStages)) return;
+              if (lane == 0) mbar_arrive(&sm.k_empty[stg]);
+              if (!wait(&sm.v_full[stg], kt / kPrStages)) return;
+              if (lane == 0) mbar_arrive(&sm.v_empty[stg]);
+              __syncwarp();
             }
-            __syncwarp();
           }
-          at = seg0 + u1;
-          seg0 += it.n;
-          if (at < end) pr_next(a, it);
+          cur += n;
+          rel += it.n;
+          if (cur < units) next_item();
         }
       }();
       // nothing may still be running when the tensor memory goes back
@@ -697,7 +756,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
   }
   tmem_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kPrIssuer) {
     tmem_fence_after();
     tmem_free(tmem, 512);
   }
