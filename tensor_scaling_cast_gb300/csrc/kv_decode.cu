@@ -237,9 +237,8 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
         const int64_t row = ok ? kv_row(a.shape, slot, head) : 0;
         const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok);
         if (lane == 0) sm.valid[st] = valid;
-        const bool pair = a.shape.page_shift > 0;
-        copy_rows<D>(smem_u32(sm.stage[st].k), smem_u32(sm.stage[st].ke), a.k, row, valid, pair);
-        copy_rows<D>(smem_u32(sm.stage[st].v), smem_u32(sm.stage[st].ve), a.v, row, valid, pair);
+        copy_rows<D>(smem_u32(sm.stage[st].k), smem_u32(sm.stage[st].ke), a.k, row, valid, a.shape.page_shift);
+        copy_rows<D>(smem_u32(sm.stage[st].v), smem_u32(sm.stage[st].ve), a.v, row, valid, a.shape.page_shift);
       }
       cp_commit();
     };

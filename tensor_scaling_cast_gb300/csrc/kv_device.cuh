@@ -159,18 +159,30 @@ __device__ __forceinline__ uint32_t code_offset(int r, int c) {
 
 // This warp's copy of the codes and scales of 32 cached rows into shared
 // memory, asynchronously: row is the cache row of the lane's token, bit t of
-// valid says whether token t exists (else zeros are written).  pair_scales:
-// two tokens' rows are neighbours (page size 2 or more).
+// valid says whether token t exists (else zeros are written).  Pages of 32
+// tokens or more hold the 32 rows in one run, as tiles start at multiples of
+// 32, so that one address serves them all.
 template <int D>
 __device__ __forceinline__ void copy_rows(uint32_t codes, uint32_t scales, const KvPool& pool, int64_t row,
-                                          uint32_t valid, bool pair_scales) {
+                                          uint32_t valid, int page_shift) {
   constexpr int RB = D / 2, CH = RB / 16;
   const int lane = threadIdx.x & 31;
+  const bool pair_scales = page_shift > 0;
+  if (page_shift >= 5) {
+    // chunk `lane` of the run and every 32nd from there: rows x * (32 / CH) on
+    const uint8_t* src = pool.q + __shfl_sync(0xFFFFFFFFu, row, 0) * RB + lane * 16;
 #pragma unroll
-  for (int x = 0; x < CH; ++x) {
-    const int r = x * (32 / CH) + lane / CH, c = lane % CH;
-    const int64_t rr = __shfl_sync(0xFFFFFFFFu, row, r);
-    cp_async16(codes + code_offset<D>(r, c), pool.q + rr * RB + c * 16, (valid >> r) & 1);
+    for (int x = 0; x < CH; ++x) {
+      const int r = x * (32 / CH) + lane / CH;
+      cp_async16(codes + code_offset<D>(r, lane % CH), src + x * 512, (valid >> r) & 1);
+    }
+  } else {
+#pragma unroll
+    for (int x = 0; x < CH; ++x) {
+      const int r = x * (32 / CH) + lane / CH, c = lane % CH;
+      const int64_t rr = __shfl_sync(0xFFFFFFFFu, row, r);
+      cp_async16(codes + code_offset<D>(r, c), pool.q + rr * RB + c * 16, (valid >> r) & 1);
+    }
   }
   const bool ok = (valid >> lane) & 1;
   if (D == 128) {

@@ -41,12 +41,9 @@ constexpr int kPrMinUnits = 4;            // units of a CTA, at least
 __device__ unsigned int g_kv_wait_timeouts = 0;
 
 constexpr int kPrInfos = 4;               // more units than the unpacking warps can be ahead
-struct PrInfo {                           // of a unit, written by the unpacking warps
-  struct Group {                          // of 32 tokens
-    float rk, rv, unscale;                // 2^Rk, Rv, 2^-Rv
-    uint32_t valid, any_nan;              // tokens that exist, tokens with a NaN block of values
-    uint32_t pad[3];
-  } g[4];
+struct __align__(16) PrInfo {             // of a unit, by its groups of 32 tokens; written by the unpacking warps
+  float rk[4], rv[4], unscale[4];         // 2^Rk, Rv, 2^-Rv
+  uint32_t valid[4], any_nan[4];          // tokens that exist, tokens with a NaN block of values
   uint32_t vnan[4][4];                    // tokens with block b of the values NaN (set where any_nan is not 0)
 };
 
@@ -327,23 +324,18 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           const PrInfo& info = sm.info[kt % kPrInfos];
           bool edge = tok + kPrKeys - 1 > first_pos || (a.window > 0 && tok <= last_pos - a.window);
           {
-            uint32_t all = 0xFFFFFFFFu, nan = 0;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              all &= info.g[x].valid;
-              nan |= info.g[x].any_nan;
-            }
-            edge |= all != 0xFFFFFFFFu || nan != 0;
+            const uint4 all = *reinterpret_cast<const uint4*>(info.valid), nan = *reinterpret_cast<const uint4*>(info.any_nan);
+            edge |= (all.x & all.y & all.z & all.w) != 0xFFFFFFFFu || (nan.x | nan.y | nan.z | nan.w) != 0;
           }
           // 16 scores from column c on: what this row does not see becomes -inf
           auto mask = [&](int c, uint32_t (&v)[16]) {
             const int x = c >> 5, base = tok + x * 32;
-            uint32_t m = info.g[x].valid & low_bits(pos - base + 1);
+            uint32_t m = info.valid[x] & low_bits(pos - base + 1);
             if (a.window > 0) m &= ~low_bits(pos - a.window + 1 - base);
             m = (m >> (c & 16)) & 0xFFFFu;
 #pragma unroll
             for (int y = 0; y < 16; ++y) v[y] = (m >> y) & 1 ? v[y] : 0xFF800000u;
-            if (info.g[x].any_nan)
+            if (info.any_nan[x])
               for (int y = 0; y < NB; ++y) nan_blocks |= ((info.vnan[x][y] >> (c & 16)) & m) ? 1u << y : 0u;
           };
 #pragma unroll 1
@@ -372,7 +364,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
 #pragma unroll
                   for (int y = 1; y < 15; y += 2) t = max3(t, __uint_as_float(v[y]), __uint_as_float(v[y + 1]));
                   t = fmaxf(t, __uint_as_float(v[15]));
-                  top = fmaxf(top, t * (f_row * info.g[c >> 5].rk) + info.g[c >> 5].rv);
+                  top = fmaxf(top, t * (f_row * info.rk[c >> 5]) + info.rv[c >> 5]);
                 }
                 const float fix = ex2(m_ref - top);
                 m_ref = top;
@@ -394,14 +386,15 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
               uint32_t s[2][16];
               float sum_p = 0.0f, sum_l = 0.0f;
               tmem_ld16(s[0], t_s);
+              const float2 rk = reinterpret_cast<const float2*>(info.rk)[h], rv = reinterpret_cast<const float2*>(info.rv)[h];
+              const float2 un = reinterpret_cast<const float2*>(info.unscale)[h];
 #pragma unroll
               for (int x = 0; x < kPrHalf / 16; ++x) {
                 uint32_t(&v)[16] = s[x & 1];
                 tmem_wait_ld(v);
                 if (x + 1 < kPrHalf / 16) tmem_ld16(s[(x + 1) & 1], t_s + (x + 1) * 16);
-                const PrInfo::Group& g = info.g[h * 2 + (x >> 1)];
                 if (edge) mask(h * kPrHalf + x * 16, v);
-                const float f = f_row * g.rk, c = g.rv - m_ref;
+                const float f = f_row * (x < 2 ? rk.x : rk.y), c = (x < 2 ? rv.x : rv.y) - m_ref;
                 const uint64_t f2 = pack2(f, f), c2 = pack2(c, c);
                 uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
@@ -421,7 +414,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
                 float a0, a1;
                 unpack2(add2(sum0, sum1), a0, a1);
                 sum_p += a0 + a1;
-                sum_l += (a0 + a1) * g.unscale;
+                sum_l += (a0 + a1) * (x < 2 ? un.x : un.y);
               }
               if (again || !__any_sync(0xFFFFFFFFu, sum_p > kMostSum)) {
                 l += sum_l;
@@ -567,7 +560,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
         const bool ok = page >= 0 && slot < a.shape.slots;
         const uint32_t there = __ballot_sync(0xFFFFFFFFu, ok);
         copy_rows<D>(smem_addr(raw.codes), smem_addr(raw.scales), pool, ok ? kv_row(a.shape, slot, it.head) : 0, there,
-                     a.shape.page_shift > 0);
+                     a.shape.page_shift);
         cp_commit();
         return there;
       };
@@ -630,13 +623,13 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
             }
           }
           if (lane == 0) {
-            info.g[grp].any_nan = any;
-            info.g[grp].rv = (float)((int)top - 127);
-            info.g[grp].unscale = pow2f(127 - (int)top);
+            info.any_nan[grp] = any;
+            info.rv[grp] = (float)((int)top - 127);
+            info.unscale[grp] = pow2f(127 - (int)top);
           }
         } else if (lane == 0) {
-          info.g[grp].rk = pow2f((int)top - 127);
-          info.g[grp].valid = valid;
+          info.rk[grp] = pow2f((int)top - 127);
+          info.valid[grp] = valid;
         }
         if (lane == 0) mbar_arrive(&sm.info_full[kt % kPrInfos]);
 
