@@ -161,6 +161,7 @@ FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int
   a.max_q = max_q;
   a.q_heads = q_heads;
   a.group = q_heads / c->kv_heads;
+  a.by_group = FastDiv((uint32_t)a.group);
   a.window = window > 0x3FFFFFFF ? 0 : window;   // no sequence is that long
   a.scale = scale;
   int launches = 0;

@@ -115,7 +115,7 @@ struct DecPlan {
 template <int D, int NT>
 __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
 kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPlan plan) {
-  constexpr int NB = D / 32, RB = D / 2, ROWS = 8 * NT;
+  constexpr int NB = D / 32, ROWS = 8 * NT;
   using Smem = DecSmem<D>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -125,6 +125,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
   __shared__ int s_start[2];
   __shared__ long long s_before;
   __shared__ uint32_t s_last;
+  __shared__ Joined s_rows[8 * NT];
 
   // ---- this CTA's range of tiles: a scan of the sequences' tile counts
   const int per_thread = (a.batch + kDecThreads - 1) / kDecThreads;
@@ -179,7 +180,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + li;
       const bool on = r < rows;
-      const int qi = on ? r / a.group : 0, g = on ? r - qi * a.group : 0;
+      const int qi = on ? a.by_group.div(r) : 0, g = on ? r - qi * a.group : 0;
       const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)(sq.q0 + qi) * a.q_tok +
                                (int64_t)(head * a.group + g) * a.q_head + lc * 8;
       uint4 w[NB];
@@ -353,7 +354,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const int pos = pos0 + (nt * 8 + lc * 2 + y) / a.group;
+            const int pos = pos0 + a.by_group.div(nt * 8 + lc * 2 + y);
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               const int t = z * 8 + li, j = tok + t;
@@ -441,7 +442,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
           for (int nt = 0; nt < NT; ++nt) {
             uint32_t b0 = mul_f16x2(p[u][nt][0], f0), b1 = mul_f16x2(p[u][nt][1], f1);
             if (edge && v_nan) {                 // a hidden token's NaN scale must not reach its zero weight
-              const int pos = pos0 + (nt * 8 + li) / a.group;
+              const int pos = pos0 + a.by_group.div(nt * 8 + li);
 #pragma unroll
               for (int z = 0; z < 4; ++z) {
                 const int j = tok + u * 16 + (z >> 1) * 8 + lc * 2 + (z & 1);
@@ -489,58 +490,59 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       }
     __syncthreads();
 
+    // Each thread has the same four columns of U rows, of the warps' sums
+    // first and of the CTAs' parts where there are several.
     const bool whole = t0 == 0 && t1 == sq.tiles;
-    const float* src = reinterpret_cast<const float*>(smem_raw);
-    // parts: [n] of stride `stride`, each [rows][D], M[rows], l[rows]; a NULL
-    // dst gives the output itself
-    auto join = [&](auto part_at, int n, float* dst) {
-      for (int w = threadIdx.x; w < rows * (D / 4); w += kDecThreads) {
-        const int r = w / (D / 4), c = w % (D / 4);
-        float m = kNoMax;
-        for (int i = 0; i < n; ++i) m = fmaxf(m, part_at(i)[ROWS * D + r]);
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float sum = 0.0f;
-        for (int i = 0; i < n; ++i) {
-          const float* q = part_at(i);
-          const float f = ex2(q[ROWS * D + r] - m);
-          const float4 v = *reinterpret_cast<const float4*>(q + r * D + c * 4);
-          s.x += v.x * f;
-          s.y += v.y * f;
-          s.z += v.z * f;
-          s.w += v.w * f;
-          sum += q[ROWS * D + ROWS + r] * f;
-        }
+    constexpr int PART = ROWS * (D + 2), U = ROWS * (D / 4) / kDecThreads, STEP = kDecThreads / (D / 4);
+    constexpr int PER_ROW = NT == 1 ? 16 : NT == 2 ? 8 : 4;     // threads that find a row's reference
+    const int r0 = threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
+    auto join = [&](auto part_at, int n, float* dst) {          // dst: where the joined part goes; NULL: the output
+      const int r = threadIdx.x / PER_ROW;
+      Joined j = {kNoMax, 0.0f};
+      if (r < rows) j = row_of_parts<ROWS, D>(part_at, threadIdx.x % PER_ROW, PER_ROW, n, r);
+#pragma unroll
+      for (int x = 1; x < PER_ROW; x <<= 1)
+        j = join2(j, {__shfl_xor_sync(0xFFFFFFFFu, j.m, x), __shfl_xor_sync(0xFFFFFFFFu, j.l, x)});
+      if (r < rows && threadIdx.x % PER_ROW == 0) {
+        s_rows[r] = j;
         if (dst) {
-          *reinterpret_cast<float4*>(dst + r * D + c * 4) = s;
-          if (c == 0) {
-            dst[ROWS * D + r] = m;
-            dst[ROWS * D + ROWS + r] = sum;
-          }
+          dst[ROWS * D + r] = j.m;
+          dst[ROWS * D + ROWS + r] = j.l;
         } else {
-          const int qi = r / a.group, h = head * a.group + r - qi * a.group;
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)(sq.q0 + qi) * a.out_tok +
-                               (int64_t)h * a.out_head + c * 4;
-          uint2 v;
-          v.x = sum == 0.0f ? 0u : cvt_bf16x2(s.x * inv, s.y * inv);
-          v.y = sum == 0.0f ? 0u : cvt_bf16x2(s.z * inv, s.w * inv);
-          *reinterpret_cast<uint2*>(out) = v;
-          if (a.lse && c == 0)
-            a.lse[(int64_t)(sq.q0 + qi) * a.q_heads + h] =
-                sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+          const int qi = a.by_group.div(r);
+          store_lse(a, sq.q0 + qi, head * a.group + r - qi * a.group, j.m, j.l);
+        }
+      }
+      __syncthreads();
+      int rs[U];
+      float m[U];
+      float4 v[U];
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        rs[x] = min(r0 + x * STEP, rows - 1);
+        m[x] = s_rows[rs[x]].m;
+      }
+      columns_of_parts<ROWS, D, U, (U >= 4 ? 2 : 8 / U)>(part_at, n, rs, c, m, v);
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        if (r0 + x * STEP >= rows) continue;
+        if (dst) {
+          *reinterpret_cast<float4*>(dst + rs[x] * D + c * 4) = v[x];
+        } else {
+          const int qi = a.by_group.div(rs[x]);
+          store_columns(a, sq.q0 + qi, head * a.group + rs[x] - qi * a.group, c, v[x], s_rows[rs[x]].l);
         }
       }
     };
-    constexpr int PART = ROWS * (D + 2);
+    const float* src = reinterpret_cast<const float*>(smem_raw);
+    auto warp_part = [&](int i) { return src + i * PART; };
     if (whole) {
-      join([&](int i) { return src + i * PART; }, kDecWarps, static_cast<float*>(nullptr));
-      __syncthreads();
+      join(warp_part, kDecWarps, nullptr);
     } else {
       // parts of this (sequence, head): CTAs first .. last; a CTA's slot is 0
       // where the (sequence, head) covers the start of its range, else 1
       const long long first = seg0 / per, last = (seg0 + sq.tiles - 1) / per;
-      float* mine_part = plan.part + (2 * (long long)blockIdx.x + (seg0 <= begin ? 0 : 1)) * PART;
-      join([&](int i) { return src + i * PART; }, kDecWarps, mine_part);
+      join(warp_part, kDecWarps, plan.part + (2 * (long long)blockIdx.x + (seg0 <= begin ? 0 : 1)) * PART);
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -553,12 +555,12 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       if (s_last) {
         __threadfence();
         join([&](int i) {
-          const long long c = first + i;
-          return const_cast<const float*>(plan.part) + (2 * c + (seg0 <= c * per ? 0 : 1)) * PART;
-        }, (int)(last - first) + 1, static_cast<float*>(nullptr));
+          const long long x = first + i;
+          return static_cast<const float*>(plan.part) + (2 * x + (seg0 <= x * per ? 0 : 1)) * PART;
+        }, (int)(last - first) + 1, nullptr);
       }
-      __syncthreads();
     }
+    __syncthreads();
 
     // ---- the next (sequence, head)
     at = seg0 + t1;

@@ -26,6 +26,7 @@ struct FastDiv {
     while ((1ull << shift) < v) ++shift;
     mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - v)) / v + 1);
   }
+  __device__ __forceinline__ int div(int n) const { return (int)div((uint32_t)n); }
   __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
 };
 
@@ -230,6 +231,7 @@ struct KvAttn {
   int64_t q_tok, q_head, out_tok, out_head;   // strides in elements
   int64_t table_stride;
   int32_t table_width, batch, total_q, max_q, q_heads, group, window;
+  FastDiv by_group;                            // division by group
   float scale;
 };
 // What a call has to do for sequence b.  Query i of the sequence sits at
@@ -247,6 +249,71 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttn& a, int b) {
   s.len = (int)min((int64_t)max(a.kv_lens[b], 0), most);
   s.pos0 = s.len - n;
   return s;
+}
+
+// ---- joining the parts of rows --------------------------------------------------
+//
+// A part holds, for R rows, the sums o [R][D] under the row's own reference
+// m [R] and softmax sum l [R].  Joined: M = max m, o = sum 2^(m - M) o and l
+// alike, in the order of the parts.  Two steps, both with several parts'
+// loads in flight: row_of_parts finds M and l per row (one thread per row),
+// then every four columns of a row are one thread's.
+
+struct Joined {
+  float m, l;
+};
+__device__ __forceinline__ Joined join2(const Joined& a, const Joined& b) {
+  const float m = fmaxf(a.m, b.m);
+  return {m, a.l * ex2(a.m - m) + b.l * ex2(b.m - m)};
+}
+// Row r of parts first, first + step, ..
+template <int R, int D, class PartAt>
+__device__ __forceinline__ Joined row_of_parts(PartAt part_at, int first, int step, int n, int r) {
+  Joined j = {kNoMax, 0.0f};
+#pragma unroll 4
+  for (int i = first; i < n; i += step) {
+    const float* q = part_at(i) + R * D + r;
+    j = join2(j, {q[0], q[R]});
+  }
+  return j;
+}
+// Columns 4 c .. 4 c + 3 of U rows r[] under their joined references m[];
+// AHEAD parts at a time.
+template <int R, int D, int U, int AHEAD, class PartAt>
+__device__ __forceinline__ void columns_of_parts(PartAt part_at, int n, const int (&r)[U], int c, const float (&m)[U],
+                                                 float4 (&o)[U]) {
+#pragma unroll
+  for (int x = 0; x < U; ++x) o[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll AHEAD
+  for (int i = 0; i < n; ++i) {
+    const float* q = part_at(i);
+    float4 v[U];
+    float f[U];
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      v[x] = *reinterpret_cast<const float4*>(q + r[x] * D + c * 4);
+      f[x] = q[R * D + r[x]];
+    }
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const float k = ex2(f[x] - m[x]);
+      o[x].x += v[x].x * k;
+      o[x].y += v[x].y * k;
+      o[x].z += v[x].z * k;
+      o[x].w += v[x].w * k;
+    }
+  }
+}
+// Four columns of one row's output, from its sums.
+__device__ __forceinline__ void store_columns(const KvAttn& a, int64_t row, int head, int c, const float4& o, float l) {
+  const float k = l == 0.0f ? 0.0f : 1.0f / l;       // a row that sees no key gets zeros
+  uint2 v;
+  v.x = l == 0.0f ? 0u : cvt_bf16x2(o.x * k, o.y * k);
+  v.y = l == 0.0f ? 0u : cvt_bf16x2(o.z * k, o.w * k);
+  *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + row * a.out_tok + head * a.out_head + c * 4) = v;
+}
+__device__ __forceinline__ void store_lse(const KvAttn& a, int64_t row, int head, float m, float l) {
+  if (a.lse) a.lse[row * a.q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // Few query rows per key/value head (kv_decode.cu).

@@ -36,7 +36,8 @@ constexpr int kPrRows = 256;              // query rows of an item: two warpgrou
 constexpr int kPrKeys = 128;              // keys of a unit
 constexpr int kPrHalf = 64;               // and of a half of it: scores are made and used by halves
 constexpr int kPrStages = 2;              // units of unpacked keys, and of values, in shared memory
-constexpr int kPrMinUnits = 4;            // units of a CTA, at least
+constexpr int kPrMinUnits = 8;            // units of a CTA, at least
+constexpr int kPrSetup = 6;               // what an item costs beyond its units, in units: queries in, output out
 
 __device__ unsigned int g_kv_wait_timeouts = 0;
 
@@ -78,7 +79,7 @@ struct PrSmem {
 
 __device__ __forceinline__ void pr_units(const KvAttn& a, const KvSeq& s, int rt, int* tile0, int* n) {
   const int rows = s.nq * a.group;
-  const int first = rt * kPrRows / a.group, last = (min(rows, (rt + 1) * kPrRows) - 1) / a.group;
+  const int first = a.by_group.div(rt * kPrRows), last = a.by_group.div(min(rows, (rt + 1) * kPrRows) - 1);
   const int begin = a.window > 0 ? max(0, s.pos0 + first - a.window + 1) : 0;
   const int end = min(s.len, s.pos0 + last + 1);
   *tile0 = begin / kPrKeys;
@@ -162,7 +163,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     for (int rt = lane; rt < tiles_r; rt += 32) {
       int t0, n;
       pr_units(a, s, rt, &t0, &n);
-      u += n;
+      u += n + kPrSetup;
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, x);
@@ -234,12 +235,26 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     const long long u = seq_units(x.sq);
     x.head = (int)((begin - seg0) / u);
     seg0 += x.head * u;
-    x.rt = 0;
-    pr_units(a, x.sq, 0, &x.tile0, &x.n);
-    while (begin >= seg0 + x.n) {
-      seg0 += x.n;
-      ++x.rt;
-      pr_units(a, x.sq, x.rt, &x.tile0, &x.n);
+    // the row tile that holds `begin`: 32 at a time
+    for (x.rt = 0;; x.rt += 32) {
+      int t0 = 0, n = 0;
+      if (x.rt + lane < x.tiles_r) pr_units(a, x.sq, x.rt + lane, &t0, &n);
+      long long upto = x.rt + lane < x.tiles_r ? n + kPrSetup : 0;
+#pragma unroll
+      for (int y = 1; y < 32; y <<= 1) {
+        const long long z = __shfl_up_sync(0xFFFFFFFFu, upto, y);
+        if (lane >= y) upto += z;
+      }
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, seg0 + upto > begin);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        x.tile0 = __shfl_sync(0xFFFFFFFFu, t0, l);
+        x.n = __shfl_sync(0xFFFFFFFFu, n, l);
+        seg0 += __shfl_sync(0xFFFFFFFFu, upto, l) - (x.n + kPrSetup);
+        x.rt += l;
+        break;
+      }
+      seg0 += __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
     if (lane == 0) it = x;
     __syncwarp();
@@ -250,10 +265,19 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     __syncwarp();
   };
 
-  // From here on units count from `begin`: an item's first one is at rel (not
-  // above 0 for the first item).
+  // From here on positions count from `begin`: an item lies at rel .. (not above
+  // 0 for the first item), kPrSetup positions and then its units.
   const int units = (int)(end - begin);
   int rel = (int)(seg0 - begin);
+  // the item's units that are this CTA's, and the step to the next item that has any
+  auto unit0 = [&]() { return max(0, -rel - kPrSetup); };
+  auto unit1 = [&]() { return min(it.n, units - rel - kPrSetup); };
+  auto advance = [&]() {
+    rel += kPrSetup + it.n;
+    if (rel + kPrSetup >= units) return false;
+    next_item();
+    return true;
+  };
 
   // Every wait is bounded; a role whose wait runs out counts it and returns,
   // and so do the others in turn, to the common end.
@@ -277,41 +301,48 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     [&]() {
       const int rl = threadIdx.x & 127;              // row within the warpgroup, tensor-memory lane
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      constexpr int CPR = D / 8, RPI = 32 / CPR;     // 16-byte chunks of a bf16 row; rows in 32 lanes' worth
       const uint32_t t_s0 = tmem + lanes + kS + wg * 128, t_o = tmem + lanes + kO + wg * 128;
-      uint32_t kt = 0, mine_t = 0, items = 0, joins = 0;   // tiles of the CTA, tiles and items of this warpgroup
-      for (int cur = 0; cur < units;) {
-        const int u0 = cur - rel, u1 = min(it.n, units - rel);
+      uint32_t kt = 0, mine_t = 0, items = 0;   // tiles of the CTA, tiles and items of this warpgroup
+      uint32_t joins = 0, all_n = 0;                 // phases of join_last, join_all
+      for (bool more = unit0() < unit1(); more; more = advance()) {
+        const int u0 = unit0(), u1 = unit1();
         const int row0 = it.rt * kPrRows + wg * 128, r = row0 + rl;
         const bool active = row0 < it.rows, on = r < it.rows;
-        const int qi = on ? r / a.group : 0, g = on ? r - qi * a.group : 0;
+        const int qi = on ? a.by_group.div(r) : 0, g = on ? r - qi * a.group : 0;
         const int pos = on ? it.sq.pos0 + qi : -1;
-        const int first_pos = it.sq.pos0 + row0 / a.group;
-        const int last_pos = it.sq.pos0 + (min(it.rows, row0 + 128) - 1) / a.group;
+        const int first_pos = it.sq.pos0 + a.by_group.div(row0);
+        const int last_pos = it.sq.pos0 + a.by_group.div(min(it.rows, row0 + 128) - 1);
         float f_row = 0.0f, m_ref = kNoMax, l = 0.0f;
         uint32_t nan_blocks = 0;
         if (active) {
-          // q: f16, scaled by a power of two to a largest magnitude in [2^14, 2^15)
-          const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                                          (int64_t)(it.sq.q0 + qi) * a.q_tok +
-                                                          (int64_t)(it.head * a.group + g) * a.q_head);
-          uint32_t m = 0;
-          if (on)
+          // q: f16, each row scaled by a power of two to a largest magnitude in
+          // [2^14, 2^15).  A warp takes its 32 rows RPI at a time, 16 bytes a lane.
+          f_row = 0.0f;
 #pragma unroll 4
-            for (int x = 0; x < D / 8; ++x) m = vmax_u16x2(m, absmax_load<FP8Q_BF16>(q[x]));
-          m = unpack_max<FP8Q_BF16>(m);
-          const int e = m == 0 ? 0 : max(-112, (int)(m >> 23) - 127) - 14;
-          const float s = pow2f(-e);
-          f_row = a.scale * 1.4426950408889634f * pow2f(e);
-          if (m >= 0x7F800000u) f_row = __uint_as_float(0x7FFFFFFFu);
-#pragma unroll 4
-          for (int x = 0; x < D / 8; ++x) {
-            const uint4 w = on ? q[x] : make_uint4(0, 0, 0, 0);
+          for (int x = 0; x < 32 / RPI; ++x) {
+            const int rw = x * RPI + lane / CPR, c = lane % CPR, rr = row0 + (warp & 3) * 32 + rw;
+            const bool there = rr < it.rows;
+            const int i = there ? a.by_group.div(rr) : 0;
+            const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)(it.sq.q0 + i) * a.q_tok +
+                                     (int64_t)(it.head * a.group + (there ? rr - i * a.group : 0)) * a.q_head + c * 8;
+            const uint4 w = there ? *reinterpret_cast<const uint4*>(q) : make_uint4(0, 0, 0, 0);
+            uint32_t m = unpack_max<FP8Q_BF16>(absmax_load<FP8Q_BF16>(w));
+#pragma unroll
+            for (int y = 1; y < CPR; y <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, y));
+            const int e = m == 0 ? 0 : max(-112, (int)(m >> 23) - 127) - 14;
+            const float s = pow2f(-e);
+            float f = a.scale * 1.4426950408889634f * pow2f(e);
+            if (m >= 0x7F800000u) f = __uint_as_float(0x7FFFFFFFu);      // NaN or Inf: the row is NaN
+            f = __shfl_sync(0xFFFFFFFFu, f, (lane % RPI) * CPR);
+            if (lane / RPI == x) f_row = f;
             uint4 h;
             h.x = cvt_f16x2(__uint_as_float(w.x << 16) * s, __uint_as_float(w.x & 0xFFFF0000u) * s);
             h.y = cvt_f16x2(__uint_as_float(w.y << 16) * s, __uint_as_float(w.y & 0xFFFF0000u) * s);
             h.z = cvt_f16x2(__uint_as_float(w.z << 16) * s, __uint_as_float(w.z & 0xFFFF0000u) * s);
             h.w = cvt_f16x2(__uint_as_float(w.w << 16) * s, __uint_as_float(w.w & 0xFFFF0000u) * s);
-            *reinterpret_cast<uint4*>(sm.q[wg] + (x >> 3) * Smem::kQHalf + rl * 128 + (((x & 7) ^ (rl & 7)) * 16)) = h;
+            const int row = (warp & 3) * 32 + rw;
+            *reinterpret_cast<uint4*>(sm.q[wg] + (c >> 3) * Smem::kQHalf + row * 128 + (((c & 7) ^ (row & 7)) * 16)) = h;
           }
           fence_proxy_async();
           arrive(&sm.q_full[wg]);
@@ -433,42 +464,62 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
         // ---- the item's end: output, or a part to be joined
         const bool whole = u0 == 0 && u1 == it.n;
         constexpr int PART = kPrRows * (D + 2);
-        float* part = plan.part + (2 * (long long)blockIdx.x + (rel <= 0 ? 0 : 1)) * PART;
+        float* part = plan.part + (2 * (long long)blockIdx.x + (rel + kPrSetup <= 0 ? 0 : 1)) * PART;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t out_row = it.sq.q0 + qi;
         const int out_head = it.head * a.group + g;
         if (active) {
           if (!wait(&sm.o_full[wg][1], mine_t - 1)) return;
           tmem_fence_after();
+          // Through shared memory (the queries' place: the products are done with
+          // them), so that rows leave RPI at a time: 16-byte chunk c of row r at
+          // chunk c ^ (r & 7).  Outputs are bf16, parts fp32 in two halves.
+          uint4* stage = reinterpret_cast<uint4*>(sm.q[wg]) + (warp & 3) * 32 * CPR;
+          const int c = lane % CPR;
+#pragma unroll 1
+          for (int z = 0; z < (whole ? 1 : 2); ++z) {
+#pragma unroll 1
+            for (int x = 0; x < (whole ? D / 32 : D / 64); ++x) {
+              const int col = z * (D / 2) + x * 32;
+              uint32_t o[32];
+              tmem_ld32(o, t_o + col);
+              tmem_wait_ld(o);
+              if ((nan_blocks >> (col >> 5)) & 1)
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            uint32_t o[32];
-            tmem_ld32(o, t_o + x * 32);
-            tmem_wait_ld(o);
-            if ((nan_blocks >> x) & 1)
+                for (int y = 0; y < 32; ++y) o[y] = 0x7FFFFFFFu;
+              if (whole) {
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = 0x7FFFFFFFu;
-            if (!on) continue;
-            if (whole) {
-              uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + out_row * a.out_tok +
-                                                    (int64_t)out_head * a.out_head + x * 32);
+                for (int y = 0; y < 4; ++y) {
+                  uint32_t w[4];
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                uint32_t w[4];
+                  for (int k = 0; k < 4; ++k)
+                    w[k] = l == 0.0f ? 0u : cvt_bf16x2(__uint_as_float(o[y * 8 + k * 2]) * inv,
+                                                       __uint_as_float(o[y * 8 + k * 2 + 1]) * inv);
+                  stage[lane * CPR + ((x * 4 + y) ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              } else {
 #pragma unroll
-                for (int z = 0; z < 4; ++z)
-                  w[z] = l == 0.0f ? 0u : cvt_bf16x2(__uint_as_float(o[y * 8 + z * 2]) * inv,
-                                                     __uint_as_float(o[y * 8 + z * 2 + 1]) * inv);
-                out[y] = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int y = 0; y < 8; ++y)
+                  stage[lane * CPR + ((x * 8 + y) ^ (lane & 7))] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
               }
-            } else {
-              uint4* d = reinterpret_cast<uint4*>(part + (wg * 128 + rl) * D + x * 32);
-#pragma unroll
-              for (int y = 0; y < 8; ++y) d[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
             }
+            __syncwarp();
+#pragma unroll 4
+            for (int x = 0; x < 32 / RPI; ++x) {
+              const int rw = x * RPI + lane / CPR, rr = row0 + (warp & 3) * 32 + rw;
+              if (rr >= it.rows) continue;
+              const uint4 v = stage[rw * CPR + (c ^ (rw & 7))];
+              if (whole) {
+                const int i = a.by_group.div(rr);
+                *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)(it.sq.q0 + i) * a.out_tok +
+                                          (int64_t)(it.head * a.group + rr - i * a.group) * a.out_head + c * 8) = v;
+              } else {
+                *reinterpret_cast<uint4*>(part + (rr - it.rt * kPrRows) * D + z * (D / 2) + c * 4) = v;
+              }
+            }
+            __syncwarp();
           }
-          if (on && whole && a.lse)
-            a.lse[out_row * a.q_heads + out_head] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * 0.6931471805599453f;
+          if (on && whole) store_lse(a, out_row, out_head, m_ref, l);
           if (on && !whole) {
             part[kPrRows * D + wg * 128 + rl] = m_ref;
             part[kPrRows * D + kPrRows + wg * 128 + rl] = l;
@@ -476,10 +527,10 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           tmem_fence_before();
         }
         if (!whole) {
-          const long long per = s_range[1], seg0 = s_range[0] + rel, first = seg0 / per, last = (seg0 + it.n - 1) / per;
+          const long long per = s_range[1], seg0 = s_range[0] + rel + kPrSetup, first = seg0 / per, last = (seg0 + it.n - 1) / per;
           __threadfence();
           arrive(&sm.join_all);
-          if (warp == 0 && !wait(&sm.join_all, joins)) return;
+          if (warp == 0 && !wait(&sm.join_all, all_n)) return;
           if (threadIdx.x == 0) {
             uint32_t* t = plan.ticket + first;       // a CTA starts at most one that others go on with
             const uint32_t got = atomicAdd(t, 1u);
@@ -489,8 +540,8 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
             mbar_arrive(&sm.join_last);
           }
           __syncwarp();
-          if (!wait(&sm.join_last, joins)) return;
-          ++joins;
+          if (!wait(&sm.join_last, joins++)) return;
+          ++all_n;
           if (*reinterpret_cast<volatile uint32_t*>(&sm.last)) {
             __threadfence();
             const int n = (int)(last - first) + 1;
@@ -499,38 +550,40 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
               const long long c = first + i;
               return static_cast<const float*>(plan.part) + (2 * c + (seg0 <= c * per ? 0 : 1)) * PART;
             };
-            for (int w = threadIdx.x; w < here * (D / 4); w += 256) {
-              const int rr = w / (D / 4), c = w % (D / 4);
-              float m = kNoMax;
-              for (int i = 0; i < n; ++i) m = fmaxf(m, part_at(i)[kPrRows * D + rr]);
-              float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              float sum = 0.0f;
-              for (int i = 0; i < n; ++i) {
-                const float* q = part_at(i);
-                const float f = ex2(q[kPrRows * D + rr] - m);
-                const float4 v = *reinterpret_cast<const float4*>(q + rr * D + c * 4);
-                o.x += v.x * f;
-                o.y += v.y * f;
-                o.z += v.z * f;
-                o.w += v.w * f;
-                sum += q[kPrRows * D + kPrRows + rr] * f;
-              }
-              const int row = it.rt * kPrRows + rr, i = row / a.group, h = it.head * a.group + row - i * a.group;
-              const float k = sum == 0.0f ? 0.0f : 1.0f / sum;
-              uint2 v;
-              v.x = sum == 0.0f ? 0u : cvt_bf16x2(o.x * k, o.y * k);
-              v.y = sum == 0.0f ? 0u : cvt_bf16x2(o.z * k, o.w * k);
-              *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)(it.sq.q0 + i) * a.out_tok +
-                                        (int64_t)h * a.out_head + c * 4) = v;
-              if (a.lse && c == 0)
-                a.lse[(int64_t)(it.sq.q0 + i) * a.q_heads + h] =
-                    sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+            // the products are done with this item's queries: their place takes
+            // the rows' references and sums
+            Joined* rows = reinterpret_cast<Joined*>(sm.q[0]);
+            if (static_cast<int>(threadIdx.x) < here) {
+              const int row = it.rt * kPrRows + threadIdx.x, i = a.by_group.div(row);
+              const Joined x = row_of_parts<kPrRows, D>(part_at, 0, 1, n, threadIdx.x);
+              rows[threadIdx.x] = x;
+              store_lse(a, it.sq.q0 + i, it.head * a.group + row - i * a.group, x.m, x.l);
             }
+            arrive(&sm.join_all);
+            if (!wait(&sm.join_all, all_n++)) return;
+            constexpr int U = 8, STEP = 256 / (D / 4);
+            const int c = threadIdx.x % (D / 4);
+            for (int r0 = threadIdx.x / (D / 4); r0 < here; r0 += U * STEP) {
+              int r[U];
+              float m[U];
+              float4 o[U];
+#pragma unroll
+              for (int x = 0; x < U; ++x) {
+                r[x] = min(r0 + x * STEP, here - 1);
+                m[x] = rows[r[x]].m;
+              }
+              columns_of_parts<kPrRows, D, U, 1>(part_at, n, r, c, m, o);
+#pragma unroll
+              for (int x = 0; x < U; ++x) {
+                if (r0 + x * STEP >= here) continue;
+                const int row = it.rt * kPrRows + r[x], i = a.by_group.div(row);
+                store_columns(a, it.sq.q0 + i, it.head * a.group + row - i * a.group, c, o[x], rows[r[x]].l);
+              }
+            }
+            arrive(&sm.join_all);                      // the queries' place is free again
+            if (!wait(&sm.join_all, all_n++)) return;
           }
         }
-        cur = rel + u1;
-        rel += it.n;
-        if (cur < units) next_item();
       }
     }();
   } else if (wg < 4) {
@@ -547,15 +600,16 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
       auto token_of = [&](int j) { return D == 128 ? j * 8 + sub : j * 16 + (lane >> 4) * 8 + sub; };
       const int page_mask = (1 << a.shape.page_shift) - 1;
       const KvPool pool = values ? a.v : a.k;
-      int cur = 0;
+      int u = unit0(), u_end = unit1();              // unit of the item, the last that is this CTA's
+      if (u >= u_end) return;
       typename Smem::Raw& raw = sm.raw[warp - 8];
       auto page_of = [&]() {
-        const int tok = (it.tile0 + cur - rel) * kPrKeys + grp * 32 + lane;
+        const int tok = (it.tile0 + u) * kPrKeys + grp * 32 + lane;
         return tok < it.sq.len ? a.table[it.b * a.table_stride + (tok >> a.shape.page_shift)] : -1;
       };
       // starts the copy of this warp's rows of the unit; gives the mask of those that exist
       auto fetch = [&](int page) {
-        const int tok = (it.tile0 + cur - rel) * kPrKeys + grp * 32 + lane;
+        const int tok = (it.tile0 + u) * kPrKeys + grp * 32 + lane;
         const int64_t slot = ((int64_t)page << a.shape.page_shift) + (tok & page_mask);
         const bool ok = page >= 0 && slot < a.shape.slots;
         const uint32_t there = __ballot_sync(0xFFFFFFFFu, ok);
@@ -567,12 +621,11 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
 
       // The items' units in turn.  A unit's codes go to registers as soon as
       // they have arrived, and the copy of the next one starts at once.
-      auto step = [&]() {                            // it, rel, cur: one unit on; false past the end
-        if (++cur >= units) return false;
-        if (cur == rel + it.n) {
-          rel += it.n;
-          next_item();
-        }
+      auto step = [&]() {                            // one unit on; false past the last
+        if (++u < u_end) return true;
+        if (!advance()) return false;
+        u = 0;
+        u_end = unit1();
         return true;
       };
       uint32_t next = fetch(page_of());
@@ -580,7 +633,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
       int page = more ? page_of() : -1;
       uint64_t* full = values ? sm.v_full : sm.k_full;
       uint64_t* empty = values ? sm.v_empty : sm.k_empty;
-      for (int kt = 0; kt < units; ++kt) {
+      for (int kt = 0;; ++kt) {
         PrInfo& info = sm.info[kt % kPrInfos];
         const int stg = kt % kPrStages;
         cp_wait<0>();
@@ -595,6 +648,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
                               : reinterpret_cast<const uint16_t*>(raw.scales)[lane];
         sc = (valid >> lane) & 1 ? sc : 0u;
         __syncwarp();
+        const bool last = !more;
         if (more) {
           next = fetch(page);
           more = step();
@@ -656,6 +710,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
         }
         fence_proxy_async();
         arrive(&full[stg]);
+        if (last) return;
       }
     }();
   } else {
@@ -701,8 +756,8 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
         };
         // Each half's scores of the next unit are made as soon as the weights
         // that lie over them have been used, while the other half is in work.
-        for (int cur = 0; cur < units;) {
-          const int n = min(it.n, units - rel) - (cur - rel);
+        for (bool go = unit0() < unit1(); go; go = advance()) {
+          const int n = unit1() - unit0();
           const bool active = it.rt * kPrRows + w * 128 < it.rows;
           if (active) {
             if (!wait(&sm.q_full[w], items++)) return;
@@ -735,9 +790,6 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
               __syncwarp();
             }
           }
-          cur += n;
-          rel += it.n;
-          if (cur < units) next_item();
         }
       }();
       // nothing may still be running when the tensor memory goes back
