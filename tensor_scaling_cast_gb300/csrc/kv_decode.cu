@@ -42,7 +42,8 @@ constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecStages = 3;
 constexpr int kTile = 32;                 // tokens of a warp tile
-constexpr int kMinTiles = 16;             // tiles of a CTA, at least
+constexpr int kDecSetup = 5;              // what a (sequence, head) costs beyond its tiles, in tiles: queries in, output out
+constexpr int kMinTiles = 8;              // tiles of a CTA, at least
 
 template <int D>
 struct DecSmem {
@@ -56,7 +57,9 @@ struct DecSmem {
   };
   struct Warp {
     Stage stage[kDecStages];
-    __half factor[kBlocks][kTile];        // value scales of the tile being used
+    // value scales of the tile being used, f16; token u * 16 + h * 8 + 2 c + i of
+    // a block at c * 8 + u * 4 + h * 2 + i: what a lane needs lies together
+    __half factor[kBlocks][kTile];
     uint32_t valid[kDecStages];           // tokens of the stage that exist
     uint32_t pad[4 - kDecStages % 4];
   };
@@ -87,6 +90,14 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// d = a * b.
+__device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%10, %10, %10, %10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 // Two E8M0 bytes (the low half of w) -> 2^(byte - 127), NaN for 0xFF.
 __device__ __forceinline__ float2 e8m0x2_f32(uint32_t w) {
   uint32_t r;
@@ -97,6 +108,7 @@ __device__ __forceinline__ float2 e8m0x2_f32(uint32_t w) {
 // A sequence's tiles: the ones that hold a key some query sees.
 struct DecSeq : KvSeq {
   int tile0, tiles;
+  int cost;              // of one head, in tiles: kDecSetup and the tiles
 };
 __device__ __forceinline__ DecSeq dec_seq(const KvAttn& a, int b) {
   DecSeq s;
@@ -104,6 +116,7 @@ __device__ __forceinline__ DecSeq dec_seq(const KvAttn& a, int b) {
   s.tile0 = (a.window > 0 ? max(0, s.pos0 - a.window + 1) : 0) / kTile;
   // a sequence with queries and no keys still has its zeros to write
   s.tiles = s.nq == 0 ? 0 : max(1, (s.len + kTile - 1) / kTile - s.tile0);
+  s.cost = s.nq == 0 ? 0 : s.tiles + kDecSetup;
   return s;
 }
 
@@ -115,7 +128,7 @@ struct DecPlan {
 template <int D, int NT>
 __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
 kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPlan plan) {
-  constexpr int NB = D / 32, ROWS = 8 * NT;
+  constexpr int NB = D / 32, RB = D / 2, ROWS = 8 * NT;
   using Smem = DecSmem<D>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -126,12 +139,17 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
   __shared__ long long s_before;
   __shared__ uint32_t s_last;
   __shared__ Joined s_rows[8 * NT];
+  // the lane's row of 8 x 8 code matrices (the swizzle repeats every 8 rows),
+  // and the place of its token's value scales
+  const uint32_t lane_at = D == 128 ? code_offset<D>(lane & 7, lane >> 3)
+                                    : code_offset<D>((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1);
+  const int factor_at = ((lane >> 1) & 3) * 8 + (lane >> 4) * 4 + ((lane >> 3) & 1) * 2 + (lane & 1);
 
   // ---- this CTA's range of tiles: a scan of the sequences' tile counts
   const int per_thread = (a.batch + kDecThreads - 1) / kDecThreads;
   const int b_lo = min(a.batch, (int)threadIdx.x * per_thread), b_hi = min(a.batch, b_lo + per_thread);
   long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += (long long)dec_seq(a, b).tiles * a.shape.heads;
+  for (int b = b_lo; b < b_hi; ++b) mine += (long long)dec_seq(a, b).cost * a.shape.heads;
   long long incl = mine;
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
@@ -152,7 +170,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
   if (before <= begin && begin < before + mine) {
     int b = b_lo;
     for (; b < b_hi; ++b) {
-      const long long n = (long long)dec_seq(a, b).tiles * a.shape.heads;
+      const long long n = (long long)dec_seq(a, b).cost * a.shape.heads;
       if (begin < before + n) break;
       before += n;
     }
@@ -161,14 +179,14 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
   }
   __syncthreads();
   int b = s_start[0];
-  long long seg0 = s_before;                    // global tile of (b, head 0)
   DecSeq sq = dec_seq(a, b);
-  int head = (int)((begin - seg0) / sq.tiles);
-  seg0 += (long long)head * sq.tiles;
+  int head = (int)((begin - s_before) / sq.cost);
+  // position of the first tile of (b, head): its cost lies from kDecSetup before
+  long long seg0 = s_before + (long long)head * sq.cost + kDecSetup;
 
-  for (long long at = begin; at < end;) {
+  while (seg0 < end) {
     // ---- one (sequence, head): tiles [t0, t1) of it
-    const int t0 = (int)(at - seg0), t1 = (int)min((long long)sq.tiles, end - seg0);
+    const int t0 = (int)max(0ll, begin - seg0), t1 = (int)min((long long)sq.tiles, end - seg0);
     const int rows = sq.nq * a.group;
     const int n_mine = t1 - t0 > warp ? (t1 - t0 - warp + kDecWarps - 1) / kDecWarps : 0;
 
@@ -195,7 +213,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
       const int e = m == 0 ? 0 : max(-112, (int)(m >> 23) - 127) - 14;   // q = q' * 2^e, e in [-126, 113]
       const float s = pow2f(-e);
-      float f = a.scale * 1.4426950408889634f * pow2f(e);
+      float f = fmaxf(a.scale * 1.4426950408889634f * pow2f(e), kMinFactor);
       if (m >= 0x7F800000u) f = __uint_as_float(0x7FFFFFFFu);            // NaN or Inf: the row is NaN
 #pragma unroll
       for (int x = 0; x < NB; ++x) {
@@ -229,9 +247,8 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       return k < n_mine && tok < sq.len ? table[tok >> a.shape.page_shift] : -1;
     };
     const int page_mask = (1 << a.shape.page_shift) - 1;
-    auto issue = [&](int k, int page) {
+    auto issue = [&](int k, int st, int page) {
       if (k < n_mine) {
-        const int st = k % kDecStages;
         const int tok = tok0 + k * (kDecWarps * kTile);
         const int64_t slot = ((int64_t)page << a.shape.page_shift) + (tok & page_mask);
         const bool ok = page >= 0 && slot < a.shape.slots;
@@ -245,43 +262,43 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
     };
 
 #pragma unroll
-    for (int k = 0; k < kDecStages - 1; ++k) issue(k, page_of(k));
+    for (int k = 0; k < kDecStages - 1; ++k) issue(k, k, page_of(k));
     int page_next = page_of(kDecStages - 1);
 
-    for (int k = 0; k < n_mine; ++k) {
+    for (int k = 0, st = 0; k < n_mine; ++k, st = st == kDecStages - 1 ? 0 : st + 1) {
       cp_wait<kDecStages - 2>();
       __syncwarp();
-      const int st = k % kDecStages;
       const typename Smem::Stage& tile = sm.stage[st];
       const uint32_t valid = sm.valid[st];
       const int tok = (sq.tile0 + t0 + warp + k * kDecWarps) * kTile;
 
       // ---- value scales: one token per lane, relative to the tile's largest
-      float rv;
+      float rv, unscale;
       bool v_nan;
       {
         const uint32_t w = NB == 4 ? reinterpret_cast<const uint32_t*>(tile.ve)[lane]
                                    : reinterpret_cast<const uint16_t*>(tile.ve)[lane];
         const bool ok = (valid >> lane) & 1;
-        uint32_t e[NB], top = 0;
-        bool bad = false;
+        float e[NB], top = 0.0f, all = 0.0f;
 #pragma unroll
-        for (int x = 0; x < NB; ++x) {
-          e[x] = (w >> (8 * x)) & 0xFFu;
-          const bool n = e[x] == 255u;
-          bad |= n;
-          top = max(top, n ? 0u : e[x]);
+        for (int x = 0; x < NB; x += 2) {
+          const float2 f = e8m0x2_f32(x ? w >> 16 : w);
+          e[x] = f.x;
+          e[x + 1] = f.y;
+          top = fmaxf(top, fmaxf(f.x, f.y));     // leaves NaN out
+          all += f.x + f.y;                      // and takes it in
         }
-        top = __reduce_max_sync(0xFFFFFFFFu, ok ? top : 0u);
-        v_nan = __any_sync(0xFFFFFFFFu, ok && bad);
-        top = min(max(top, (uint32_t)kMinScale), (uint32_t)kMaxScale);
-        rv = (float)((int)top - 127);
+        v_nan = __any_sync(0xFFFFFFFFu, ok && all != all);
+        // positive floats order like their bits
+        const uint32_t most = min(max(__reduce_max_sync(0xFFFFFFFFu, ok ? __float_as_uint(top) : 0u), kMinScale << 23),
+                                  kMaxScale << 23) & 0x7F800000u;
+        rv = (float)((int)(most >> 23) - 127);
+        unscale = __uint_as_float((254u << 23) - most);
 #pragma unroll
-        for (int x = 0; x < NB; ++x) {
-          const int d = min(126, (int)(top - e[x]));
-          float f = __uint_as_float((uint32_t)(127 - d) << 23);
-          if (e[x] == 255u) f = __uint_as_float(0x7FFFFFFFu);
-          sm.factor[x][lane] = __float2half_rn(ok ? f : 0.0f);
+        for (int x = 0; x < NB; x += 2) {
+          const uint32_t f = ok ? cvt_f16x2(e[x] * unscale, e[x + 1] * unscale) : 0u;
+          reinterpret_cast<uint16_t*>(sm.factor[x])[factor_at] = (uint16_t)f;
+          reinterpret_cast<uint16_t*>(sm.factor[x + 1])[factor_at] = (uint16_t)(f >> 16);
         }
         __syncwarp();
       }
@@ -300,13 +317,13 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t r[4];
-            ldmatrix4<false>(r, base + code_offset<D>(u * 16 + h * 8 + (lane & 7), lane >> 3));
+            ldmatrix4<false>(r, base + (u * 16 + h * 8) * RB + lane_at);
 #pragma unroll
             for (int x = 0; x < NB; ++x) kw[h][x] = r[x & 3];
           }
         } else {
           uint32_t r[4];
-          ldmatrix4<false>(r, base + code_offset<D>(u * 16 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1));
+          ldmatrix4<false>(r, base + u * 16 * RB + lane_at);
           kw[0][0] = r[0]; kw[0][1] = r[1]; kw[1][0] = r[2]; kw[1][1] = r[3];
         }
         float ks[2][NB];                         // scales of tokens li, li + 8
@@ -329,8 +346,8 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
           e2m1x8_f16(kw[1][x], kb);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma(c, ka[0], kb[0], ka[1], kb[1], qf[nt][x][0], qf[nt][x][1]);
+            float c[4];
+            mma_zero(c, ka[0], kb[0], ka[1], kb[1], qf[nt][x][0], qf[nt][x][1]);
             mma(c, ka[2], kb[2], ka[3], kb[3], qf[nt][x][2], qf[nt][x][3]);
             s[u][nt][0] += c[0] * ks[0][x];
             s[u][nt][1] += c[1] * ks[0][x];
@@ -343,12 +360,6 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       // ---- masks, only where the tile has any
       const bool edge = valid != 0xFFFFFFFFu || tok + kTile - 1 > pos0 ||
                         (a.window > 0 && tok <= pos0 + sq.nq - 1 - a.window);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) s[u][nt][y] *= fx[nt][y & 1];
       if (edge) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -372,7 +383,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          top[nt][y] = fmaxf(fmaxf(s[0][nt][y], s[0][nt][y + 2]), fmaxf(s[1][nt][y], s[1][nt][y + 2])) + rv;
+          top[nt][y] = fmaxf(fmaxf(s[0][nt][y], s[0][nt][y + 2]), fmaxf(s[1][nt][y], s[1][nt][y + 2])) * fx[nt][y] + rv;
           move |= top[nt][y] > mref[nt][y] + kSlack;
         }
       if (__any_sync(0xFFFFFFFFu, move)) {
@@ -398,19 +409,22 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       }
 
       // ---- weights, their sum, and the second product
-      const float unscale = pow2f(-(int)rv);
       uint32_t p[2][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float a0 = ex2(s[u][nt][0] + (rv - mref[nt][0])), a1 = ex2(s[u][nt][1] + (rv - mref[nt][1]));
-          const float a2 = ex2(s[u][nt][2] + (rv - mref[nt][0])), a3 = ex2(s[u][nt][3] + (rv - mref[nt][1]));
+          const float c0 = rv - mref[nt][0], c1 = rv - mref[nt][1];
+          const float a0 = ex2(fmaf(s[u][nt][0], fx[nt][0], c0)), a1 = ex2(fmaf(s[u][nt][1], fx[nt][1], c1));
+          const float a2 = ex2(fmaf(s[u][nt][2], fx[nt][0], c0)), a3 = ex2(fmaf(s[u][nt][3], fx[nt][1], c1));
           l[nt][0] += (a0 + a2) * unscale;
           l[nt][1] += (a1 + a3) * unscale;
           p[u][nt][0] = movmatrix(cvt_f16x2(a0, a1));
           p[u][nt][1] = movmatrix(cvt_f16x2(a2, a3));
         }
+      uint4 fac[NB];
+#pragma unroll
+      for (int x = 0; x < NB; ++x) fac[x] = *reinterpret_cast<const uint4*>(&sm.factor[x][lc * 8]);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t vw[2][NB];                      // [token half][block]: codes 4 li .. 4 li + 3 of tokens 2 lc, 2 lc + 1
@@ -419,13 +433,13 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t r[4];
-            ldmatrix4<true>(r, base + code_offset<D>(u * 16 + h * 8 + (lane & 7), lane >> 3));
+            ldmatrix4<true>(r, base + (u * 16 + h * 8) * RB + lane_at);
 #pragma unroll
             for (int x = 0; x < NB; ++x) vw[h][x] = r[x & 3];
           }
         } else {
           uint32_t r[4];
-          ldmatrix4<true>(r, base + code_offset<D>(u * 16 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1));
+          ldmatrix4<true>(r, base + u * 16 * RB + lane_at);
           vw[0][0] = r[0]; vw[0][1] = r[1]; vw[1][0] = r[2]; vw[1][1] = r[3];
         }
 #pragma unroll
@@ -436,8 +450,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
           uint32_t c02[4], c13[4];               // columns 0, 2 then 1, 3; token halves 0, 1
           e2m1x8_f16((even & m) | ((odd << 4) & ~m), c02);
           e2m1x8_f16(((even >> 4) & m) | (odd & ~m), c13);
-          const uint32_t f0 = *reinterpret_cast<const uint32_t*>(&sm.factor[x][u * 16 + lc * 2]);
-          const uint32_t f1 = *reinterpret_cast<const uint32_t*>(&sm.factor[x][u * 16 + 8 + lc * 2]);
+          const uint32_t f0 = u ? fac[x].z : fac[x].x, f1 = u ? fac[x].w : fac[x].y;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             uint32_t b0 = mul_f16x2(p[u][nt][0], f0), b1 = mul_f16x2(p[u][nt][1], f1);
@@ -456,7 +469,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
         }
       }
       __syncwarp();
-      issue(k + kDecStages - 1, page_next);
+      issue(k + kDecStages - 1, st == 0 ? kDecStages - 1 : st - 1, page_next);
       page_next = page_of(k + kDecStages);
     }
 
@@ -563,11 +576,10 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
     __syncthreads();
 
     // ---- the next (sequence, head)
-    at = seg0 + t1;
-    seg0 += sq.tiles;
+    seg0 += sq.cost;
     if (++head == a.shape.heads) {
       head = 0;
-      if (at < end) {
+      if (seg0 < end) {                          // then there is one
         do sq = dec_seq(a, ++b);
         while (sq.tiles == 0);
       }
@@ -599,14 +611,14 @@ static DecLaunch dec_pick(int nt) {
   }
 }
 
-// CTAs of a call: as many as are resident at once, or one per kMinTiles tiles
-// of the longest the sequences can be, if that is fewer.
+// CTAs of a call: as many as are resident at once, or one per kMinTiles of the
+// cost that the longest sequences would have, if that is fewer.
 static cudaError_t dec_grid(const DecLaunch& k, const KvShape& s, int batch, int table_width, int sms, int* grid) {
   int occ = 1;
   const cudaError_t e = kernel_occupancy(k.kernel, kDecThreads, k.smem, &occ);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (((int64_t)table_width << s.page_shift) + kTile - 1) / kTile;
-  const int64_t most = (tiles * batch * s.heads + kMinTiles - 1) / kMinTiles;
+  const int64_t most = ((tiles + kDecSetup) * batch * s.heads + kMinTiles - 1) / kMinTiles;
   int64_t n = most < (int64_t)sms * occ ? most : (int64_t)sms * occ;
   *grid = (int)(n < kMaxGrid ? n : kMaxGrid);
   return cudaSuccess;

@@ -203,8 +203,10 @@ __device__ __forceinline__ void copy_rows(uint32_t codes, uint32_t scales, const
 // times 2^-R, are finite and 2^-R is a normal number.
 constexpr float kNoMax = -3.0e38f;        // M before the first score
 constexpr float kSlack = 8.0f;
-constexpr int kMinScale = 127 - 80;
-constexpr int kMaxScale = 127 + 126;
+constexpr uint32_t kMinScale = 127 - 80;
+constexpr uint32_t kMaxScale = 127 + 126;
+// Score factors stay above zero: a hidden key's -inf times one stays -inf.
+constexpr float kMinFactor = 1.17549435e-38f;
 
 // A workspace: tickets (zero between calls), then the parts of rows whose
 // keys several CTAs share.

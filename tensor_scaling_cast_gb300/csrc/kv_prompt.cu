@@ -395,7 +395,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
 #pragma unroll
                   for (int y = 1; y < 15; y += 2) t = max3(t, __uint_as_float(v[y]), __uint_as_float(v[y + 1]));
                   t = fmaxf(t, __uint_as_float(v[15]));
-                  top = fmaxf(top, t * (f_row * info.rk[c >> 5]) + info.rv[c >> 5]);
+                  top = fmaxf(top, t * fmaxf(f_row * info.rk[c >> 5], kMinFactor) + info.rv[c >> 5]);
                 }
                 const float fix = ex2(m_ref - top);
                 m_ref = top;
@@ -425,7 +425,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
                 tmem_wait_ld(v);
                 if (x + 1 < kPrHalf / 16) tmem_ld16(s[(x + 1) & 1], t_s + (x + 1) * 16);
                 if (edge) mask(h * kPrHalf + x * 16, v);
-                const float f = f_row * (x < 2 ? rk.x : rk.y), c = (x < 2 ? rv.x : rv.y) - m_ref;
+                const float f1 = f_row * (x < 2 ? rk.x : rk.y), f = f1 < kMinFactor ? kMinFactor : f1, c = (x < 2 ? rv.x : rv.y) - m_ref;
                 const uint64_t f2 = pack2(f, f), c2 = pack2(c, c);
                 uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
@@ -666,7 +666,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           top = max(top, e == 255u ? 0u : e);
         }
         top = __reduce_max_sync(0xFFFFFFFFu, top);   // tokens that do not exist have scale bytes 0
-        top = min(max(top, (uint32_t)kMinScale), (uint32_t)kMaxScale);
+        top = min(max(top, kMinScale), kMaxScale);
         if (values) {
           const uint32_t any = __ballot_sync(0xFFFFFFFFu, bad);
           if (any) {
@@ -818,7 +818,7 @@ static int pr_grid(const KvShape& s, int group, int batch, int64_t total_q, int 
   const int64_t by_max = (int64_t)batch * (((int64_t)max_q * group + kPrRows - 1) / kPrRows);
   const int64_t by_total = total_q * group / kPrRows + batch;
   const int64_t units = (((int64_t)table_width << s.page_shift) + kPrKeys - 1) / kPrKeys;
-  const int64_t all = (by_max < by_total ? by_max : by_total) * s.heads * units;
+  const int64_t all = (by_max < by_total ? by_max : by_total) * s.heads * (units + kPrSetup);
   const int64_t most = (all + kPrMinUnits - 1) / kPrMinUnits;
   const int64_t n = most < sms ? most : sms;
   return (int)(n < kMaxGrid ? n : kMaxGrid);
