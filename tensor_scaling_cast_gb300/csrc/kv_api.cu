@@ -43,7 +43,7 @@ static int check_copy(const mx_kv_cache* c, const void* k, const void* v, int dt
   int st = check_cache(c, s);
   if (st != FP8Q_OK) return st;
   if (dtype != FP8Q_F32 && dtype != FP8Q_BF16) return FP8Q_EDTYPE;
-  if (tokens < 0 || tokens > (int64_t(1) << 40)) return FP8Q_EINVAL;
+  if (tokens < 0 || tokens > 0x7FFFFFFF) return FP8Q_EINVAL;
   if (tokens == 0) return FP8Q_OK;
   if (!slots) return FP8Q_EINVAL;
   st = check_rows(k, dtype, tokens, c->kv_heads, k_tok, k_head);

@@ -5,13 +5,17 @@
 // work is eight elements of a row: 16 bytes of bf16, 4 of E2M1, so that a
 // warp's accesses cover whole 128-byte lines of the plain tensor and 64-byte
 // runs of a cached row; four neighbouring lanes hold one block and share its
-// maximum by two shuffles.  Each thread has kKvUnroll units in flight.
+// maximum by two shuffles.  A thread keeps its place in the rows (head and
+// columns) and goes over tokens, several of them in flight: per unit only the
+// slot's address is left to find.  (With a division per unit the 16384-token
+// write was bound by its instructions, 23 us a launch.)
 #include "kv_device.cuh"
 
 namespace fp8q {
 
 constexpr int kKvThreads = 256;
-constexpr int kKvUnroll = 4;
+constexpr int kKvWriteAhead = 4;          // tokens a thread has in flight
+constexpr int kKvReadAhead = 8;
 
 struct KvCopy {
   KvShape s;
@@ -21,152 +25,150 @@ struct KvCopy {
   const int64_t* slots;
   int64_t tokens;
   FastDiv row_units, dim_units;   // units per token (heads * dim / 8) and per row (dim / 8)
-  int32_t tokens_per_cta, rule;
+  int32_t abreast, rule;          // tokens side by side in a CTA
 };
 
-// Where unit i of the CTA's tokens lives.
-struct KvUnit {
-  int64_t slot, x, q;   // cache slot (< 0: none), element offsets into the plain tensor and the cache
+// A thread's place: its units lie at x + token * tok in the plain tensor and
+// at q + page * page_elems + (token of the page) * dim in the cache.
+struct KvPlace {
+  int64_t token, x, q;
+  bool on;
 };
-
-__device__ __forceinline__ KvUnit kv_unit(const KvCopy& p, int which, int64_t token0, uint32_t i) {
-  KvUnit u;
+__device__ __forceinline__ KvPlace kv_place(const KvCopy& p, int which, int ahead) {
+  KvPlace u;
+  const uint32_t i = blockIdx.z * kKvThreads + threadIdx.x;
   const uint32_t t = p.row_units.div(i), r = i - t * p.row_units.d;
   const uint32_t h = p.dim_units.div(r), c = r - h * p.dim_units.d;
-  const int64_t token = token0 + t;
-  u.slot = __ldg(p.slots + token);
-  if (u.slot >= p.s.slots) u.slot = -1;
-  u.x = token * p.tok[which] + h * p.head[which] + c * 8;
-  u.q = u.slot < 0 ? 0 : kv_row(p.s, u.slot, (int)h) * p.s.dim + c * 8;
+  u.on = t < (uint32_t)p.abreast;
+  u.token = (int64_t)blockIdx.x * (p.abreast * ahead) + t;
+  u.x = h * p.head[which] + c * 8;
+  u.q = ((int64_t)h << p.s.page_shift) * p.s.dim + c * 8;
   return u;
+}
+// Slot of the j-th token of a thread; below 0: none.
+__device__ __forceinline__ int64_t kv_slot(const KvCopy& p, const KvPlace& u, int j) {
+  const int64_t t = u.token + j * p.abreast;
+  if (!u.on || t >= p.tokens) return -1;
+  const int64_t s = __ldg(p.slots + t);
+  return s < p.s.slots ? s : -1;
+}
+__device__ __forceinline__ int64_t kv_at(const KvCopy& p, const KvPlace& u, int64_t slot) {
+  const int64_t page = slot >> p.s.page_shift, off = slot & ((1ll << p.s.page_shift) - 1);
+  return u.q + ((page * p.s.heads << p.s.page_shift) + off) * p.s.dim;
 }
 
 template <int FMT, int DT>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_constant__ KvCopy p) {
-  constexpr int W = DT == FP8Q_BF16 ? 1 : 2;        // 16-byte loads per unit
+  constexpr int W = DT == FP8Q_BF16 ? 1 : 2, U = kKvWriteAhead;        // W: 16-byte loads per unit
   const int which = blockIdx.y;
-  const int64_t token0 = (int64_t)blockIdx.x * p.tokens_per_cta;
-  const uint32_t n = (uint32_t)min((int64_t)p.tokens_per_cta, p.tokens - token0) * p.row_units.d;
+  const KvPlace u = kv_place(p, which, U);
   const KvPool pool = p.pool[which];
-  for (uint32_t base = 0; base < n; base += kKvThreads * kKvUnroll) {
-    KvUnit u[kKvUnroll];
-    uint4 v[kKvUnroll][W];
+  int64_t slot[U];
+  uint4 v[U][W];
 #pragma unroll
-    for (int j = 0; j < kKvUnroll; ++j) {
-      const uint32_t i = base + j * kKvThreads + threadIdx.x;
-      u[j].slot = -1;
+  for (int j = 0; j < U; ++j) {
+    slot[j] = kv_slot(p, u, j);
 #pragma unroll
-      for (int w = 0; w < W; ++w) v[j][w] = make_uint4(0, 0, 0, 0);
-      if (i < n) {
-        u[j] = kv_unit(p, which, token0, i);
-        const uint4* src = reinterpret_cast<const uint4*>(p.x[which] + u[j].x * (DT == FP8Q_BF16 ? 2 : 4));
+    for (int w = 0; w < W; ++w) v[j][w] = make_uint4(0, 0, 0, 0);
+    if (slot[j] < 0) continue;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        p.x[which] + (u.x + (u.token + j * p.abreast) * p.tok[which]) * (DT == FP8Q_BF16 ? 2 : 4));
 #pragma unroll
-        for (int w = 0; w < W; ++w) v[j][w] = __ldcs(src + w);
-      }
+    for (int w = 0; w < W; ++w) v[j][w] = __ldcs(src + w);
+  }
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    // rows are whole blocks: the four lanes of one have the same token or none
+    uint32_t m = absmax_load<DT>(v[j][0]);
+    if (W == 2) m = absmax_merge<DT>(m, absmax_load<DT>(v[j][W - 1]));
+    m = unpack_max<DT>(m);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    if (slot[j] < 0) continue;
+    const int64_t at = kv_at(p, u, slot[j]);
+    const bool finite = m < 0x7F800000u;
+    constexpr int F8 = FMT == FP8Q_E2M1 ? FP8Q_E4M3 : FMT;
+    const int E = !finite ? 0 : FMT == FP8Q_E2M1 ? block_exp_e2m1(m, p.rule) : block_exp<F8>(m, p.rule, 0);
+    const float s = pow2f(-E);
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      f[k] = __uint_as_float(elem_bits<DT>(v[j][W == 1 ? 0 : k >> 2], W == 1 ? k : k & 3)) * s;
+    uint2 o;
+    if (FMT == FP8Q_E2M1) {
+      o.x = cvt_e2m1x8(f);
+    } else {
+      o.x = cvt_pair<F8>(f[0], f[1]) | (cvt_pair<F8>(f[2], f[3]) << 16);
+      o.y = cvt_pair<F8>(f[4], f[5]) | (cvt_pair<F8>(f[6], f[7]) << 16);
     }
-#pragma unroll
-    for (int j = 0; j < kKvUnroll; ++j) {
-      // n and the strides between units are multiples of 4: a block's four
-      // lanes are all in range or none is
-      uint32_t m = absmax_load<DT>(v[j][0]);
-      if (W == 2) m = absmax_merge<DT>(m, absmax_load<DT>(v[j][W - 1]));
-      m = unpack_max<DT>(m);
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      if (u[j].slot < 0) continue;
-      const bool finite = m < 0x7F800000u;
-      const int E = !finite ? 0 : FMT == FP8Q_E2M1 ? block_exp_e2m1(m, p.rule) : block_exp<FMT == FP8Q_E2M1 ? FP8Q_E4M3 : FMT>(m, p.rule, 0);
-      const float s = pow2f(-E);
-      float f[8];
+    if (!finite) {                         // sign|largest for every element
       uint32_t sign = 0;
 #pragma unroll
+      for (int k = 0; k < 8; ++k)
+        sign |= (elem_bits<DT>(v[j][W == 1 ? 0 : k >> 2], W == 1 ? k : k & 3) >> 31) << k;
+      o.x = FMT == FP8Q_E2M1 ? 0x77777777u : 0x7F7F7F7Fu;
+      o.y = 0x7F7F7F7Fu;
+#pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const uint32_t b = elem_bits<DT>(v[j][W == 1 ? 0 : k >> 2], W == 1 ? k : k & 3);
-        f[k] = __uint_as_float(b) * s;
-        sign |= (b >> 31) << k;
+        const uint32_t b = (sign >> k) & 1u;
+        if (FMT == FP8Q_E2M1) o.x |= b << (4 * k + 3);
+        else if (k < 4) o.x |= b << (8 * k + 7);
+        else o.y |= b << (8 * (k - 4) + 7);
       }
-      if (FMT == FP8Q_E2M1) {
-        uint32_t o = cvt_e2m1x8(f);
-        if (!finite) {
-          o = 0x77777777u;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) o |= ((sign >> k) & 1u) << (4 * k + 3);
-        }
-        *reinterpret_cast<uint32_t*>(pool.q + (u[j].q >> 1)) = o;
-      } else {
-        constexpr int F8 = FMT == FP8Q_E2M1 ? FP8Q_E4M3 : FMT;
-        uint2 o;
-        o.x = cvt_pair<F8>(f[0], f[1]) | (cvt_pair<F8>(f[2], f[3]) << 16);
-        o.y = cvt_pair<F8>(f[4], f[5]) | (cvt_pair<F8>(f[6], f[7]) << 16);
-        if (!finite) {
-          o.x = o.y = 0x7F7F7F7Fu;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            o.x |= ((sign >> k) & 1u) << (8 * k + 7);
-            o.y |= ((sign >> (k + 4)) & 1u) << (8 * k + 7);
-          }
-        }
-        *reinterpret_cast<uint2*>(pool.q + u[j].q) = o;
-      }
-      if ((threadIdx.x & 3) == 0) pool.e8m0[u[j].q >> 5] = (uint8_t)(finite ? E + 127 : 255);
     }
+    if (FMT == FP8Q_E2M1) *reinterpret_cast<uint32_t*>(pool.q + (at >> 1)) = o.x;
+    else *reinterpret_cast<uint2*>(pool.q + at) = o;
+    if ((threadIdx.x & 3) == 0) pool.e8m0[at >> 5] = (uint8_t)(finite ? E + 127 : 255);
   }
 }
 
 template <int FMT, int DT>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_constant__ KvCopy p) {
+  constexpr int U = kKvReadAhead;
   const int which = blockIdx.y;
-  const int64_t token0 = (int64_t)blockIdx.x * p.tokens_per_cta;
-  const uint32_t n = (uint32_t)min((int64_t)p.tokens_per_cta, p.tokens - token0) * p.row_units.d;
+  const KvPlace u = kv_place(p, which, U);
   const KvPool pool = p.pool[which];
-  for (uint32_t base = 0; base < n; base += kKvThreads * kKvUnroll) {
-    KvUnit u[kKvUnroll];
-    uint2 v[kKvUnroll];
-    uint32_t e[kKvUnroll];
+  uint2 v[U];
+  uint32_t e[U];
 #pragma unroll
-    for (int j = 0; j < kKvUnroll; ++j) {
-      const uint32_t i = base + j * kKvThreads + threadIdx.x;
-      u[j].slot = -1;
-      v[j] = make_uint2(0, 0);
-      e[j] = 127;
-      if (i < n) {
-        u[j] = kv_unit(p, which, token0, i);
-        if (u[j].slot >= 0) {
-          if (FMT == FP8Q_E2M1) v[j].x = __ldcs(reinterpret_cast<const uint32_t*>(pool.q + (u[j].q >> 1)));
-          else v[j] = __ldcs(reinterpret_cast<const uint2*>(pool.q + u[j].q));
-          e[j] = pool.e8m0[u[j].q >> 5];
-        }
-      }
+  for (int j = 0; j < U; ++j) {
+    const int64_t slot = kv_slot(p, u, j);
+    v[j] = make_uint2(0, 0);
+    e[j] = 127;
+    if (slot < 0) continue;
+    const int64_t at = kv_at(p, u, slot);
+    if (FMT == FP8Q_E2M1) v[j].x = __ldcs(reinterpret_cast<const uint32_t*>(pool.q + (at >> 1)));
+    else v[j] = __ldcs(reinterpret_cast<const uint2*>(pool.q + at));
+    e[j] = pool.e8m0[at >> 5];
+  }
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int64_t t = u.token + j * p.abreast;
+    if (!u.on || t >= p.tokens) continue;
+    uint32_t h[4];
+    if (FMT == FP8Q_E2M1) {
+      e2m1x8_f16(v[j].x, h);
+    } else {
+      constexpr int F8 = FMT == FP8Q_E2M1 ? FP8Q_E4M3 : FMT;
+      fp8x4_f16<F8>(v[j].x, h[0], h[1]);
+      fp8x4_f16<F8>(v[j].y, h[2], h[3]);
     }
+    const float s = e8m0_value(e[j]);
+    float f[8];
 #pragma unroll
-    for (int j = 0; j < kKvUnroll; ++j) {
-      const uint32_t i = base + j * kKvThreads + threadIdx.x;
-      if (i >= n) continue;
-      uint32_t h[4];
-      if (FMT == FP8Q_E2M1) {
-        e2m1x8_f16(v[j].x, h);
-      } else {
-        constexpr int F8 = FMT == FP8Q_E2M1 ? FP8Q_E4M3 : FMT;
-        fp8x4_f16<F8>(v[j].x, h[0], h[1]);
-        fp8x4_f16<F8>(v[j].y, h[2], h[3]);
-      }
-      const float s = e8m0_value(e[j]);
-      float f[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 a = f16x2_f32(h[k]);
-        f[2 * k] = a.x * s;
-        f[2 * k + 1] = a.y * s;
-      }
-      uint4* dst = reinterpret_cast<uint4*>(p.x[which] + u[j].x * (DT == FP8Q_BF16 ? 2 : 4));
-      if (DT == FP8Q_BF16) {
-        __stcs(dst, make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
-                               cvt_bf16x2(f[6], f[7])));
-      } else {
-        const uint32_t* b = reinterpret_cast<const uint32_t*>(f);
-        __stcs(dst, make_uint4(b[0], b[1], b[2], b[3]));
-        __stcs(dst + 1, make_uint4(b[4], b[5], b[6], b[7]));
-      }
+    for (int k = 0; k < 4; ++k) {
+      const float2 a = f16x2_f32(h[k]);
+      f[2 * k] = a.x * s;
+      f[2 * k + 1] = a.y * s;
+    }
+    uint4* dst = reinterpret_cast<uint4*>(p.x[which] + (u.x + t * p.tok[which]) * (DT == FP8Q_BF16 ? 2 : 4));
+    if (DT == FP8Q_BF16) {
+      __stcs(dst, make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
+                             cvt_bf16x2(f[6], f[7])));
+    } else {
+      const uint32_t* b = reinterpret_cast<const uint32_t*>(f);
+      __stcs(dst, make_uint4(b[0], b[1], b[2], b[3]));
+      __stcs(dst + 1, make_uint4(b[4], b[5], b[6], b[7]));
     }
   }
 }
@@ -197,12 +199,10 @@ static cudaError_t launch_any(bool write, const KvShape& s, int format, KvPool k
   const uint32_t row = (uint32_t)s.heads * (s.dim / 8);
   p.row_units = FastDiv(row);
   p.dim_units = FastDiv((uint32_t)s.dim / 8);
-  // one pass of a CTA over its units, or more where the grid would pass 2^31
-  int64_t per = (kKvThreads * kKvUnroll + row - 1) / row;
-  per = per < 1 ? 1 : per;
-  while ((tokens + per - 1) / per > 0x7FFFFFFF) per *= 2;
-  p.tokens_per_cta = (int32_t)per;
-  const dim3 grid((unsigned)((tokens + per - 1) / per), 2);
+  // a CTA has several tokens abreast, or one token's row takes several CTAs (grid z)
+  p.abreast = row >= kKvThreads ? 1 : kKvThreads / row;
+  const int64_t per = (int64_t)p.abreast * (write ? kKvWriteAhead : kKvReadAhead);
+  const dim3 grid((unsigned)((tokens + per - 1) / per), 2, (row + kKvThreads - 1) / kKvThreads);
   cudaError_t e;
   const bool b = dtype == FP8Q_BF16;
   if (format == FP8Q_E2M1)

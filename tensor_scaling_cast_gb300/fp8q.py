@@ -362,6 +362,7 @@ class MXKVCache:
         self._struct = _KVCacheStruct(k_q.data_ptr(), k_e8m0.data_ptr(), v_q.data_ptr(), v_e8m0.data_ptr(),
                                       pages, page, heads, dim, fmt)
         self._ref = ctypes.addressof(self._struct)
+        self._tail, self._scale = torch.Size((heads, dim)), dim ** -0.5
 
     @classmethod
     def allocate(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int = E2M1,
@@ -372,35 +373,38 @@ class MXKVCache:
         return cls(*(torch.zeros(s, dtype=torch.uint8, device=device) for s in (q, e, q, e)), fmt=fmt)
 
 
-def _kv_rows(x: torch.Tensor, cache: MXKVCache, heads: int, what: str):
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != cache.head_dim or (x.stride(2) != 1 and x.numel()):
-        raise TypeError(f"{what}: rows [tokens, {heads}, {cache.head_dim}] with consecutive elements expected, "
-                        f"got {tuple(x.shape)} with strides {x.stride()}")
-
-
-def _kv_pair(k, v, slots, cache, what):
-    _kv_rows(k, cache, cache.kv_heads, what)
-    _kv_rows(v, cache, cache.kv_heads, what)
-    if slots.dtype != torch.int64 or not slots.is_contiguous() or slots.numel() != k.shape[0] or \
-            v.shape[0] != k.shape[0] or v.dtype != k.dtype:
-        raise TypeError(f"{what}: slots are contiguous int64, one per token, and k and v alike")
+# Few-token calls are bound by the host: the checks read each shape and stride
+# once, and the entry points' results are what is left to check.
+def _kv_pair(cache, k, v, slots, what):
+    """(tokens, dtype code, strides of k and v) of a write's or read's rows."""
+    shape, ks, vs, dtype = k.shape, k.stride(), v.stride(), k.dtype
+    if (shape != v.shape or shape[1:] != cache._tail or ks[2] != 1 or vs[2] != 1 or v.dtype is not dtype
+            or slots.dtype is not torch.int64 or slots.shape != shape[:1] or not slots.is_contiguous()):
+        raise TypeError(f"{what}: k and v alike, [tokens, {cache.kv_heads}, {cache.head_dim}] with consecutive "
+                        f"elements, and contiguous int64 slots [tokens]: got {tuple(shape)}, {tuple(v.shape)} "
+                        f"with strides {ks}, {vs}, slots {slots.dtype} {tuple(slots.shape)}")
+    return shape[0], BF16 if dtype is torch.bfloat16 else _dtype(k), ks, vs
 
 
 def mx_kv_write(cache: MXKVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, rule: int = MX_FLOOR,
                 stream=None):
     """Quantise k and v [tokens, kv_heads, head_dim] (bf16 or fp32, any token and
     head stride) into the cache slots `slots` (int64; negative: not written)."""
-    _kv_pair(k, v, slots, cache, "mx_kv_write")
-    _check(load().mx_kv_write(cache._ref, _ptr(k), _ptr(v), _dtype(k), k.shape[0], k.stride(0), k.stride(1),
-                              v.stride(0), v.stride(1), _ptr(slots), rule, _stream(stream)), "mx_kv_write")
+    n, dtype, ks, vs = _kv_pair(cache, k, v, slots, "mx_kv_write")
+    st = (_lib or load()).mx_kv_write(cache._ref, k.data_ptr(), v.data_ptr(), dtype, n, ks[0], ks[1], vs[0], vs[1],
+                                      slots.data_ptr(), rule, _stream(stream))
+    if st:
+        _check(st, "mx_kv_write")
 
 
 def mx_kv_read(cache: MXKVCache, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None):
     """Read the slots back into k and v [tokens, kv_heads, head_dim] (bf16 or
     fp32); a negative slot gives zeros."""
-    _kv_pair(k, v, slots, cache, "mx_kv_read")
-    _check(load().mx_kv_read(cache._ref, _ptr(slots), k.shape[0], _ptr(k), _ptr(v), _dtype(k), k.stride(0),
-                             k.stride(1), v.stride(0), v.stride(1), _stream(stream)), "mx_kv_read")
+    n, dtype, ks, vs = _kv_pair(cache, k, v, slots, "mx_kv_read")
+    st = (_lib or load()).mx_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), dtype, ks[0],
+                                     ks[1], vs[0], vs[1], _stream(stream))
+    if st:
+        _check(st, "mx_kv_read")
 
 
 def mx_kv_attention_workspace(cache: MXKVCache, q: torch.Tensor, page_table: torch.Tensor, max_q: int = 1):
@@ -422,25 +426,28 @@ def mx_kv_attention(cache: MXKVCache, q: torch.Tensor, out: torch.Tensor, page_t
     [batch], cu_q int32 [batch + 1] (None: one query per sequence), max_q >= the
     queries of any sequence, scale (None: head_dim ** -0.5), lse float32
     [total_q, q_heads] or None, workspace of mx_kv_attention_workspace."""
-    heads = q.shape[1] if q.dim() == 3 else 0
-    _kv_rows(q, cache, heads, "mx_kv_attention q")
-    _kv_rows(out, cache, heads, "mx_kv_attention out")
-    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or out.shape != q.shape:
-        raise TypeError("mx_kv_attention: q and out are bf16 of one shape")
-    batch = page_table.shape[0]
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or (page_table.stride(1) != 1 and page_table.shape[1] > 1) or \
-            kv_lens.dtype != torch.int32 or kv_lens.numel() != batch or not kv_lens.is_contiguous() or \
-            (cu_q is not None and (cu_q.dtype != torch.int32 or cu_q.numel() != batch + 1 or
-                                   not cu_q.is_contiguous())) or \
-            (lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or
-                                  not lse.is_contiguous())):
+    shape, qs, os_ = q.shape, q.stride(), out.stride()
+    table, ts = page_table.shape, page_table.stride()
+    if (len(shape) != 3 or shape[2] != cache.head_dim or out.shape != shape or qs[2] != 1 or os_[2] != 1
+            or q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16):
+        raise TypeError(f"mx_kv_attention: q and out are bf16 [total_q, q_heads, {cache.head_dim}] with consecutive "
+                        f"elements: got {q.dtype} {tuple(shape)}, {out.dtype} {tuple(out.shape)}, strides {qs}, {os_}")
+    if (page_table.dtype is not torch.int32 or len(table) != 2 or (ts[1] != 1 and table[1] > 1)
+            or kv_lens.dtype is not torch.int32 or kv_lens.shape != table[:1] or not kv_lens.is_contiguous()
+            or (cu_q is not None and (cu_q.dtype is not torch.int32 or cu_q.numel() != table[0] + 1
+                                      or not cu_q.is_contiguous()))
+            or (lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2]
+                                     or not lse.is_contiguous()))):
         raise TypeError("mx_kv_attention: page_table int32 [batch, pages], kv_lens int32 [batch], "
                         "cu_q int32 [batch + 1], lse float32 [total_q, q_heads]")
-    _check(load().mx_kv_attention(
-        cache._ref, _ptr(q), BF16, q.shape[0], heads, q.stride(0), q.stride(1), _ptr(out), out.stride(0),
-        out.stride(1), _ptr(lse), _ptr(cu_q), _ptr(kv_lens), _ptr(page_table), page_table.stride(0),
-        page_table.shape[1], batch, max_q, cache.head_dim ** -0.5 if scale is None else scale, window,
-        _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)), "mx_kv_attention")
+    st = (_lib or load()).mx_kv_attention(
+        cache._ref, q.data_ptr(), BF16, shape[0], shape[1], qs[0], qs[1], out.data_ptr(), os_[0], os_[1],
+        None if lse is None else lse.data_ptr(), None if cu_q is None else cu_q.data_ptr(), kv_lens.data_ptr(),
+        page_table.data_ptr(), ts[0], table[1], table[0], max_q, cache._scale if scale is None else scale, window,
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+        _stream(stream))
+    if st:
+        _check(st, "mx_kv_attention")
 
 
 # ---- convenience wrapper ---------------------------------------------------
