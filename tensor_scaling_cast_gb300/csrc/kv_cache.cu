@@ -15,7 +15,7 @@ namespace fp8q {
 
 constexpr int kKvThreads = 256;
 constexpr int kKvWriteAhead = 4;          // tokens a thread has in flight
-constexpr int kKvReadAhead = 8;
+constexpr int kKvReadAhead = 4;
 
 struct KvCopy {
   KvShape s;

@@ -42,7 +42,7 @@ constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecStages = 3;
 constexpr int kTile = 32;                 // tokens of a warp tile
-constexpr int kDecSetup = 5;              // what a (sequence, head) costs beyond its tiles, in tiles: queries in, output out
+constexpr int kDecSetup = 8;              // what a (sequence, head) costs beyond its tiles, in tiles: queries in, output out
 constexpr int kMinTiles = 8;              // tiles of a CTA, at least
 
 template <int D>
@@ -190,10 +190,46 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
     const int rows = sq.nq * a.group;
     const int n_mine = t1 - t0 > warp ? (t1 - t0 - warp + kDecWarps - 1) / kDecWarps : 0;
 
-    // ---- queries: f16, each row scaled by a power of two to a largest
-    // magnitude in [2^14, 2^15), which keeps bf16 exact down to 2^-29 of it
-    uint32_t qf[NT][NB][4];
-    float fx[NT][2];                             // score factor of query rows 2 lc, 2 lc + 1
+    const int pos0 = sq.pos0;
+    const int32_t* table = a.table + b * a.table_stride;
+    // The warp's k-th tile begins at token tile0_at + k * (kDecWarps * kTile).
+    // Pages of 32 tokens or more hold all of a tile's rows in one run; smaller
+    // ones are looked up by each lane for its own token.
+    const int tile0_at = (sq.tile0 + t0 + warp) * kTile;
+    const bool runs = a.shape.page_shift >= 5;
+    auto page_of = [&](int k) {
+      const int tok = tile0_at + k * (kDecWarps * kTile) + (runs ? 0 : lane);
+      return k < n_mine && tok < sq.len ? table[tok >> a.shape.page_shift] : -1;
+    };
+    const int page_mask = (1 << a.shape.page_shift) - 1;
+    auto issue = [&](int k, int st, int page) {
+      if (k < n_mine) {
+        const int at = tile0_at + k * (kDecWarps * kTile), tok = at + (runs ? 0 : lane);
+        const int64_t slot = ((int64_t)page << a.shape.page_shift) + (tok & page_mask);
+        const bool ok = page >= 0 && slot < a.shape.slots;
+        const int64_t row = ok ? kv_row(a.shape, slot, head) : 0;
+        const uint32_t kd = smem_u32(sm.stage[st].k), vd = smem_u32(sm.stage[st].v);
+        const uint32_t ke = smem_u32(sm.stage[st].ke), ve = smem_u32(sm.stage[st].ve);
+        uint32_t valid;
+        if (runs) {
+          valid = ok ? low_bits(sq.len - at) : 0u;
+          copy_run<D>(kd, ke, a.k, row, valid);
+          copy_run<D>(vd, ve, a.v, row, valid);
+        } else {
+          valid = __ballot_sync(0xFFFFFFFFu, ok);
+          copy_rows<D>(kd, ke, a.k, row, valid, a.shape.page_shift);
+          copy_rows<D>(vd, ve, a.v, row, valid, a.shape.page_shift);
+        }
+        sm.valid[st] = valid;                    // the same from every lane
+      }
+      cp_commit();
+    };
+
+    // pages, queries and the first tiles are fetched side by side
+    int pages[kDecStages];
+#pragma unroll
+    for (int k = 0; k < kDecStages; ++k) pages[k] = page_of(k);
+    uint4 qw[NT][NB];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + li;
@@ -201,13 +237,22 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       const int qi = on ? a.by_group.div(r) : 0, g = on ? r - qi * a.group : 0;
       const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)(sq.q0 + qi) * a.q_tok +
                                (int64_t)(head * a.group + g) * a.q_head + lc * 8;
-      uint4 w[NB];
+#pragma unroll
+      for (int x = 0; x < NB; ++x) qw[nt][x] = on ? *reinterpret_cast<const uint4*>(q + x * 32) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kDecStages - 1; ++k) issue(k, k, pages[k]);
+    int page_next = pages[kDecStages - 1];
+
+    // ---- queries: f16, each row scaled by a power of two to a largest
+    // magnitude in [2^14, 2^15), which keeps bf16 exact down to 2^-29 of it
+    uint32_t qf[NT][NB][4];
+    float fx[NT][2];                             // score factor of query rows 2 lc, 2 lc + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       uint32_t m = 0;
 #pragma unroll
-      for (int x = 0; x < NB; ++x) {
-        w[x] = on ? *reinterpret_cast<const uint4*>(q + x * 32) : make_uint4(0, 0, 0, 0);
-        m = vmax_u16x2(m, absmax_load<FP8Q_BF16>(w[x]));
-      }
+      for (int x = 0; x < NB; ++x) m = vmax_u16x2(m, absmax_load<FP8Q_BF16>(qw[nt][x]));
       m = unpack_max<FP8Q_BF16>(m);
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
@@ -217,7 +262,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       if (m >= 0x7F800000u) f = __uint_as_float(0x7FFFFFFFu);            // NaN or Inf: the row is NaN
 #pragma unroll
       for (int x = 0; x < NB; ++x) {
-        const uint32_t ws[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+        const uint32_t ws[4] = {qw[nt][x].x, qw[nt][x].y, qw[nt][x].z, qw[nt][x].w};
 #pragma unroll
         for (int y = 0; y < 4; ++y)
           qf[nt][x][y] = cvt_f16x2(__uint_as_float(ws[y] << 16) * s, __uint_as_float(ws[y] & 0xFFFF0000u) * s);
@@ -228,6 +273,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
 
     float o[NT][NB][2][4];
     float mref[NT][2], l[NT][2];
+    uint32_t nan_blocks = 0;                     // bit x * 8 + nt * 2 + y: block x of query row 8 nt + 2 lc + y is NaN
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -237,33 +283,6 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
 #pragma unroll
         for (int y = 0; y < 8; ++y) o[nt][x][y >> 2][y & 3] = 0.0f;
     }
-
-    const int pos0 = sq.pos0;
-    const int32_t* table = a.table + b * a.table_stride;
-    // token of this lane in the warp's k-th tile, and the page that holds it
-    const int tok0 = (sq.tile0 + t0 + warp) * kTile + lane;
-    auto page_of = [&](int k) {
-      const int tok = tok0 + k * (kDecWarps * kTile);
-      return k < n_mine && tok < sq.len ? table[tok >> a.shape.page_shift] : -1;
-    };
-    const int page_mask = (1 << a.shape.page_shift) - 1;
-    auto issue = [&](int k, int st, int page) {
-      if (k < n_mine) {
-        const int tok = tok0 + k * (kDecWarps * kTile);
-        const int64_t slot = ((int64_t)page << a.shape.page_shift) + (tok & page_mask);
-        const bool ok = page >= 0 && slot < a.shape.slots;
-        const int64_t row = ok ? kv_row(a.shape, slot, head) : 0;
-        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok);
-        if (lane == 0) sm.valid[st] = valid;
-        copy_rows<D>(smem_u32(sm.stage[st].k), smem_u32(sm.stage[st].ke), a.k, row, valid, a.shape.page_shift);
-        copy_rows<D>(smem_u32(sm.stage[st].v), smem_u32(sm.stage[st].ve), a.v, row, valid, a.shape.page_shift);
-      }
-      cp_commit();
-    };
-
-#pragma unroll
-    for (int k = 0; k < kDecStages - 1; ++k) issue(k, k, page_of(k));
-    int page_next = page_of(kDecStages - 1);
 
     for (int k = 0, st = 0; k < n_mine; ++k, st = st == kDecStages - 1 ? 0 : st + 1) {
       cp_wait<kDecStages - 2>();
@@ -275,6 +294,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       // ---- value scales: one token per lane, relative to the tile's largest
       float rv, unscale;
       bool v_nan;
+      uint32_t nan_tokens[NB];
       {
         const uint32_t w = NB == 4 ? reinterpret_cast<const uint32_t*>(tile.ve)[lane]
                                    : reinterpret_cast<const uint16_t*>(tile.ve)[lane];
@@ -289,6 +309,13 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
           all += f.x + f.y;                      // and takes it in
         }
         v_nan = __any_sync(0xFFFFFFFFu, ok && all != all);
+        if (v_nan) {                             // NaN blocks count as zeros here; which rows see them is noted below
+#pragma unroll
+          for (int x = 0; x < NB; ++x) {
+            nan_tokens[x] = __ballot_sync(0xFFFFFFFFu, ok && e[x] != e[x]);
+            if (e[x] != e[x]) e[x] = 0.0f;
+          }
+        }
         // positive floats order like their bits
         const uint32_t most = min(max(__reduce_max_sync(0xFFFFFFFFu, ok ? __float_as_uint(top) : 0u), kMinScale << 23),
                                   kMaxScale << 23) & 0x7F800000u;
@@ -376,6 +403,19 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
           }
       }
 
+      if (v_nan) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int pos = pos0 + a.by_group.div(nt * 8 + lc * 2 + y);
+            uint32_t seen = valid & low_bits(pos - tok + 1);
+            if (a.window > 0) seen &= ~low_bits(pos - a.window + 1 - tok);
+#pragma unroll
+            for (int x = 0; x < NB; ++x) nan_blocks |= (nan_tokens[x] & seen) ? 1u << (x * 8 + nt * 2 + y) : 0u;
+          }
+      }
+
       // ---- the reference moves when some score passes it by 2^kSlack
       bool move = false;
       float top[NT][2];
@@ -453,16 +493,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
           const uint32_t f0 = u ? fac[x].z : fac[x].x, f1 = u ? fac[x].w : fac[x].y;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            uint32_t b0 = mul_f16x2(p[u][nt][0], f0), b1 = mul_f16x2(p[u][nt][1], f1);
-            if (edge && v_nan) {                 // a hidden token's NaN scale must not reach its zero weight
-              const int pos = pos0 + a.by_group.div(nt * 8 + li);
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const int j = tok + u * 16 + (z >> 1) * 8 + lc * 2 + (z & 1);
-                if (j > pos || (a.window > 0 && j <= pos - a.window))
-                  (z >> 1 ? b1 : b0) &= (z & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-              }
-            }
+            const uint32_t b0 = mul_f16x2(p[u][nt][0], f0), b1 = mul_f16x2(p[u][nt][1], f1);
             mma(o[nt][x][0], c02[0], c13[0], c02[2], c13[2], b0, b1);
             mma(o[nt][x][1], c02[1], c13[1], c02[3], c13[3], b0, b1);
           }
@@ -480,6 +511,16 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       for (int y = 0; y < 2; ++y)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[nt][y] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][y], x);
+    if (nan_blocks) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            if ((nan_blocks >> (x * 8 + nt * 2 + (y & 1))) & 1)
+              o[nt][x][0][y] = o[nt][x][1][y] = __uint_as_float(0x7FFFFFFFu);
+    }
     cp_wait<0>();
     __syncthreads();                             // the rings are free
     float* so = reinterpret_cast<float*>(smem_raw) + warp * ROWS * (D + 2);   // [rows][D], then M, then l

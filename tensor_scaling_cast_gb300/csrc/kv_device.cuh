@@ -158,37 +158,42 @@ __device__ __forceinline__ uint32_t code_offset(int r, int c) {
   return D == 128 ? r * 64 + ((c ^ (r >> 1)) & 3) * 16 : r * 32 + ((c ^ (r >> 2)) & 1) * 16;
 }
 
+// Low n bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // This warp's copy of the codes and scales of 32 cached rows into shared
-// memory, asynchronously: row is the cache row of the lane's token, bit t of
-// valid says whether token t exists (else zeros are written).  Pages of 32
-// tokens or more hold the 32 rows in one run, as tiles start at multiples of
-// 32, so that one address serves them all.
+// memory, asynchronously; bit t of valid says whether token t exists (else
+// zeros are written).  One run of rows from `row` on (pages of 32 tokens or
+// more: tiles start at multiples of 32):
+template <int D>
+__device__ __forceinline__ void copy_run(uint32_t codes, uint32_t scales, const KvPool& pool, int64_t row, uint32_t valid) {
+  constexpr int RB = D / 2, NB = D / 32, CH = RB / 16;
+  const int lane = threadIdx.x & 31;
+  const uint8_t* src = pool.q + row * RB + lane * 16;       // chunk `lane` and every 32nd from there
+#pragma unroll
+  for (int x = 0; x < CH; ++x) {
+    const int r = x * (32 / CH) + lane / CH;
+    cp_async16(codes + code_offset<D>(r, lane % CH), src + x * 512, (valid >> r) & 1);
+  }
+  if (D == 128) cp_async4(scales + lane * 4, pool.e8m0 + row * NB + lane * 4, (valid >> lane) & 1);
+  else if (lane < 16) cp_async4(scales + lane * 4, pool.e8m0 + row * NB + lane * 4, (valid >> (2 * lane)) & 1);
+}
+// Or any rows, `row` being that of the lane's token (smaller pages).
 template <int D>
 __device__ __forceinline__ void copy_rows(uint32_t codes, uint32_t scales, const KvPool& pool, int64_t row,
                                           uint32_t valid, int page_shift) {
   constexpr int RB = D / 2, CH = RB / 16;
   const int lane = threadIdx.x & 31;
-  const bool pair_scales = page_shift > 0;
-  if (page_shift >= 5) {
-    // chunk `lane` of the run and every 32nd from there: rows x * (32 / CH) on
-    const uint8_t* src = pool.q + __shfl_sync(0xFFFFFFFFu, row, 0) * RB + lane * 16;
 #pragma unroll
-    for (int x = 0; x < CH; ++x) {
-      const int r = x * (32 / CH) + lane / CH;
-      cp_async16(codes + code_offset<D>(r, lane % CH), src + x * 512, (valid >> r) & 1);
-    }
-  } else {
-#pragma unroll
-    for (int x = 0; x < CH; ++x) {
-      const int r = x * (32 / CH) + lane / CH, c = lane % CH;
-      const int64_t rr = __shfl_sync(0xFFFFFFFFu, row, r);
-      cp_async16(codes + code_offset<D>(r, c), pool.q + rr * RB + c * 16, (valid >> r) & 1);
-    }
+  for (int x = 0; x < CH; ++x) {
+    const int r = x * (32 / CH) + lane / CH, c = lane % CH;
+    const int64_t rr = __shfl_sync(0xFFFFFFFFu, row, r);
+    cp_async16(codes + code_offset<D>(r, c), pool.q + rr * RB + c * 16, (valid >> r) & 1);
   }
   const bool ok = (valid >> lane) & 1;
   if (D == 128) {
     cp_async4(scales + lane * 4, pool.e8m0 + row * 4, ok);
-  } else if (pair_scales) {              // two tokens' scales are one word, the even one's row even
+  } else if (page_shift > 0) {           // two tokens' scales are one word, the even one's row even
     if (!(lane & 1)) cp_async4(scales + lane * 2, pool.e8m0 + row * 2, ok);
   } else {
     const uint16_t e = ok ? *reinterpret_cast<const uint16_t*>(pool.e8m0 + row * 2) : 0;

@@ -137,9 +137,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Low n bits.
-__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
-
 template <int D>
 __global__ void __launch_bounds__(kPrThreads, 1)
 kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPlan plan) {
@@ -603,18 +600,27 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
       int u = unit0(), u_end = unit1();              // unit of the item, the last that is this CTA's
       if (u >= u_end) return;
       typename Smem::Raw& raw = sm.raw[warp - 8];
+      // pages of 32 tokens or more hold a group's rows in one run; smaller ones
+      // are looked up by each lane for its own token
+      const bool runs = a.shape.page_shift >= 5;
       auto page_of = [&]() {
-        const int tok = (it.tile0 + u) * kPrKeys + grp * 32 + lane;
+        const int tok = (it.tile0 + u) * kPrKeys + grp * 32 + (runs ? 0 : lane);
         return tok < it.sq.len ? a.table[it.b * a.table_stride + (tok >> a.shape.page_shift)] : -1;
       };
       // starts the copy of this warp's rows of the unit; gives the mask of those that exist
       auto fetch = [&](int page) {
-        const int tok = (it.tile0 + u) * kPrKeys + grp * 32 + lane;
+        const int at = (it.tile0 + u) * kPrKeys + grp * 32, tok = at + (runs ? 0 : lane);
         const int64_t slot = ((int64_t)page << a.shape.page_shift) + (tok & page_mask);
         const bool ok = page >= 0 && slot < a.shape.slots;
-        const uint32_t there = __ballot_sync(0xFFFFFFFFu, ok);
-        copy_rows<D>(smem_addr(raw.codes), smem_addr(raw.scales), pool, ok ? kv_row(a.shape, slot, it.head) : 0, there,
-                     a.shape.page_shift);
+        const int64_t row = ok ? kv_row(a.shape, slot, it.head) : 0;
+        uint32_t there;
+        if (runs) {
+          there = ok ? low_bits(it.sq.len - at) : 0u;
+          copy_run<D>(smem_addr(raw.codes), smem_addr(raw.scales), pool, row, there);
+        } else {
+          there = __ballot_sync(0xFFFFFFFFu, ok);
+          copy_rows<D>(smem_addr(raw.codes), smem_addr(raw.scales), pool, row, there, a.shape.page_shift);
+        }
         cp_commit();
         return there;
       };
