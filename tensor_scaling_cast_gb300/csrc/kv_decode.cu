@@ -213,12 +213,12 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
         uint32_t valid;
         if (runs) {
           valid = ok ? low_bits(sq.len - at) : 0u;
-          copy_run<D>(kd, ke, a.k, row, valid);
-          copy_run<D>(vd, ve, a.v, row, valid);
+          copy_run<D, false>(kd, ke, a.k, row, valid);
+          copy_run<D, true>(vd, ve, a.v, row, valid);
         } else {
           valid = __ballot_sync(0xFFFFFFFFu, ok);
-          copy_rows<D>(kd, ke, a.k, row, valid, a.shape.page_shift);
-          copy_rows<D>(vd, ve, a.v, row, valid, a.shape.page_shift);
+          copy_rows<D, false>(kd, ke, a.k, row, valid, a.shape.page_shift);
+          copy_rows<D, true>(vd, ve, a.v, row, valid, a.shape.page_shift);
         }
         sm.valid[st] = valid;                    // the same from every lane
       }
@@ -467,7 +467,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       for (int x = 0; x < NB; ++x) fac[x] = *reinterpret_cast<const uint4*>(&sm.factor[x][lc * 8]);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        uint32_t vw[2][NB];                      // [token half][block]: codes 4 li .. 4 li + 3 of tokens 2 lc, 2 lc + 1
+        uint32_t vw[2][NB];                      // [matrix][block]: codes 4 li .. 4 li + 3 of two tokens
         const uint32_t base = smem_u32(tile.v);
         if (D == 128) {
 #pragma unroll
@@ -484,12 +484,13 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
         }
 #pragma unroll
         for (int x = 0; x < NB; ++x) {
-          // bytes that pair a token's code with its neighbour's
-          const uint32_t even = __byte_perm(vw[0][x], vw[1][x], 0x5410), odd = __byte_perm(vw[0][x], vw[1][x], 0x7632);
+          // Bytes that pair a token's code with its neighbour's: the rows lie
+          // swapped, so that the first matrix holds tokens 2 lc and 2 lc + 8,
+          // the second the ones after them.
           const uint32_t m = 0x0F0F0F0Fu;
-          uint32_t c02[4], c13[4];               // columns 0, 2 then 1, 3; token halves 0, 1
-          e2m1x8_f16((even & m) | ((odd << 4) & ~m), c02);
-          e2m1x8_f16(((even >> 4) & m) | (odd & ~m), c13);
+          uint32_t c02[4], c13[4];               // columns 0, 2 then 1, 3; tokens 2 lc, + 1, then 2 lc + 8, + 9
+          e2m1x8_f16((vw[0][x] & m) | ((vw[1][x] << 4) & ~m), c02);
+          e2m1x8_f16(((vw[0][x] >> 4) & m) | (vw[1][x] & ~m), c13);
           const uint32_t f0 = u ? fac[x].z : fac[x].x, f1 = u ? fac[x].w : fac[x].y;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {

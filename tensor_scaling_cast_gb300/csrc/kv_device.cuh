@@ -147,6 +147,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool o
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -163,23 +169,36 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFF
 
 // This warp's copy of the codes and scales of 32 cached rows into shared
 // memory, asynchronously; bit t of valid says whether token t exists (else
-// zeros are written).  One run of rows from `row` on (pages of 32 tokens or
-// more: tiles start at multiples of 32):
-template <int D>
+// zeros are written).  SWAP: token t's codes go to row t with bits 0 and 3
+// exchanged (see the decode kernel's values).  One run of rows from `row` on
+// (pages of 32 tokens or more: tiles start at multiples of 32):
+template <bool SWAP>
+__device__ __forceinline__ int tile_row(int t) {
+  return SWAP ? (t & ~9) | ((t >> 3) & 1) | ((t & 1) << 3) : t;
+}
+template <int D, bool SWAP>
 __device__ __forceinline__ void copy_run(uint32_t codes, uint32_t scales, const KvPool& pool, int64_t row, uint32_t valid) {
   constexpr int RB = D / 2, NB = D / 32, CH = RB / 16;
   const int lane = threadIdx.x & 31;
   const uint8_t* src = pool.q + row * RB + lane * 16;       // chunk `lane` and every 32nd from there
+  const uint8_t* es = pool.e8m0 + row * NB + lane * 4;
+  if (valid == 0xFFFFFFFFu) {
+#pragma unroll
+    for (int x = 0; x < CH; ++x)
+      cp_async16(codes + code_offset<D>(tile_row<SWAP>(x * (32 / CH) + lane / CH), lane % CH), src + x * 512);
+    if (D == 128 || lane < 16) cp_async4(scales + lane * 4, es);
+    return;
+  }
 #pragma unroll
   for (int x = 0; x < CH; ++x) {
     const int r = x * (32 / CH) + lane / CH;
-    cp_async16(codes + code_offset<D>(r, lane % CH), src + x * 512, (valid >> r) & 1);
+    cp_async16(codes + code_offset<D>(tile_row<SWAP>(r), lane % CH), src + x * 512, (valid >> r) & 1);
   }
-  if (D == 128) cp_async4(scales + lane * 4, pool.e8m0 + row * NB + lane * 4, (valid >> lane) & 1);
-  else if (lane < 16) cp_async4(scales + lane * 4, pool.e8m0 + row * NB + lane * 4, (valid >> (2 * lane)) & 1);
+  if (D == 128) cp_async4(scales + lane * 4, es, (valid >> lane) & 1);
+  else if (lane < 16) cp_async4(scales + lane * 4, es, (valid >> (2 * lane)) & 1);
 }
 // Or any rows, `row` being that of the lane's token (smaller pages).
-template <int D>
+template <int D, bool SWAP>
 __device__ __forceinline__ void copy_rows(uint32_t codes, uint32_t scales, const KvPool& pool, int64_t row,
                                           uint32_t valid, int page_shift) {
   constexpr int RB = D / 2, CH = RB / 16;
@@ -188,7 +207,7 @@ __device__ __forceinline__ void copy_rows(uint32_t codes, uint32_t scales, const
   for (int x = 0; x < CH; ++x) {
     const int r = x * (32 / CH) + lane / CH, c = lane % CH;
     const int64_t rr = __shfl_sync(0xFFFFFFFFu, row, r);
-    cp_async16(codes + code_offset<D>(r, c), pool.q + rr * RB + c * 16, (valid >> r) & 1);
+    cp_async16(codes + code_offset<D>(tile_row<SWAP>(r), c), pool.q + rr * RB + c * 16, (valid >> r) & 1);
   }
   const bool ok = (valid >> lane) & 1;
   if (D == 128) {

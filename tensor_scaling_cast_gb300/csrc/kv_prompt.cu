@@ -616,10 +616,10 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
         uint32_t there;
         if (runs) {
           there = ok ? low_bits(it.sq.len - at) : 0u;
-          copy_run<D>(smem_addr(raw.codes), smem_addr(raw.scales), pool, row, there);
+          copy_run<D, false>(smem_addr(raw.codes), smem_addr(raw.scales), pool, row, there);
         } else {
           there = __ballot_sync(0xFFFFFFFFu, ok);
-          copy_rows<D>(smem_addr(raw.codes), smem_addr(raw.scales), pool, row, there, a.shape.page_shift);
+          copy_rows<D, false>(smem_addr(raw.codes), smem_addr(raw.scales), pool, row, there, a.shape.page_shift);
         }
         cp_commit();
         return there;
