@@ -60,6 +60,7 @@ __device__ __forceinline__ int64_t kv_at(const KvCopy& p, const KvPlace& u, int6
 template <int FMT, int DT>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_constant__ KvCopy p) {
   constexpr int W = DT == FP8Q_BF16 ? 1 : 2, U = kKvWriteAhead;        // W: 16-byte loads per unit
+  grid_begin();
   const int which = blockIdx.y;
   const KvPlace u = kv_place(p, which, U);
   const KvPool pool = p.pool[which];
@@ -125,6 +126,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_const
 template <int FMT, int DT>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_constant__ KvCopy p) {
   constexpr int U = kKvReadAhead;
+  grid_begin();
   const int which = blockIdx.y;
   const KvPlace u = kv_place(p, which, U);
   const KvPool pool = p.pool[which];
@@ -174,10 +176,9 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_consta
 }
 
 template <int FMT, int DT>
-static cudaError_t launch_copy(bool write, const KvCopy& p, dim3 grid, cudaStream_t st) {
-  if (write) kv_write_kernel<FMT, DT><<<grid, kKvThreads, 0, st>>>(p);
-  else kv_read_kernel<FMT, DT><<<grid, kKvThreads, 0, st>>>(p);
-  return cudaGetLastError();
+static const void* copy_kernel(bool write) {
+  return write ? reinterpret_cast<const void*>(kv_write_kernel<FMT, DT>)
+               : reinterpret_cast<const void*>(kv_read_kernel<FMT, DT>);
 }
 
 static cudaError_t launch_any(bool write, const KvShape& s, int format, KvPool k, KvPool v, void* kx, void* vx,
@@ -203,16 +204,13 @@ static cudaError_t launch_any(bool write, const KvShape& s, int format, KvPool k
   p.abreast = row >= kKvThreads ? 1 : kKvThreads / row;
   const int64_t per = (int64_t)p.abreast * (write ? kKvWriteAhead : kKvReadAhead);
   const dim3 grid((unsigned)((tokens + per - 1) / per), 2, (row + kKvThreads - 1) / kKvThreads);
-  cudaError_t e;
   const bool b = dtype == FP8Q_BF16;
-  if (format == FP8Q_E2M1)
-    e = b ? launch_copy<FP8Q_E2M1, FP8Q_BF16>(write, p, grid, st) : launch_copy<FP8Q_E2M1, FP8Q_F32>(write, p, grid, st);
-  else if (format == FP8Q_E4M3)
-    e = b ? launch_copy<FP8Q_E4M3, FP8Q_BF16>(write, p, grid, st) : launch_copy<FP8Q_E4M3, FP8Q_F32>(write, p, grid, st);
-  else
-    e = b ? launch_copy<FP8Q_E5M2, FP8Q_BF16>(write, p, grid, st) : launch_copy<FP8Q_E5M2, FP8Q_F32>(write, p, grid, st);
-  *launches += 1;
-  return e;
+  const void* kernel;
+  if (format == FP8Q_E2M1) kernel = b ? copy_kernel<FP8Q_E2M1, FP8Q_BF16>(write) : copy_kernel<FP8Q_E2M1, FP8Q_F32>(write);
+  else if (format == FP8Q_E4M3) kernel = b ? copy_kernel<FP8Q_E4M3, FP8Q_BF16>(write) : copy_kernel<FP8Q_E4M3, FP8Q_F32>(write);
+  else kernel = b ? copy_kernel<FP8Q_E5M2, FP8Q_BF16>(write) : copy_kernel<FP8Q_E5M2, FP8Q_F32>(write);
+  void* args[1] = {&p};
+  return launch_dependent(kernel, grid, kKvThreads, 0, args, st, launches);
 }
 
 cudaError_t launch_kv_write(const KvShape& s, int format, KvPool k, KvPool v, const void* kx, const void* vx,

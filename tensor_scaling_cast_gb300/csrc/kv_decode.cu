@@ -145,6 +145,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
                                     : code_offset<D>((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1);
   const int factor_at = ((lane >> 1) & 3) * 8 + (lane >> 4) * 4 + ((lane >> 3) & 1) * 2 + (lane & 1);
 
+  grid_begin();
   // ---- this CTA's range of tiles: a scan of the sequences' tile counts
   const int per_thread = (a.batch + kDecThreads - 1) / kDecThreads;
   const int b_lo = min(a.batch, (int)threadIdx.x * per_thread), b_hi = min(a.batch, b_lo + per_thread);
@@ -688,9 +689,7 @@ cudaError_t launch_kv_decode(const KvAttn& a, void* workspace, int sms, cudaStre
   plan.ticket = static_cast<uint32_t*>(workspace);
   plan.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMaxGrid * 4);
   void* args[2] = {const_cast<KvAttn*>(&a), &plan};
-  e = cudaLaunchKernel(k.kernel, dim3(grid), dim3(kDecThreads), args, (size_t)k.smem, st);
-  if (e == cudaSuccess) *launches += 1;
-  return e;
+  return launch_dependent(k.kernel, dim3(grid), kDecThreads, k.smem, args, st, launches);
 }
 
 }  // namespace fp8q

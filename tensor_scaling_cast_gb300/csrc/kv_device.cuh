@@ -30,6 +30,31 @@ struct FastDiv {
   __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
 };
 
+// Programmatic dependent launch: every CTA waits until the grid before it in
+// the stream has completed, before any access to memory, and then lets the
+// next one be set up, so that back-to-back calls (a step's write, then its
+// attention) do not pay for launches one after the other.
+__device__ __forceinline__ void grid_begin() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+inline cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, int smem, void** args, cudaStream_t st,
+                                    int* launches) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
 // One kind (keys or values) of the cache as the kernels see it.
 struct KvPool {
   uint8_t* q;

@@ -147,6 +147,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
 
+  grid_begin();
   // ---- this CTA's range of units
   __shared__ long long s_scan[kPrThreads / 32];
   __shared__ long long s_first[2];                   // begin's (sequence, its first unit)
@@ -849,9 +850,7 @@ cudaError_t launch_kv_prompt(const KvAttn& a, void* workspace, int sms, cudaStre
   plan.ticket = static_cast<uint32_t*>(workspace);
   plan.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMaxGrid * 4);
   void* args[2] = {const_cast<KvAttn*>(&a), &plan};
-  e = cudaLaunchKernel(k, dim3(grid), dim3(kPrThreads), args, (size_t)smem, st);
-  if (e == cudaSuccess) *launches += 1;
-  return e;
+  return launch_dependent(k, dim3(grid), kPrThreads, smem, args, st, launches);
 }
 
 cudaError_t read_kv_wait_timeouts(unsigned int* count) {
