@@ -134,14 +134,7 @@ FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int
   st = check_rows(q, dtype, total_q, q_heads, q_token_stride, q_head_stride);
   if (st == FP8Q_OK) st = check_rows(out, dtype, total_q, q_heads, out_token_stride, out_head_stride);
   if (st != FP8Q_OK) return st;
-  const int sms = sm_count(device_of_current());
   if (max_q > total_q) max_q = (int)total_q;
-  int64_t need = 0;
-  const cudaError_t we = kv_attention_workspace(a.shape, q_heads, batch, total_q, max_q, table_width, sms, &need);
-  if (we != cudaSuccess) return record_cuda_error(we);
-  if (need > workspace_bytes) return FP8Q_ESIZE;
-  if (need > 0 && !workspace) return FP8Q_EINVAL;
-  if (need > 0 && !kv_aligned16(workspace)) return FP8Q_EALIGN;
   a.k = {c->k_q, c->k_e8m0};
   a.v = {c->v_q, c->v_e8m0};
   a.q = q;
@@ -165,7 +158,9 @@ FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int
   a.window = window > 0x3FFFFFFF ? 0 : window;   // no sequence is that long
   a.scale = scale;
   int launches = 0;
-  const cudaError_t e = launch_kv_attention(a, workspace, sms, reinterpret_cast<cudaStream_t>(stream), &launches);
+  const cudaError_t e = launch_kv_attention(a, {workspace, workspace_bytes}, sm_count(device_of_current()),
+                                            reinterpret_cast<cudaStream_t>(stream), &st, &launches);
+  if (st != FP8Q_OK) return st;
   return finish(e, launches);
 }
 

@@ -10,9 +10,9 @@ cudaError_t kv_attention_workspace(const KvShape& s, int q_heads, int batch, int
   return kv_prompt_workspace(s, group, batch, total_q, max_q, table_width, sms, bytes);
 }
 
-cudaError_t launch_kv_attention(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches) {
-  if (kv_decode_takes(a.max_q, a.group)) return launch_kv_decode(a, workspace, sms, st, launches);
-  return launch_kv_prompt(a, workspace, sms, st, launches);
+cudaError_t launch_kv_attention(const KvAttn& a, const KvWork& w, int sms, cudaStream_t st, int* status, int* launches) {
+  if (kv_decode_takes(a.max_q, a.group)) return launch_kv_decode(a, w, sms, st, status, launches);
+  return launch_kv_prompt(a, w, sms, st, status, launches);
 }
 
 }  // namespace fp8q

@@ -669,25 +669,29 @@ static cudaError_t dec_grid(const DecLaunch& k, const KvShape& s, int batch, int
 
 bool kv_decode_takes(int max_q, int group) { return (int64_t)max_q * group <= 32; }
 
+static int64_t dec_bytes(int grid, int nt, int dim) {
+  return grid < 2 ? 0 : kMaxGrid * 4 + (int64_t)grid * 2 * 8 * nt * (dim + 2) * 4;
+}
+
 cudaError_t kv_decode_workspace(const KvShape& s, int group, int batch, int max_q, int table_width, int sms,
                                 int64_t* bytes) {
   const int nt = dec_nt(max_q * group);
   const DecLaunch k = s.dim == 128 ? dec_pick<128>(nt) : dec_pick<64>(nt);
   int grid = 0;
   const cudaError_t e = dec_grid(k, s, batch, table_width, sms, &grid);
-  *bytes = grid < 2 ? 0 : kMaxGrid * 4 + (int64_t)grid * 2 * 8 * nt * (s.dim + 2) * 4;
+  *bytes = dec_bytes(grid, nt, s.dim);
   return e;
 }
 
-cudaError_t launch_kv_decode(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches) {
+cudaError_t launch_kv_decode(const KvAttn& a, const KvWork& w, int sms, cudaStream_t st, int* status, int* launches) {
   const int nt = dec_nt(a.max_q * a.group);
   const DecLaunch k = a.shape.dim == 128 ? dec_pick<128>(nt) : dec_pick<64>(nt);
   int grid = 0;
   cudaError_t e = dec_grid(k, a.shape, a.batch, a.table_width, sms, &grid);
   if (e != cudaSuccess) return e;
-  DecPlan plan;
-  plan.ticket = static_cast<uint32_t*>(workspace);
-  plan.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMaxGrid * 4);
+  *status = w.check(dec_bytes(grid, nt, a.shape.dim));
+  if (*status != FP8Q_OK) return cudaSuccess;
+  DecPlan plan = {w.tickets(), w.parts()};
   void* args[2] = {const_cast<KvAttn*>(&a), &plan};
   return launch_dependent(k.kernel, dim3(grid), kDecThreads, k.smem, args, st, launches);
 }

@@ -260,6 +260,18 @@ constexpr float kMinFactor = 1.17549435e-38f;
 // A workspace: tickets (zero between calls), then the parts of rows whose
 // keys several CTAs share.
 constexpr int kMaxGrid = 4096;            // tickets, and CTAs of a call at most
+struct KvWork {
+  void* at;
+  int64_t bytes;
+  // FP8Q_OK, or why it cannot serve a call that needs `need` bytes
+  int check(int64_t need) const {
+    if (need > bytes) return FP8Q_ESIZE;
+    if (need > 0 && !at) return FP8Q_EINVAL;
+    return need > 0 && (reinterpret_cast<uintptr_t>(at) & 15u) ? FP8Q_EALIGN : FP8Q_OK;
+  }
+  uint32_t* tickets() const { return static_cast<uint32_t*>(at); }
+  float* parts() const { return at ? reinterpret_cast<float*>(static_cast<char*>(at) + kMaxGrid * 4) : nullptr; }
+};
 
 // ---- launches (kv_cache.cu, kv_attention.cu) --------------------------------
 cudaError_t launch_kv_write(const KvShape& s, int format, KvPool k, KvPool v, const void* kx, const void* vx,
@@ -371,15 +383,15 @@ __device__ __forceinline__ void store_lse(const KvAttn& a, int64_t row, int head
 bool kv_decode_takes(int max_q, int group);
 cudaError_t kv_decode_workspace(const KvShape& s, int group, int batch, int max_q, int table_width, int sms,
                                 int64_t* bytes);
-cudaError_t launch_kv_decode(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches);
+cudaError_t launch_kv_decode(const KvAttn& a, const KvWork& w, int sms, cudaStream_t st, int* status, int* launches);
 // Any number of them (kv_prompt.cu).
 cudaError_t kv_prompt_workspace(const KvShape& s, int group, int batch, int64_t total_q, int max_q, int table_width,
                                 int sms, int64_t* bytes);
-cudaError_t launch_kv_prompt(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches);
+cudaError_t launch_kv_prompt(const KvAttn& a, const KvWork& w, int sms, cudaStream_t st, int* status, int* launches);
 cudaError_t read_kv_wait_timeouts(unsigned int* count);   // and reset to 0
 // Any call: the kernel that fits it (kv_attention.cu).
 cudaError_t kv_attention_workspace(const KvShape& s, int q_heads, int batch, int64_t total_q, int max_q,
                                    int table_width, int sms, int64_t* bytes);
-cudaError_t launch_kv_attention(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches);
+cudaError_t launch_kv_attention(const KvAttn& a, const KvWork& w, int sms, cudaStream_t st, int* status, int* launches);
 
 }  // namespace fp8q

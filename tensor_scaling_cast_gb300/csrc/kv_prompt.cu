@@ -37,7 +37,7 @@ constexpr int kPrKeys = 128;              // keys of a unit
 constexpr int kPrHalf = 64;               // and of a half of it: scores are made and used by halves
 constexpr int kPrStages = 2;              // units of unpacked keys, and of values, in shared memory
 constexpr int kPrMinUnits = 8;            // units of a CTA, at least
-constexpr int kPrSetup = 6;               // what an item costs beyond its units, in units: queries in, output out
+constexpr int kPrSetup = 4;               // what an item costs beyond its units, in units: queries in, output out
 
 __device__ unsigned int g_kv_wait_timeouts = 0;
 
@@ -317,30 +317,39 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           // q: f16, each row scaled by a power of two to a largest magnitude in
           // [2^14, 2^15).  A warp takes its 32 rows RPI at a time, 16 bytes a lane.
           f_row = 0.0f;
-#pragma unroll 4
-          for (int x = 0; x < 32 / RPI; ++x) {
-            const int rw = x * RPI + lane / CPR, c = lane % CPR, rr = row0 + (warp & 3) * 32 + rw;
-            const bool there = rr < it.rows;
-            const int i = there ? a.by_group.div(rr) : 0;
-            const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)(it.sq.q0 + i) * a.q_tok +
-                                     (int64_t)(it.head * a.group + (there ? rr - i * a.group : 0)) * a.q_head + c * 8;
-            const uint4 w = there ? *reinterpret_cast<const uint4*>(q) : make_uint4(0, 0, 0, 0);
-            uint32_t m = unpack_max<FP8Q_BF16>(absmax_load<FP8Q_BF16>(w));
+          constexpr int QN = 32 / RPI < 8 ? 32 / RPI : 8;          // loads in flight
+#pragma unroll 1
+          for (int x0 = 0; x0 < 32 / RPI; x0 += QN) {
+            const int c = lane % CPR, rw0 = (warp & 3) * 32 + x0 * RPI + lane / CPR;
+            uint4 w[QN];
 #pragma unroll
-            for (int y = 1; y < CPR; y <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, y));
-            const int e = m == 0 ? 0 : max(-112, (int)(m >> 23) - 127) - 14;
-            const float s = pow2f(-e);
-            float f = a.scale * 1.4426950408889634f * pow2f(e);
-            if (m >= 0x7F800000u) f = __uint_as_float(0x7FFFFFFFu);      // NaN or Inf: the row is NaN
-            f = __shfl_sync(0xFFFFFFFFu, f, (lane % RPI) * CPR);
-            if (lane / RPI == x) f_row = f;
-            uint4 h;
-            h.x = cvt_f16x2(__uint_as_float(w.x << 16) * s, __uint_as_float(w.x & 0xFFFF0000u) * s);
-            h.y = cvt_f16x2(__uint_as_float(w.y << 16) * s, __uint_as_float(w.y & 0xFFFF0000u) * s);
-            h.z = cvt_f16x2(__uint_as_float(w.z << 16) * s, __uint_as_float(w.z & 0xFFFF0000u) * s);
-            h.w = cvt_f16x2(__uint_as_float(w.w << 16) * s, __uint_as_float(w.w & 0xFFFF0000u) * s);
-            const int row = (warp & 3) * 32 + rw;
-            *reinterpret_cast<uint4*>(sm.q[wg] + (c >> 3) * Smem::kQHalf + row * 128 + (((c & 7) ^ (row & 7)) * 16)) = h;
+            for (int x = 0; x < QN; ++x) {
+              const int rr = row0 + rw0 + x * RPI, i = a.by_group.div(rr);
+              w[x] = make_uint4(0, 0, 0, 0);
+              if (rr < it.rows)
+                w[x] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                                       (int64_t)(it.sq.q0 + i) * a.q_tok +
+                                                       (int64_t)(it.head * a.group + rr - i * a.group) * a.q_head + c * 8);
+            }
+#pragma unroll
+            for (int x = 0; x < QN; ++x) {
+              uint32_t m = unpack_max<FP8Q_BF16>(absmax_load<FP8Q_BF16>(w[x]));
+#pragma unroll
+              for (int y = 1; y < CPR; y <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, y));
+              const int e = m == 0 ? 0 : max(-112, (int)(m >> 23) - 127) - 14;
+              const float s = pow2f(-e);
+              float f = a.scale * 1.4426950408889634f * pow2f(e);
+              if (m >= 0x7F800000u) f = __uint_as_float(0x7FFFFFFFu);    // NaN or Inf: the row is NaN
+              f = __shfl_sync(0xFFFFFFFFu, f, (lane % RPI) * CPR);
+              if (lane / RPI == x0 + x) f_row = f;
+              uint4 h;
+              h.x = cvt_f16x2(__uint_as_float(w[x].x << 16) * s, __uint_as_float(w[x].x & 0xFFFF0000u) * s);
+              h.y = cvt_f16x2(__uint_as_float(w[x].y << 16) * s, __uint_as_float(w[x].y & 0xFFFF0000u) * s);
+              h.z = cvt_f16x2(__uint_as_float(w[x].z << 16) * s, __uint_as_float(w[x].z & 0xFFFF0000u) * s);
+              h.w = cvt_f16x2(__uint_as_float(w[x].w << 16) * s, __uint_as_float(w[x].w & 0xFFFF0000u) * s);
+              const int row = rw0 + x * RPI;
+              *reinterpret_cast<uint4*>(sm.q[wg] + (c >> 3) * Smem::kQHalf + row * 128 + (((c & 7) ^ (row & 7)) * 16)) = h;
+            }
           }
           fence_proxy_async();
           arrive(&sm.q_full[wg]);
@@ -831,14 +840,18 @@ static int pr_grid(const KvShape& s, int group, int batch, int64_t total_q, int 
   return (int)(n < kMaxGrid ? n : kMaxGrid);
 }
 
+static int64_t pr_bytes(int grid, int dim) {
+  return grid < 2 ? 0 : kMaxGrid * 4 + (int64_t)grid * 2 * kPrRows * (dim + 2) * 4;
+}
+
 cudaError_t kv_prompt_workspace(const KvShape& s, int group, int batch, int64_t total_q, int max_q, int table_width,
                                 int sms, int64_t* bytes) {
   const int grid = pr_grid(s, group, batch, total_q, max_q, table_width, sms);
-  *bytes = grid < 2 ? 0 : kMaxGrid * 4 + (int64_t)grid * 2 * kPrRows * (s.dim + 2) * 4;
+  *bytes = pr_bytes(grid, s.dim);
   return cudaSuccess;
 }
 
-cudaError_t launch_kv_prompt(const KvAttn& a, void* workspace, int sms, cudaStream_t st, int* launches) {
+cudaError_t launch_kv_prompt(const KvAttn& a, const KvWork& w, int sms, cudaStream_t st, int* status, int* launches) {
   const int grid = pr_grid(a.shape, a.group, a.batch, a.total_q, a.max_q, a.table_width, sms);
   const void* k = a.shape.dim == 128 ? reinterpret_cast<const void*>(kv_prompt_kernel<128>)
                                      : reinterpret_cast<const void*>(kv_prompt_kernel<64>);
@@ -846,9 +859,9 @@ cudaError_t launch_kv_prompt(const KvAttn& a, void* workspace, int sms, cudaStre
   int occ = 1;
   cudaError_t e = kernel_occupancy(k, kPrThreads, smem, &occ);
   if (e != cudaSuccess) return e;
-  PrPlan plan;
-  plan.ticket = static_cast<uint32_t*>(workspace);
-  plan.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMaxGrid * 4);
+  *status = w.check(pr_bytes(grid, a.shape.dim));
+  if (*status != FP8Q_OK) return cudaSuccess;
+  PrPlan plan = {w.tickets(), w.parts()};
   void* args[2] = {const_cast<KvAttn*>(&a), &plan};
   return launch_dependent(k, dim3(grid), kPrThreads, smem, args, st, launches);
 }
