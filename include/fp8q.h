@@ -401,6 +401,7 @@ typedef struct mx_kv_cache {
  * elements of a row are consecutive), likewise v, and goes to slot slots[t].
  *   dtype    FP8Q_BF16 or FP8Q_F32; bases and strides multiples of 16 bytes
  *            (else FP8Q_EALIGN)
+ *   tokens   0 .. 2^31 - 1
  *   slots    device int64 [tokens]; a slot below 0 or past the cache is not
  *            written (padding tokens).  Slots of one call must be distinct.
  *   rule     FP8Q_MX_FLOOR, FP8Q_MX_CEIL or FP8Q_MX_NEAREST
@@ -440,9 +441,10 @@ FP8Q_API int mx_kv_read(const mx_kv_cache* c, const int64_t* slots, int64_t toke
  *                past it are left unwritten)
  *   scale        > 0;  window >= 0 (0: no window)
  *   workspace    device memory of mx_kv_attention_workspace(...) bytes,
- *                16-byte aligned, zeroed before its first use; every call
- *                leaves it ready for the next one.  Calls that may overlap on
- *                the GPU need one each.  FP8Q_ESIZE if it is too small.
+ *                16-byte aligned, its first MX_KV_WORKSPACE_ZEROED bytes zero
+ *                before its first use; every call leaves it ready for the
+ *                next one, of whatever sizes.  Calls that may overlap on the
+ *                GPU need one each.  FP8Q_ESIZE if it is too small.
  * Scores, softmax statistics and sums are fp32.  Capturable into CUDA graphs;
  * the lengths and the table are read by the kernel, so replays see their
  * current contents. */
@@ -451,6 +453,8 @@ FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int
                              int64_t out_head_stride, float* lse, const int32_t* cu_q, const int32_t* kv_lens,
                              const int32_t* page_table, int64_t table_stride, int table_width, int batch, int max_q,
                              float scale, int window, void* workspace, int64_t workspace_bytes, void* stream);
+
+#define MX_KV_WORKSPACE_ZEROED 16384
 
 /* Workspace bytes that mx_kv_attention needs for these sizes on the current
  * device (possibly 0), or a negative status. */

@@ -129,6 +129,7 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
 kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPlan plan) {
   constexpr int NB = D / 32, RB = D / 2, ROWS = 8 * NT;
+  constexpr bool QS = NT > 1;                    // queries in shared memory
   using Smem = DecSmem<D>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -139,6 +140,8 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
   __shared__ long long s_before;
   __shared__ uint32_t s_last;
   __shared__ Joined s_rows[8 * NT];
+  __shared__ uint4 s_q[QS ? NT * NB * 32 : 1];
+  __shared__ float s_f[8 * NT];
   // the lane's row of 8 x 8 code matrices (the swizzle repeats every 8 rows),
   // and the place of its token's value scales
   const uint32_t lane_at = D == 128 ? code_offset<D>(lane & 7, lane >> 3)
@@ -230,46 +233,62 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
     int pages[kDecStages];
 #pragma unroll
     for (int k = 0; k < kDecStages; ++k) pages[k] = page_of(k);
-    uint4 qw[NT][NB];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    // With one group of eight rows the queries stay in registers; with more
+    // each warp prepares some of the groups and all read them from shared
+    // memory, which leaves the registers to the sums.
+    constexpr int QN = QS ? 1 : NT;              // groups of a warp at a time
+    uint4 qw[QN][NB];
+    auto load_q = [&](int nt, uint4 (&w)[NB]) {
       const int r = nt * 8 + li;
       const bool on = r < rows;
       const int qi = on ? a.by_group.div(r) : 0, g = on ? r - qi * a.group : 0;
       const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)(sq.q0 + qi) * a.q_tok +
                                (int64_t)(head * a.group + g) * a.q_head + lc * 8;
 #pragma unroll
-      for (int x = 0; x < NB; ++x) qw[nt][x] = on ? *reinterpret_cast<const uint4*>(q + x * 32) : make_uint4(0, 0, 0, 0);
-    }
+      for (int x = 0; x < NB; ++x) w[x] = on ? *reinterpret_cast<const uint4*>(q + x * 32) : make_uint4(0, 0, 0, 0);
+    };
+    if (!QS) load_q(0, qw[0]);
+    else if (warp < NT) load_q(warp, qw[0]);
 #pragma unroll
     for (int k = 0; k < kDecStages - 1; ++k) issue(k, k, pages[k]);
     int page_next = pages[kDecStages - 1];
 
     // ---- queries: f16, each row scaled by a power of two to a largest
     // magnitude in [2^14, 2^15), which keeps bf16 exact down to 2^-29 of it
-    uint32_t qf[NT][NB][4];
+    uint32_t qf[QN][NB][4];
     float fx[NT][2];                             // score factor of query rows 2 lc, 2 lc + 1
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    float f = 0.0f;                              // of row li of the warp's group
+    if (!QS || warp < NT) {
       uint32_t m = 0;
 #pragma unroll
-      for (int x = 0; x < NB; ++x) m = vmax_u16x2(m, absmax_load<FP8Q_BF16>(qw[nt][x]));
+      for (int x = 0; x < NB; ++x) m = vmax_u16x2(m, absmax_load<FP8Q_BF16>(qw[0][x]));
       m = unpack_max<FP8Q_BF16>(m);
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
       const int e = m == 0 ? 0 : max(-112, (int)(m >> 23) - 127) - 14;   // q = q' * 2^e, e in [-126, 113]
       const float s = pow2f(-e);
-      float f = fmaxf(a.scale * 1.4426950408889634f * pow2f(e), kMinFactor);
+      f = fmaxf(a.scale * 1.4426950408889634f * pow2f(e), kMinFactor);
       if (m >= 0x7F800000u) f = __uint_as_float(0x7FFFFFFFu);            // NaN or Inf: the row is NaN
 #pragma unroll
       for (int x = 0; x < NB; ++x) {
-        const uint32_t ws[4] = {qw[nt][x].x, qw[nt][x].y, qw[nt][x].z, qw[nt][x].w};
+        const uint32_t ws[4] = {qw[0][x].x, qw[0][x].y, qw[0][x].z, qw[0][x].w};
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-          qf[nt][x][y] = cvt_f16x2(__uint_as_float(ws[y] << 16) * s, __uint_as_float(ws[y] & 0xFFFF0000u) * s);
+          qf[0][x][y] = cvt_f16x2(__uint_as_float(ws[y] << 16) * s, __uint_as_float(ws[y] & 0xFFFF0000u) * s);
+        if (QS) s_q[(warp * NB + x) * 32 + lane] = make_uint4(qf[0][x][0], qf[0][x][1], qf[0][x][2], qf[0][x][3]);
       }
-      fx[nt][0] = __shfl_sync(0xFFFFFFFFu, f, lc * 8);
-      fx[nt][1] = __shfl_sync(0xFFFFFFFFu, f, lc * 8 + 4);
+      if (QS && lc == 0) s_f[warp * 8 + li] = f;
+    }
+    if (QS) {
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        fx[nt][0] = s_f[nt * 8 + lc * 2];
+        fx[nt][1] = s_f[nt * 8 + lc * 2 + 1];
+      }
+    } else {
+      fx[0][0] = __shfl_sync(0xFFFFFFFFu, f, lc * 8);
+      fx[0][1] = __shfl_sync(0xFFFFFFFFu, f, lc * 8 + 4);
     }
 
     float o[NT][NB][2][4];
@@ -375,8 +394,10 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float c[4];
-            mma_zero(c, ka[0], kb[0], ka[1], kb[1], qf[nt][x][0], qf[nt][x][1]);
-            mma(c, ka[2], kb[2], ka[3], kb[3], qf[nt][x][2], qf[nt][x][3]);
+            const uint4 q = QS ? s_q[(nt * NB + x) * 32 + lane]
+                               : make_uint4(qf[0][x][0], qf[0][x][1], qf[0][x][2], qf[0][x][3]);
+            mma_zero(c, ka[0], kb[0], ka[1], kb[1], q.x, q.y);
+            mma(c, ka[2], kb[2], ka[3], kb[3], q.z, q.w);
             s[u][nt][0] += c[0] * ks[0][x];
             s[u][nt][1] += c[1] * ks[0][x];
             s[u][nt][2] += c[2] * ks[1][x];

@@ -260,6 +260,7 @@ constexpr float kMinFactor = 1.17549435e-38f;
 // A workspace: tickets (zero between calls), then the parts of rows whose
 // keys several CTAs share.
 constexpr int kMaxGrid = 4096;            // tickets, and CTAs of a call at most
+static_assert(kMaxGrid * 4 == MX_KV_WORKSPACE_ZEROED, "the tickets are what a caller zeroes");
 struct KvWork {
   void* at;
   int64_t bytes;

@@ -729,6 +729,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
         if (last) return;
       }
     }();
+    cp_wait<0>();                                    // no copy outlives its warp
   } else {
     // ================= two warps issue the products, one for each 128 rows =================
     // Issuing blocks while the tensor cores are busy and a wait costs a hundred

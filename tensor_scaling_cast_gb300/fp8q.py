@@ -23,6 +23,7 @@ EST_MAX_WINDOW, EST_SMOOTHED = 0, 1
 F32, BF16 = 0, 1
 NO_EXP = -(2 ** 31)
 MAX_WINDOW = 256
+WORKSPACE_ZEROED = 16384      # MX_KV_WORKSPACE_ZEROED
 
 _STATUS = {0: "FP8Q_OK", -1: "FP8Q_EINVAL", -2: "FP8Q_EALIGN", -3: "FP8Q_EDTYPE", -4: "FP8Q_ECUDA",
            -5: "FP8Q_EHANDLE", -6: "FP8Q_ENOMEM", -7: "FP8Q_EDEVICE", -8: "FP8Q_ESIZE"}
@@ -408,14 +409,18 @@ def mx_kv_read(cache: MXKVCache, slots: torch.Tensor, k: torch.Tensor, v: torch.
 
 
 def mx_kv_attention_workspace(cache: MXKVCache, q: torch.Tensor, page_table: torch.Tensor, max_q: int = 1):
-    """A zeroed workspace for mx_kv_attention calls of these shapes, or None
-    where they need none.  One per stream; reusable by every call of the same
-    or smaller shapes whose own query asks for no more."""
+    """A workspace for mx_kv_attention calls of these shapes, ready for its first
+    use, or None where they need none.  One per stream; it serves every call
+    whose own shapes ask for no more bytes."""
     n = load().mx_kv_attention_workspace(cache._ref, q.shape[0], q.shape[1], page_table.shape[0], max_q,
                                          page_table.shape[1])
     if n < 0:
         _check(n, "mx_kv_attention_workspace")
-    return torch.zeros(n, dtype=torch.uint8, device=q.device) if n else None
+    if not n:
+        return None
+    ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+    ws[:WORKSPACE_ZEROED].zero_()
+    return ws
 
 
 def mx_kv_attention(cache: MXKVCache, q: torch.Tensor, out: torch.Tensor, page_table: torch.Tensor,
