@@ -144,7 +144,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
   constexpr int NB = D / 32;
   constexpr uint32_t kS = 0, kO = 256;               // tensor-memory columns of warpgroup 0 (+ 128 for 1)
   extern __shared__ uint8_t smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + (-smem_addr(smem_raw) & 1023u));      // 1024-byte aligned
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
 
   grid_begin();
@@ -280,7 +280,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
   // Every wait is bounded; a role whose wait runs out counts it and returns,
   // and so do the others in turn, to the common end.
   auto wait1 = [&](uint64_t* bar, uint32_t parity) {             // one thread
-    if (mbar_sleep(bar, parity & 1)) return true;
+    if (mbar_wait_lean(bar, parity & 1)) return true;
     atomicAdd(&g_kv_wait_timeouts, 1u);
     return false;
   };

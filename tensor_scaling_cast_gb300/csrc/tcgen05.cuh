@@ -128,21 +128,18 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// mbar_wait for warps that share the SM's issue slots with busy ones: each
-// try suspends the warp (up to the hint, in ns) instead of coming back at
-// once; false after kWaitCycles.
-__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
-  long long deadline = 0;
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}" : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u) : "memory");
-    if (ok) return true;
-    const long long now = clock64();
-    if (deadline == 0) deadline = now + kWaitCycles;
-    else if (now > deadline) return false;
-  }
+// mbar_wait for warps that share the SM's issue slots with busy ones: the
+// clock is read only every 64th try (each try suspends the warp for a while
+// by itself; one with a time hint becomes a loop of sleeps, which wakes late).
+__device__ __forceinline__ bool mbar_wait_lean(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long deadline = clock64() + kWaitCycles;
+  do {
+#pragma unroll 1
+    for (int n = 0; n < 64; ++n)
+      if (mbar_try_wait(bar, parity)) return true;
+  } while (clock64() < deadline);
+  return false;
 }
 
 template <int N>
