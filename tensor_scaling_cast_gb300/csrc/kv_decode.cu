@@ -40,9 +40,9 @@ namespace fp8q {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kDecStages = 3;
+constexpr int kDecStages = 4;
 constexpr int kTile = 32;                 // tokens of a warp tile
-constexpr int kDecSetup = 8;              // what a (sequence, head) costs beyond its tiles, in tiles: queries in, output out
+constexpr int kDecSetup = 12;             // what a (sequence, head) costs beyond its tiles, in tiles: queries in, output out
 constexpr int kMinTiles = 8;              // tiles of a CTA, at least
 
 template <int D>
@@ -126,7 +126,7 @@ struct DecPlan {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
+__global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 3 : 2)
 kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPlan plan) {
   constexpr int NB = D / 32, RB = D / 2, ROWS = 8 * NT;
   constexpr bool QS = NT > 1;                    // queries in shared memory
