@@ -424,7 +424,8 @@ FP8Q_API int mx_kv_read(const mx_kv_cache* c, const int64_t* slots, int64_t toke
  * cu_q[b + 1) of q and are its last tokens: query i of n sits at position
  * kv_lens[b] - n + i and sees the keys j <= its position and, with window
  * W > 0, j > its position - W.  A query that sees no key gets zeros.
- *   c            format FP8Q_E2M1 (else FP8Q_EDTYPE), head_dim 64 or 128
+ *   c            format FP8Q_E2M1 (else FP8Q_EDTYPE), head_dim 64 or 128;
+ *                q_heads a multiple of its kv_heads, up to MX_KV_MAX_HEADS
  *   q, out       FP8Q_BF16 rows [total_q, q_heads, head_dim] with the given
  *                element strides (multiples of 8), bases 16-byte aligned; they may not overlap
  *   lse          device float [total_q, q_heads]: log of the softmax sum
@@ -434,8 +435,9 @@ FP8Q_API int mx_kv_read(const mx_kv_cache* c, const int64_t* slots, int64_t toke
  *   kv_lens      device int32 [batch]: tokens in each sequence's cache, its
  *                queries included (values below 0 or past the table are
  *                clamped)
+ *   batch        0 .. 65535
  *   page_table   device int32 [batch, table_width], rows table_stride apart:
- *                the pages of a sequence in order; entries past its length
+ *                the pages of a sequence in order (fewer than 2^30 tokens); entries past its length
  *                are not used, a page outside the cache hides its tokens
  *   max_q        at least the largest number of queries of a sequence (rows
  *                past it are left unwritten)
@@ -445,7 +447,9 @@ FP8Q_API int mx_kv_read(const mx_kv_cache* c, const int64_t* slots, int64_t toke
  *                before its first use; every call leaves it ready for the
  *                next one, of whatever sizes.  Calls that may overlap on the
  *                GPU need one each.  FP8Q_ESIZE if it is too small.
- * Scores, softmax statistics and sums are fp32.  Capturable into CUDA graphs;
+ * Scores, softmax statistics and sums are fp32; the softmax weights are held
+ * in f16 next to the row's largest, and codes times their scale in f16 next
+ * to the largest scale of their 32 tokens (exact down to 2^-22 of it).  Capturable into CUDA graphs;
  * the lengths and the table are read by the kernel, so replays see their
  * current contents. */
 FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int64_t total_q, int q_heads,
@@ -463,8 +467,8 @@ FP8Q_API int64_t mx_kv_attention_workspace(const mx_kv_cache* c, int64_t total_q
 
 /* Number of pipeline waits on the current device that ran out of time since
  * the last call (and reset it).  Kernels that stage tiles through TMA
- * (column-wise mx_cast_ex, mx_cast_dual, fp8q_cast_transpose) bound every
- * wait for a tile; on timeout they count it here and stop instead of
+ * (column-wise mx_cast_ex, mx_cast_dual, fp8q_cast_transpose) and the
+ * prompt kernel of mx_kv_attention bound every wait for a tile; on timeout they count it here and stop instead of
  * hanging, leaving their outputs incomplete.  A healthy run reads 0.
  * Synchronous. */
 FP8Q_API int fp8q_pipeline_status(unsigned int* timed_out_waits);

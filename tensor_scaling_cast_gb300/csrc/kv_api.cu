@@ -112,9 +112,13 @@ FP8Q_API int64_t mx_kv_attention_workspace(const mx_kv_cache* c, int64_t total_q
   if (total_q == 0 || batch == 0) return 0;
   if (max_q > total_q) max_q = (int)total_q;
   int64_t bytes = 0;
-  const cudaError_t e = kv_attention_workspace(s, q_heads, batch, total_q, max_q, table_width,
-                                               sm_count(device_of_current()), &bytes);
-  return e == cudaSuccess ? bytes : record_cuda_error(e);
+  try {                            // the occupancy cache allocates
+    const cudaError_t e = kv_attention_workspace(s, q_heads, batch, total_q, max_q, table_width,
+                                                 sm_count(device_of_current()), &bytes);
+    return e == cudaSuccess ? bytes : record_cuda_error(e);
+  } catch (...) {
+    return FP8Q_ENOMEM;
+  }
 }
 
 FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int64_t total_q, int q_heads,
@@ -158,8 +162,13 @@ FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int
   a.window = window > 0x3FFFFFFF ? 0 : window;   // no sequence is that long
   a.scale = scale;
   int launches = 0;
-  const cudaError_t e = launch_kv_attention(a, {workspace, workspace_bytes}, sm_count(device_of_current()),
-                                            reinterpret_cast<cudaStream_t>(stream), &st, &launches);
+  cudaError_t e;
+  try {                            // the occupancy cache allocates
+    e = launch_kv_attention(a, {workspace, workspace_bytes}, sm_count(device_of_current()),
+                            reinterpret_cast<cudaStream_t>(stream), &st, &launches);
+  } catch (...) {
+    return FP8Q_ENOMEM;
+  }
   if (st != FP8Q_OK) return st;
   return finish(e, launches);
 }

@@ -424,13 +424,15 @@ def mx_kv_attention_workspace(cache: MXKVCache, q: torch.Tensor, page_table: tor
 
 
 def mx_kv_attention(cache: MXKVCache, q: torch.Tensor, out: torch.Tensor, page_table: torch.Tensor,
-                    kv_lens: torch.Tensor, cu_q=None, max_q: int = 1, scale=None, window: int = 0, lse=None,
+                    kv_lens: torch.Tensor, cu_q=None, max_q=None, scale=None, window: int = 0, lse=None,
                     workspace=None, stream=None):
     """Attention of q [total_q, q_heads, head_dim] (bf16) over the 4-bit cache,
     into out of the same shape.  page_table int32 [batch, pages], kv_lens int32
     [batch], cu_q int32 [batch + 1] (None: one query per sequence), max_q >= the
-    queries of any sequence, scale (None: head_dim ** -0.5), lse float32
-    [total_q, q_heads] or None, workspace of mx_kv_attention_workspace."""
+    queries of any sequence (None: 1 without cu_q, total_q with it; the closer
+    the bound, the better the plan), scale (None: head_dim ** -0.5), lse
+    float32 [total_q, q_heads] or None, workspace of mx_kv_attention_workspace
+    for the same max_q."""
     shape, qs, os_ = q.shape, q.stride(), out.stride()
     table, ts = page_table.shape, page_table.stride()
     if (len(shape) != 3 or shape[2] != cache.head_dim or out.shape != shape or qs[2] != 1 or os_[2] != 1
@@ -445,6 +447,8 @@ def mx_kv_attention(cache: MXKVCache, q: torch.Tensor, out: torch.Tensor, page_t
                                      or not lse.is_contiguous()))):
         raise TypeError("mx_kv_attention: page_table int32 [batch, pages], kv_lens int32 [batch], "
                         "cu_q int32 [batch + 1], lse float32 [total_q, q_heads]")
+    if max_q is None:
+        max_q = 1 if cu_q is None else max(1, shape[0])
     st = (_lib or load()).mx_kv_attention(
         cache._ref, q.data_ptr(), BF16, shape[0], shape[1], qs[0], qs[1], out.data_ptr(), os_[0], os_[1],
         None if lse is None else lse.data_ptr(), None if cu_q is None else cu_q.data_ptr(), kv_lens.data_ptr(),
