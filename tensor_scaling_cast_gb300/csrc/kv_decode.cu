@@ -12,28 +12,36 @@
 // takes p * 2^-R.  M moves only when a tile passes it by 2^8 (one vote per
 // tile), which is when the sums are rescaled.
 //
-// What bounds it: 68 bytes of cache per token and head at D = 128 against 512
-// multiply-adds for each query row, HBM as long as the unpacking keeps up:
-// the codes of 8 tokens cross the SM in 80 instructions.  mma.sync and not
-// tcgen05: with 16 tokens x 8 query rows a product it takes 2 of the 23 issue
-// slots that a token has at the full HBM rate, its operands come straight
-// from the unpacked registers, and nothing waits on a tensor-memory round
-// trip.
+// What bounds it: HBM and the unpacking together.  A token and head at D = 128
+// is 136 bytes of cache, and a tile of 32 of them 590 warp instructions for up
+// to eight query rows, a fifth of them the conversions of the 8192 codes.  8
+// sequences of 131072 tokens, 32 heads over 8: 229 us, 5.0 TB/s, 0.75 of the
+// measured copy rate (the same copies without the arithmetic: 180 us; ALU pipe
+// 58%, issue slots 57%, DRAM reads 1.00 of the cache's bytes); half as wide
+// rows (D = 64, the same softmax for half the bytes) 158 us.  mma.sync and not
+// tcgen05: with 16 tokens x 8 query rows a product it takes 1 of the 18
+// instructions of a token, its operands come straight from the unpacked
+// registers, and nothing waits on a tensor-memory round trip.
 //
 // Layout.  A warp owns tiles of 32 tokens, copied by cp.async into a ring of
-// its own (no CTA barrier while it streams).  Keys are the A operand (16
-// tokens x 16 columns, the columns of a block permuted alike in q so that a
-// lane's 32-bit word of codes is one lane's share of two products); values
-// are the A operand of the transposed product (16 columns x 16 tokens), read
-// by ldmatrix.trans, which pairs a token's codes with its neighbour's.  The
-// scores come out with tokens down and query rows across, so that a weight
-// tile needs one movmatrix per 8 x 8 to become the B operand.
+// its own (no CTA barrier while it streams; four stages at three CTAs per SM
+// 229 us, three stages at four CTAs 233).  Keys are the A operand (16 tokens x
+// 16 columns, the columns of a block permuted alike in q so that a lane's
+// 32-bit word of codes is one lane's share of two products); values are the A
+// operand of the transposed product (16 columns x 16 tokens), read by
+// ldmatrix.trans from rows stored in an order that puts the codes of two
+// tokens where one mask makes a byte of them.  The scores come out with tokens
+// down and query rows across, so that a weight tile needs one movmatrix per
+// 8 x 8 to become the B operand.
 //
-// Work is split over the tiles of all sequences and heads: CTA i takes tiles
-// [i * per, (i + 1) * per) in (sequence, head) order, so that uneven lengths
-// fill the GPU evenly and the host needs to know none of them.  A (sequence,
-// head) that spans several CTAs is joined by the last of them to arrive, in
-// the order of the tiles (the result does not depend on which that is).
+// Work is split over the tiles of all sequences and heads: CTA i takes
+// positions [i * per, (i + 1) * per) in (sequence, head) order, each of them
+// kDecSetup positions and its tiles, so that uneven lengths fill the GPU
+// evenly and the host needs to know none of them.  (Set-up of 12 against 5
+// tiles: 64 sequences of 512 tokens 14 us against 19; the default batch of 64
+// ragged ones 44 against 46.)  A (sequence, head) that spans several CTAs is
+// joined by the last of them to arrive, in the order of the tiles (the result
+// does not depend on which that is).
 #include "kv_device.cuh"
 
 namespace fp8q {
@@ -42,7 +50,7 @@ constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecStages = 4;
 constexpr int kTile = 32;                 // tokens of a warp tile
-constexpr int kDecSetup = 12;             // what a (sequence, head) costs beyond its tiles, in tiles: queries in, output out
+constexpr int kDecSetup = 12;             // what a (sequence, head) costs beyond its tiles, in tiles
 constexpr int kMinTiles = 8;              // tiles of a CTA, at least
 
 template <int D>
@@ -197,8 +205,9 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
     const int pos0 = sq.pos0;
     const int32_t* table = a.table + b * a.table_stride;
     // The warp's k-th tile begins at token tile0_at + k * (kDecWarps * kTile).
-    // Pages of 32 tokens or more hold all of a tile's rows in one run; smaller
-    // ones are looked up by each lane for its own token.
+    // Pages of 32 tokens or more hold all of a tile's rows in one run (229 us
+    // against 235 by rows, D = 128; 158 against 168 at D = 64); smaller ones are
+    // looked up by each lane for its own token (254 us at 16 tokens a page).
     const int tile0_at = (sq.tile0 + t0 + warp) * kTile;
     const bool runs = a.shape.page_shift >= 5;
     auto page_of = [&](int k) {
@@ -235,7 +244,8 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
     for (int k = 0; k < kDecStages; ++k) pages[k] = page_of(k);
     // With one group of eight rows the queries stay in registers; with more
     // each warp prepares some of the groups and all read them from shared
-    // memory, which leaves the registers to the sums.
+    // memory, which leaves the registers to the sums (four groups over 8 x 131072
+    // tokens: 539 us against 681 from registers).
     constexpr int QN = QS ? 1 : NT;              // groups of a warp at a time
     uint4 qw[QN][NB];
     auto load_q = [&](int nt, uint4 (&w)[NB]) {
@@ -688,6 +698,10 @@ static cudaError_t dec_grid(const DecLaunch& k, const KvShape& s, int batch, int
   return cudaSuccess;
 }
 
+// Up to 32 rows a key/value head: 20 rows over a 4096 window take 26 us here
+// and 50 in kv_prompt.cu, 32 rows over 8 x 131072 tokens 539 and 782; beyond,
+// every further 32 rows would read and unpack the cache again, while that
+// kernel does it once for 256.
 bool kv_decode_takes(int max_q, int group) { return (int64_t)max_q * group <= 32; }
 
 static int64_t dec_bytes(int grid, int nt, int dim) {

@@ -8,23 +8,34 @@
 // f16 down to 2^-22 of the largest; a score is then 2^Rk * (q . k'), the
 // weights are 2^(x + Rv - M) and the softmax sum takes them times 2^-Rv.
 //
-// What bounds it: 4 D flops per visible pair on the tensor cores (4096 f16
-// multiply-adds a clock and SM), against one exponential (32 a clock) and
-// about six other instructions per pair, and 2 x 16 K elements to unpack per
-// tile of 128 tokens.
+// What bounds it: the issue slots.  A unit (128 keys x 256 rows, D = 128)
+// takes 2560 clocks of the tensor cores (4096 f16 multiply-adds a clock, the
+// score products at two thirds of that: 64 keys wide, they are fed at the
+// shared memory's 128 bytes a clock), 1024 of the exponentials, and 11.5 K
+// warp instructions, 2900 clocks of the SM's four schedulers; measured are
+// 4200.  2048 queries after 14336 tokens, 32 heads over 8: 453 us, 1138
+// TFLOP/s, 0.59 of the measured bf16 rate; at D = 64, where the exponentials
+// and the instructions are the same and the products half, 416 us.
 //
 // Layout: one CTA per SM.  Two warpgroups hold the softmax of 128 rows each
-// (rows are query tokens times the heads that share a key/value head; one row
-// per thread, scores read from tensor memory at once), a third unpacks keys
-// and values into two-stage rings of 128-byte-swizzled tiles, and one thread
-// issues the products in turn, scores of one warpgroup's rows while the other
-// one's weights are made.  Weights return to tensor memory over the scores
-// (f16, the A operand of the second product); values are the B operand with D
-// consecutive, so neither is transposed.
+// (rows are query tokens times the heads that share a key/value head, one row
+// per thread), two unpack keys and values (a warp's 32 rows come by cp.async
+// and go, as f16, into two-stage rings of 128-byte-swizzled tiles), and two
+// warps issue the products, one for each softmax warpgroup.  A unit's scores
+// are made and used in two halves of 64 keys, so that a warpgroup works on one
+// half while the other half's products run; weights return to tensor memory
+// over the scores they came from (f16, the A operand of the second product);
+// values are the B operand with D consecutive, so neither is transposed.
+// Sizes: scores 2 x 128 and sums 2 x D columns fill the 512 of tensor memory
+// at D = 128; queries 64 KB, keys and values 128 KB, raw rows 17 KB of shared
+// memory.  Registers: 640 threads launch with 96, which setmaxnreg turns into
+// 144 for the softmax and 64 for the others.
 //
-// Work is split as in kv_decode.cu: CTA i takes units [i * per, (i + 1) * per)
-// of 128 keys x 256 rows in (sequence, head, rows) order, and what spans CTAs
-// is joined by the last of them to arrive.
+// Work is split as in kv_decode.cu: CTA i takes positions [i * per, (i + 1) *
+// per) over all units in (sequence, head, rows) order, each item of 256 rows
+// with kPrSetup positions more for its queries and output, and what spans CTAs
+// is joined by the last of them to arrive.  (Set-up of 4 against 3, 6 and 8
+// positions: four ragged prompts 282 us against 298, 294 and 303.)
 #include "kv_device.cuh"
 #include "tcgen05.cuh"
 
@@ -37,7 +48,7 @@ constexpr int kPrKeys = 128;              // keys of a unit
 constexpr int kPrHalf = 64;               // and of a half of it: scores are made and used by halves
 constexpr int kPrStages = 2;              // units of unpacked keys, and of values, in shared memory
 constexpr int kPrMinUnits = 8;            // units of a CTA, at least
-constexpr int kPrSetup = 4;               // what an item costs beyond its units, in units: queries in, output out
+constexpr int kPrSetup = 4;               // what an item costs beyond its units, in units
 
 __device__ unsigned int g_kv_wait_timeouts = 0;
 
@@ -732,7 +743,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     cp_wait<0>();                                    // no copy outlives its warp
   } else {
     // ================= two warps issue the products, one for each 128 rows =================
-    // Issuing blocks while the tensor cores are busy and a wait costs a hundred
+    // Issuing blocks while the tensor cores are busy, and a wait costs about 80
     // clocks even where nothing is waited for; with a warp each, one side's waits
     // pass while the other's products run.  The whole warp goes through the
     // loop, so that addresses and descriptors stay in uniform registers; one
