@@ -13,9 +13,9 @@
 // score products at two thirds of that: 64 keys wide, they are fed at the
 // shared memory's 128 bytes a clock), 1024 of the exponentials, and 11.5 K
 // warp instructions, 2900 clocks of the SM's four schedulers; measured are
-// 4200.  2048 queries after 14336 tokens, 32 heads over 8: 453 us, 1138
-// TFLOP/s, 0.59 of the measured bf16 rate; at D = 64, where the exponentials
-// and the instructions are the same and the products half, 416 us.
+// 4100.  2048 queries after 14336 tokens, 32 heads over 8: 440 us, 1171
+// TFLOP/s, 0.61 of the measured bf16 rate; at D = 64, where the exponentials
+// and the instructions are the same and the products half, about a tenth less.
 //
 // Layout: one CTA per SM.  Two warpgroups hold the softmax of 128 rows each
 // (rows are query tokens times the heads that share a key/value head, one row
@@ -49,6 +49,12 @@ constexpr int kPrHalf = 64;               // and of a half of it: scores are mad
 constexpr int kPrStages = 2;              // units of unpacked keys, and of values, in shared memory
 constexpr int kPrMinUnits = 8;            // units of a CTA, at least
 constexpr int kPrSetup = 4;               // what an item costs beyond its units, in units
+
+// Registers a thread: what a launch gives (__launch_bounds__ of 640 threads),
+// and the roles' shares of it.  setmaxnreg waits for registers, so shares
+// beyond the launch's would wait forever.
+constexpr int kPrRegs = 96, kSoftmaxRegs = 144, kUnpackRegs = 64, kIssueRegs = 64;
+static_assert(256 * kSoftmaxRegs + 256 * kUnpackRegs + 128 * kIssueRegs <= kPrThreads * kPrRegs, "register shares");
 
 __device__ unsigned int g_kv_wait_timeouts = 0;
 
@@ -289,16 +295,16 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
   };
 
   // Every wait is bounded; a role whose wait runs out counts it and returns,
-  // and so do the others in turn, to the common end.
-  auto wait1 = [&](uint64_t* bar, uint32_t parity) {             // one thread
+  // and so do the others in turn, to the common end.  A warp's lanes wait as
+  // one (they come converged, and try, read the clock and leave by the same
+  // instructions), so that they need no vote on the outcome: with one, which
+  // costs every wait some 30 clocks, the 2048-query chunk takes 455 us and
+  // not 441.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_wait_lean(bar, parity & 1)) return true;
     atomicAdd(&g_kv_wait_timeouts, 1u);
     return false;
   };
-  auto wait = [&](uint64_t* bar, uint32_t parity) {              // a whole warp: one answer for all its lanes
-    return __all_sync(0xFFFFFFFFu, wait1(bar, parity)) != 0;
-  };
-
   auto arrive = [&](uint64_t* bar) {                             // of a whole warp, as one
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -306,7 +312,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
 
   if (wg < 2) {
     // ================= softmax of 128 rows, one per thread =================
-    regs_inc<144>();
+    regs_inc<kSoftmaxRegs>();
     [&]() {
       const int rl = threadIdx.x & 127;              // row within the warpgroup, tensor-memory lane
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -606,7 +612,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     }();
   } else if (wg < 4) {
     // ================= unpacking keys and values =================
-    regs_dec<64>();
+    regs_dec<kUnpackRegs>();
     [&]() {
       const bool values = wg == 3;                   // a warpgroup for keys, one for values
       const int grp = warp & 3;                      // tokens 32 grp .. + 31 of a unit
@@ -748,7 +754,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     // pass while the other's products run.  The whole warp goes through the
     // loop, so that addresses and descriptors stay in uniform registers; one
     // elected lane issues.
-    regs_dec<64>();
+    regs_dec<kIssueRegs>();
     if (warp < kPrIssuer + 2) {
       [&]() {
         constexpr uint32_t kQK = f16_idesc(128, kPrHalf, false), kPV = f16_idesc(128, D, true);
@@ -852,6 +858,11 @@ static int pr_grid(const KvShape& s, int group, int batch, int64_t total_q, int 
   return (int)(n < kMaxGrid ? n : kMaxGrid);
 }
 
+static bool pr_regs_ok(const void* kernel) {
+  cudaFuncAttributes f;
+  return cudaFuncGetAttributes(&f, kernel) == cudaSuccess && f.numRegs >= kPrRegs;
+}
+
 static int64_t pr_bytes(int grid, int dim) {
   return grid < 2 ? 0 : kMaxGrid * 4 + (int64_t)grid * 2 * kPrRows * (dim + 2) * 4;
 }
@@ -873,6 +884,10 @@ cudaError_t launch_kv_prompt(const KvAttn& a, const KvWork& w, int sms, cudaStre
   if (e != cudaSuccess) return e;
   *status = w.check(pr_bytes(grid, a.shape.dim));
   if (*status != FP8Q_OK) return cudaSuccess;
+  // built with fewer registers than the shares count on, it is not launched
+  static const bool regs64 = pr_regs_ok(reinterpret_cast<const void*>(kv_prompt_kernel<64>));
+  static const bool regs128 = pr_regs_ok(reinterpret_cast<const void*>(kv_prompt_kernel<128>));
+  if (!(a.shape.dim == 128 ? regs128 : regs64)) return cudaErrorInvalidKernelImage;
   PrPlan plan = {w.tickets(), w.parts()};
   void* args[2] = {const_cast<KvAttn*>(&a), &plan};
   return launch_dependent(k, dim3(grid), kPrThreads, smem, args, st, launches);
