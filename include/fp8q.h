@@ -384,7 +384,7 @@ FP8Q_API int fp8q_error_stats_noalloc(const void* x, int dtype, int64_t n, const
  *   k_e8m0, v_e8m0    [num_pages, kv_heads, page_size, head_dim / 32]
  * Slot s is token s % page_size of page s / page_size.  page_size is a power
  * of two (1 .. 2^20), kv_heads 1 .. MX_KV_MAX_HEADS, head_dim a multiple of
- * 32 up to 256.  The struct itself is host memory, read during the call. */
+ * 32 up to 256, kv_heads * page_size below 2^31.  The struct itself is host memory, read during the call. */
 #define MX_KV_MAX_HEADS 4096
 typedef struct mx_kv_cache {
   uint8_t* k_q;

@@ -17,12 +17,15 @@ static int check_cache(const mx_kv_cache* c, KvShape* s) {
     return FP8Q_EINVAL;
   if (c->page_size < 1 || c->page_size > (1 << 20) || (c->page_size & (c->page_size - 1)) != 0) return FP8Q_EINVAL;
   if (c->num_pages < 0 || c->num_pages > 0x7FFFFFFF) return FP8Q_EINVAL;
+  if ((int64_t)c->kv_heads * c->page_size > 0x7FFFFFFF) return FP8Q_EINVAL;
   if (c->num_pages > 0 && (!c->k_q || !c->k_e8m0 || !c->v_q || !c->v_e8m0)) return FP8Q_EINVAL;
   if (!kv_aligned16(c->k_q) || !kv_aligned16(c->k_e8m0) || !kv_aligned16(c->v_q) || !kv_aligned16(c->v_e8m0))
     return FP8Q_EALIGN;
   s->page_shift = 0;
   while ((1 << s->page_shift) < c->page_size) ++s->page_shift;
   s->slots = c->num_pages << s->page_shift;
+  s->pages = (int32_t)c->num_pages;
+  s->page_rows = (uint32_t)(c->kv_heads * c->page_size);
   s->heads = c->kv_heads;
   s->dim = c->head_dim;
   return FP8Q_OK;

@@ -13,19 +13,19 @@
 // tile), which is when the sums are rescaled.
 //
 // What bounds it: HBM and the unpacking together.  A token and head at D = 128
-// is 136 bytes of cache, and a tile of 32 of them 590 warp instructions for up
-// to eight query rows, a fifth of them the conversions of the 8192 codes.  8
-// sequences of 131072 tokens, 32 heads over 8: 229 us, 5.0 TB/s, 0.75 of the
+// is 136 bytes of cache, and a tile of 32 of them 554 warp instructions for up
+// to eight query rows, a quarter of them the conversions of the 8192 codes.  8
+// sequences of 131072 tokens, 32 heads over 8: 224 us, 5.1 TB/s, 0.76 of the
 // measured copy rate (the same copies without the arithmetic: 180 us; ALU pipe
-// 58%, issue slots 57%, DRAM reads 1.00 of the cache's bytes); half as wide
+// 55%, issue slots 55%, DRAM reads 1.00 of the cache's bytes); half as wide
 // rows (D = 64, the same softmax for half the bytes) 158 us.  mma.sync and not
-// tcgen05: with 16 tokens x 8 query rows a product it takes 1 of the 18
+// tcgen05: with 16 tokens x 8 query rows a product it takes 1 of the 17
 // instructions of a token, its operands come straight from the unpacked
 // registers, and nothing waits on a tensor-memory round trip.
 //
 // Layout.  A warp owns tiles of 32 tokens, copied by cp.async into a ring of
 // its own (no CTA barrier while it streams; four stages at three CTAs per SM
-// 229 us, three stages at four CTAs 233).  Keys are the A operand (16 tokens x
+// took 229 us when three stages at four CTAs took 233).  Keys are the A operand (16 tokens x
 // 16 columns, the columns of a block permuted alike in q so that a lane's
 // 32-bit word of codes is one lane's share of two products); values are the A
 // operand of the transposed product (16 columns x 16 tokens), read by
@@ -218,16 +218,16 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
     auto issue = [&](int k, int st, int page) {
       if (k < n_mine) {
         const int at = tile0_at + k * (kDecWarps * kTile), tok = at + (runs ? 0 : lane);
-        const int64_t slot = ((int64_t)page << a.shape.page_shift) + (tok & page_mask);
-        const bool ok = page >= 0 && slot < a.shape.slots;
-        const int64_t row = ok ? kv_row(a.shape, slot, head) : 0;
+        const bool ok = (uint32_t)page < (uint32_t)a.shape.pages;
+        const int64_t row = ok ? kv_row(a.shape, page, tok & page_mask, head) : 0;
         const uint32_t kd = smem_u32(sm.stage[st].k), vd = smem_u32(sm.stage[st].v);
         const uint32_t ke = smem_u32(sm.stage[st].ke), ve = smem_u32(sm.stage[st].ve);
         uint32_t valid;
         if (runs) {
-          valid = ok ? low_bits(sq.len - at) : 0u;
-          copy_run<D, false>(kd, ke, a.k, row, valid);
-          copy_run<D, true>(vd, ve, a.v, row, valid);
+          const int n = ok ? min(sq.len - at, 32) : 0;
+          valid = low_bits(n);
+          copy_run<D, false>(kd, ke, a.k, row, n);
+          copy_run<D, true>(vd, ve, a.v, row, n);
         } else {
           valid = __ballot_sync(0xFFFFFFFFu, ok);
           copy_rows<D, false>(kd, ke, a.k, row, valid, a.shape.page_shift);

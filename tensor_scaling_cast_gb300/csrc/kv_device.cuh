@@ -63,15 +63,16 @@ struct KvPool {
 
 struct KvShape {
   int64_t slots;        // num_pages * page_size
+  int32_t pages;
+  uint32_t page_rows;   // rows of a page, all heads: heads * page_size < 2^31
   int32_t page_shift;   // log2(page_size)
   int32_t heads, dim;
 };
 
-// Row index of (slot, head): the codes of a row start at row * row bytes, its
-// E8M0 bytes at row * (dim / 32).
-__device__ __forceinline__ int64_t kv_row(const KvShape& s, int64_t slot, int head) {
-  const int64_t page = slot >> s.page_shift, off = slot & ((1ll << s.page_shift) - 1);
-  return (((page * s.heads + head) << s.page_shift) + off);
+// Row index of a page's off-th token for a head: the codes of a row start at
+// row * row bytes, its E8M0 bytes at row * (dim / 32).
+__device__ __forceinline__ int64_t kv_row(const KvShape& s, int page, int off, int head) {
+  return (int64_t)((uint64_t)(uint32_t)page * s.page_rows) + (((int64_t)head << s.page_shift) + off);
 }
 
 // 2^(byte - 127) of an E8M0 byte as fp32; 0xFF is NaN.
@@ -166,17 +167,13 @@ __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+// 16 (4) bytes into shared memory, asynchronously; zeros past the first
+// `bytes` of them, which alone are read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -193,36 +190,37 @@ __device__ __forceinline__ uint32_t code_offset(int r, int c) {
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
 
 // This warp's copy of the codes and scales of 32 cached rows into shared
-// memory, asynchronously; bit t of valid says whether token t exists (else
-// zeros are written).  SWAP: token t's codes go to row t with bits 0 and 3
+// memory, asynchronously; zeros are written for tokens that do not exist.  SWAP: token t's codes go to row t with bits 0 and 3
 // exchanged (see the decode kernel's values).  One run of rows from `row` on
-// (pages of 32 tokens or more: tiles start at multiples of 32):
+// (pages of 32 tokens or more: tiles start at multiples of 32), the first n of
+// which exist:
 template <bool SWAP>
 __device__ __forceinline__ int tile_row(int t) {
   return SWAP ? (t & ~9) | ((t >> 3) & 1) | ((t & 1) << 3) : t;
 }
 template <int D, bool SWAP>
-__device__ __forceinline__ void copy_run(uint32_t codes, uint32_t scales, const KvPool& pool, int64_t row, uint32_t valid) {
+__device__ __forceinline__ void copy_run(uint32_t codes, uint32_t scales, const KvPool& pool, int64_t row, int n) {
   constexpr int RB = D / 2, NB = D / 32, CH = RB / 16;
   const int lane = threadIdx.x & 31;
   const uint8_t* src = pool.q + row * RB + lane * 16;       // chunk `lane` and every 32nd from there
   const uint8_t* es = pool.e8m0 + row * NB + lane * 4;
-  if (valid == 0xFFFFFFFFu) {
+  if (n == 32) {
 #pragma unroll
     for (int x = 0; x < CH; ++x)
-      cp_async16(codes + code_offset<D>(tile_row<SWAP>(x * (32 / CH) + lane / CH), lane % CH), src + x * 512);
-    if (D == 128 || lane < 16) cp_async4(scales + lane * 4, es);
-    return;
+      cp_async16(codes + code_offset<D>(tile_row<SWAP>(x * (32 / CH) + lane / CH), lane % CH), src + x * 512, 16);
+    if (D == 128 || lane < 16) cp_async4(scales + lane * 4, es, 4);
+  } else {
+    // rolled up: a branch, and not both sides' instructions under predicates
+#pragma unroll 1
+    for (int x = 0; x < CH; ++x) {
+      const int r = x * (32 / CH) + lane / CH;
+      cp_async16(codes + code_offset<D>(tile_row<SWAP>(r), lane % CH), src + x * 512, r < n ? 16 : 0);
+    }
+    if (D == 128 || lane < 16) cp_async4(scales + lane * 4, es, lane * (D == 128 ? 1 : 2) < n ? 4 : 0);
   }
-#pragma unroll
-  for (int x = 0; x < CH; ++x) {
-    const int r = x * (32 / CH) + lane / CH;
-    cp_async16(codes + code_offset<D>(tile_row<SWAP>(r), lane % CH), src + x * 512, (valid >> r) & 1);
-  }
-  if (D == 128) cp_async4(scales + lane * 4, es, (valid >> lane) & 1);
-  else if (lane < 16) cp_async4(scales + lane * 4, es, (valid >> (2 * lane)) & 1);
 }
-// Or any rows, `row` being that of the lane's token (smaller pages).
+// Or any rows, `row` being that of the lane's token (smaller pages), bit t of
+// valid saying whether token t exists.
 template <int D, bool SWAP>
 __device__ __forceinline__ void copy_rows(uint32_t codes, uint32_t scales, const KvPool& pool, int64_t row,
                                           uint32_t valid, int page_shift) {
@@ -232,13 +230,13 @@ __device__ __forceinline__ void copy_rows(uint32_t codes, uint32_t scales, const
   for (int x = 0; x < CH; ++x) {
     const int r = x * (32 / CH) + lane / CH, c = lane % CH;
     const int64_t rr = __shfl_sync(0xFFFFFFFFu, row, r);
-    cp_async16(codes + code_offset<D>(tile_row<SWAP>(r), c), pool.q + rr * RB + c * 16, (valid >> r) & 1);
+    cp_async16(codes + code_offset<D>(tile_row<SWAP>(r), c), pool.q + rr * RB + c * 16, (valid >> r) & 1 ? 16 : 0);
   }
   const bool ok = (valid >> lane) & 1;
   if (D == 128) {
-    cp_async4(scales + lane * 4, pool.e8m0 + row * 4, ok);
+    cp_async4(scales + lane * 4, pool.e8m0 + row * 4, ok ? 4 : 0);
   } else if (page_shift > 0) {           // two tokens' scales are one word, the even one's row even
-    if (!(lane & 1)) cp_async4(scales + lane * 2, pool.e8m0 + row * 2, ok);
+    if (!(lane & 1)) cp_async4(scales + lane * 2, pool.e8m0 + row * 2, ok ? 4 : 0);
   } else {
     const uint16_t e = ok ? *reinterpret_cast<const uint16_t*>(pool.e8m0 + row * 2) : 0;
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(scales + lane * 2), "h"(e) : "memory");

@@ -637,13 +637,13 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
       // starts the copy of this warp's rows of the unit; gives the mask of those that exist
       auto fetch = [&](int page) {
         const int at = (it.tile0 + u) * kPrKeys + grp * 32, tok = at + (runs ? 0 : lane);
-        const int64_t slot = ((int64_t)page << a.shape.page_shift) + (tok & page_mask);
-        const bool ok = page >= 0 && slot < a.shape.slots;
-        const int64_t row = ok ? kv_row(a.shape, slot, it.head) : 0;
+        const bool ok = (uint32_t)page < (uint32_t)a.shape.pages;
+        const int64_t row = ok ? kv_row(a.shape, page, tok & page_mask, it.head) : 0;
         uint32_t there;
         if (runs) {
-          there = ok ? low_bits(it.sq.len - at) : 0u;
-          copy_run<D, false>(smem_addr(raw.codes), smem_addr(raw.scales), pool, row, there);
+          const int n = ok ? min(it.sq.len - at, 32) : 0;
+          there = low_bits(n);
+          copy_run<D, false>(smem_addr(raw.codes), smem_addr(raw.scales), pool, row, n);
         } else {
           there = __ballot_sync(0xFFFFFFFFu, ok);
           copy_rows<D, false>(smem_addr(raw.codes), smem_addr(raw.scales), pool, row, there, a.shape.page_shift);
