@@ -363,7 +363,7 @@ class MXKVCache:
         self._struct = _KVCacheStruct(k_q.data_ptr(), k_e8m0.data_ptr(), v_q.data_ptr(), v_e8m0.data_ptr(),
                                       pages, page, heads, dim, fmt)
         self._ref = ctypes.addressof(self._struct)
-        self._tail, self._scale = torch.Size((heads, dim)), dim ** -0.5
+        self._scale = dim ** -0.5
 
     @classmethod
     def allocate(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int = E2M1,
@@ -379,11 +379,12 @@ class MXKVCache:
 def _kv_pair(cache, k, v, slots, what):
     """(tokens, dtype code, strides of k and v) of a write's or read's rows."""
     shape, ks, vs, dtype = k.shape, k.stride(), v.stride(), k.dtype
-    if (shape != v.shape or shape[1:] != cache._tail or ks[2] != 1 or vs[2] != 1 or v.dtype is not dtype
-            or slots.dtype is not torch.int64 or slots.shape != shape[:1] or not slots.is_contiguous()):
+    if (len(ks) != 3 or shape != v.shape or shape[2] != cache.head_dim or shape[1] != cache.kv_heads
+            or ks[2] != 1 or vs[2] != 1 or v.dtype is not dtype or slots.dtype is not torch.int64
+            or slots.numel() != shape[0] or not slots.is_contiguous()):
         raise TypeError(f"{what}: k and v alike, [tokens, {cache.kv_heads}, {cache.head_dim}] with consecutive "
-                        f"elements, and contiguous int64 slots [tokens]: got {tuple(shape)}, {tuple(v.shape)} "
-                        f"with strides {ks}, {vs}, slots {slots.dtype} {tuple(slots.shape)}")
+                        f"elements, and contiguous int64 slots, one per token: got {tuple(shape)}, "
+                        f"{tuple(v.shape)} with strides {ks}, {vs}, slots {slots.dtype} {tuple(slots.shape)}")
     return shape[0], BF16 if dtype is torch.bfloat16 else _dtype(k), ks, vs
 
 
@@ -440,7 +441,7 @@ def mx_kv_attention(cache: MXKVCache, q: torch.Tensor, out: torch.Tensor, page_t
         raise TypeError(f"mx_kv_attention: q and out are bf16 [total_q, q_heads, {cache.head_dim}] with consecutive "
                         f"elements: got {q.dtype} {tuple(shape)}, {out.dtype} {tuple(out.shape)}, strides {qs}, {os_}")
     if (page_table.dtype is not torch.int32 or len(table) != 2 or (ts[1] != 1 and table[1] > 1)
-            or kv_lens.dtype is not torch.int32 or kv_lens.shape != table[:1] or not kv_lens.is_contiguous()
+            or kv_lens.dtype is not torch.int32 or kv_lens.numel() != table[0] or not kv_lens.is_contiguous()
             or (cu_q is not None and (cu_q.dtype is not torch.int32 or cu_q.numel() != table[0] + 1
                                       or not cu_q.is_contiguous()))
             or (lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2]
