@@ -13,8 +13,8 @@
 // score products at two thirds of that: 64 keys wide, they are fed at the
 // shared memory's 128 bytes a clock), 1024 of the exponentials, and 11.5 K
 // warp instructions, 2900 clocks of the SM's four schedulers; measured are
-// 4100.  2048 queries after 14336 tokens, 32 heads over 8: 440 us, 1171
-// TFLOP/s, 0.61 of the measured bf16 rate; at D = 64, where the exponentials
+// 4100.  2048 queries after 14336 tokens, 32 heads over 8: 435 us, 1184
+// TFLOP/s, 0.62 of the measured bf16 rate; at D = 64, where the exponentials
 // and the instructions are the same and the products half, about a tenth less.
 //
 // Layout: one CTA per SM.  Two warpgroups hold the softmax of 128 rows each
@@ -129,6 +129,14 @@ struct PrPlan {
   float* part;             // [2 * grid][kPrRows * (D + 2)]
 };
 
+// a / b of values that are not negative, in 32 bits where both fit (they do in
+// all but the largest calls): four divisions per CTA and join, and the prompt
+// of 2048 takes 435 us against 440 with 64-bit ones.  The decode kernel gains
+// nothing from it and divides in 64 bits.
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -193,7 +201,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  const long long per = max((long long)kPrMinUnits, (total + gridDim.x - 1) / gridDim.x);
+  const long long per = max((long long)kPrMinUnits, div_pos(total + gridDim.x - 1, gridDim.x));
   const long long begin = (long long)blockIdx.x * per, end = min(total, begin + per);
   if (begin >= end) return;
   if (threadIdx.x == 0) {
@@ -248,7 +256,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     x.sq = kv_seq(a, x.b);
     pr_set(a, x);
     const long long u = seq_units(x.sq);
-    x.head = (int)((begin - seg0) / u);
+    x.head = (int)div_pos(begin - seg0, u);
     seg0 += x.head * u;
     // the row tile that holds `begin`: 32 at a time
     for (x.rt = 0;; x.rt += 32) {
@@ -551,7 +559,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           tmem_fence_before();
         }
         if (!whole) {
-          const long long per = s_range[1], seg0 = s_range[0] + rel + kPrSetup, first = seg0 / per, last = (seg0 + it.n - 1) / per;
+          const long long per = s_range[1], seg0 = s_range[0] + rel + kPrSetup, first = div_pos(seg0, per), last = div_pos(seg0 + it.n - 1, per);
           __threadfence();
           arrive(&sm.join_all);
           if (warp == 0 && !wait(&sm.join_all, all_n)) return;
