@@ -276,9 +276,10 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
       const int e = m == 0 ? 0 : max(-112, (int)(m >> 23) - 127) - 14;   // q = q' * 2^e, e in [-126, 113]
-      const float s = pow2f(-e);
+      // NaN or Inf: every score of the row is NaN, but those the masks replace
+      // (a NaN factor would spoil them too: -inf times NaN)
+      const float s = m >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : pow2f(-e);
       f = fmaxf(a.scale * 1.4426950408889634f * pow2f(e), kMinFactor);
-      if (m >= 0x7F800000u) f = __uint_as_float(0x7FFFFFFFu);            // NaN or Inf: the row is NaN
 #pragma unroll
       for (int x = 0; x < NB; ++x) {
         const uint32_t ws[4] = {qw[0][x].x, qw[0][x].y, qw[0][x].z, qw[0][x].w};

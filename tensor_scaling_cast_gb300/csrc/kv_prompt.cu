@@ -362,9 +362,11 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
 #pragma unroll
               for (int y = 1; y < CPR; y <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, y));
               const int e = m == 0 ? 0 : max(-112, (int)(m >> 23) - 127) - 14;
-              const float s = pow2f(-e);
+              // 2^-e; NaN or Inf: every score of the row is NaN, but those the masks
+              // replace.  (Picked as bits: between floats, four ragged prompts take
+              // 269 us and not 260.)
+              const float s = __uint_as_float(m >= 0x7F800000u ? 0x7FFFFFFFu : (uint32_t)(127 - e) << 23);
               float f = a.scale * 1.4426950408889634f * pow2f(e);
-              if (m >= 0x7F800000u) f = __uint_as_float(0x7FFFFFFFu);    // NaN or Inf: the row is NaN
               f = __shfl_sync(0xFFFFFFFFu, f, (lane % RPI) * CPR);
               if (lane / RPI == x0 + x) f_row = f;
               uint4 h;

@@ -303,6 +303,32 @@ def test_attention_nan_stays_where_it_is_seen(nq):
     assert torch.equal(torch.isnan(out).cpu(), want)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("nq", [1, 4, 66])
+def test_attention_nan_queries_that_see_no_key_get_zeros(nq, bad):
+    """An empty sequence, more queries than keys, and a sequence whose only
+    page is outside the cache: NaN is for rows that see a key."""
+    heads, group, dim, page = 2, 2, 128, 64
+    lens = [0, nq // 2, 50]
+    cache = new_cache(2, page, heads, dim, kv.E2M1, fill=255)
+    k = torch.randn(page, heads, dim, generator=torch.Generator().manual_seed(nq))
+    F.mx_kv_write(cache, k.cuda(), k.cuda(), torch.arange(page, device="cuda"))
+    table = torch.tensor([[-1], [0], [2]], dtype=torch.int32, device="cuda")
+    q = torch.ones(3 * nq, heads * group, dim, dtype=torch.bfloat16)
+    q[:, 1:, 5] = bad
+    out = G.full((3 * nq, heads * group, dim), 3.0, torch.bfloat16)
+    lse = G.full((3 * nq, heads * group), 3.0, torch.float32)
+    cu = torch.arange(4, dtype=torch.int32, device="cuda") * nq
+    F.mx_kv_attention(cache, q.cuda(), out, table, torch.tensor(lens, dtype=torch.int32).cuda(), cu_q=cu, max_q=nq,
+                      lse=lse, workspace=F.mx_kv_attention_workspace(cache, q.cuda(), table, max_q=nq))
+    sees = torch.zeros(3 * nq, dtype=torch.bool)
+    sees[2 * nq - nq // 2:2 * nq] = True
+    out, lse = out.float().cpu(), lse.cpu()
+    assert (out[~sees] == 0).all() and (lse[~sees] == -float("inf")).all()
+    assert torch.isnan(out[sees][:, 1:]).all() and torch.isnan(lse[sees][:, 1:]).all()
+    assert torch.isfinite(out[sees][:, 0]).all()
+
+
 def test_attention_large_queries_and_zero_values():
     q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(1))
     attend_case([100, 30], [1, 1], 1, 4, 64, 16, q=(q * 1e20).bfloat16(), scale=1e-20, seed=8)
