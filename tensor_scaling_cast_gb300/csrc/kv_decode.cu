@@ -15,7 +15,7 @@
 // What bounds it: HBM and the unpacking together.  A token and head at D = 128
 // is 136 bytes of cache, and a tile of 32 of them 554 warp instructions for up
 // to eight query rows, a quarter of them the conversions of the 8192 codes.  8
-// sequences of 131072 tokens, 32 heads over 8: 224 us, 5.1 TB/s, 0.76 of the
+// sequences of 131072 tokens, 32 heads over 8: 219 us, 5.2 TB/s, 0.78 of the
 // measured copy rate (the same copies without the arithmetic: 180 us; ALU pipe
 // 55%, issue slots 55%, DRAM reads 1.00 of the cache's bytes); half as wide
 // rows (D = 64, the same softmax for half the bytes) 158 us.  mma.sync and not
@@ -37,9 +37,9 @@
 // Work is split over the tiles of all sequences and heads: CTA i takes
 // positions [i * per, (i + 1) * per) in (sequence, head) order, each of them
 // kDecSetup positions and its tiles, so that uneven lengths fill the GPU
-// evenly and the host needs to know none of them.  (Set-up of 12 against 5
-// tiles: 64 sequences of 512 tokens 14 us against 19; the default batch of 64
-// ragged ones 44 against 46.)  A (sequence, head) that spans several CTAs is
+// evenly and the host needs to know none of them.  (Set-up of 12 against 6
+// tiles: 64 sequences of 512 tokens 13.7 us against 17.7, 64 of up to 8192 42.3
+// against 44.5.)  A (sequence, head) that spans several CTAs is
 // joined by the last of them to arrive, in the order of the tiles (the result
 // does not depend on which that is).
 #include "kv_device.cuh"
@@ -196,71 +196,95 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
   // position of the first tile of (b, head): its cost lies from kDecSetup before
   long long seg0 = s_before + (long long)head * sq.cost + kDecSetup;
 
-  while (seg0 < end) {
-    // ---- one (sequence, head): tiles [t0, t1) of it
-    const int t0 = (int)max(0ll, begin - seg0), t1 = (int)min((long long)sq.tiles, end - seg0);
-    const int rows = sq.nq * a.group;
-    const int n_mine = t1 - t0 > warp ? (t1 - t0 - warp + kDecWarps - 1) / kDecWarps : 0;
+  if (seg0 >= end) return;                       // only the set-up of one: its tiles are the next CTA's
 
-    const int pos0 = sq.pos0;
-    const int32_t* table = a.table + b * a.table_stride;
-    // The warp's k-th tile begins at token tile0_at + k * (kDecWarps * kTile).
-    // Pages of 32 tokens or more hold all of a tile's rows in one run (229 us
-    // against 235 by rows, D = 128; 158 against 168 at D = 64); smaller ones are
-    // looked up by each lane for its own token (254 us at 16 tokens a page).
-    const int tile0_at = (sq.tile0 + t0 + warp) * kTile;
-    const bool runs = a.shape.page_shift >= 5;
-    auto page_of = [&](int k) {
-      const int tok = tile0_at + k * (kDecWarps * kTile) + (runs ? 0 : lane);
-      return k < n_mine && tok < sq.len ? table[tok >> a.shape.page_shift] : -1;
-    };
-    const int page_mask = (1 << a.shape.page_shift) - 1;
-    auto issue = [&](int k, int st, int page) {
-      if (k < n_mine) {
-        const int at = tile0_at + k * (kDecWarps * kTile), tok = at + (runs ? 0 : lane);
-        const bool ok = (uint32_t)page < (uint32_t)a.shape.pages;
-        const int64_t row = ok ? kv_row(a.shape, page, tok & page_mask, head) : 0;
-        const uint32_t kd = smem_u32(sm.stage[st].k), vd = smem_u32(sm.stage[st].v);
-        const uint32_t ke = smem_u32(sm.stage[st].ke), ve = smem_u32(sm.stage[st].ve);
-        uint32_t valid;
-        if (runs) {
-          const int n = ok ? min(sq.len - at, 32) : 0;
-          valid = low_bits(n);
-          copy_run<D, false>(kd, ke, a.k, row, n);
-          copy_run<D, true>(vd, ve, a.v, row, n);
-        } else {
-          valid = __ballot_sync(0xFFFFFFFFu, ok);
-          copy_rows<D, false>(kd, ke, a.k, row, valid, a.shape.page_shift);
-          copy_rows<D, true>(vd, ve, a.v, row, valid, a.shape.page_shift);
-        }
-        sm.valid[st] = valid;                    // the same from every lane
+  // ---- what is fetched: tiles [t0, t1) of the (sequence, head) at seg0
+  int t0, t1, n_mine, tile0_at;
+  const int32_t* table;
+  // The warp's k-th tile begins at token tile0_at + k * (kDecWarps * kTile).
+  // Pages of 32 tokens or more hold all of a tile's rows in one run (229 us
+  // against 235 by rows, D = 128; 158 against 168 at D = 64); smaller ones are
+  // looked up by each lane for its own token (254 us at 16 tokens a page).
+  const bool runs = a.shape.page_shift >= 5;
+  auto page_of = [&](int k) {
+    const int tok = tile0_at + k * (kDecWarps * kTile) + (runs ? 0 : lane);
+    return k < n_mine && tok < sq.len ? table[tok >> a.shape.page_shift] : -1;
+  };
+  const int page_mask = (1 << a.shape.page_shift) - 1;
+  auto issue = [&](int k, int st, int page) {
+    if (k < n_mine) {
+      const int at = tile0_at + k * (kDecWarps * kTile), tok = at + (runs ? 0 : lane);
+      const bool ok = (uint32_t)page < (uint32_t)a.shape.pages;
+      const int64_t row = ok ? kv_row(a.shape, page, tok & page_mask, head) : 0;
+      const uint32_t kd = smem_u32(sm.stage[st].k), vd = smem_u32(sm.stage[st].v);
+      const uint32_t ke = smem_u32(sm.stage[st].ke), ve = smem_u32(sm.stage[st].ve);
+      uint32_t valid;
+      if (runs) {
+        const int n = ok ? min(sq.len - at, 32) : 0;
+        valid = low_bits(n);
+        copy_run<D, false>(kd, ke, a.k, row, n);
+        copy_run<D, true>(vd, ve, a.v, row, n);
+      } else {
+        valid = __ballot_sync(0xFFFFFFFFu, ok);
+        copy_rows<D, false>(kd, ke, a.k, row, valid, a.shape.page_shift);
+        copy_rows<D, true>(vd, ve, a.v, row, valid, a.shape.page_shift);
       }
-      cp_commit();
-    };
-
-    // pages, queries and the first tiles are fetched side by side
-    int pages[kDecStages];
+      sm.valid[st] = valid;                    // the same from every lane
+    }
+    cp_commit();
+  };
+  int pages[kDecStages];
+  auto open = [&]() {
+    t0 = (int)max(0ll, begin - seg0);
+    t1 = (int)min((long long)sq.tiles, end - seg0);
+    n_mine = t1 - t0 > warp ? (t1 - t0 - warp + kDecWarps - 1) / kDecWarps : 0;
+    tile0_at = (sq.tile0 + t0 + warp) * kTile;
+    table = a.table + b * a.table_stride;
 #pragma unroll
     for (int k = 0; k < kDecStages; ++k) pages[k] = page_of(k);
-    // With one group of eight rows the queries stay in registers; with more
-    // each warp prepares some of the groups and all read them from shared
-    // memory, which leaves the registers to the sums (four groups over 8 x 131072
-    // tokens: 539 us against 681 from registers).
-    constexpr int QN = QS ? 1 : NT;              // groups of a warp at a time
-    uint4 qw[QN][NB];
-    auto load_q = [&](int nt, uint4 (&w)[NB]) {
-      const int r = nt * 8 + li;
-      const bool on = r < rows;
-      const int qi = on ? a.by_group.div(r) : 0, g = on ? r - qi * a.group : 0;
-      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)(sq.q0 + qi) * a.q_tok +
-                               (int64_t)(head * a.group + g) * a.q_head + lc * 8;
+  };
+  // With one group of eight rows the queries stay in registers; with more
+  // each warp prepares some of the groups and all read them from shared
+  // memory, which leaves the registers to the sums (four groups over 8 x 131072
+  // tokens: 539 us against 681 from registers).
+  constexpr int QN = QS ? 1 : NT;              // groups of a warp at a time
+  uint4 qw[QN][NB];
+  auto load_q = [&]() {
+    if (QS && warp >= NT) return;
+    const int r = (QS ? warp : 0) * 8 + li;
+    const bool on = r < sq.nq * a.group;
+    const int qi = on ? a.by_group.div(r) : 0, g = on ? r - qi * a.group : 0;
+    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)(sq.q0 + qi) * a.q_tok +
+                             (int64_t)(head * a.group + g) * a.q_head + lc * 8;
 #pragma unroll
-      for (int x = 0; x < NB; ++x) w[x] = on ? *reinterpret_cast<const uint4*>(q + x * 32) : make_uint4(0, 0, 0, 0);
-    };
-    if (!QS) load_q(0, qw[0]);
-    else if (warp < NT) load_q(warp, qw[0]);
+    for (int x = 0; x < NB; ++x) qw[0][x] = on ? *reinterpret_cast<const uint4*>(q + x * 32) : make_uint4(0, 0, 0, 0);
+  };
+  // The join takes a warp's last NT stages, so that with one group of rows the
+  // queries and the first EARLY tiles of the next (sequence, head) are on their
+  // way meanwhile: 8 x 131072 tokens 219 us against 223, 64 sequences of up to
+  // 8192 42.3 against 43.4.  With more groups the registers for it are missing
+  // (five queries of four heads over a 4096 window 26.5 us with it, 25.8 without).
+  constexpr int EARLY = kDecStages - NT;
+  static_assert(ROWS * (D + 2) * 4 <= NT * (int)sizeof(typename Smem::Stage) && EARLY >= 0, "the join's place");
+  constexpr bool AHEAD = NT == 1;
+  auto fetch = [&]() {
+    load_q();
 #pragma unroll
-    for (int k = 0; k < kDecStages - 1; ++k) issue(k, k, pages[k]);
+    for (int k = 0; k < EARLY; ++k) issue(k, k, pages[k]);
+  };
+  open();
+  fetch();
+
+  while (true) {
+    // ---- one (sequence, head)
+    const DecSeq cur = sq;
+    const int cur_head = head;
+    const long long cur_seg0 = seg0;
+    const int rows = cur.nq * a.group, pos0 = cur.pos0;
+    const bool whole = t0 == 0 && t1 == cur.tiles;
+    const int first_tile = cur.tile0 + t0 + warp;
+#pragma unroll
+    for (int k = EARLY; k < kDecStages - 1; ++k) issue(k, k, pages[k]);
     int page_next = pages[kDecStages - 1];
 
     // ---- queries: f16, each row scaled by a power of two to a largest
@@ -320,7 +344,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       __syncwarp();
       const typename Smem::Stage& tile = sm.stage[st];
       const uint32_t valid = sm.valid[st];
-      const int tok = (sq.tile0 + t0 + warp + k * kDecWarps) * kTile;
+      const int tok = (first_tile + k * kDecWarps) * kTile;
 
       // ---- value scales: one token per lane, relative to the tile's largest
       float rv, unscale;
@@ -419,7 +443,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
 
       // ---- masks, only where the tile has any
       const bool edge = valid != 0xFFFFFFFFu || tok + kTile - 1 > pos0 ||
-                        (a.window > 0 && tok <= pos0 + sq.nq - 1 - a.window);
+                        (a.window > 0 && tok <= pos0 + cur.nq - 1 - a.window);
       if (edge) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -538,6 +562,18 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       page_next = page_of(k + kDecStages);
     }
 
+    // ---- the next (sequence, head): its pages
+    seg0 += sq.cost;
+    const bool more = seg0 < end;
+    if (++head == a.shape.heads) {
+      head = 0;
+      if (more) {                                // then there is one
+        do sq = dec_seq(a, ++b);
+        while (sq.tiles == 0);
+      }
+    }
+    if (AHEAD && more) open();
+
     // ---- join the warps: sums of a row over its lanes, then over the warps
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -555,9 +591,10 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
             if ((nan_blocks >> (x * 8 + nt * 2 + (y & 1))) & 1)
               o[nt][x][0][y] = o[nt][x][1][y] = __uint_as_float(0x7FFFFFFFu);
     }
-    cp_wait<0>();
-    __syncthreads();                             // the rings are free
-    float* so = reinterpret_cast<float*>(smem_raw) + warp * ROWS * (D + 2);   // [rows][D], then M, then l
+    auto warp_part = [&](int i) {                // [rows][D], then M, then l
+      return reinterpret_cast<const float*>(&reinterpret_cast<typename Smem::Warp*>(smem_raw)[i].stage[EARLY]);
+    };
+    float* so = const_cast<float*>(warp_part(warp));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -576,11 +613,11 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
           so[ROWS * D + ROWS + r] = l[nt][y];
         }
       }
+    if (AHEAD && more) fetch();
     __syncthreads();
 
     // Each thread has the same four columns of U rows, of the warps' sums
     // first and of the CTAs' parts where there are several.
-    const bool whole = t0 == 0 && t1 == sq.tiles;
     constexpr int PART = ROWS * (D + 2), U = ROWS * (D / 4) / kDecThreads, STEP = kDecThreads / (D / 4);
     constexpr int PER_ROW = NT == 1 ? 16 : NT == 2 ? 8 : 4;     // threads that find a row's reference
     const int r0 = threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
@@ -598,7 +635,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
           dst[ROWS * D + ROWS + r] = j.l;
         } else {
           const int qi = a.by_group.div(r);
-          store_lse(a, sq.q0 + qi, head * a.group + r - qi * a.group, j.m, j.l);
+          store_lse(a, cur.q0 + qi, cur_head * a.group + r - qi * a.group, j.m, j.l);
         }
       }
       __syncthreads();
@@ -618,19 +655,17 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
           *reinterpret_cast<float4*>(dst + rs[x] * D + c * 4) = v[x];
         } else {
           const int qi = a.by_group.div(rs[x]);
-          store_columns(a, sq.q0 + qi, head * a.group + rs[x] - qi * a.group, c, v[x], s_rows[rs[x]].l);
+          store_columns(a, cur.q0 + qi, cur_head * a.group + rs[x] - qi * a.group, c, v[x], s_rows[rs[x]].l);
         }
       }
     };
-    const float* src = reinterpret_cast<const float*>(smem_raw);
-    auto warp_part = [&](int i) { return src + i * PART; };
     if (whole) {
       join(warp_part, kDecWarps, nullptr);
     } else {
       // parts of this (sequence, head): CTAs first .. last; a CTA's slot is 0
       // where the (sequence, head) covers the start of its range, else 1
-      const long long first = seg0 / per, last = (seg0 + sq.tiles - 1) / per;
-      join(warp_part, kDecWarps, plan.part + (2 * (long long)blockIdx.x + (seg0 <= begin ? 0 : 1)) * PART);
+      const long long first = cur_seg0 / per, last = (cur_seg0 + cur.tiles - 1) / per;
+      join(warp_part, kDecWarps, plan.part + (2 * (long long)blockIdx.x + (cur_seg0 <= begin ? 0 : 1)) * PART);
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -644,20 +679,15 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
         __threadfence();
         join([&](int i) {
           const long long x = first + i;
-          return static_cast<const float*>(plan.part) + (2 * x + (seg0 <= x * per ? 0 : 1)) * PART;
+          return static_cast<const float*>(plan.part) + (2 * x + (cur_seg0 <= x * per ? 0 : 1)) * PART;
         }, (int)(last - first) + 1, nullptr);
       }
     }
+    if (!more) break;
     __syncthreads();
-
-    // ---- the next (sequence, head)
-    seg0 += sq.cost;
-    if (++head == a.shape.heads) {
-      head = 0;
-      if (seg0 < end) {                          // then there is one
-        do sq = dec_seq(a, ++b);
-        while (sq.tiles == 0);
-      }
+    if (!AHEAD) {
+      open();
+      fetch();
     }
   }
 }
