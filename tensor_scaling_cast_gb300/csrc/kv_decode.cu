@@ -13,11 +13,11 @@
 // tile), which is when the sums are rescaled.
 //
 // What bounds it: HBM and the unpacking together.  A token and head at D = 128
-// is 136 bytes of cache, and a tile of 32 of them 554 warp instructions for up
+// is 136 bytes of cache, and a tile of 32 of them 559 warp instructions for up
 // to eight query rows, a quarter of them the conversions of the 8192 codes.  8
 // sequences of 131072 tokens, 32 heads over 8: 219 us, 5.2 TB/s, 0.78 of the
 // measured copy rate (the same copies without the arithmetic: 180 us; ALU pipe
-// 55%, issue slots 55%, DRAM reads 1.00 of the cache's bytes); half as wide
+// 56%, issue slots 56%, DRAM reads 1.00 of the cache's bytes); half as wide
 // rows (D = 64, the same softmax for half the bytes) 158 us.  mma.sync and not
 // tcgen05: with 16 tokens x 8 query rows a product it takes 1 of the 17
 // instructions of a token, its operands come straight from the unpacked
