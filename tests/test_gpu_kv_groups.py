@@ -1,0 +1,192 @@
+"""Attention over the 4-bit cache where neighbouring groups of 32 tokens have
+different scales, and where a CTA goes from one (sequence, head) to the next:
+every row and column against the formula in 64 bits, within a bound per column
+that follows from the kernels' roundings."""
+import numpy as np
+import pytest
+import torch
+
+from canary import Guards
+from tensor_scaling_cast_gb300 import fp8q as F
+
+pytestmark = pytest.mark.gpu
+
+G = Guards(seed=0x47)
+GROUP = 32                                # tokens whose largest value scale is R
+MIN_R, MAX_R = -80, 126                   # where R is held
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.fail("a CUDA GPU is required for the gpu tests")
+    from tensor_scaling_cast_gb300 import build
+    build.build()
+    F.load()
+    torch.cuda.set_device(0)
+
+
+@pytest.fixture(autouse=True)
+def _guards():
+    G.release()
+    yield
+    G.check_and_release("at the end of the test")
+    assert F.fp8q_pipeline_status() == 0
+
+
+def values(codes, e8):
+    """E2M1 codes [.., D / 2] and E8M0 bytes [.., D / 32] -> 64-bit values."""
+    one = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device=codes.device)
+    table = torch.cat([one, -one])
+    v = torch.stack([table[(codes & 15).long()], table[(codes >> 4).long()]], -1).flatten(-2)
+    scale = torch.exp2(e8.double() - 127).masked_fill(e8 == 255, torch.nan)
+    return v * scale.repeat_interleave(32, -1)
+
+
+class Batch:
+    """Sequences of random codes in the pages of one cache.  Scales are 2^(a
+    whole number up to `apart` either way) per sequence, head and group of 32
+    tokens, times 2^(up to 1 either way) per block; everything that belongs to
+    no sequence holds 0xFF bytes."""
+
+    def __init__(self, lens, heads, dim, page, seed, k_apart=1, v_apart=6):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.lens, self.heads, self.dim, self.page = lens, heads, dim, page
+        per = [-(-n // page) for n in lens]
+        pages, width = sum(per) + 2, max(1, max(per))
+        shape, scales = (pages, heads, page, dim // 2), (pages, heads, page, dim // 32)
+        arrays = [torch.full(s, 255, dtype=torch.uint8, device="cuda") for s in (shape, scales, shape, scales)]
+        order = torch.randperm(pages, generator=g, device="cuda").int()
+        self.table = torch.full((len(lens), width), -7, dtype=torch.int32, device="cuda")
+        self.rows, at = [], 0
+        for b, n in enumerate(lens):
+            self.table[b, :per[b]] = order[at:at + per[b]]
+            at += per[b]
+            one = []
+            for a, apart in enumerate((k_apart, v_apart)):
+                codes = torch.randint(0, 256, (n, heads, dim // 2), generator=g, device="cuda", dtype=torch.uint8)
+                e8 = torch.randint(-1, 2, (n, heads, dim // 32), generator=g, device="cuda") + 127 - 2
+                shift = torch.randint(-apart, apart + 1, (-(-n // GROUP), heads, 1), generator=g, device="cuda")
+                one += [codes, (e8 + shift.repeat_interleave(GROUP, 0)[:n]).to(torch.uint8)]
+            self.rows.append(one)
+        self.arrays, self.pages = arrays, pages
+        self.lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.hidden = [torch.zeros(n, dtype=torch.bool, device="cuda") for n in lens]
+        self.gen = g
+        self.store()
+
+    def store(self):
+        """Bring the arrays in line with `rows`."""
+        for b, n in enumerate(self.lens):
+            t = torch.arange(n, device="cuda")
+            page = self.table[b, t // self.page].long() if n else t
+            for array, x in zip(self.arrays, self.rows[b]):
+                array[page, :, t % self.page] = x
+
+    def hide(self, b, p):
+        """Send page p of sequence b out of the cache (once stored)."""
+        self.table[b, p] = (-1, self.pages, 2 ** 31 - 1)[b % 3]
+        self.hidden[b][p * self.page:(p + 1) * self.page] = True
+
+    def attend(self, q, nqs, window=0, lse=None):
+        cache = F.MXKVCache(*self.arrays, fmt=F.E2M1)
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(nqs)]), dtype=torch.int32, device="cuda")
+        out = G.empty(q.shape, torch.bfloat16)
+        ws = F.mx_kv_attention_workspace(cache, q, self.table, max_q=max(nqs))
+        F.mx_kv_attention(cache, q, out, self.table, self.lens_t, cu_q=cu, max_q=max(nqs), window=window, lse=lse,
+                          workspace=ws)
+        return out
+
+    def check(self, nqs, group, window=0, q=None):
+        dim, total = self.dim, sum(nqs)
+        if q is None:
+            q = torch.randn(total, self.heads * group, dim, generator=self.gen, device="cuda").bfloat16()
+        lse = G.full((total, self.heads * group), 77.0, torch.float32)
+        out = self.attend(q, nqs, window, lse)
+        again = self.attend(q, nqs, window)
+        assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+        at = 0
+        for b, n in enumerate(nqs):
+            rows, at = slice(at, at + n), at + n
+            if not n:
+                continue
+            kc, ke, vc, ve = self.rows[b]
+            for h in range(self.heads):
+                heads = slice(h * group, (h + 1) * group)
+                self._check_head(out[rows, heads].double(), lse[rows, heads].double(), q[rows, heads].double(),
+                                 values(kc[:, h], ke[:, h]), vc[:, h], ve[:, h], self.hidden[b], window, (b, h))
+
+    def _check_head(self, got, got_lse, q, k, v_codes, v_e8, hidden, window, where):
+        n, length, dim, scale = q.shape[0], k.shape[0], self.dim, self.dim ** -0.5
+        v = values(v_codes, v_e8)
+        nan = v.isnan()
+        v = v.nan_to_num(0.0)
+        key = torch.arange(length, device="cuda")
+        pos = torch.arange(length - n, length, device="cuda")[:, None]
+        seen = (key <= pos) & ~hidden
+        if window:
+            seen &= key > pos - window
+        seen = seen[:, None].expand(n, q.shape[1], length)
+        s = (q @ k.T) * scale
+        s = s.masked_fill(~seen, -torch.inf)
+        none = ~seen.any(-1, keepdim=True)
+        top = s.amax(-1, keepdim=True).masked_fill(none, 0.0) if length else torch.zeros(*q.shape[:2], 1, device="cuda")
+        p = torch.exp(s - top)
+        total = p.sum(-1, keepdim=True).masked_fill(none, 1.0)
+        want = p @ v / total
+        size = p @ v.abs() / total
+        # The bound.  The output's rounding: half a bf16 step, up to 2^-8.  Weights: 11 bits, 2^-11 of their
+        # share.  Scores: D products summed by the tensor cores in steps of 16 (at most 8 of them, each off by 2^-23
+        # of sum |q k|), so 2^-20 of it in a weight, doubled for the scaling around them; sums over keys: 2^-23
+        # for every 16 keys.  A weight times 2^R is held in f16 next to the row's largest such product, so that
+        # below 2^-14 of that it is off by up to 2^-25 of it.
+        r = v_e8.double().masked_fill((v_e8 == 255) | hidden[:, None], 0).amax(-1) - 127
+        r = torch.nn.functional.pad(r, (0, -length % GROUP), value=-127.0).view(-1, GROUP).amax(-1)
+        r = r.clamp(MIN_R, MAX_R).repeat_interleave(GROUP)[:length]
+        most = (q.abs() @ k.abs().T * scale).masked_fill(~seen, 0.0).amax(-1, keepdim=True) if length else 0.0
+        largest = (p * torch.exp2(r)).amax(-1, keepdim=True) if length else 0.0
+        lost = 2 ** -25 * largest * (seen.double() @ (v.abs() * torch.exp2(-r)[:, None])) / total
+        tol = 2 ** -8 * 1.01 * want.abs() + (2 ** -11 + 2 ** -19 * most + 2 ** -27 * length) * size + 1.01 * lost
+        spoilt = (seen.double() @ nan.double()) > 0
+        assert torch.equal(got.isnan(), spoilt), where
+        bad = ((got - want).abs() > tol) & ~spoilt
+        assert not bad.any(), (where, bad.sum().item(), bad.nonzero()[:4].tolist(), got[bad][:4], want[bad][:4], tol[bad][:4])
+        want_lse = (top + torch.log(total)).masked_fill(none, -torch.inf)[..., 0]
+        assert torch.equal(got_lse.isinf(), want_lse.isinf()), where
+        off = (got_lse - want_lse).abs().nan_to_num(0.0)
+        assert (off <= (2 ** -19 * most + 2 ** -16)[..., 0] + 2 ** -22 * want_lse.abs().nan_to_num(posinf=0.0)).all(), where
+
+
+# ---- prompt chunks: row counts that leave 1 to 128 modulo 256, so that half of
+# the prompt kernel has no rows in some item, and many such items per CTA
+
+CHUNKS = [  # lens, queries, kv_heads, group, head_dim, page
+    ([2560] * 32, [80] * 32, 8, 4, 128, 64),
+    ([2048] * 16, [300] * 16, 8, 1, 128, 16),
+    ([1056] * 8, [1056] * 8, 8, 4, 64, 32),
+    ([4096, 2742, 1300, 33], [4096, 2742, 1300, 33], 8, 2, 64, 64),
+]
+
+
+@pytest.mark.parametrize("lens,nqs,heads,group,dim,page", CHUNKS)
+def test_chunks_with_a_remainder_of_rows(lens, nqs, heads, group, dim, page):
+    Batch(lens, heads, dim, page, seed=sum(nqs)).check(nqs, group)
+
+
+@pytest.mark.parametrize("lens,nqs,heads,group,dim,page", CHUNKS[:2])
+def test_chunks_with_a_remainder_of_rows_and_a_hidden_first_page(lens, nqs, heads, group, dim, page):
+    batch = Batch(lens, heads, dim, page, seed=1 + sum(nqs))
+    for b in range(1, len(lens), 2):
+        batch.hide(b, 0)
+    batch.check(nqs, group)
+
+
+@pytest.mark.parametrize("lens,nqs,heads,group,dim,page", CHUNKS[:2])
+def test_chunks_with_a_remainder_of_rows_and_nan_among_the_first_keys(lens, nqs, heads, group, dim, page):
+    batch = Batch(lens, heads, dim, page, seed=2 + sum(nqs))
+    for b in range(len(lens)):
+        for h in range(heads):
+            if (b + h) % 3 == 0:                   # one block of values
+                batch.rows[b][3][7 * b % 128, h, h % (dim // 32)] = 255
+    batch.store()
+    batch.check(nqs, group)
