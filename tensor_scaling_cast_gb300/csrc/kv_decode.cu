@@ -4,18 +4,20 @@
 // Mathematics.  With a row's codes c (E2M1) and block exponents E, a score is
 //   x = scale * log2(e) * sum_blocks 2^E * (q . c)
 // and the output sum_j 2^(x_j - M) v_j over the same factors' sum.  The codes
-// are exact in 16-bit floats, so both products run on them unscaled: the key
-// scales multiply the fp32 sums of each block, the value scales the weights.
-// Values are held relative to the largest block scale 2^R of their 32 tokens,
-// and the running reference M is of x + R, so that the weights p = 2^(x + R -
-// M) stay at or below 2^8 in f16 whatever the scales are; the softmax sum
-// takes p * 2^-R.  M moves only when a tile passes it by 2^8 (one vote per
-// tile), which is when the sums are rescaled.
+// are exact in 16-bit floats.  The key scales multiply the fp32 sums of each
+// block.  Values are held relative to the largest block scale 2^R of their 32
+// tokens, code times 2^(E - R) in f16, exact down to 2^-22; the running
+// reference M is of x + R, so that the weights p = 2^(x + R - M) stay at or
+// below 2^8 in f16 whatever the scales are, and the softmax sum takes p * 2^-R.
+// (The scales on the weights instead, 2 products for 8, take 219 us where this
+// takes 223, but p * 2^(E - R) leaves f16's range where a small weight meets a
+// small block.)  M moves only when a tile passes it by 2^8 (one vote per tile),
+// which is when the sums are rescaled.
 //
 // What bounds it: HBM and the unpacking together.  A token and head at D = 128
 // is 136 bytes of cache, and a tile of 32 of them 559 warp instructions for up
 // to eight query rows, a quarter of them the conversions of the 8192 codes.  8
-// sequences of 131072 tokens, 32 heads over 8: 219 us, 5.2 TB/s, 0.78 of the
+// sequences of 131072 tokens, 32 heads over 8: 223 us, 5.1 TB/s, 0.77 of the
 // measured copy rate (the same copies without the arithmetic: 180 us; ALU pipe
 // 56%, issue slots 56%, DRAM reads 1.00 of the cache's bytes); half as wide
 // rows (D = 64, the same softmax for half the bytes) 158 us.  mma.sync and not
@@ -550,10 +552,14 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
           e2m1x8_f16(((vw[0][x] >> 4) & m) | (vw[1][x] & ~m), c13);
           const uint32_t f0 = u ? fac[x].z : fac[x].x, f1 = u ? fac[x].w : fac[x].y;
 #pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            c02[y] = mul_f16x2(c02[y], y < 2 ? f0 : f1);
+            c13[y] = mul_f16x2(c13[y], y < 2 ? f0 : f1);
+          }
+#pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t b0 = mul_f16x2(p[u][nt][0], f0), b1 = mul_f16x2(p[u][nt][1], f1);
-            mma(o[nt][x][0], c02[0], c13[0], c02[2], c13[2], b0, b1);
-            mma(o[nt][x][1], c02[1], c13[1], c02[3], c13[3], b0, b1);
+            mma(o[nt][x][0], c02[0], c13[0], c02[2], c13[2], p[u][nt][0], p[u][nt][1]);
+            mma(o[nt][x][1], c02[1], c13[1], c02[3], c13[3], p[u][nt][0], p[u][nt][1]);
           }
         }
       }

@@ -46,10 +46,10 @@ def values(codes, e8):
 class Batch:
     """Sequences of random codes in the pages of one cache.  Scales are 2^(a
     whole number up to `apart` either way) per sequence, head and group of 32
-    tokens, times 2^(up to 1 either way) per block; everything that belongs to
-    no sequence holds 0xFF bytes."""
+    tokens, times 2^(up to 1 either way) per block, and the values' x-th block
+    times 2^v_blocks[x]; everything that belongs to no sequence holds 0xFF bytes."""
 
-    def __init__(self, lens, heads, dim, page, seed, k_apart=1, v_apart=6):
+    def __init__(self, lens, heads, dim, page, seed, k_apart=1, v_apart=6, v_blocks=None):
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.lens, self.heads, self.dim, self.page = lens, heads, dim, page
         per = [-(-n // page) for n in lens]
@@ -66,6 +66,8 @@ class Batch:
             for a, apart in enumerate((k_apart, v_apart)):
                 codes = torch.randint(0, 256, (n, heads, dim // 2), generator=g, device="cuda", dtype=torch.uint8)
                 e8 = torch.randint(-1, 2, (n, heads, dim // 32), generator=g, device="cuda") + 127 - 2
+                if a and v_blocks:
+                    e8 += torch.tensor(v_blocks, device="cuda")
                 shift = torch.randint(-apart, apart + 1, (-(-n // GROUP), heads, 1), generator=g, device="cuda")
                 one += [codes, (e8 + shift.repeat_interleave(GROUP, 0)[:n]).to(torch.uint8)]
             self.rows.append(one)
@@ -88,22 +90,22 @@ class Batch:
         self.table[b, p] = (-1, self.pages, 2 ** 31 - 1)[b % 3]
         self.hidden[b][p * self.page:(p + 1) * self.page] = True
 
-    def attend(self, q, nqs, window=0, lse=None):
+    def attend(self, q, nqs, window=0, lse=None, scale=None):
         cache = F.MXKVCache(*self.arrays, fmt=F.E2M1)
         cu = torch.tensor(np.concatenate([[0], np.cumsum(nqs)]), dtype=torch.int32, device="cuda")
         out = G.empty(q.shape, torch.bfloat16)
         ws = F.mx_kv_attention_workspace(cache, q, self.table, max_q=max(nqs))
         F.mx_kv_attention(cache, q, out, self.table, self.lens_t, cu_q=cu, max_q=max(nqs), window=window, lse=lse,
-                          workspace=ws)
+                          scale=scale, workspace=ws)
         return out
 
-    def check(self, nqs, group, window=0, q=None):
-        dim, total = self.dim, sum(nqs)
+    def check(self, nqs, group, window=0, q=None, scale=None):
+        dim, total, scale = self.dim, sum(nqs), self.dim ** -0.5 if scale is None else scale
         if q is None:
             q = torch.randn(total, self.heads * group, dim, generator=self.gen, device="cuda").bfloat16()
         lse = G.full((total, self.heads * group), 77.0, torch.float32)
-        out = self.attend(q, nqs, window, lse)
-        again = self.attend(q, nqs, window)
+        out = self.attend(q, nqs, window, lse, scale)
+        again = self.attend(q, nqs, window, scale=scale)
         assert torch.equal(out.view(torch.int16), again.view(torch.int16))
         at = 0
         for b, n in enumerate(nqs):
@@ -114,10 +116,10 @@ class Batch:
             for h in range(self.heads):
                 heads = slice(h * group, (h + 1) * group)
                 self._check_head(out[rows, heads].double(), lse[rows, heads].double(), q[rows, heads].double(),
-                                 values(kc[:, h], ke[:, h]), vc[:, h], ve[:, h], self.hidden[b], window, (b, h))
+                                 values(kc[:, h], ke[:, h]), vc[:, h], ve[:, h], self.hidden[b], window, scale, (b, h))
 
-    def _check_head(self, got, got_lse, q, k, v_codes, v_e8, hidden, window, where):
-        n, length, dim, scale = q.shape[0], k.shape[0], self.dim, self.dim ** -0.5
+    def _check_head(self, got, got_lse, q, k, v_codes, v_e8, hidden, window, scale, where):
+        n, length = q.shape[0], k.shape[0]
         v = values(v_codes, v_e8)
         nan = v.isnan()
         v = v.nan_to_num(0.0)
@@ -190,3 +192,14 @@ def test_chunks_with_a_remainder_of_rows_and_nan_among_the_first_keys(lens, nqs,
                 batch.rows[b][3][7 * b % 128, h, h % (dim // 32)] = 255
     batch.store()
     batch.check(nqs, group)
+
+
+# ---- blocks of values far smaller than the others of their tokens, under
+# weights of which a few are thousands of times the rest
+
+@pytest.mark.parametrize("rows", [8, 16, 24, 32, 100])
+@pytest.mark.parametrize("dim,blocks", [(128, (0, -10, -14, -4)), (64, (-12, 0))])
+def test_small_value_blocks_keep_their_bits(rows, dim, blocks):
+    nq = rows // 4
+    batch = Batch([8192, 1000, 33], 2, dim, 16, seed=rows, v_apart=1, v_blocks=blocks)
+    batch.check([nq] * 3, 4, scale=4 * dim ** -0.5)
