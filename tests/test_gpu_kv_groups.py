@@ -132,7 +132,8 @@ class Batch:
         s = (q @ k.T) * scale
         s = s.masked_fill(~seen, -torch.inf)
         none = ~seen.any(-1, keepdim=True)
-        top = s.amax(-1, keepdim=True).masked_fill(none, 0.0) if length else torch.zeros(*q.shape[:2], 1, device="cuda")
+        zero = torch.zeros(*q.shape[:2], 1, dtype=torch.float64, device="cuda")
+        top = s.amax(-1, keepdim=True).masked_fill(none, 0.0) if length else zero
         p = torch.exp(s - top)
         total = p.sum(-1, keepdim=True).masked_fill(none, 1.0)
         want = p @ v / total
@@ -145,8 +146,8 @@ class Batch:
         r = v_e8.double().masked_fill((v_e8 == 255) | hidden[:, None], 0).amax(-1) - 127
         r = torch.nn.functional.pad(r, (0, -length % GROUP), value=-127.0).view(-1, GROUP).amax(-1)
         r = r.clamp(MIN_R, MAX_R).repeat_interleave(GROUP)[:length]
-        most = (q.abs() @ k.abs().T * scale).masked_fill(~seen, 0.0).amax(-1, keepdim=True) if length else 0.0
-        largest = (p * torch.exp2(r)).amax(-1, keepdim=True) if length else 0.0
+        most = (q.abs() @ k.abs().T * scale).masked_fill(~seen, 0.0).amax(-1, keepdim=True) if length else zero
+        largest = (p * torch.exp2(r)).amax(-1, keepdim=True) if length else zero
         lost = 2 ** -25 * largest * (seen.double() @ (v.abs() * torch.exp2(-r)[:, None])) / total
         tol = 2 ** -8 * 1.01 * want.abs() + (2 ** -11 + 2 ** -19 * most + 2 ** -27 * length) * size + 1.01 * lost
         spoilt = (seen.double() @ nan.double()) > 0
@@ -203,3 +204,23 @@ def test_small_value_blocks_keep_their_bits(rows, dim, blocks):
     nq = rows // 4
     batch = Batch([8192, 1000, 33], 2, dim, 16, seed=rows, v_apart=1, v_blocks=blocks)
     batch.check([nq] * 3, 4, scale=4 * dim ** -0.5)
+
+
+# ---- few query rows: batches of more (sequence, head)s than CTAs, so that a
+# CTA ends one, joins it and goes on to the next, whole ones and parts in turn
+
+@pytest.mark.parametrize("rows", [3, 8, 16, 24, 32])
+@pytest.mark.parametrize("dim,page", [(128, 64), (64, 16)])
+def test_many_sequences_and_heads_of_few_rows(rows, dim, page):
+    group, nq = (3, 1) if rows == 3 else (8, rows // 8)
+    batch = Batch([1 + 37 * i % 2000 for i in range(64)], 8, dim, page, seed=rows + dim)
+    batch.check([nq] * 64, group)
+
+
+@pytest.mark.parametrize("nq", [1, 2, 3, 4])
+def test_many_short_sequences_some_without_keys_or_queries(nq):
+    lens = [53 * i % 230 for i in range(300)]
+    batch = Batch(lens, 6, 128, 32, seed=nq)
+    batch.hide(4, 0)
+    batch.check([nq if i % 6 else 0 for i in range(300)], 8)
+    batch.check([nq if i % 5 else 1 for i in range(300)], 8, window=70)
