@@ -303,13 +303,13 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
   };
 
   // Every wait is bounded; a role whose wait runs out counts it and returns,
-  // and so do the others in turn, to the common end.  A warp's lanes wait as
-  // one (they come converged, and try, read the clock and leave by the same
-  // instructions), so that they need no vote on the outcome: with one, which
-  // costs every wait some 30 clocks, the 2048-query chunk takes 455 us and
-  // not 441.
+  // and so do the others in turn, to the common end.  A warp's lanes each try
+  // for themselves and might see a barrier complete at different tries; the
+  // vote brings them together again, and to one outcome, before the aligned
+  // instructions that follow.  (It costs every wait some 30 clocks: the
+  // 2048-query chunk takes 445 us and not 438.)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_wait_lean(bar, parity & 1)) return true;
+    if (__all_sync(0xFFFFFFFFu, mbar_wait_lean(bar, parity & 1))) return true;
     atomicAdd(&g_kv_wait_timeouts, 1u);
     return false;
   };
