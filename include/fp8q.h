@@ -445,7 +445,8 @@ FP8Q_API int mx_kv_read(const mx_kv_cache* c, const int64_t* slots, int64_t toke
  *   workspace    device memory of mx_kv_attention_workspace(...) bytes,
  *                16-byte aligned, its first MX_KV_WORKSPACE_ZEROED bytes zero
  *                before its first use; every call leaves it ready for the
- *                next one, of whatever sizes.  Calls that may overlap on the
+ *                next one, of whatever sizes (one whose waits ran out, see
+ *                fp8q_pipeline_status, too).  Calls that may overlap on the
  *                GPU need one each.  FP8Q_ESIZE if it is too small.
  * Scores, softmax statistics and sums are fp32; the softmax weights are held
  * in f16 next to the row's largest, and codes times their scale in f16 next

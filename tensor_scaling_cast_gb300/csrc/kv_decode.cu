@@ -675,10 +675,8 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
-        uint32_t* t = plan.ticket + first;       // a CTA starts at most one that others go on with
-        const uint32_t got = atomicAdd(t, 1u);
-        s_last = got == (uint32_t)(last - first);
-        if (s_last) *t = 0;
+        // a CTA starts at most one that others go on with
+        s_last = take_ticket(plan.ticket + first, (uint32_t)(last - first), 0);
       }
       __syncthreads();
       if (s_last) {

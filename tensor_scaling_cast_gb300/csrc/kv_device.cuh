@@ -271,6 +271,20 @@ struct KvWork {
   uint32_t* tickets() const { return static_cast<uint32_t*>(at); }
   float* parts() const { return at ? reinterpret_cast<float*>(static_cast<char*>(at) + kMaxGrid * 4) : nullptr; }
 };
+// A ticket: the CTAs of a row's parts that have arrived, and above them those
+// that gave up (one whose wait ran out takes its tickets all the same, so that
+// the count is complete and the last one can set it back).
+constexpr uint32_t kGaveUp = 1u << 16;
+static_assert(kMaxGrid < (int)kGaveUp, "the count's place");
+// Called by one thread once its CTA's part is written, which it has seen
+// through a barrier: true for the last of `others` + 1 CTAs, where no part is
+// missing.  The ticket is zero again then.
+__device__ __forceinline__ bool take_ticket(uint32_t* t, uint32_t others, uint32_t mark) {
+  const uint32_t got = atomicAdd(t, 1u + mark);
+  if ((got & (kGaveUp - 1)) != others) return false;
+  *t = 0;
+  return got + mark < kGaveUp;
+}
 
 // ---- launches (kv_cache.cu, kv_attention.cu) --------------------------------
 cudaError_t launch_kv_write(const KvShape& s, int format, KvPool k, KvPool v, const void* kx, const void* vx,

@@ -92,6 +92,7 @@ struct PrSmem {
   uint64_t info_full[kPrInfos];
   uint64_t join_all, join_last, drain;
   uint32_t tmem, last;
+  uint32_t taken, gave_up;                            // tickets taken; some wait ran out
 };
 
 __device__ __forceinline__ void pr_units(const KvAttn& a, const KvSeq& s, int rt, int* tile0, int* n) {
@@ -239,6 +240,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     mbar_init(&sm.join_all, 8);
     mbar_init(&sm.join_last, 1);
     mbar_init(&sm.drain, 2);
+    sm.taken = sm.gave_up = 0;
     fence_barrier_init();
   }
   if (warp == kPrIssuer) tmem_alloc(&sm.tmem, 512);
@@ -311,6 +313,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xFFFFFFFFu, mbar_wait_lean(bar, parity & 1))) return true;
     atomicAdd(&g_kv_wait_timeouts, 1u);
+    sm.gave_up = 1;
     return false;
   };
   auto arrive = [&](uint64_t* bar) {                             // of a whole warp, as one
@@ -575,10 +578,9 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           arrive(&sm.join_all);
           if (warp == 0 && !wait(&sm.join_all, all_n)) return;
           if (threadIdx.x == 0) {
-            uint32_t* t = plan.ticket + first;       // a CTA starts at most one that others go on with
-            const uint32_t got = atomicAdd(t, 1u);
-            sm.last = got == (uint32_t)(last - first);
-            if (sm.last) *t = 0;
+            // a CTA starts at most one that others go on with
+            sm.last = take_ticket(plan.ticket + first, (uint32_t)(last - first), 0);
+            ++sm.taken;
             __threadfence();
             mbar_arrive(&sm.join_last);
           }
@@ -857,6 +859,19 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
   if (warp == kPrIssuer) {
     tmem_fence_after();
     tmem_free(tmem, 512);
+  }
+  // A CTA that gave up still takes the tickets of the parts it owes, so that
+  // none outlives the call: by a warp that had no role and is at the first item.
+  if (warp == kPrIssuer + 2 && sm.gave_up) {
+    uint32_t parts = 0;
+    for (bool go = unit0() < unit1(); go; go = advance()) {
+      if (unit0() == 0 && unit1() == it.n) continue;
+      if (lane == 0 && parts >= sm.taken) {
+        const long long per = s_range[1], seg0 = s_range[0] + rel + kPrSetup, first = seg0 / per;
+        take_ticket(plan.ticket + first, (uint32_t)((seg0 + it.n - 1) / per - first), kGaveUp);
+      }
+      ++parts;
+    }
   }
 }
 

@@ -224,3 +224,33 @@ def test_many_short_sequences_some_without_keys_or_queries(nq):
     batch.hide(4, 0)
     batch.check([nq if i % 6 else 0 for i in range(300)], 8)
     batch.check([nq if i % 5 else 1 for i in range(300)], 8, window=70)
+
+
+# ---- the workspace's tickets
+
+@pytest.mark.parametrize("nq", [1, 5, 70])
+def test_a_part_that_was_given_up_does_not_outlive_the_call(nq):
+    """Tickets as a CTA that gave up leaves them: with its mark.  Rows joined
+    over one stay unwritten, and the next call finds the tickets zero."""
+    batch = Batch([6000, 5000, 40], 2, 128, 16, seed=nq)
+    cache = F.MXKVCache(*batch.arrays, fmt=F.E2M1)
+    q = torch.randn(3 * nq, 8, 128, generator=batch.gen, device="cuda").bfloat16()
+    cu = torch.arange(4, dtype=torch.int32, device="cuda") * nq
+    ws = F.mx_kv_attention_workspace(cache, q, batch.table, max_q=nq)
+    tickets = ws[:F.WORKSPACE_ZEROED].view(torch.int32)
+
+    def call():
+        out = G.full(q.shape, 77.0, torch.bfloat16)
+        F.mx_kv_attention(cache, q, out, batch.table, batch.lens_t, cu_q=cu, max_q=nq, workspace=ws)
+        return out
+    want = call()
+    assert (tickets == 0).all() and not (want == 77).any()
+    tickets.fill_(1 << 16)
+    marked = call()
+    left = (marked == 77).all(-1)
+    assert left.any() and torch.equal(marked[~left], want[~left])
+    assert (tickets == 0).any()
+    assert ((tickets == 0) | (tickets == 1 << 16)).all()
+    assert torch.equal(call(), want)
+    tickets.zero_()
+    batch.check([nq] * 3, 4, q=q)
