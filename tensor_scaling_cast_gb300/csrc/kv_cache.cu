@@ -54,7 +54,9 @@ __device__ __forceinline__ KvPlace kv_place(const KvCopy& p, int which, int ahea
 __device__ __forceinline__ int64_t kv_slot(const KvCopy& p, const KvPlace& u, int j) {
   const int64_t t = u.token + j * p.abreast;
   if (!u.on || t >= p.tokens) return -1;
-  const int64_t s = __ldg(p.slots + t);
+  // a plain load: the grid before this one may still be writing slots when this
+  // CTA comes to the SM, so they are not read-only for the whole kernel
+  const int64_t s = p.slots[t];
   return s < p.s.slots ? s : -1;
 }
 __device__ __forceinline__ int64_t kv_at(const KvCopy& p, const KvPlace& u, int64_t slot) {

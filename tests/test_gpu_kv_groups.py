@@ -254,3 +254,22 @@ def test_a_part_that_was_given_up_does_not_outlive_the_call(nq):
     assert torch.equal(call(), want)
     tickets.zero_()
     batch.check([nq] * 3, 4, q=q)
+
+
+# ---- slots from the kernel just before
+
+def test_slots_written_just_before_the_call():
+    """Each step's slots come from a kernel queued right before its write and
+    read, into the array that the step before used."""
+    tokens, heads, dim, page, steps = 700, 2, 64, 16, 40
+    cache = F.MXKVCache.allocate(64, page, heads, dim, fmt=F.E4M3)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    orders = torch.stack([torch.randperm(64 * page, generator=g, device="cuda")[:tokens] for _ in range(steps)])
+    x = torch.randint(-8, 9, (steps, tokens, heads, dim), generator=g, device="cuda").float()      # exact in E4M3
+    slots = torch.zeros(tokens, dtype=torch.int64, device="cuda")
+    k, v = G.empty((steps, tokens, heads, dim), torch.float32), G.empty((steps, tokens, heads, dim), torch.float32)
+    for i in range(steps):
+        torch.add(orders[i], 0, out=slots)
+        F.mx_kv_write(cache, x[i], -x[i], slots)
+        F.mx_kv_read(cache, slots, k[i], v[i])
+    assert torch.equal(k, x) and torch.equal(v, -x)
