@@ -74,7 +74,7 @@ def main(prompts=(900, 33, 2500, 128), steps=8, seed=0, quiet=False):
                               for h in (Q_HEADS, KV_HEADS, KV_HEADS))
     step_slots = torch.full((batch,), -1, device="cuda")
     step_out = torch.empty_like(step_q)
-    step_ws = F.mx_kv_attention_workspace(cache, step_q, table)
+    step_ws = F.mx_kv_attention_workspace(cache, step_q, table, max_q=1)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         F.mx_kv_write(cache, step_k, step_v, step_slots, rule=F.MX_CEIL)

@@ -409,12 +409,19 @@ def mx_kv_read(cache: MXKVCache, slots: torch.Tensor, k: torch.Tensor, v: torch.
         _check(st, "mx_kv_read")
 
 
-def mx_kv_attention_workspace(cache: MXKVCache, q: torch.Tensor, page_table: torch.Tensor, max_q: int = 1):
+def mx_kv_attention_workspace(cache: MXKVCache, q: torch.Tensor, page_table: torch.Tensor, max_q=None):
     """A workspace for mx_kv_attention calls of these shapes, ready for its first
-    use, or None where they need none.  One per stream; it serves every call
-    whose own shapes ask for no more bytes."""
-    n = load().mx_kv_attention_workspace(cache._ref, q.shape[0], q.shape[1], page_table.shape[0], max_q,
-                                         page_table.shape[1])
+    use, or None where they need none.  max_q None: enough whatever max_q those
+    calls have or leave out; with the call's own it can be far smaller (decode
+    steps: 1).  One per stream; it serves every call whose own shapes ask for no
+    more bytes."""
+    total, q_heads = q.shape[0], q.shape[1]
+    # the plans differ by rows per key/value head: up to 8, 16, 24, 32, and more
+    group = max(1, q_heads // cache.kv_heads)
+    bounds = [max_q] if max_q is not None else [max(1, r) for r in (8 // group, 16 // group, 24 // group, 32 // group, total)]
+    sizes = [load().mx_kv_attention_workspace(cache._ref, total, q_heads, page_table.shape[0], m, page_table.shape[1])
+             for m in bounds]
+    n = min(sizes) if min(sizes) < 0 else max(sizes)
     if n < 0:
         _check(n, "mx_kv_attention_workspace")
     if not n:
@@ -433,7 +440,7 @@ def mx_kv_attention(cache: MXKVCache, q: torch.Tensor, out: torch.Tensor, page_t
     queries of any sequence (None: 1 without cu_q, total_q with it; the closer
     the bound, the better the plan), scale (None: head_dim ** -0.5), lse
     float32 [total_q, q_heads] or None, workspace of mx_kv_attention_workspace
-    for the same max_q."""
+    for the same max_q, or without one."""
     shape, qs, os_ = q.shape, q.stride(), out.stride()
     table, ts = page_table.shape, page_table.stride()
     if (len(shape) != 3 or shape[2] != cache.head_dim or out.shape != shape or qs[2] != 1 or os_[2] != 1

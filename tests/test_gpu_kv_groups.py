@@ -273,3 +273,21 @@ def test_slots_written_just_before_the_call():
         F.mx_kv_write(cache, x[i], -x[i], slots)
         F.mx_kv_read(cache, slots, k[i], v[i])
     assert torch.equal(k, x) and torch.equal(v, -x)
+
+
+# ---- bounds left out
+
+@pytest.mark.parametrize("nqs", [[1, 1], [2, 0], [9, 3], [150, 70]])
+def test_workspace_and_call_without_a_bound(nqs):
+    batch = Batch([9000, 300], 2, 128, 16, seed=sum(nqs))
+    cache = F.MXKVCache(*batch.arrays, fmt=F.E2M1)
+    q = torch.randn(sum(nqs), 8, 128, generator=batch.gen, device="cuda").bfloat16()
+    cu = torch.tensor([0, nqs[0], sum(nqs)], dtype=torch.int32, device="cuda")
+    out = G.empty(q.shape, torch.bfloat16)
+    ws = F.mx_kv_attention_workspace(cache, q, batch.table)
+    F.mx_kv_attention(cache, q, out, batch.table, batch.lens_t, cu_q=cu, workspace=ws)
+    bounded = G.empty(q.shape, torch.bfloat16)
+    F.mx_kv_attention(cache, q, bounded, batch.table, batch.lens_t, cu_q=cu, max_q=max(nqs), workspace=ws)
+    batch.check(nqs, 4, q=q)
+    # both are right to a rounding or two of bf16
+    assert (out.float() - bounded.float()).abs().max() <= 2 ** -6 * bounded.float().abs().max()

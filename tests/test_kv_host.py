@@ -151,3 +151,30 @@ def test_binding_refuses_wrong_tensors():
         with pytest.raises(TypeError):
             F.mx_kv_attention(cache, a["q"], a["out"], a["table"], a["lens"], cu_q=bad.get("cu_q"),
                               lse=bad.get("lse"))
+
+
+def test_a_workspace_without_a_bound_serves_every_plan(monkeypatch):
+    """max_q left out: the largest of the plans that any max_q can get, and
+    refusals are passed on."""
+    from tensor_scaling_cast_gb300 import fp8q as F
+    cache = F.MXKVCache.allocate(2, 16, 2, 64, device="cpu")
+    asked = []
+
+    class Fake:
+        sizes = {1: 20000, 2: 60000, 4: 50000, 8: 70000, 90: 65536}
+
+        def mx_kv_attention_workspace(self, ref, total, heads, batch, max_q, width):
+            asked.append((total, heads, batch, max_q, width))
+            return self.sizes.get(max_q, 0)
+    monkeypatch.setattr(F, "_lib", Fake())
+    q, table = torch.zeros(90, 8, 64, dtype=torch.bfloat16), torch.zeros(5, 3, dtype=torch.int32)
+    ws = F.mx_kv_attention_workspace(cache, q, table)
+    assert ws.numel() == 70000 and not ws[:F.WORKSPACE_ZEROED].any()
+    assert {a[3] for a in asked} == {2, 4, 6, 8, 90}           # rows: 8, 16, 24, 32 and all, four per query
+    assert {a[:3] + a[4:] for a in asked} == {(90, 8, 5, 3)}
+    assert F.mx_kv_attention_workspace(cache, q, table, max_q=1).numel() == 20000
+    assert F.mx_kv_attention_workspace(cache, q, table, max_q=3) is None
+    Fake.sizes = {90: -3, 8: 70000}
+    with pytest.raises(F.Fp8qError) as e:
+        F.mx_kv_attention_workspace(cache, q, table)
+    assert e.value.status == -3
