@@ -450,9 +450,13 @@ FP8Q_API int mx_kv_read(const mx_kv_cache* c, const int64_t* slots, int64_t toke
  *                GPU need one each.  FP8Q_ESIZE if it is too small.
  * Scores, softmax statistics and sums are fp32; the softmax weights are held
  * in f16 next to the row's largest, and codes times their scale in f16 next
- * to the largest scale of their 32 tokens (exact down to 2^-22 of it).  Capturable into CUDA graphs;
- * the lengths and the table are read by the kernel, so replays see their
- * current contents. */
+ * to the largest scale of their 32 tokens (exact down to 2^-22 of it).
+ * Ranges: key block scales up to 2^80, scale * |q| up to 2^100, and R of a
+ * sequence's tokens within 2^100 of one another (tokens with zero values count
+ * as 2^-80, so that value scales up to 2^20 always do); beyond, finite inputs
+ * can give Inf or NaN.
+ * Capturable into CUDA graphs; the lengths and the table are read by the
+ * kernel, so replays see their current contents. */
 FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int64_t total_q, int q_heads,
                              int64_t q_token_stride, int64_t q_head_stride, void* out, int64_t out_token_stride,
                              int64_t out_head_stride, float* lse, const int32_t* cu_q, const int32_t* kv_lens,

@@ -720,7 +720,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           top = max(top, e == 255u ? 0u : e);
         }
         top = __reduce_max_sync(0xFFFFFFFFu, top);   // tokens that do not exist have scale bytes 0
-        top = min(max(top, kMinScale), kMaxScale);
+        top = min(max(top, values ? kMinScale : 1u), kMaxScale);      // keys: 2^Rk is a normal number
         if (values) {
           const uint32_t any = __ballot_sync(0xFFFFFFFFu, bad);
           if (any) {

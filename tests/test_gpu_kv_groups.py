@@ -291,3 +291,26 @@ def test_workspace_and_call_without_a_bound(nqs):
     batch.check(nqs, 4, q=q)
     # both are right to a rounding or two of bf16
     assert (out.float() - bounded.float()).abs().max() <= 2 ** -6 * bounded.float().abs().max()
+
+
+# ---- what the documented roundings and ranges say
+
+RANGES = [  # key scales, queries, value scales: times 2^this
+    (80, -80, 0), (-100, 98, 0), (0, 0, -72), (0, 0, 110), (40, -40, 20), (0, -60, 0)]
+
+
+@pytest.mark.parametrize("k_up,q_up,v_up", RANGES)
+@pytest.mark.parametrize("rows", [8, 24, 160])
+def test_ends_of_the_ranges(rows, k_up, q_up, v_up):
+    """And with tokens whose values are all zero (E8M0 byte 0), where they are in range."""
+    batch = Batch([1500, 90], 2, 128, 32, seed=rows, v_apart=2)
+    for one in batch.rows:
+        one[1] += k_up % 256
+        one[3] += v_up % 256
+        if v_up <= 20:
+            one[2][32:80] = 0
+            one[3][32:80] = 0
+    batch.store()
+    nq = rows // 4
+    q = torch.randn(2 * nq, 8, 128, generator=batch.gen, device="cuda") * 2.0 ** q_up
+    batch.check([nq] * 2, 4, q=q.bfloat16())
