@@ -295,6 +295,16 @@ def test_workspace_and_call_without_a_bound(nqs):
 
 # ---- what the documented roundings and ranges say
 
+@pytest.mark.parametrize("rows", [4, 20, 280])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_one_block_of_large_values_costs_the_other_columns_no_more_than_documented(rows, dim):
+    batch = Batch([3000, 700], 2, dim, 16, seed=rows, v_apart=1)
+    batch.rows[0][3][1234, :, 1] += 20
+    batch.rows[1][3][5, 0, 0] += 24
+    batch.store()
+    batch.check([rows // 4] * 2, 4)
+
+
 RANGES = [  # key scales, queries, value scales: times 2^this
     (80, -80, 0), (-100, 98, 0), (0, 0, -72), (0, 0, 110), (40, -40, 20), (0, -60, 0)]
 
