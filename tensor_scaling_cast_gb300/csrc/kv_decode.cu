@@ -672,7 +672,6 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       // where the (sequence, head) covers the start of its range, else 1
       const long long first = cur_seg0 / per, last = (cur_seg0 + cur.tiles - 1) / per;
       join(warp_part, kDecWarps, plan.part + (2 * (long long)blockIdx.x + (cur_seg0 <= begin ? 0 : 1)) * PART);
-      __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
         // a CTA starts at most one that others go on with
@@ -680,7 +679,6 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
       }
       __syncthreads();
       if (s_last) {
-        __threadfence();
         join([&](int i) {
           const long long x = first + i;
           return static_cast<const float*>(plan.part) + (2 * x + (cur_seg0 <= x * per ? 0 : 1)) * PART;

@@ -276,12 +276,16 @@ struct KvWork {
 // the count is complete and the last one can set it back).
 constexpr uint32_t kGaveUp = 1u << 16;
 static_assert(kMaxGrid < (int)kGaveUp, "the count's place");
-// Called by one thread once its CTA's part is written, which it has seen
-// through a barrier: true for the last of `others` + 1 CTAs, where no part is
-// missing.  The ticket is zero again then.
+// Called by one thread between two barriers of its CTA, whose part is written
+// before the first: true for the last of `others` + 1 CTAs, where no part is
+// missing.  The ticket is zero again then.  The fences are this thread's, next
+// to the atomic: what the CTA's other threads wrote, the first barrier orders
+// before them; what they read, the second after them.
 __device__ __forceinline__ bool take_ticket(uint32_t* t, uint32_t others, uint32_t mark) {
+  __threadfence();
   const uint32_t got = atomicAdd(t, 1u + mark);
   if ((got & (kGaveUp - 1)) != others) return false;
+  __threadfence();
   *t = 0;
   return got + mark < kGaveUp;
 }

@@ -574,21 +574,18 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
         }
         if (!whole) {
           const long long per = s_range[1], seg0 = s_range[0] + rel + kPrSetup, first = div_pos(seg0, per), last = div_pos(seg0 + it.n - 1, per);
-          __threadfence();
           arrive(&sm.join_all);
           if (warp == 0 && !wait(&sm.join_all, all_n)) return;
           if (threadIdx.x == 0) {
             // a CTA starts at most one that others go on with
             sm.last = take_ticket(plan.ticket + first, (uint32_t)(last - first), 0);
             ++sm.taken;
-            __threadfence();
             mbar_arrive(&sm.join_last);
           }
           __syncwarp();
           if (!wait(&sm.join_last, joins++)) return;
           ++all_n;
           if (*reinterpret_cast<volatile uint32_t*>(&sm.last)) {
-            __threadfence();
             const int n = (int)(last - first) + 1;
             const int here = min(kPrRows, it.rows - it.rt * kPrRows);
             auto part_at = [&](int i) {
