@@ -135,8 +135,12 @@ struct DecPlan {
   float* part;           // [2 * grid][rows * (D + 2)]
 };
 
+// Three CTAs per SM for one group of eight rows; with more, two, as three leave
+// 168 registers a thread and the sums spill (16 rows over 8 x 131072 tokens 306
+// us at two, 345 at three; three queries of four heads over a 4096 window 20.7
+// and 26.8; 24 rows 28 and 35).
 template <int D, int NT>
-__global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 3 : 2)
+__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
 kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPlan plan) {
   constexpr int NB = D / 32, RB = D / 2, ROWS = 8 * NT;
   constexpr bool QS = NT > 1;                    // queries in shared memory
