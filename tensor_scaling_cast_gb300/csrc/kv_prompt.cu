@@ -130,14 +130,6 @@ struct PrPlan {
   float* part;             // [2 * grid][kPrRows * (D + 2)]
 };
 
-// a / b of values that are not negative, in 32 bits where both fit (they do in
-// all but the largest calls): four divisions per CTA and join, and the prompt
-// of 2048 takes 435 us against 440 with 64-bit ones.  The decode kernel gains
-// nothing from it and divides in 64 bits.
-__device__ __forceinline__ long long div_pos(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -202,7 +194,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  const long long per = max((long long)kPrMinUnits, div_pos(total + gridDim.x - 1, gridDim.x));
+  const long long per = max((long long)kPrMinUnits, (total + gridDim.x - 1) / gridDim.x);
   const long long begin = (long long)blockIdx.x * per, end = min(total, begin + per);
   if (begin >= end) return;
   if (threadIdx.x == 0) {
@@ -258,7 +250,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
     x.sq = kv_seq(a, x.b);
     pr_set(a, x);
     const long long u = seq_units(x.sq);
-    x.head = (int)div_pos(begin - seg0, u);
+    x.head = (int)((begin - seg0) / u);
     seg0 += x.head * u;
     // the row tile that holds `begin`: 32 at a time
     for (x.rt = 0;; x.rt += 32) {
@@ -308,8 +300,8 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
   // and so do the others in turn, to the common end.  A warp's lanes each try
   // for themselves and might see a barrier complete at different tries; the
   // vote brings them together again, and to one outcome, before the aligned
-  // instructions that follow.  (It costs every wait some 30 clocks: the
-  // 2048-query chunk takes 445 us and not 438.)
+  // instructions that follow.  (The 2048-query chunk takes 435 us with it and 437
+  // without at D = 128, 409 and 400 at D = 64.)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xFFFFFFFFu, mbar_wait_lean(bar, parity & 1))) return true;
     atomicAdd(&g_kv_wait_timeouts, 1u);
@@ -389,9 +381,9 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           // info_full, where the parity says nothing; once its scores are made, the
           // unpacking warps are past unit kt - 4, the slot's one before (kt - 1 for
           // the values, whose stage the issuing warp has waited for), and cannot be
-          // at kt + 4.  From unit to unit that stays so.  (The 2048-query chunk 437 us
-          // against 435.5 without it; with this order in every unit, so that the
-          // masks' test follows the scores, 454.)
+          // at kt + 4.  From unit to unit that stays so.  (It cost the 2048-query
+          // chunk 1.5 us of 436; with this order in every unit, so that the masks'
+          // test follows the scores, 18.)
           if (!wait(&sm.s_full[wg][0], mine_t)) return;
         }
         for (int u = u0; u < u1; ++u, ++kt) {
@@ -573,7 +565,7 @@ kv_prompt_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ PrPla
           tmem_fence_before();
         }
         if (!whole) {
-          const long long per = s_range[1], seg0 = s_range[0] + rel + kPrSetup, first = div_pos(seg0, per), last = div_pos(seg0 + it.n - 1, per);
+          const long long per = s_range[1], seg0 = s_range[0] + rel + kPrSetup, first = seg0 / per, last = (seg0 + it.n - 1) / per;
           arrive(&sm.join_all);
           if (warp == 0 && !wait(&sm.join_all, all_n)) return;
           if (threadIdx.x == 0) {
