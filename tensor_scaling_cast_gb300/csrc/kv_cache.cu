@@ -10,10 +10,10 @@
 // slot's address is left to find.  (With a division per unit the 16384-token
 // write was bound by its instructions, 23 us a launch against 18.)  Four tokens
 // in flight: with eight, a read of 131072 tokens takes 138 us against 115.
-// Measured, 8 heads x 128 columns, E2M1, bf16: 131072 tokens read in 115 us,
+// Measured, 8 heads x 128 columns, E2M1, bf16: 131072 tokens read in 116 us,
 // 5.9 TB/s, 0.88 of the measured copy rate; 16384 written and read back in 37
 // us (4.6 TB/s, 0.69: the two launches' ramps are a third of it); one token
-// 2.9 us for both calls in a graph, all launch.
+// 2.8 us for both calls in a graph, all launch.
 #include "kv_device.cuh"
 
 namespace fp8q {

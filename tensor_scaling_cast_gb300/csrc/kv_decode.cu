@@ -15,19 +15,19 @@
 // which is when the sums are rescaled.
 //
 // What bounds it: HBM and the unpacking together.  A token and head at D = 128
-// is 136 bytes of cache, and a tile of 32 of them 559 warp instructions for up
+// is 136 bytes of cache, and a tile of 32 of them 606 warp instructions for up
 // to eight query rows, a quarter of them the conversions of the 8192 codes.  8
 // sequences of 131072 tokens, 32 heads over 8: 223 us, 5.1 TB/s, 0.77 of the
 // measured copy rate (the same copies without the arithmetic: 180 us; ALU pipe
-// 56%, issue slots 56%, DRAM reads 1.00 of the cache's bytes); half as wide
-// rows (D = 64, the same softmax for half the bytes) 158 us.  mma.sync and not
-// tcgen05: with 16 tokens x 8 query rows a product it takes 1 of the 17
+// 55%, issue slots 59%, DRAM reads 1.00 of the cache's bytes); half as wide
+// rows (D = 64, the same softmax for half the bytes) 153 us.  mma.sync and not
+// tcgen05: with 16 tokens x 8 query rows a product it takes 1 of the 19
 // instructions of a token, its operands come straight from the unpacked
 // registers, and nothing waits on a tensor-memory round trip.
 //
 // Layout.  A warp owns tiles of 32 tokens, copied by cp.async into a ring of
 // its own (no CTA barrier while it streams; four stages at three CTAs per SM
-// took 229 us when three stages at four CTAs took 233).  Keys are the A operand (16 tokens x
+// took 229 us when three stages at four CTAs took 233, both before later steps).  Keys are the A operand (16 tokens x
 // 16 columns, the columns of a block permuted alike in q so that a lane's
 // 32-bit word of codes is one lane's share of two products); values are the A
 // operand of the transposed product (16 columns x 16 tokens), read by
@@ -40,8 +40,8 @@
 // positions [i * per, (i + 1) * per) in (sequence, head) order, each of them
 // kDecSetup positions and its tiles, so that uneven lengths fill the GPU
 // evenly and the host needs to know none of them.  (Set-up of 12 against 6
-// tiles: 64 sequences of 512 tokens 13.7 us against 17.7, 64 of up to 8192 42.3
-// against 44.5.)  A (sequence, head) that spans several CTAs is
+// and 20 tiles: 64 sequences of 512 tokens and 8 heads 20.4 us against 21.3 and
+// 21.3, 64 of up to 8192 and 4 heads 43.5 against 45.9 and 44.3.)  A (sequence, head) that spans several CTAs is
 // joined by the last of them to arrive, in the order of the tiles (the result
 // does not depend on which that is).
 #include "kv_device.cuh"
@@ -53,7 +53,11 @@ constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecStages = 4;
 constexpr int kTile = 32;                 // tokens of a warp tile
 constexpr int kDecSetup = 12;             // what a (sequence, head) costs beyond its tiles, in tiles
-constexpr int kMinTiles = 8;              // tiles of a CTA, at least
+// Positions of a CTA, at least.  With fewer, short calls have more parts to join:
+// of two sequences of 4000 and 900 tokens (window 4096, 20 rows) 16.7 us at 8,
+// 19.9 at 4, 16.8 at 16; one of 4096 tokens and 8 heads 11.7, 13.3, 11.7; one of
+// 1000 tokens and 4 heads 8.8, 8.6, 9.6.
+constexpr int kMinTiles = 8;
 
 template <int D>
 struct DecSmem {
@@ -210,7 +214,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
   // The warp's k-th tile begins at token tile0_at + k * (kDecWarps * kTile).
   // Pages of 32 tokens or more hold all of a tile's rows in one run; smaller ones
   // are looked up by each lane for its own token (8 x 131072 tokens in pages of
-  // 64: 219 us, of 16 or 8: 232).
+  // 64: 223 us, of 16 or 8: 236).
   const bool runs = a.shape.page_shift >= 5;
   auto page_of = [&](int k) {
     const int tok = tile0_at + k * (kDecWarps * kTile) + (runs ? 0 : lane);
@@ -252,7 +256,7 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
   // With one group of eight rows the queries stay in registers; with more
   // each warp prepares some of the groups and all read them from shared
   // memory, which leaves the registers to the sums (four groups over 8 x 131072
-  // tokens: 539 us against 681 from registers).
+  // tokens: 539 us against 681 from registers, 515 by now).
   constexpr int QN = QS ? 1 : NT;              // groups of a warp at a time
   uint4 qw[QN][NB];
   auto load_q = [&]() {
@@ -267,8 +271,8 @@ kv_decode_kernel(const __grid_constant__ KvAttn a, const __grid_constant__ DecPl
   };
   // The join takes a warp's last NT stages, so that with one group of rows the
   // queries and the first EARLY tiles of the next (sequence, head) are on their
-  // way meanwhile: 8 x 131072 tokens 219 us against 223, 64 sequences of up to
-  // 8192 42.3 against 43.4.  With more groups the registers for it are missing
+  // way meanwhile: 8 x 131072 tokens 223 us against 227 (in pages of 16: 236
+  // against 256), at D = 64 153 against 151, 64 sequences of up to 8192 the same.  With more groups the registers for it are missing
   // (five queries of four heads over a 4096 window 26.5 us with it, 25.8 without).
   constexpr int EARLY = kDecStages - NT;
   static_assert(ROWS * (D + 2) * 4 <= NT * (int)sizeof(typename Smem::Stage) && EARLY >= 0, "the join's place");
@@ -735,10 +739,11 @@ static cudaError_t dec_grid(const DecLaunch& k, const KvShape& s, int batch, int
   return cudaSuccess;
 }
 
-// Up to 32 rows a key/value head: 20 rows over a 4096 window take 26 us here
-// and 50 in kv_prompt.cu, 32 rows over 8 x 131072 tokens 539 and 782; beyond,
-// every further 32 rows would read and unpack the cache again, while that
-// kernel does it once for 256.
+// Up to 32 rows a key/value head: 8, 16, 24, 32 rows over a 4096 window take 18,
+// 21, 26, 32 us here and 45 to 47 in kv_prompt.cu, over 8 x 131072 tokens 223,
+// 306, 401, 515 and 708 to 712; beyond, every further 32 rows would read and
+// unpack the cache again, while that kernel does it once for 256 (64 rows:
+// 48 and 714 us).
 bool kv_decode_takes(int max_q, int group) { return (int64_t)max_q * group <= 32; }
 
 static int64_t dec_bytes(int grid, int nt, int dim) {

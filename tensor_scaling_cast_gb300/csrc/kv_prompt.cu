@@ -11,8 +11,8 @@
 // What bounds it: the issue slots.  A unit (128 keys x 256 rows, D = 128)
 // takes 2560 clocks of the tensor cores (4096 f16 multiply-adds a clock, the
 // score products at two thirds of that: 64 keys wide, they are fed at the
-// shared memory's 128 bytes a clock), 1024 of the exponentials, and 11.5 K
-// warp instructions, 2900 clocks of the SM's four schedulers; measured are
+// shared memory's 128 bytes a clock), 1024 of the exponentials, and 11.2 K
+// warp instructions, 2800 clocks of the SM's four schedulers; measured are
 // 4100.  2048 queries after 14336 tokens, 32 heads over 8: 435 us, 1184
 // TFLOP/s, 0.62 of the measured bf16 rate; at D = 64, where the exponentials
 // and the instructions are the same and the products half, about a tenth less.
@@ -35,7 +35,8 @@
 // per) over all units in (sequence, head, rows) order, each item of 256 rows
 // with kPrSetup positions more for its queries and output, and what spans CTAs
 // is joined by the last of them to arrive.  (Set-up of 4 against 3, 6 and 8
-// positions: four ragged prompts 282 us against 298, 294 and 303.)
+// positions: four ragged prompts 282 us against 298, 294 and 303 when it was
+// chosen; 262 now, some 14 more with 3 and 10 more with 6.)
 #include "kv_device.cuh"
 #include "tcgen05.cuh"
 
@@ -47,7 +48,10 @@ constexpr int kPrRows = 256;              // query rows of an item: two warpgrou
 constexpr int kPrKeys = 128;              // keys of a unit
 constexpr int kPrHalf = 64;               // and of a half of it: scores are made and used by halves
 constexpr int kPrStages = 2;              // units of unpacked keys, and of values, in shared memory
-constexpr int kPrMinUnits = 8;            // units of a CTA, at least
+// Units of a CTA, at least.  128 queries after 896 tokens, 32 heads over 8: 33 us
+// at 8, 35 at 5, 54 at 16; 64 queries after 1984, 8 heads over one: 40, 36, 56;
+// four ragged prompts up to 256 tokens: 28, 27, 41.
+constexpr int kPrMinUnits = 8;
 constexpr int kPrSetup = 4;               // what an item costs beyond its units, in units
 
 // Registers a thread: what a launch gives (__launch_bounds__ of 640 threads),
