@@ -448,13 +448,15 @@ FP8Q_API int mx_kv_read(const mx_kv_cache* c, const int64_t* slots, int64_t toke
  *                next one, of whatever sizes (one whose waits ran out, see
  *                fp8q_pipeline_status, too).  Calls that may overlap on the
  *                GPU need one each.  FP8Q_ESIZE if it is too small.
- * Roundings: scores, softmax statistics and sums are fp32.  Values are held in
- * f16 as code * 2^(E - R), 2^R the largest block scale of their 32 tokens
- * (kept within 2^-80 .. 2^126): exact down to 2^-22 of it.  A weight is held in
- * f16 next to the query's largest weight * 2^R over all keys and columns: 11 bits where
- * its own weight * 2^R is above 2^-14 of that, and off by up to 2^-25 of that
- * below.  A token with values far above the others' thus takes bits from the
- * others' weights in every column.
+ * Roundings: scores, softmax statistics and sums are fp32.  Queries are held in
+ * f16 next to the row's largest magnitude, exact down to 2^-29 of it.  Values
+ * are held in f16 as code * 2^(E - R), 2^R the largest block scale of their 32
+ * tokens (kept within 2^-80 .. 2^126): exact down to 2^-22 of it; so are keys
+ * where a key/value head has more than 32 query rows (2^-126 .. 2^126).  A
+ * weight is held in f16 next to the query's largest weight * 2^R over all keys
+ * and columns: 11 bits where its own weight * 2^R is above 2^-14 of that, and
+ * off by up to 2^-25 of that below.  A token with values far above the others'
+ * thus takes bits from the others' weights in every column.
  * Ranges: key block scales up to 2^80, scale * |q| up to 2^100, and R of a
  * sequence's tokens within 2^100 of one another (tokens with zero values count
  * as 2^-80, so that value scales up to 2^20 always do); beyond, finite inputs
