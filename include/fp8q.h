@@ -73,9 +73,10 @@ extern "C" {
 #define FP8Q_API
 #endif
 
-/* 8-bit target formats, and the 4-bit format of the key/value cache (OCP
- * E2M1: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6; accepted by the mx_kv_*
- * calls alone) */
+/* 8-bit target formats, and the 4-bit one (OCP E2M1: magnitudes 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6; two codes per byte, the even element in the low four bits;
+ * MX blocks only: the row-wise and dual MX casts, mx_decode, mx_matmul, the h
+ * of mx_act_forward and the key/value cache) */
 enum { FP8Q_E4M3 = 0, FP8Q_E5M2 = 1, FP8Q_E2M1 = 2 };
 /* input element types */
 enum { FP8Q_F32 = 0, FP8Q_BF16 = 1 };
@@ -238,10 +239,14 @@ FP8Q_API int fp8q_loss_scaler_read(fp8q_loss_scaler ls, float* scale, int* good_
  * the measurements said"): x is a row-major [rows, cols] tensor; each 32
  * consecutive elements of a row share E = floor(log2(block amax)) -
  * emax_elem + headroom_bits (emax_elem 8 for E4M3, 15 for E5M2).
+ *   format        FP8Q_E4M3, FP8Q_E5M2 or FP8Q_E2M1 (emax_elem 2)
  *   cols          > 0 and a multiple of 32 (else FP8Q_EINVAL)
  *   headroom_bits 0 (OCP rule) .. 4
- *   q             device [rows, cols] bytes; e8m0: device [rows, cols/32] bytes (E+127)
- *   d_clipped     device uint64 out (clipped elements), or NULL
+ *   q             device [rows, cols] bytes (E2M1: [rows, cols/2]);
+ *                 e8m0: device [rows, cols/32] bytes (E+127)
+ *   d_clipped     device uint64 out (clipped elements; E2M1: scaled values of
+ *                 7 and more, which round past 6), or NULL
+ * An E2M1 block holding NaN or Inf gets E8M0 0xFF and every code sign|7.
  * One kernel launch (plus a memset of d_clipped). */
 FP8Q_API int mx_cast(const void* x, int dtype, int64_t rows, int64_t cols, int format,
                      int headroom_bits, uint8_t* q, uint8_t* e8m0,
@@ -263,7 +268,9 @@ enum { FP8Q_MX_ROWWISE = 0, FP8Q_MX_COLWISE = 1 };
  * FP8Q_MX_FLOOR / FP8Q_MX_ROWWISE case).  E += headroom_bits (0..4), then
  * clamped to [-127, 127].  q is row-major [rows, cols] in both directions.
  *   rowwise: cols a multiple of 32.
- *   colwise: rows a multiple of 32, cols a multiple of 16.
+ *   colwise: rows a multiple of 32, cols a multiple of 16; not E2M1
+ *            (FP8Q_EDTYPE: its codes are pairs along the block, which
+ *            mx_cast_dual writes as the transpose's rows).
  * One kernel launch (plus a memset of d_clipped). */
 FP8Q_API int mx_cast_ex(const void* x, int dtype, int64_t rows, int64_t cols, int format,
                         int rule, int headroom_bits, int axis, uint8_t* q, uint8_t* e8m0,
@@ -285,7 +292,8 @@ FP8Q_API int fp8q_cast_transpose(fp8q_handle h, const void* x, int dtype, int64_
 /* MX dual cast: from one read of x [rows, cols], the row-wise MX cast
  * (q_row [rows, cols], e8m0_row [rows, cols/32]) and the column-wise one
  * written transposed, i.e. the row-wise MX cast of x^T (q_colt [cols, rows],
- * e8m0_colt [cols, rows/32]).  Rule and headroom as mx_cast_ex.  rows and
+ * e8m0_colt [cols, rows/32]; E2M1: q_row [rows, cols/2], q_colt [cols,
+ * rows/2]).  Rule and headroom as mx_cast_ex.  rows and
  * cols multiples of 32; x, q_row, q_colt 16-byte aligned.  d_clipped_row /
  * d_clipped_col: device uint64 or NULL.  One launch (plus memsets). */
 FP8Q_API int mx_cast_dual(const void* x, int dtype, int64_t rows, int64_t cols, int format, int rule,
@@ -476,10 +484,91 @@ FP8Q_API int mx_kv_attention(const mx_kv_cache* c, const void* q, int dtype, int
 FP8Q_API int64_t mx_kv_attention_workspace(const mx_kv_cache* c, int64_t total_q, int q_heads, int batch, int max_q,
                                            int table_width);
 
+/* ---- linear layers in MX form ---------------------------------------------------
+ *
+ * A matrix held in MX blocks along its rows, as the row-wise and dual casts
+ * write it: row r is cols codes from q + r * q_stride on (cols / 2 bytes for
+ * E2M1, cols bytes otherwise) and cols / 32 E8M0 bytes from e8m0 +
+ * r * e8m0_stride on.  Caller-owned device memory; the struct itself is host
+ * memory, read during the call.
+ *   cols       > 0 and a multiple of 32;  rows 0 .. 2^31 - 1
+ *   q          16-byte aligned, q_stride a multiple of 16 (else FP8Q_EALIGN)
+ *   strides    not below a row's bytes (FP8Q_EINVAL); a slice of a wider
+ *              matrix is one with that matrix's strides.  A single row's are
+ *              not used. */
+typedef struct mx_matrix {
+  uint8_t* q;
+  uint8_t* e8m0;
+  int64_t rows, cols;
+  int64_t q_stride, e8m0_stride;   /* bytes */
+  int32_t format;                  /* FP8Q_E2M1, FP8Q_E4M3 or FP8Q_E5M2 */
+} mx_matrix;
+
+/* The values that a matrix's codes stand for, code * 2^E ("what actually breaks
+ * low precision training": a block's elements share one power of two), into out
+ * [rows, cols] of dtype (rows out_stride elements apart), rounded to nearest
+ * even where it is bf16 (exact there unless subnormal).  A block with E8M0 0xFF
+ * reads as NaN.  out and its stride in bytes: multiples of 16.  One launch. */
+FP8Q_API int mx_decode(const mx_matrix* m, void* out, int dtype, int64_t out_stride, void* stream);
+
+/* out[i, j] = sum_k a[i, k] b[j, k] (+ add[i, j]) of two matrices in MX blocks
+ * along the summed dimension ("Mixed Precision FP16/BF16/FP8": weights and
+ * activations in E4M3, gradients in E5M2; "what actually breaks low precision
+ * training": the products whose operands are cast).  With row-wise casts of x
+ * [tokens, in] and w [out, in] it is the linear layer x w^T; with the dual
+ * casts' transposes it is both of its gradients.
+ *   a, b    cols alike (K); both E2M1, or each E4M3 or E5M2 (else FP8Q_EDTYPE)
+ *   out     device [a.rows, b.rows] of dtype, rows out_stride elements apart
+ *   add     device, of the same type and shape, rows add_stride elements
+ *           apart, or NULL; it may be out itself
+ *   out and add aligned to their elements; strides >= b.rows
+ * Roundings: products are exact, sums are held in 32 bits by the tensor cores
+ * (K / 64 or K / 32 additions of a tile's partial sums, each cut to 24 bits or
+ * more), add is added in 32 bits, and the result is rounded once to dtype.
+ * NaN and Inf (codes, blocks with E8M0 0xFF) go where the products take them.
+ * Products of scales below 2^-126 may be taken as zero.  The order of the sums
+ * is fixed by the sizes: results repeat from call to call.
+ * One launch, no workspace; capturable. */
+FP8Q_API int mx_matmul(const mx_matrix* a, const mx_matrix* b, void* out, int dtype, int64_t out_stride,
+                       const void* add, int64_t add_stride, void* stream);
+
+/* Activation of an MLP with its inputs kept in 8 bits for the backward pass
+ * ("Mixed Precision FP16/BF16/FP8": activations in E4M3; "what actually breaks
+ * low precision training": casts after the fact do not diverge).
+ *   MX_ACT_SILU       f(z) = z / (1 + e^-z)
+ *   MX_ACT_GELU       f(z) = z (1 + erf(z / sqrt 2)) / 2
+ *   MX_ACT_GELU_TANH  f(z) = z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2
+ * Forward: h = f(z) * u, or f(z) where u is NULL, from z and u [rows, cols] of
+ * dtype.
+ *   z_saved, u_saved  MX(z) and MX(u) under `rule`, E4M3 or E5M2, or NULL (not
+ *                     kept; with u, both or neither)
+ *   h                 [rows, cols] of dtype, or NULL
+ *   h_mx              MX(h) under `rule` in any format, of h before its
+ *                     rounding to dtype, or NULL
+ * One of h, h_mx, z_saved at least.
+ * Backward: z and u as the saved blocks hold them,
+ *   dz = dh * u * f'(z) (dh * f'(z) without u),  du = dh * f(z),
+ * and h = f(z) * u again where h is not NULL (the operand of the weight
+ * gradient after the activation).  u_saved and du: both or neither.
+ * All plain tensors are of dtype, rows *_stride elements apart; bases and
+ * strides in bytes are multiples of 16.  The outputs may not overlap the inputs, but for
+ * dz or du on dh and h on z or u, exactly (same base and stride).  A z or u block with NaN
+ * or Inf gives NaN gradients for its 32 elements.
+ * Computed in 32 bits; where dtype is bf16 with approximate exponentials and
+ * reciprocals, off by less than 2^-18 of the value for |z| up to 80.
+ * One launch each; capturable. */
+enum { MX_ACT_SILU = 0, MX_ACT_GELU = 1, MX_ACT_GELU_TANH = 2 };
+FP8Q_API int mx_act_forward(int act, const void* z, int64_t z_stride, const void* u, int64_t u_stride, int dtype,
+                            int64_t rows, int64_t cols, const mx_matrix* z_saved, const mx_matrix* u_saved, int rule,
+                            void* h, int64_t h_stride, const mx_matrix* h_mx, void* stream);
+FP8Q_API int mx_act_backward(int act, const mx_matrix* z_saved, const mx_matrix* u_saved, const void* dh,
+                             int64_t dh_stride, int dtype, void* dz, int64_t dz_stride, void* du, int64_t du_stride,
+                             void* h, int64_t h_stride, void* stream);
+
 /* Number of pipeline waits on the current device that ran out of time since
  * the last call (and reset it).  Kernels that stage tiles through TMA
- * (column-wise mx_cast_ex, mx_cast_dual, fp8q_cast_transpose) and the
- * prompt kernel of mx_kv_attention bound every wait for a tile; on timeout they count it here and stop instead of
+ * (column-wise mx_cast_ex, mx_cast_dual, fp8q_cast_transpose), the
+ * prompt kernel of mx_kv_attention and mx_matmul bound every wait for a tile; on timeout they count it here and stop instead of
  * hanging, leaving their outputs incomplete.  A healthy run reads 0.
  * Synchronous. */
 FP8Q_API int fp8q_pipeline_status(unsigned int* timed_out_waits);

@@ -30,7 +30,7 @@ def grid(fmt: int) -> np.ndarray:
     return np.array(got)
 
 
-def _exponent(amax: float, fmt: int, rule: int) -> int:
+def _exponent(amax: float, fmt: int, rule: int, headroom: int = 0) -> int:
     if amax == 0:
         return -127
     top = _FORMAT[fmt][3]
@@ -43,10 +43,10 @@ def _exponent(amax: float, fmt: int, rule: int) -> int:
         e += 1
     if rule == NEAREST and 2 * mu * mu < tmu * tmu:    # log2(amax / top) below the middle
         e -= 1
-    return min(127, max(-127, e))
+    return min(127, max(-127, e + headroom))
 
 
-def encode(x: np.ndarray, fmt: int, rule: int = FLOOR):
+def encode(x: np.ndarray, fmt: int, rule: int = FLOOR, headroom: int = 0):
     """x [..., D] -> (codes uint8 [..., D], one per element, E8M0 uint8 [..., D / 32])."""
     x = np.asarray(x, dtype=np.float64)
     g = grid(fmt)
@@ -55,7 +55,7 @@ def encode(x: np.ndarray, fmt: int, rule: int = FLOOR):
     b = x.reshape(*x.shape[:-1], -1, BLOCK)
     finite = np.isfinite(b).all(-1)
     amax = np.where(finite, np.abs(np.where(np.isfinite(b), b, 0)).max(-1), 0)
-    e = np.vectorize(lambda a: _exponent(a, fmt, rule), otypes=[np.int64])(amax)
+    e = np.vectorize(lambda a: _exponent(a, fmt, rule, headroom), otypes=[np.int64])(amax)
     m = np.abs(np.where(finite[..., None], b, 0)) * np.exp2(-e.astype(np.float64))[..., None]
     low = np.searchsorted(mids, m)                 # on a middle: the lower neighbour
     at = np.minimum(low, len(mids) - 1)

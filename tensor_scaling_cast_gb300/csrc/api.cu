@@ -17,6 +17,7 @@
 #include "fp8q_internal.cuh"
 #include "kv_device.cuh"
 #include "mx_device.cuh"
+#include "mx_linear.cuh"
 
 namespace fp8q {
 
@@ -202,11 +203,13 @@ FP8Q_API int fp8q_pipeline_selftest(void* stream) {
 FP8Q_API int fp8q_pipeline_status(unsigned int* timed_out_waits) {
   FP8Q_TRACE_CALL();
   if (!timed_out_waits) return FP8Q_EINVAL;
-  unsigned int a = 0, b = 0, c = 0;
+  unsigned int a = 0, b = 0, c = 0, d = 0, f = 0;
   cudaError_t e = read_wait_timeouts(&a);
   if (e == cudaSuccess) e = read_tp_wait_timeouts(&b);
   if (e == cudaSuccess) e = read_kv_wait_timeouts(&c);
-  *timed_out_waits = a + b + c;
+  if (e == cudaSuccess) e = read_mx4_wait_timeouts(&d);
+  if (e == cudaSuccess) e = read_mm_wait_timeouts(&f);
+  *timed_out_waits = a + b + c + d + f;
   return e == cudaSuccess ? FP8Q_OK : fail_cuda(e);
 }
 
@@ -496,7 +499,9 @@ FP8Q_API int mx_cast_ex(const void* x, int dtype, int64_t rows, int64_t cols, in
                         int rule, int headroom_bits, int axis, uint8_t* q, uint8_t* e8m0,
                         unsigned long long* d_clipped, void* stream) {
   FP8Q_TRACE_CALL();
-  if (!dtype_ok(dtype) || !format_ok(format)) return FP8Q_EDTYPE;
+  const bool four = format == FP8Q_E2M1;
+  if (!dtype_ok(dtype) || !(format_ok(format) || four)) return FP8Q_EDTYPE;
+  if (four && axis == FP8Q_MX_COLWISE) return FP8Q_EDTYPE;
   if (rule < FP8Q_MX_FLOOR || rule > FP8Q_MX_NEAREST) return FP8Q_EINVAL;
   if (axis != FP8Q_MX_ROWWISE && axis != FP8Q_MX_COLWISE) return FP8Q_EINVAL;
   if (rows < 0 || cols <= 0 || headroom_bits < 0 || headroom_bits > kMaxHeadroom) return FP8Q_EINVAL;
@@ -513,7 +518,8 @@ FP8Q_API int mx_cast_ex(const void* x, int dtype, int64_t rows, int64_t cols, in
   }
   if (n == 0) return FP8Q_OK;
   int launches = 0;
-  cudaError_t e = axis == FP8Q_MX_ROWWISE
+  cudaError_t e = four ? launch_mx4_rows(x, dtype, n, headroom_bits, rule, q, e8m0, d_clipped, s, &launches)
+                  : axis == FP8Q_MX_ROWWISE
                       ? launch_mx(x, dtype, n, format, headroom_bits, rule, q, e8m0, d_clipped, s, &launches)
                       : launch_mx_colwise(x, dtype, rows, cols, format, headroom_bits, rule, q, e8m0,
                                           d_clipped, s, &launches);
@@ -526,7 +532,8 @@ FP8Q_API int mx_cast_dual(const void* x, int dtype, int64_t rows, int64_t cols, 
                           uint8_t* e8m0_colt, unsigned long long* d_clipped_row,
                           unsigned long long* d_clipped_col, void* stream) {
   FP8Q_TRACE_CALL();
-  if (!dtype_ok(dtype) || !format_ok(format)) return FP8Q_EDTYPE;
+  const bool four = format == FP8Q_E2M1;
+  if (!dtype_ok(dtype) || !(format_ok(format) || four)) return FP8Q_EDTYPE;
   if (rule < FP8Q_MX_FLOOR || rule > FP8Q_MX_NEAREST) return FP8Q_EINVAL;
   if (rows < 0 || cols <= 0 || rows % 32 != 0 || cols % 32 != 0 || headroom_bits < 0 ||
       headroom_bits > kMaxHeadroom)
@@ -544,8 +551,10 @@ FP8Q_API int mx_cast_dual(const void* x, int dtype, int64_t rows, int64_t cols, 
   }
   if (n == 0) return FP8Q_OK;
   int launches = 0;
-  cudaError_t e = launch_mx_dual(x, dtype, rows, cols, format, rule, headroom_bits, q_row, e8m0_row,
-                                 q_colt, e8m0_colt, d_clipped_row, d_clipped_col, s, &launches);
+  cudaError_t e = four ? launch_mx4_dual(x, dtype, rows, cols, rule, headroom_bits, q_row, e8m0_row, q_colt, e8m0_colt,
+                                         d_clipped_row, d_clipped_col, s, &launches)
+                       : launch_mx_dual(x, dtype, rows, cols, format, rule, headroom_bits, q_row, e8m0_row,
+                                        q_colt, e8m0_colt, d_clipped_row, d_clipped_col, s, &launches);
   g_launches += launches;
   return e == cudaSuccess ? FP8Q_OK : fail_cuda(e);
 }

@@ -9,11 +9,12 @@
 
 namespace fp8q {
 
-// fp32 bit patterns of the formats' largest finite values (1.75 * 2^emax).
+// fp32 bit patterns of the formats' largest finite values (1.75 * 2^emax;
+// E2M1: 1.5 * 2^emax).
 __host__ __device__ constexpr uint32_t fmax_bits(int fmt) {
-  return fmt == FP8Q_E4M3 ? 0x43E00000u /* 448 */ : 0x47600000u /* 57344 */;
+  return fmt == FP8Q_E4M3 ? 0x43E00000u /* 448 */ : fmt == FP8Q_E2M1 ? 0x40C00000u /* 6 */ : 0x47600000u /* 57344 */;
 }
-__host__ __device__ constexpr int emax_elem(int fmt) { return fmt == FP8Q_E4M3 ? 8 : 15; }
+__host__ __device__ constexpr int emax_elem(int fmt) { return fmt == FP8Q_E4M3 ? 8 : fmt == FP8Q_E2M1 ? 2 : 15; }
 
 // Two fp32 -> two FP8 bytes, round to nearest even, saturating to +-max
 // (`lo` lands in the low byte).  Blackwell converts a pair per instruction.
@@ -34,9 +35,11 @@ __device__ __forceinline__ uint32_t vmax_u16x2(uint32_t a, uint32_t b) {
 }
 
 // Rounded-past-max test on the scaled value: E4M3's tie at 464 goes to the
-// even 448, E5M2's tie at 61440 goes to the even 65536 (beyond the max).
+// even 448, E5M2's tie at 61440 goes to the even 65536 and E2M1's at 7 to the
+// even 8 (beyond the max).
 template <int FMT>
 __device__ __forceinline__ bool clips(float v) {
+  if (FMT == FP8Q_E2M1) return fabsf(v) >= 7.0f;
   return FMT == FP8Q_E4M3 ? (fabsf(v) > 464.0f) : (fabsf(v) >= 61440.0f);
 }
 

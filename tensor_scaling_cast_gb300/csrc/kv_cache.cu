@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_const
     const int64_t at = kv_at(p, u, slot[j]);
     const bool finite = m < 0x7F800000u;
     constexpr int F8 = FMT == FP8Q_E2M1 ? FP8Q_E4M3 : FMT;
-    const int E = !finite ? 0 : FMT == FP8Q_E2M1 ? block_exp_e2m1(m, p.rule) : block_exp<F8>(m, p.rule, 0);
+    const int E = !finite ? 0 : block_exp<FMT>(m, p.rule, 0);
     const float s = pow2f(-E);
     float f[8];
 #pragma unroll

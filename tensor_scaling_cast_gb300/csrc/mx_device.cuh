@@ -41,10 +41,11 @@ __device__ __forceinline__ uint32_t mag_bits(uint32_t m) {
 // Shared exponent of a block from its amax bits m (finite), per rule:
 //   floor (OCP): E = floor(log2 A) - emax_elem
 //   ceil:        smallest E with A * 2^-E <= fmax; with A = mu * 2^k this is
-//                k - emax_elem + [mu > 1.75]   (fmax = 1.75 * 2^emax_elem)
+//                k - emax_elem + [mu > 1.75]   (fmax = 1.75 * 2^emax_elem; E2M1: 1.5)
 //   nearest:     E nearest to log2(A / fmax):   k - emax_elem - [mu < 1.75/sqrt 2],
 //                tested exactly as M^2 < 49 * 2^41 on the 24-bit significand M,
-//                i.e. M <= isqrt(49 * 2^41 - 1) = 10380372 (0x9E6454)
+//                i.e. M <= isqrt(49 * 2^41 - 1) = 10380372 (E2M1: 1.5/sqrt 2,
+//                M^2 < 9 * 2^43, M <= isqrt(9 * 2^43 - 1) = 8897462)
 // then + headroom, clamped to [-127, 127]; a zero block gets -127.
 template <int FMT>
 __device__ __forceinline__ int block_exp(uint32_t m, int rule, int headroom) {
@@ -60,8 +61,8 @@ __device__ __forceinline__ int block_exp(uint32_t m, int rule, int headroom) {
     M = m << (23 - lb);
   }
   int E = k - emax_elem(FMT);
-  if (rule == FP8Q_MX_CEIL) E += (M > 0xE00000u) ? 1 : 0;
-  else if (rule == FP8Q_MX_NEAREST) E -= (M <= 0x9E6454u) ? 1 : 0;
+  if (rule == FP8Q_MX_CEIL) E += (M > (FMT == FP8Q_E2M1 ? 0xC00000u : 0xE00000u)) ? 1 : 0;
+  else if (rule == FP8Q_MX_NEAREST) E -= (M <= (FMT == FP8Q_E2M1 ? 8897462u : 10380372u)) ? 1 : 0;
   return min(127, max(-127, E + headroom));
 }
 
@@ -71,6 +72,12 @@ __device__ __forceinline__ int block_exp(uint32_t m, int rule, int headroom) {
 // capped (the C ABI rejects more than kMaxHeadroom).
 constexpr int kMaxHeadroom = 4;
 static_assert(127 - 8 + 1 + kMaxHeadroom <= 126, "2^-E must stay a normal fp32 number");
+// 2^-E of a block; E2M1 blocks under headroom can reach E = 127, whose 2^-127
+// is a subnormal number.
+template <int FMT>
+__device__ __forceinline__ float block_inv_scale(int E) {
+  return __uint_as_float(FMT == FP8Q_E2M1 && E == 127 ? 0x00400000u : (uint32_t)(127 - E) << 23);
+}
 
 // Can a finite block with max |x| bits m and shared exponent E hold a clipped
 // element?  Only if its scaled maximum m * 2^-E passes fmax, i.e. m exceeds

@@ -112,6 +112,49 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
       "r"((uint32_t)accumulate)
       : "memory");
 }
+// Block-scaled products: each 32 elements along K of a row of A and B are
+// scaled by an E8M0 byte in tensor memory.  Scales of 128 rows x 128 elements
+// are four columns of words, word j of lane i (of each 32) being row 32 j + i's
+// four bytes; sf_copy brings them there from 512 bytes of shared memory, row
+// 32 j + i at byte 16 i + 4 j.  A product takes 64 elements of 4 bits (bytes
+// 2 s and 2 s + 1 of the words, s = 0 or 1) or 32 of 8 bits (byte s).
+__host__ __device__ constexpr uint32_t mx_idesc(bool four, int a_format, int b_format, int m, int n) {
+  // the E8M0 scales' bit, M and N; operand formats: E2M1 is 1 in the 4-bit kind, E4M3 0 and E5M2 1 in the 8-bit one
+  return (1u << 23) | ((uint32_t)(four ? 1 : a_format) << 7) | ((uint32_t)(four ? 1 : b_format) << 10) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// The same with step s of a word's bytes chosen for both operands.
+template <bool F4>
+__host__ __device__ constexpr uint32_t mx_idesc_step(uint32_t idesc, int s) {
+  return idesc | ((uint32_t)(F4 ? 2 * s : s) << 4) | ((uint32_t)(F4 ? 2 * s : s) << 29);
+}
+// Shared-memory descriptor of sf_copy's 32 rows of 16 bytes (no swizzle, eight
+// rows every 128 bytes).
+__device__ __forceinline__ uint64_t sf_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((128u >> 4) | (1u << 14)) << 32);
+}
+template <int CTAS>
+__device__ __forceinline__ void sf_copy(uint32_t tmem, uint64_t desc) {
+  if (CTAS == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+#define FP8Q_MX_MMA(group, kind)                                                                               \
+  asm volatile(                                                                                                \
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %7, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n" \
+      " tcgen05.mma.cta_group::" group ".kind::" kind " [%0], a, b, %4, [%5], [%6], p;\n}" ::"r"(d),           \
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sf_a), "r"(sf_b), "r"((uint32_t)accumulate)               \
+      : "memory")
+template <bool F4, int CTAS>
+__device__ __forceinline__ void mma_mx(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                       uint32_t sf_a, uint32_t sf_b, bool accumulate) {
+  if (F4 && CTAS == 1) FP8Q_MX_MMA("1", "mxf4.block_scale.scale_vec::2X");
+  if (F4 && CTAS == 2) FP8Q_MX_MMA("2", "mxf4.block_scale.scale_vec::2X");
+  if (!F4 && CTAS == 1) FP8Q_MX_MMA("1", "mxf8f6f4.block_scale.scale_vec::1X");
+  if (!F4 && CTAS == 2) FP8Q_MX_MMA("2", "mxf8f6f4.block_scale.scale_vec::1X");
+}
+#undef FP8Q_MX_MMA
 // One arrival on bar once every product issued so far by this thread is done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))

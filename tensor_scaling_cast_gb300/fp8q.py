@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(PKG, "libfp8q.so")
 E4M3, E5M2, E2M1 = 0, 1, 2
 MX_FLOOR, MX_CEIL, MX_NEAREST = 0, 1, 2
 MX_ROWWISE, MX_COLWISE = 0, 1
+MX_ACT_SILU, MX_ACT_GELU, MX_ACT_GELU_TANH = 0, 1, 2
 EST_MAX_WINDOW, EST_SMOOTHED = 0, 1
 F32, BF16 = 0, 1
 NO_EXP = -(2 ** 31)
@@ -79,6 +80,10 @@ def load() -> ctypes.CDLL:
                                   i64, p]
     L.mx_kv_attention_workspace.argtypes = [p, i64, i, i, i, i]
     L.mx_kv_attention_workspace.restype = i64
+    L.mx_decode.argtypes = [p, p, i, i64, p]
+    L.mx_matmul.argtypes = [p, p, p, i, i64, p, i64, p]
+    L.mx_act_forward.argtypes = [i, p, i64, p, i64, i, i64, i64, p, p, i, p, i64, p, p]
+    L.mx_act_backward.argtypes = [i, p, p, p, i64, i, p, i64, p, i64, p, i64, p]
     L.fp8q_pipeline_status.argtypes = [ctypes.POINTER(ctypes.c_uint)]
     L.fp8q_pipeline_status.restype = i
     L.fp8q_pipeline_selftest.argtypes = [p]
@@ -93,7 +98,8 @@ def load() -> ctypes.CDLL:
                  "fp8q_set_estimator_state", "fp8q_destroy", "fp8q_cast", "fp8q_cast_multi", "mx_cast", "mx_cast_ex",
                  "fp8q_amax_history", "fp8q_scale_state", "fp8q_set_history", "fp8q_reset",
                  "fp8q_error_stats", "mx_error_stats", "fp8q_error_stats_noalloc",
-                 "mx_kv_write", "mx_kv_read", "mx_kv_attention"):
+                 "mx_kv_write", "mx_kv_read", "mx_kv_attention",
+                 "mx_decode", "mx_matmul", "mx_act_forward", "mx_act_backward"):
         getattr(L, name).restype = i
     _lib = L
     return L
@@ -259,7 +265,8 @@ def mx_cast(x: torch.Tensor, fmt: int, headroom: int, q: torch.Tensor, e8m0: tor
 
 def mx_cast_ex(x: torch.Tensor, fmt: int, rule: int, headroom: int, axis: int, q: torch.Tensor,
                e8m0: torch.Tensor, clipped=None, stream=None):
-    """axis MX_ROWWISE: e8m0 [rows, cols/32]; MX_COLWISE: e8m0 [rows/32, cols]."""
+    """axis MX_ROWWISE: e8m0 [rows, cols/32]; MX_COLWISE: e8m0 [rows/32, cols].
+    E2M1 (row-wise): q [rows, cols/2]."""
     rows, cols = x.shape
     _check(load().mx_cast_ex(_ptr(x), _dtype(x), rows, cols, fmt, rule, headroom, axis, _ptr(q),
                              _ptr(e8m0), _ptr(clipped), _stream(stream)), "mx_cast_ex")
@@ -269,7 +276,8 @@ def mx_cast_dual(x: torch.Tensor, fmt: int, rule: int, headroom: int, q_row, e8_
                  clipped_row=None, clipped_col=None, stream=None):
     """Row-wise MX of x and row-wise MX of x^T (column-wise blocks written
     transposed) from one read: q_row [rows, cols], e8_row [rows, cols/32],
-    q_colt [cols, rows], e8_colt [cols, rows/32]."""
+    q_colt [cols, rows], e8_colt [cols, rows/32] (E2M1: q_row [rows, cols/2],
+    q_colt [cols, rows/2])."""
     rows, cols = x.shape
     _check(load().mx_cast_dual(_ptr(x), _dtype(x), rows, cols, fmt, rule, headroom, _ptr(q_row),
                                _ptr(e8_row), _ptr(q_colt), _ptr(e8_colt), _ptr(clipped_row),
@@ -465,6 +473,106 @@ def mx_kv_attention(cache: MXKVCache, q: torch.Tensor, out: torch.Tensor, page_t
         _stream(stream))
     if st:
         _check(st, "mx_kv_attention")
+
+
+# ---- linear layers in MX form ------------------------------------------------
+
+class _MXMatrixStruct(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("e8m0", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("e8m0_stride", ctypes.c_int64),
+                ("format", ctypes.c_int32)]
+
+
+class MXMatrix:
+    """A matrix in MX blocks along its rows and its description for the C
+    calls: q uint8 [rows, cols] (E2M1: [rows, cols / 2]) and e8m0 uint8
+    [rows, cols / 32], as the row-wise casts write them.  Both may be slices of
+    wider ones (consecutive elements within a row)."""
+
+    def __init__(self, q: torch.Tensor, e8m0: torch.Tensor, fmt: int = E4M3):
+        if (q.dtype is not torch.uint8 or e8m0.dtype is not torch.uint8 or q.dim() != 2 or e8m0.dim() != 2
+                or q.shape != (e8m0.shape[0], (16 if fmt == E2M1 else 32) * e8m0.shape[1])
+                or (q.stride(1) != 1 and q.shape[1] > 1) or (e8m0.stride(1) != 1 and e8m0.shape[1] > 1)):
+            raise TypeError(f"an MX matrix is uint8 codes [rows, cols] (E2M1: [rows, cols / 2]) and uint8 E8M0 bytes "
+                            f"[rows, cols / 32] with consecutive elements: got {q.dtype} {tuple(q.shape)}, "
+                            f"{e8m0.dtype} {tuple(e8m0.shape)}")
+        self.q, self.e8m0, self.fmt = q, e8m0, fmt
+        self.shape = (e8m0.shape[0], 32 * e8m0.shape[1])
+        self._struct = _MXMatrixStruct(q.data_ptr(), e8m0.data_ptr(), *self.shape, q.stride(0), e8m0.stride(0), fmt)
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def allocate(cls, rows: int, cols: int, fmt: int = E4M3, device="cuda") -> "MXMatrix":
+        """One for a cast to write into."""
+        return cls(torch.empty(rows, cols // 2 if fmt == E2M1 else cols, dtype=torch.uint8, device=device),
+                   torch.empty(rows, cols // 32, dtype=torch.uint8, device=device), fmt)
+
+
+def _mx(m):
+    return None if m is None else m._ref
+
+
+def _plain(what, t, shape, dtype):
+    """(pointer, row stride) of a plain matrix, or of one left out."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype or t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
+        raise TypeError(f"{what}: {dtype} {tuple(shape)} with consecutive elements in a row: got {t.dtype} "
+                        f"{tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr(), t.stride(0)
+
+
+def mx_decode(m: MXMatrix, out: torch.Tensor, stream=None):
+    """The values that m's codes stand for, into out [rows, cols] (bf16 or fp32)."""
+    ptr, stride = _plain("mx_decode: out", out, m.shape, out.dtype)
+    st = (_lib or load()).mx_decode(m._ref, ptr, _dtype(out), stride, _stream(stream))
+    if st:
+        _check(st, "mx_decode")
+
+
+def mx_matmul(a: MXMatrix, b: MXMatrix, out: torch.Tensor, add=None, stream=None):
+    """out [a rows, b rows] (bf16 or fp32) = a b^T, + add of out's type and
+    shape (out itself, to accumulate).  Both E2M1, or each E4M3 or E5M2."""
+    shape, dtype = (a.shape[0], b.shape[0]), out.dtype
+    ptr, stride = _plain("mx_matmul: out", out, shape, dtype)
+    add_ptr, add_stride = _plain("mx_matmul: add", add, shape, dtype)
+    st = (_lib or load()).mx_matmul(a._ref, b._ref, ptr, BF16 if dtype is torch.bfloat16 else _dtype(out), stride,
+                                    add_ptr, add_stride, _stream(stream))
+    if st:
+        _check(st, "mx_matmul")
+
+
+def mx_act_forward(act: int, z: torch.Tensor, u=None, z_saved=None, u_saved=None, h=None, h_mx=None,
+                   rule: int = MX_FLOOR, stream=None):
+    """h = f(z) * u (u None: f(z)) of z, u [rows, cols] (bf16 or fp32), into the
+    plain h and / or the MXMatrix h_mx; MX(z), MX(u) into the 8-bit MXMatrix
+    z_saved, u_saved for mx_act_backward."""
+    shape, dtype = z.shape, z.dtype
+    if len(shape) != 2:
+        raise TypeError(f"mx_act_forward: z is [rows, cols]: got {tuple(shape)}")
+    zp, zs = _plain("mx_act_forward: z", z, shape, dtype)
+    up, us = _plain("mx_act_forward: u", u, shape, dtype)
+    hp, hs = _plain("mx_act_forward: h", h, shape, dtype)
+    st = (_lib or load()).mx_act_forward(act, zp, zs, up, us, _dtype(z), shape[0], shape[1], _mx(z_saved),
+                                         _mx(u_saved), rule, hp, hs, _mx(h_mx), _stream(stream))
+    if st:
+        _check(st, "mx_act_forward")
+
+
+def mx_act_backward(act: int, z_saved: MXMatrix, u_saved, dh: torch.Tensor, dz: torch.Tensor, du=None, h=None,
+                    stream=None):
+    """dz = dh u f'(z) and du = dh f(z) (u_saved and du None: dz = dh f'(z)) from
+    the saved blocks, and h = f(z) u again where it is given; dh, dz, du and h
+    [rows, cols], all bf16 or all fp32."""
+    shape, dtype = z_saved.shape, dh.dtype
+    gp, gs = _plain("mx_act_backward: dh", dh, shape, dtype)
+    zp, zs = _plain("mx_act_backward: dz", dz, shape, dtype)
+    up, us = _plain("mx_act_backward: du", du, shape, dtype)
+    hp, hs = _plain("mx_act_backward: h", h, shape, dtype)
+    st = (_lib or load()).mx_act_backward(act, z_saved._ref, _mx(u_saved), gp, gs, _dtype(dh), zp, zs, up, us, hp, hs,
+                                          _stream(stream))
+    if st:
+        _check(st, "mx_act_backward")
 
 
 # ---- convenience wrapper ---------------------------------------------------
