@@ -29,47 +29,80 @@ struct MmScales {
   const uint8_t* e8m0;
   int64_t stride;
   int32_t rows, bytes;
-  int32_t whole;             // rows start at multiples of a K block's bytes
+  int32_t align;             // every row starts at a multiple of 16, 8 or 4 bytes, or 1
 };
 struct MmArgs {
   CUtensorMap w, t;          // codes of the operand with 128-row tiles, of the other
   MmScales ws, ts;
-  int32_t kblocks, w_tiles, splits;
+  int32_t kblocks, w_tiles, t_tiles, splits;
   uint32_t idesc;
   void* out;
   const void* add;
   int64_t out_stride, add_stride;
   int32_t fp32, w_is_a;      // out row: index in w (else in t)
+  int32_t out_vector, add_vector;   // rows start at multiples of 32 (out) and 16 bytes
 };
 
-// E8M0 bytes of a row's K block (8 in 4 bits, 4 in 8 bits); 1 where there are
-// none: the codes there are zeros.
-template <bool F4>
-__device__ __forceinline__ uint2 load_scales(const MmScales& s, int64_t row, int kb) {
-  constexpr int SB = F4 ? 8 : 4;
-  uint2 v = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  if (row >= s.rows) return v;
-  const int at = kb * SB;
-  const uint8_t* src = s.e8m0 + row * s.stride + at;
-  if (s.whole && at + SB <= s.bytes) {
-    if (F4) v = *reinterpret_cast<const uint2*>(src);
-    else v.x = *reinterpret_cast<const uint32_t*>(src);
-    return v;
-  }
-#pragma unroll
-  for (int k = 0; k < SB; ++k) {
-    if (at + k >= s.bytes) break;
-    uint32_t& word = k < 4 ? v.x : v.y;
-    word = (word & ~(0xFFu << (8 * (k & 3)))) | ((uint32_t)src[k] << (8 * (k & 3)));
-  }
-  return v;
+// Up to four bytes from src on, `left` of them in the row; 1 (0x7F) for the
+// others: the codes there are zeros.  Two aligned words hold them, each with a
+// byte of the row in it.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* src, int left) {
+  if (left <= 0) return 0x7F7F7F7Fu;
+  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(src) & 3u);
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(src - off);
+  const uint32_t v = __funnelshift_r(w[0], off && left > (int)(4 - off) ? w[1] : 0u, 8 * off);
+  const uint32_t mask = left >= 4 ? 0xFFFFFFFFu : (1u << (8 * left)) - 1u;
+  return (v & mask) | (0x7F7F7F7Fu & ~mask);
 }
-// Into the place of row r of 128: 512 bytes for each 128 elements.
+// E8M0 bytes of four K blocks of a row, kb, kb + 1, ..: two words each in 4
+// bits, one in 8.
 template <bool F4>
-__device__ __forceinline__ void store_scales(uint32_t smem, int r, uint2 v) {
+struct ScaleGroup {
+  uint32_t w[F4 ? 8 : 4];
+};
+template <bool F4>
+__device__ __forceinline__ ScaleGroup<F4> load_scales(const MmScales& s, int64_t row, int kb) {
+  constexpr int W = F4 ? 8 : 4;
+  ScaleGroup<F4> g;
+  const int at = kb * W;
+  if (row >= s.rows) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) g.w[k] = 0x7F7F7F7Fu;
+    return g;
+  }
+  const uint8_t* src = s.e8m0 + row * s.stride + at;
+  if (s.align == 16 && (kb & (F4 ? 1 : 3)) == 0 && at + 4 * W <= s.bytes) {
+#pragma unroll
+    for (int k = 0; k < W; k += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src + 4 * k);
+      g.w[k] = v.x;
+      g.w[k + 1] = v.y;
+      g.w[k + 2] = v.z;
+      g.w[k + 3] = v.w;
+    }
+  } else if (s.align >= (F4 ? 8 : 4) && at + 4 * W <= s.bytes) {
+#pragma unroll
+    for (int k = 0; k < W; k += F4 ? 2 : 1) {
+      if (F4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(src + 4 * k);
+        g.w[k] = v.x;
+        g.w[k + (F4 ? 1 : 0)] = v.y;
+      } else {
+        g.w[k] = *reinterpret_cast<const uint32_t*>(src + 4 * k);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < W; ++k) g.w[k] = scale_word(src + 4 * k, s.bytes - at - 4 * k);
+  }
+  return g;
+}
+// Block j's into the place of row r of 128: 512 bytes for each 128 elements.
+template <bool F4>
+__device__ __forceinline__ void store_scales(uint32_t smem, int r, const ScaleGroup<F4>& g, int j, int pitch = 512) {
   const uint32_t at = smem + (r & 31) * 16 + (r >> 5) * 4;
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v.x) : "memory");
-  if (F4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 512), "r"(v.y) : "memory");
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(g.w[F4 ? 2 * j : j]) : "memory");
+  if (F4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + pitch), "r"(g.w[F4 ? 2 * j + 1 : j]) : "memory");
 }
 
 __device__ __forceinline__ float add_of(const MmArgs& p, int64_t m, int64_t n) {
@@ -85,6 +118,13 @@ __device__ __forceinline__ void put(const MmArgs& p, int64_t m, int64_t n, float
   else static_cast<uint16_t*>(p.out)[at] = (uint16_t)cvt_bf16x2(v, v);
 }
 
+// 32 bytes at a multiple of 32: a whole sector.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -94,10 +134,13 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}"
-               : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
   return v;
 }
 
@@ -115,7 +158,6 @@ struct SplitCfg {
   static_assert(kStage % 1024 == 0 && 128 * NT * 4 <= kStages * kStage, "swizzled tiles; the parts of the sum");
 };
 constexpr int kSplitThreads = 192;         // TMA, products, and four warps of scales that end as the epilogue
-constexpr int kScalesAhead = 4;            // K blocks whose scales a thread has in flight
 
 template <bool F4, int NT>
 __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid_constant__ MmArgs p) {
@@ -201,22 +243,13 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
   } else {
     const int r = threadIdx.x - 64;
     const int64_t wr = (int64_t)tw * 128 + r, tr = r < NT ? (int64_t)tt * NT + r : p.ts.rows;
-    uint2 w[kScalesAhead], t[kScalesAhead], w2[kScalesAhead], t2[kScalesAhead];
+    ScaleGroup<F4> w = load_scales<F4>(p.ws, wr, kb0), t = load_scales<F4>(p.ts, tr, kb0);
+    for (int b = 0; b < n && ok; b += 4) {
+      // the next four blocks' are on their way meanwhile
+      const ScaleGroup<F4> w2 = load_scales<F4>(p.ws, b + 4 < n ? wr : p.ws.rows, kb0 + b + 4);
+      const ScaleGroup<F4> t2 = load_scales<F4>(p.ts, b + 4 < n ? tr : p.ts.rows, kb0 + b + 4);
 #pragma unroll
-    for (int j = 0; j < kScalesAhead; ++j) {
-      if (j >= n) break;
-      w[j] = load_scales<F4>(p.ws, wr, kb0 + j);
-      t[j] = load_scales<F4>(p.ts, tr, kb0 + j);
-    }
-    for (int b = 0; b < n && ok; b += kScalesAhead) {
-#pragma unroll
-      for (int j = 0; j < kScalesAhead; ++j) {
-        if (b + kScalesAhead + j >= n) break;
-        w2[j] = load_scales<F4>(p.ws, wr, kb0 + b + kScalesAhead + j);
-        t2[j] = load_scales<F4>(p.ts, tr, kb0 + b + kScalesAhead + j);
-      }
-#pragma unroll
-      for (int j = 0; j < kScalesAhead; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const int i = b + j, st = i % ST;
         if (i >= n) break;
         if (i >= ST) {
@@ -227,14 +260,14 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
           }
         }
         const uint32_t at = smem + st * C::kStage;
-        store_scales<F4>(at + C::kWs, r, w[j]);
-        if (r < NT) store_scales<F4>(at + C::kTs, r, t[j]);
+        store_scales<F4>(at + C::kWs, r, w, j);
+        if (r < NT) store_scales<F4>(at + C::kTs, r, t, j);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
-        w[j] = w2[j];
-        t[j] = t2[j];
       }
+      w = w2;
+      t = t2;
     }
     if (!mbar_wait(&done, 0)) ok = false;
     __syncwarp();
@@ -266,16 +299,28 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
     // each CTA of the cluster adds up its share of the columns, parts in order
     cluster_barrier();
     if (warp >= 2) {
-      const int row = threadIdx.x - 64;
-      const int64_t wi = (int64_t)tw * 128 + row;
-      const int c1 = NT * ((int)rank + 1) / p.splits;
-      for (int c = NT * (int)rank / p.splits; c < c1; ++c) {
-        const int64_t ti = (int64_t)tt * NT + c;
+      // four rows of a column at a time, all parts' loads in flight together
+      const int c0 = NT * (int)rank / p.splits, c1 = NT * ((int)rank + 1) / p.splits;
+      for (int u = threadIdx.x - 64; u < (c1 - c0) * 32; u += 128) {
+        const int c = c0 + (u >> 5), row = (u & 31) * 4;
+        const int64_t ti = (int64_t)tt * NT + c, wi = (int64_t)tw * 128 + row;
         if (ti >= p.ts.rows) break;
-        float sum = 0.0f;
-#pragma unroll 4
-        for (int s = 0; s < p.splits; ++s) sum += cluster_load(smem + (c * 128 + row) * 4, s);
-        if (wi < p.ws.rows) put(p, p.w_is_a ? wi : ti, p.w_is_a ? ti : wi, sum);
+        float4 part[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          part[s] = s < p.splits ? cluster_load4(smem + (c * 128 + row) * 4, s) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float4 sum = part[0];
+#pragma unroll
+        for (int s = 1; s < 8; ++s) {
+          sum.x += part[s].x;
+          sum.y += part[s].y;
+          sum.z += part[s].z;
+          sum.w += part[s].w;
+        }
+        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (wi + k < p.ws.rows) put(p, p.w_is_a ? wi + k : ti, p.w_is_a ? ti : wi + k, v[k]);
       }
     }
     cluster_barrier();                               // nobody leaves while its part is read
@@ -285,6 +330,277 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
   if (warp == 1) {
     tmem_fence_after();
     tmem_free(tmem, C::kColumns);
+  }
+}
+
+// ---- large products: tiles of 256 x NT on pairs of SMs ----------------------------
+//
+// A cluster of two CTAs, one per SM and as many as there are SMs, goes over
+// tiles of 256 rows of a and NT of b.  Each CTA loads half the rows of both, so
+// that an SM reads 32 bytes of K of (128 + NT / 2) rows for 128 x NT sums: for
+// NT = 256 64 bytes a cycle at the 4-bit rate, and one CTA by itself would read
+// 96.  Sums stay in tensor memory, in two buffers that end at column 480 (the
+// scales have the rest); for NT > 240 the buffers share some columns, which the
+// epilogue reads first, so that the next tile's products start while the others
+// are still being stored.
+constexpr int kPairThreads = 320;          // TMA, products, four warps of epilogue, four of scales
+constexpr int kPairSums = 480;             // tensor-memory columns of the sums
+constexpr int kPairBand = 8;               // tiles of a in a band: pairs in flight cover a compact block
+
+template <bool F4, int NT>
+struct PairCfg {
+  static constexpr int kB = 128 * 128;                             // codes of b within a stage
+  static constexpr int kCodes = kB + NT / 2 * 128;
+  static constexpr int kScaleA = F4 ? 1024 : 512, kScales = 3 * kScaleA;   // 128 rows of a, 256 of b
+  static constexpr int kStages = (226 * 1024 - 1024) / (kCodes + kScales);
+  static constexpr int kSmem = kStages * (kCodes + kScales) + 1024;
+  static constexpr int kOver = 2 * NT > kPairSums ? 2 * NT - kPairSums : 0;
+  static_assert(kCodes % 1024 == 0 && kOver % 32 == 0 && NT % 32 == 0 && NT <= 256, "whole chunks of columns");
+};
+
+// 32 sums of row m from column n on.
+__device__ __forceinline__ void put32(const MmArgs& p, int64_t m, int64_t n, int64_t cols, uint32_t (&v)[32]) {
+  const bool whole = n + 32 <= cols;
+  if (p.add) {
+    const int64_t at = m * p.add_stride + n;
+    const char* src = static_cast<const char*>(p.add) + at * (p.fp32 ? 4 : 2);
+    if (whole && p.add_vector) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 4) {
+        if (p.fp32) {
+          const float4 x = *reinterpret_cast<const float4*>(src + 4 * k);
+          v[k] = __float_as_uint(__uint_as_float(v[k]) + x.x);
+          v[k + 1] = __float_as_uint(__uint_as_float(v[k + 1]) + x.y);
+          v[k + 2] = __float_as_uint(__uint_as_float(v[k + 2]) + x.z);
+          v[k + 3] = __float_as_uint(__uint_as_float(v[k + 3]) + x.w);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(src + 2 * k);
+          v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(x.x << 16));
+          v[k + 1] = __float_as_uint(__uint_as_float(v[k + 1]) + __uint_as_float(x.x & 0xFFFF0000u));
+          v[k + 2] = __float_as_uint(__uint_as_float(v[k + 2]) + __uint_as_float(x.y << 16));
+          v[k + 3] = __float_as_uint(__uint_as_float(v[k + 3]) + __uint_as_float(x.y & 0xFFFF0000u));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (n + k < cols) v[k] = __float_as_uint(__uint_as_float(v[k]) + add_of(p, m, n + k));
+    }
+  }
+  const int64_t at = m * p.out_stride + n;
+  char* dst = static_cast<char*>(p.out) + at * (p.fp32 ? 4 : 2);
+  if (whole && p.out_vector) {
+    if (p.fp32) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 8) store32(dst + 4 * k, v + k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; k += 16) {
+        uint32_t h[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) h[x] = cvt_bf16x2(__uint_as_float(v[k + 2 * x]), __uint_as_float(v[k + 2 * x + 1]));
+        store32(dst + 2 * k, h);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      if (n + k >= cols) break;
+      if (p.fp32) reinterpret_cast<uint32_t*>(dst)[k] = v[k];
+      else reinterpret_cast<uint16_t*>(dst)[k] = (uint16_t)cvt_bf16x2(__uint_as_float(v[k]), __uint_as_float(v[k]));
+    }
+  }
+}
+
+template <bool F4, int NT>
+__global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_constant__ MmArgs p) {
+  using C = PairCfg<F4, NT>;
+  constexpr int ST = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], sums_full[2], sums_empty[2], shared_empty;
+  __shared__ uint32_t s_tmem;
+  const uint32_t smem = smem_addr(smem_raw) + (-smem_addr(smem_raw) & 1023u);
+  const uint32_t scales = smem + ST * C::kCodes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], 1 + 8);          // the even CTA's: bytes of both, and both CTAs' scales
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sums_full[i], 1);
+      mbar_init(&sums_empty[i], 8);        // the even CTA's: both epilogues
+    }
+    mbar_init(&shared_empty, 8);
+    fence_barrier_init();
+    prefetch_tensormap(&p.w);
+    prefetch_tensormap(&p.t);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 1) tmem_alloc_pair(&s_tmem, 512);
+  tmem_fence_before();
+  __syncthreads();
+  cluster_barrier();                       // the other CTA's barriers and tensor memory are there
+  tmem_fence_after();
+  // not before: the next grid's CTAs may take tensor memory once they come to the SM
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = s_tmem;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int tiles = p.w_tiles * p.t_tiles;
+  const auto place = [&](int tile, int* tw, int* tt) {
+    const int band = tile / (kPairBand * p.t_tiles), in = tile - band * (kPairBand * p.t_tiles);
+    const int height = min(kPairBand, p.w_tiles - band * kPairBand);
+    *tt = in / height;
+    *tw = band * kPairBand + in - *tt * height;
+  };
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      for (int tile = pair; tile < tiles && ok; tile += pairs) {
+        int tw, tt;
+        place(tile, &tw, &tt);
+        for (int i = 0; i < p.kblocks; ++i, ++it) {
+          const int st = it % ST;
+          if (it >= ST && !mbar_wait(&empty[st], (it / ST - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * C::kCodes);
+          const uint32_t bar = lead_bar(&full[st]), at = smem + st * C::kCodes;
+          tma_load_2d_pair(at, &p.w, bar, i * 128, tw * 256 + (int)rank * 128);
+          tma_load_2d_pair(at + C::kB, &p.t, bar, i * 128, tt * NT + (int)rank * (NT / 2));
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t sf_a = tmem + kPairSums, sf_b = sf_a + (F4 ? 8 : 4);
+      const uint32_t hi = desc_hi(1024);
+      int it = 0, lt = 0;
+      for (int tile = pair; tile < tiles && ok; tile += pairs, ++lt) {
+        const int b = lt & 1;
+        const uint32_t d = tmem + (b ? kPairSums - NT : 0);
+        if (lt >= 2 && !mbar_wait_cluster(&sums_empty[b], (lt / 2 - 1) & 1)) ok = false;
+        if (C::kOver && lt >= 1 && !mbar_wait_cluster(&shared_empty, (lt - 1) & 1)) ok = false;
+        tmem_fence_after();
+        for (int i = 0; i < p.kblocks && ok; ++i, ++it) {
+          const int st = it % ST;
+          if (!mbar_wait_cluster(&full[st], (it / ST) & 1)) {
+            ok = false;
+            break;
+          }
+          tmem_fence_after();
+          const uint32_t sf = scales + st * C::kScales, at = smem + st * C::kCodes;
+          // copies and products are carried out in the order of their issue
+#pragma unroll
+          for (int c = 0; c < (F4 ? 2 : 1); ++c) {
+            sf_copy<2>(sf_a + 4 * c, sf_desc(sf + 512 * c));
+            sf_copy<2>(sf_b + 8 * c, sf_desc(sf + C::kScaleA + 1024 * c));
+            sf_copy<2>(sf_b + 8 * c + 4, sf_desc(sf + C::kScaleA + 1024 * c + 512));
+          }
+          const uint32_t a_lo = desc_lo(at, 16), b_lo = desc_lo(at + C::kB, 16);
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            mma_mx<F4, 2>(d, a_lo + 2 * s, b_lo + 2 * s, hi, mx_idesc_step<F4>(p.idesc, F4 ? s & 1 : s),
+                          sf_a + (F4 ? 4 * (s >> 1) : 0), sf_b + (F4 ? 8 * (s >> 1) : 0), i > 0 || s > 0);
+          mma_commit_pair(&empty[st]);
+        }
+        mma_commit_pair(&sums_full[b]);
+      }
+    }
+  } else if (warp < 6) {
+    const int q = warp & 3, row = 32 * q + lane;     // this warp's lanes of tensor memory
+    const uint32_t lane_at = tmem + ((uint32_t)(32 * q) << 16);
+    int lt = 0;
+    for (int tile = pair; tile < tiles; tile += pairs, ++lt) {
+      int tw, tt;
+      place(tile, &tw, &tt);
+      const int b = lt & 1;
+      const bool got = mbar_wait(&sums_full[b], (lt / 2) & 1);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        ok = false;
+        break;
+      }
+      tmem_fence_after();
+      const int64_t m = (int64_t)tw * 256 + rank * 128 + row, n0 = (int64_t)tt * NT;
+      const uint32_t from = lane_at + (b ? kPairSums - NT : 0);
+#pragma unroll 1
+      for (int x = 0; x < NT / 32; ++x) {
+        // the columns that the other buffer shares first: the last ones of the first, the first of the second
+        const int c = 32 * (C::kOver && !b ? NT / 32 - 1 - x : x);
+        uint32_t v[32];
+        tmem_ld32(v, from + c);
+        tmem_wait_ld(v);
+        if (C::kOver && x == C::kOver / 32 - 1) {
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead_bar(&shared_empty));
+        }
+        if (x == NT / 32 - 1) {
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead_bar(&sums_empty[b]));
+        }
+        if (m < p.ws.rows && n0 + c < p.ts.rows) put32(p, m, n0 + c, p.ts.rows, v);
+      }
+    }
+  } else {
+    const int r = threadIdx.x - 192;
+    int it = 0;
+    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+      int tw, tt;
+      place(tile, &tw, &tt);
+      const int64_t ar = (int64_t)tw * 256 + rank * 128 + r;
+      const int64_t b0 = (int64_t)tt * NT + r, b1 = NT > 128 && r + 128 < NT ? b0 + 128 : (int64_t)p.ts.rows;
+      ScaleGroup<F4> a = load_scales<F4>(p.ws, ar, 0), u = load_scales<F4>(p.ts, b0, 0), v = load_scales<F4>(p.ts, b1, 0);
+      for (int i0 = 0; i0 < p.kblocks && ok; i0 += 4) {
+        // the next four blocks' are on their way meanwhile
+        const bool more = i0 + 4 < p.kblocks;
+        const ScaleGroup<F4> a2 = load_scales<F4>(p.ws, more ? ar : p.ws.rows, i0 + 4);
+        const ScaleGroup<F4> u2 = load_scales<F4>(p.ts, more ? b0 : p.ts.rows, i0 + 4);
+        const ScaleGroup<F4> v2 = load_scales<F4>(p.ts, more ? b1 : p.ts.rows, i0 + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (i0 + j >= p.kblocks) break;
+          const int st = it % ST;
+          if (it >= ST) {
+            const bool got = mbar_wait(&empty[st], (it / ST - 1) & 1);
+            if (!__all_sync(0xFFFFFFFFu, got)) {
+              ok = false;
+              break;
+            }
+          }
+          const uint32_t at = scales + st * C::kScales;
+          store_scales<F4>(at, r, a, j);
+          store_scales<F4>(at + C::kScaleA, r, u, j, 1024);
+          store_scales<F4>(at + C::kScaleA + 512, r, v, j, 1024);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead_bar(&full[st]));
+          ++it;
+        }
+        a = a2;
+        u = u2;
+        v = v2;
+      }
+    }
+  }
+  if (!ok) {
+    // loads in flight land (within microseconds) before the CTAs leave
+    if (lane == 0) atomicAdd(&g_mm_wait_timeouts, 1u);
+    const long long until = clock64() + (1ll << 24);
+    while (clock64() < until) __nanosleep(1000);
+  }
+  __syncwarp();
+  tmem_fence_before();
+  cluster_barrier();                       // barriers and shared memory are no longer used by the other CTA
+  if (warp == 1) {
+    tmem_fence_after();
+    tmem_free_pair(tmem, 512);
   }
 }
 
@@ -303,14 +619,52 @@ static cudaError_t encode_codes(CUtensorMap* map, const MxView& m, int box) {
              : cudaErrorInvalidValue;
 }
 static MmScales scales_of(const MxView& m) {
-  const int64_t block = m.format == FP8Q_E2M1 ? 8 : 4;
+  const uintptr_t starts = reinterpret_cast<uintptr_t>(m.e8m0) | (m.rows == 1 ? 0u : (uintptr_t)m.e_stride);
   MmScales s;
   s.e8m0 = m.e8m0;
   s.stride = m.e_stride;
   s.rows = (int32_t)m.rows;
   s.bytes = (int32_t)(m.cols / 32);
-  s.whole = reinterpret_cast<uintptr_t>(m.e8m0) % block == 0 && (m.rows == 1 || m.e_stride % block == 0);
+  s.align = starts % 16 == 0 ? 16 : starts % 8 == 0 ? 8 : starts % 4 == 0 ? 4 : 1;
   return s;
+}
+
+static cudaError_t set_args(MmArgs* a, const MxProduct& p, const MxView& w, const MxView& t, int w_box, int t_box) {
+  cudaError_t e = encode_codes(&a->w, w, w_box);
+  if (e == cudaSuccess) e = encode_codes(&a->t, t, t_box);
+  a->ws = scales_of(w);
+  a->ts = scales_of(t);
+  a->kblocks = (int32_t)((w.row_bytes() + 127) / 128);
+  a->out = p.out;
+  a->add = p.add;
+  a->out_stride = p.out_stride;
+  a->add_stride = p.add_stride;
+  a->fp32 = p.fp32;
+  const int size = p.fp32 ? 4 : 2;
+  a->out_vector = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size)) % 32) == 0;
+  a->add_vector = ((reinterpret_cast<uintptr_t>(p.add) | (uintptr_t)(p.add_stride * size)) % 16) == 0;
+  return e;
+}
+static cudaError_t launch_clusters(const void* kern, MmArgs& a, int64_t ctas, int cluster, int threads, int smem,
+                                   cudaStream_t s, int* launches) {
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  void* args[] = {&a};
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, kern, args);
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
 template <bool F4, int NT>
@@ -322,46 +676,43 @@ static cudaError_t launch_split(const MxProduct& p, const MxView& w, const MxVie
   cudaError_t e = kernel_occupancy(kern, kSplitThreads, C::kSmem, &occ);
   if (e != cudaSuccess) return e;
   MmArgs a;
-  if ((e = encode_codes(&a.w, w, 128)) != cudaSuccess) return e;
-  if ((e = encode_codes(&a.t, t, NT)) != cudaSuccess) return e;
-  a.ws = scales_of(w);
-  a.ts = scales_of(t);
-  a.kblocks = (int32_t)((w.row_bytes() + 127) / 128);
+  if ((e = set_args(&a, p, w, t, 128, NT)) != cudaSuccess) return e;
   a.w_tiles = (int32_t)((w.rows + 127) / 128);
-  const int64_t tiles = (int64_t)a.w_tiles * ((t.rows + NT - 1) / NT);
+  a.t_tiles = (int32_t)((t.rows + NT - 1) / NT);
+  const int64_t tiles = (int64_t)a.w_tiles * a.t_tiles;
   const int sms = sm_count(device_of_current());
   int splits = 1;
   while (splits < 8 && tiles * splits * 2 <= 2 * sms && a.kblocks / (splits * 2) >= 2) splits *= 2;
   a.splits = splits;
   a.idesc = mx_idesc(F4, w.format, t.format, 128, NT);
-  a.out = p.out;
-  a.add = p.add;
-  a.out_stride = p.out_stride;
-  a.add_stride = p.add_stride;
-  a.fp32 = p.fp32;
   a.w_is_a = w_is_a;
-  if (tiles * splits > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * splits));
-  cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = splits;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = splits > 1 ? 2 : 1;
-  void* args[] = {&a};
-  e = cudaLaunchKernelExC(&cfg, kern, args);
-  if (e == cudaSuccess) ++*launches;
-  return e;
+  return launch_clusters(kern, a, tiles * splits, splits, kSplitThreads, C::kSmem, s, launches);
+}
+
+template <bool F4, int NT>
+static cudaError_t launch_pair(const MxProduct& p, cudaStream_t s, int* launches) {
+  using C = PairCfg<F4, NT>;
+  const void* kern = reinterpret_cast<const void*>(mm_pair_kernel<F4, NT>);
+  int occ = 1;
+  cudaError_t e = kernel_occupancy(kern, kPairThreads, C::kSmem, &occ);
+  if (e != cudaSuccess) return e;
+  MmArgs a;
+  if ((e = set_args(&a, p, p.a, p.b, 128, NT / 2)) != cudaSuccess) return e;
+  a.w_tiles = (int32_t)((p.a.rows + 255) / 256);
+  a.t_tiles = (int32_t)((p.b.rows + NT - 1) / NT);
+  const int64_t tiles = (int64_t)a.w_tiles * a.t_tiles;
+  if (tiles > (1 << 27)) return cudaErrorInvalidValue;          // 32-bit tile counts
+  a.splits = 1;
+  a.idesc = mx_idesc(F4, p.a.format, p.b.format, 256, NT);
+  a.w_is_a = 1;
+  const int64_t pairs = sm_count(device_of_current()) / 2;
+  return launch_clusters(kern, a, 2 * (tiles < pairs ? tiles : pairs), 2, kPairThreads, C::kSmem, s, launches);
 }
 
 template <bool F4>
 static cudaError_t launch_format(const MxProduct& p, cudaStream_t s, int* launches) {
+  const int64_t pair_tiles = ((p.a.rows + 255) / 256) * ((p.b.rows + 255) / 256);
+  if (pair_tiles >= 40) return launch_pair<F4, 256>(p, s, launches);
   const bool w_is_a = p.a.rows > p.b.rows;           // the operand with more rows has the 128-row tiles
   const MxView &w = w_is_a ? p.a : p.b, &t = w_is_a ? p.b : p.a;
   if (t.rows <= 16) return launch_split<F4, 16>(p, w, t, w_is_a, s, launches);

@@ -188,7 +188,8 @@ def check_product(a, b, out, add=None):
 
 SHAPES = [(1, 1, 32), (1, 8192, 2048), (2, 130, 64), (3, 7, 96), (16, 2048, 8192), (17, 300, 352), (31, 129, 1056),
           (33, 128, 256), (64, 2048, 4096), (65, 257, 512), (128, 128, 128), (129, 4100, 288), (200, 200, 4096),
-          (1001, 1055, 2080), (1024, 40, 32), (4097, 3, 160), (300, 9000, 96), (777, 1300, 8224), (2500, 2100, 224)]
+          (1001, 1055, 2080), (1024, 40, 32), (4097, 3, 160), (300, 9000, 96), (777, 1300, 8224), (2500, 2100, 224), (9000, 5000, 32),
+          (5120, 4096, 1024), (4100, 2060, 8224)]
 PAIRS = [(kv.E2M1, kv.E2M1), (kv.E4M3, kv.E4M3), (kv.E5M2, kv.E4M3), (kv.E4M3, kv.E5M2), (kv.E5M2, kv.E5M2)]
 
 
@@ -204,7 +205,7 @@ def test_products(m, n, k, fmts):
 
 
 @pytest.mark.parametrize("fmts", PAIRS)
-@pytest.mark.parametrize("m,n,k", [(5, 333, 416), (300, 257, 608), (1300, 1500, 1056)])
+@pytest.mark.parametrize("m,n,k", [(5, 333, 416), (300, 257, 608), (1300, 1500, 1056), (2100, 2601, 800), (6000, 600, 4640)])
 def test_products_of_slices_with_add(m, n, k, fmts):
     """Slices as operands, out and add rows inside wider ones whose other
     values stay; add of its own, and out itself."""
@@ -254,7 +255,7 @@ def test_one_scale_and_one_element_at_a_time():
             assert torch.equal(out.double(), values(x) @ values(y).T)
 
 
-@pytest.mark.parametrize("m,n", [(3, 200), (300, 500), (1200, 1400)])
+@pytest.mark.parametrize("m,n", [(3, 200), (300, 500), (1200, 1400), (2300, 2400)])
 def test_products_pass_nan_on_to_their_rows_only(m, n):
     a, b = random_mx(m, 256, kv.E4M3, 1), random_mx(n, 256, kv.E4M3, 2)
     a.e8m0[1, 3] = 255
@@ -272,7 +273,7 @@ def test_products_pass_nan_on_to_their_rows_only(m, n):
     assert torch.equal(out.isnan(), nan)
 
 
-@pytest.mark.parametrize("m,n,k", [(4, 500, 4096), (700, 900, 2048)])
+@pytest.mark.parametrize("m,n,k", [(4, 500, 4096), (700, 900, 2048), (2600, 2400, 1024)])
 def test_products_repeat_and_replay(m, n, k):
     """The same bits from call to call, on another stream and from a graph whose inputs change."""
     a, b = random_mx(m, k, kv.E2M1, 1), random_mx(n, k, kv.E2M1, 2)
