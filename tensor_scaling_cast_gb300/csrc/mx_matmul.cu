@@ -125,6 +125,12 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
                : "memory");
 }
 
+// The warp's index as a value that the compiler knows to be the warp's: the
+// issuing warps' addresses and descriptors then stay in uniform registers,
+// where the tensor core instructions take them from.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -154,7 +160,7 @@ struct SplitCfg {
   // two CTAs per SM, so that one's loads run while the other starts or ends
   static constexpr int kStages = 112 * 1024 / kStage;
   static constexpr int kSmem = kStages * kStage + 1024;
-  static constexpr int kColumns = NT + 16 <= 32 ? 32 : NT + 16 <= 64 ? 64 : NT + 16 <= 128 ? 128 : 256;
+  static constexpr int kColumns = NT + 32 <= 64 ? 64 : NT + 32 <= 128 ? 128 : 256;    // sums, scales of two K blocks
   static_assert(kStage % 1024 == 0 && 128 * NT * 4 <= kStages * kStage, "swizzled tiles; the parts of the sum");
 };
 constexpr int kSplitThreads = 192;         // TMA, products, and four warps of scales that end as the epilogue
@@ -166,8 +172,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[ST], empty[ST], done;
   __shared__ uint32_t s_tmem;
-  const uint32_t smem = smem_addr(smem_raw) + (-smem_addr(smem_raw) & 1023u);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t smem = uniform(smem_addr(smem_raw) + (-smem_addr(smem_raw) & 1023u));
+  const int warp = warp_index(), lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x == 0) {
@@ -186,7 +192,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
   tmem_fence_after();
   // not before: the next grid's CTAs may take tensor memory once they come to the SM
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = uniform(s_tmem);
   const uint32_t rank = p.splits > 1 ? cluster_rank() : 0u;
   const int tile = blockIdx.x / p.splits;
   const int tt = tile / p.w_tiles, tw = tile - tt * p.w_tiles;
@@ -212,34 +218,45 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
         for (int k = max(0, i - ST); k < i; ++k) mbar_wait(&full[k % ST], (k / ST) & 1);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t sf_w = tmem + NT, sf_t = tmem + NT + 8;
-      const uint32_t hi = desc_hi(1024);
-      for (int i = 0; i < n; ++i) {
-        const int st = i % ST;
-        if (!mbar_wait(&full[st], (i / ST) & 1)) {
-          ok = false;
-          break;
-        }
-        tmem_fence_after();
-        const uint32_t at = smem + st * C::kStage;
-        // copies and products are carried out in the order of their issue
+    const uint32_t hi = desc_hi(1024);
+    // a block's scales are copied before the block before it is multiplied (see mm_pair_kernel)
+    const auto copy = [&](int i) {
+      const int st = i % ST;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (i / ST) & 1))) return false;
+      tmem_fence_after();
+      const uint32_t at = smem + st * C::kStage, to = tmem + NT + (i & 1) * 16;
+      if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < (F4 ? 2 : 1); ++c) {
-          sf_copy<1>(sf_w + 4 * c, sf_desc(at + C::kWs + 512 * c));
-          sf_copy<1>(sf_t + 4 * c, sf_desc(at + C::kTs + 512 * c));
+          sf_copy<1>(to + 4 * c, sf_desc(at + C::kWs + 512 * c));
+          sf_copy<1>(to + 8 + 4 * c, sf_desc(at + C::kTs + 512 * c));
         }
-        const uint32_t w_lo = desc_lo(at, 16), t_lo = desc_lo(at + C::kT, 16);
+      }
+      __syncwarp();
+      return true;
+    };
+    ok = copy(0);
+    for (int i = 0; i < n && ok; ++i) {
+      if (i + 1 < n && !copy(i + 1)) {
+        ok = false;
+        break;
+      }
+      const int st = i % ST;
+      const uint32_t at = smem + st * C::kStage, sf = tmem + NT + (i & 1) * 16;
+      const uint32_t w_lo = desc_lo(at, 16), t_lo = desc_lo(at + C::kT, 16);
+      if (elect_one()) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const uint32_t col = F4 ? 4 * (s >> 1) : 0;
-          mma_mx<F4, 1>(tmem, w_lo + 2 * s, t_lo + 2 * s, hi, mx_idesc_step<F4>(p.idesc, F4 ? s & 1 : s), sf_w + col,
-                        sf_t + col, i > 0 || s > 0);
+          mma_mx<F4, 1>(tmem, w_lo + 2 * s, t_lo + 2 * s, hi, mx_idesc_step<F4>(p.idesc, F4 ? s & 1 : s), sf + col,
+                        sf + 8 + col, i > 0 || s > 0);
         }
         mma_commit(&empty[st]);
       }
-      mma_commit(&done);
+      __syncwarp();
     }
+    if (elect_one()) mma_commit(&done);
+    __syncwarp();
   } else {
     const int r = threadIdx.x - 64;
     const int64_t wr = (int64_t)tw * 128 + r, tr = r < NT ? (int64_t)tt * NT + r : p.ts.rows;
@@ -339,12 +356,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
 // tiles of 256 rows of a and NT of b.  Each CTA loads half the rows of both, so
 // that an SM reads 32 bytes of K of (128 + NT / 2) rows for 128 x NT sums: for
 // NT = 256 64 bytes a cycle at the 4-bit rate, and one CTA by itself would read
-// 96.  Sums stay in tensor memory, in two buffers that end at column 480 (the
-// scales have the rest); for NT > 240 the buffers share some columns, which the
+// 96.  Sums stay in tensor memory, in two buffers (the scales have the last
+// columns); where the two do not fit, they share some columns, which the
 // epilogue reads first, so that the next tile's products start while the others
 // are still being stored.
 constexpr int kPairThreads = 320;          // TMA, products, four warps of epilogue, four of scales
-constexpr int kPairSums = 480;             // tensor-memory columns of the sums
 constexpr int kPairBand = 8;               // tiles of a in a band: pairs in flight cover a compact block
 
 template <bool F4, int NT>
@@ -354,7 +370,11 @@ struct PairCfg {
   static constexpr int kScaleA = F4 ? 1024 : 512, kScales = 3 * kScaleA;   // 128 rows of a, 256 of b
   static constexpr int kStages = (226 * 1024 - 1024) / (kCodes + kScales);
   static constexpr int kSmem = kStages * (kCodes + kScales) + 1024;
-  static constexpr int kOver = 2 * NT > kPairSums ? 2 * NT - kPairSums : 0;
+  // Tensor-memory columns of the scales of a K block, and of the sums: two
+  // buffers of each.
+  static constexpr int kSfB = F4 ? 8 : 4, kSf = 3 * kSfB;
+  static constexpr int kSums = (512 - 2 * kSf) / 32 * 32;
+  static constexpr int kOver = 2 * NT > kSums ? 2 * NT - kSums : 0;
   static_assert(kCodes % 1024 == 0 && kOver % 32 == 0 && NT % 32 == 0 && NT <= 256, "whole chunks of columns");
 };
 
@@ -419,9 +439,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[ST], empty[ST], sums_full[2], sums_empty[2], shared_empty;
   __shared__ uint32_t s_tmem;
-  const uint32_t smem = smem_addr(smem_raw) + (-smem_addr(smem_raw) & 1023u);
+  const uint32_t smem = uniform(smem_addr(smem_raw) + (-smem_addr(smem_raw) & 1023u));
   const uint32_t scales = smem + ST * C::kCodes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
 
   if (threadIdx.x == 0) {
@@ -446,7 +466,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
   tmem_fence_after();
   // not before: the next grid's CTAs may take tensor memory once they come to the SM
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = uniform(s_tmem);
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int tiles = p.w_tiles * p.t_tiles;
   const auto place = [&](int tile, int* tw, int* tt) {
@@ -477,39 +497,60 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      const uint32_t sf_a = tmem + kPairSums, sf_b = sf_a + (F4 ? 8 : 4);
+    if (rank == 0) {
       const uint32_t hi = desc_hi(1024);
-      int it = 0, lt = 0;
-      for (int tile = pair; tile < tiles && ok; tile += pairs, ++lt) {
+      const int own = tiles > pair ? (tiles - pair - 1) / pairs + 1 : 0, total = own * p.kblocks;
+      // A block's scales are copied before the block before it is multiplied:
+      // copies and products are carried out in the order of their issue, and a
+      // product waits for its copies to arrive.
+      int cst = 0, cphase = 0;
+      const auto copy = [&](int it) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[cst], cphase))) return false;
+        tmem_fence_after();
+        const uint32_t from = scales + cst * C::kScales, to = tmem + C::kSums + (it & 1) * C::kSf;
+        if (elect_one()) {
+#pragma unroll
+          for (int c = 0; c < (F4 ? 2 : 1); ++c) {
+            sf_copy<2>(to + 4 * c, sf_desc(from + 512 * c));
+            sf_copy<2>(to + C::kSfB + 8 * c, sf_desc(from + C::kScaleA + 1024 * c));
+            sf_copy<2>(to + C::kSfB + 8 * c + 4, sf_desc(from + C::kScaleA + 1024 * c + 512));
+          }
+        }
+        __syncwarp();
+        if (++cst == ST) {
+          cst = 0;
+          cphase ^= 1;
+        }
+        return true;
+      };
+      if (total) ok = copy(0);
+      int it = 0, st = 0;
+      for (int lt = 0; lt < own && ok; ++lt) {
         const int b = lt & 1;
-        const uint32_t d = tmem + (b ? kPairSums - NT : 0);
-        if (lt >= 2 && !mbar_wait_cluster(&sums_empty[b], (lt / 2 - 1) & 1)) ok = false;
-        if (C::kOver && lt >= 1 && !mbar_wait_cluster(&shared_empty, (lt - 1) & 1)) ok = false;
+        const uint32_t d = tmem + (b ? C::kSums - NT : 0);
+        if (lt >= 2 && !mbar_wait(&sums_empty[b], (lt / 2 - 1) & 1)) ok = false;
+        if (C::kOver && lt >= 1 && !mbar_wait(&shared_empty, (lt - 1) & 1)) ok = false;
+        ok = __all_sync(0xFFFFFFFFu, ok);
         tmem_fence_after();
         for (int i = 0; i < p.kblocks && ok; ++i, ++it) {
-          const int st = it % ST;
-          if (!mbar_wait_cluster(&full[st], (it / ST) & 1)) {
+          if (it + 1 < total && !copy(it + 1)) {
             ok = false;
             break;
           }
-          tmem_fence_after();
-          const uint32_t sf = scales + st * C::kScales, at = smem + st * C::kCodes;
-          // copies and products are carried out in the order of their issue
-#pragma unroll
-          for (int c = 0; c < (F4 ? 2 : 1); ++c) {
-            sf_copy<2>(sf_a + 4 * c, sf_desc(sf + 512 * c));
-            sf_copy<2>(sf_b + 8 * c, sf_desc(sf + C::kScaleA + 1024 * c));
-            sf_copy<2>(sf_b + 8 * c + 4, sf_desc(sf + C::kScaleA + 1024 * c + 512));
-          }
+          const uint32_t at = smem + st * C::kCodes, sf = tmem + C::kSums + (it & 1) * C::kSf;
           const uint32_t a_lo = desc_lo(at, 16), b_lo = desc_lo(at + C::kB, 16);
+          if (elect_one()) {
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
-            mma_mx<F4, 2>(d, a_lo + 2 * s, b_lo + 2 * s, hi, mx_idesc_step<F4>(p.idesc, F4 ? s & 1 : s),
-                          sf_a + (F4 ? 4 * (s >> 1) : 0), sf_b + (F4 ? 8 * (s >> 1) : 0), i > 0 || s > 0);
-          mma_commit_pair(&empty[st]);
+            for (int s = 0; s < 4; ++s)
+              mma_mx<F4, 2>(d, a_lo + 2 * s, b_lo + 2 * s, hi, mx_idesc_step<F4>(p.idesc, F4 ? s & 1 : s),
+                            sf + (F4 ? 4 * (s >> 1) : 0), sf + C::kSfB + (F4 ? 8 * (s >> 1) : 0), i > 0 || s > 0);
+            mma_commit_pair(&empty[st]);
+          }
+          __syncwarp();
+          if (++st == ST) st = 0;
         }
-        mma_commit_pair(&sums_full[b]);
+        if (elect_one()) mma_commit_pair(&sums_full[b]);
+        __syncwarp();
       }
     }
   } else if (warp < 6) {
@@ -527,7 +568,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
       }
       tmem_fence_after();
       const int64_t m = (int64_t)tw * 256 + rank * 128 + row, n0 = (int64_t)tt * NT;
-      const uint32_t from = lane_at + (b ? kPairSums - NT : 0);
+      const uint32_t from = lane_at + (b ? C::kSums - NT : 0);
 #pragma unroll 1
       for (int x = 0; x < NT / 32; ++x) {
         // the columns that the other buffer shares first: the last ones of the first, the first of the second
