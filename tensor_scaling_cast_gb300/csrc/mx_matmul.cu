@@ -29,10 +29,11 @@ struct MmScales {
   const uint8_t* e8m0;
   int64_t stride;
   int32_t rows, bytes;
-  int32_t align;             // every row starts at a multiple of 16, 8 or 4 bytes, or 1
+  int32_t align;             // every row starts at a multiple of 32, 16, 8 or 4 bytes, or 1
 };
 struct MmArgs {
   CUtensorMap w, t;          // codes of the operand with 128-row tiles, of the other
+  CUtensorMap o;             // out, where tma_out
   MmScales ws, ts;
   int32_t kblocks, w_tiles, t_tiles, splits;
   uint32_t idesc;
@@ -40,7 +41,8 @@ struct MmArgs {
   const void* add;
   int64_t out_stride, add_stride;
   int32_t fp32, w_is_a;      // out row: index in w (else in t)
-  int32_t out_vector, add_vector;   // rows start at multiples of 32 (out) and 16 bytes
+  int32_t tma_out;           // out has a tensor map: rows start at multiples of 16 bytes
+  int32_t add_vector;        // so do add's
 };
 
 // Up to four bytes from src on, `left` of them in the row; 1 (0x7F) for the
@@ -71,7 +73,7 @@ __device__ __forceinline__ ScaleGroup<F4> load_scales(const MmScales& s, int64_t
     return g;
   }
   const uint8_t* src = s.e8m0 + row * s.stride + at;
-  if (s.align == 16 && (kb & (F4 ? 1 : 3)) == 0 && at + 4 * W <= s.bytes) {
+  if (s.align >= 16 && (kb & (F4 ? 1 : 3)) == 0 && at + 4 * W <= s.bytes) {
 #pragma unroll
     for (int k = 0; k < W; k += 4) {
       const uint4 v = *reinterpret_cast<const uint4*>(src + 4 * k);
@@ -116,13 +118,6 @@ __device__ __forceinline__ void put(const MmArgs& p, int64_t m, int64_t n, float
   const int64_t at = m * p.out_stride + n;
   if (p.fp32) static_cast<float*>(p.out)[at] = v;
   else static_cast<uint16_t*>(p.out)[at] = (uint16_t)cvt_bf16x2(v, v);
-}
-
-// 32 bytes at a multiple of 32: a whole sector.
-__device__ __forceinline__ void store32(void* dst, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
 }
 
 // The warp's index as a value that the compiler knows to be the warp's: the
@@ -360,7 +355,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
 // columns); where the two do not fit, they share some columns, which the
 // epilogue reads first, so that the next tile's products start while the others
 // are still being stored.
-constexpr int kPairThreads = 320;          // TMA, products, four warps of epilogue, four of scales
+constexpr int kPairThreads = 288;          // TMA, products, four warps of epilogue, three of scales
 constexpr int kPairBand = 8;               // tiles of a in a band: pairs in flight cover a compact block
 
 template <bool F4, int NT>
@@ -368,68 +363,84 @@ struct PairCfg {
   static constexpr int kB = 128 * 128;                             // codes of b within a stage
   static constexpr int kCodes = kB + NT / 2 * 128;
   static constexpr int kScaleA = F4 ? 1024 : 512, kScales = 3 * kScaleA;   // 128 rows of a, 256 of b
-  static constexpr int kStages = (226 * 1024 - 1024) / (kCodes + kScales);
-  static constexpr int kSmem = kStages * (kCodes + kScales) + 1024;
+  static constexpr int kStages = 5;
+  static constexpr int kOut = 4096;                                // 32 rows x 128 bytes of out
+  static constexpr int kSmem = kStages * (kCodes + kScales) + 4 * 2 * kOut + 2048;
+  static constexpr int kGroup = F4 ? 4 : 8;                        // K blocks with 32 bytes of a row's scales
   // Tensor-memory columns of the scales of a K block, and of the sums: two
   // buffers of each.
   static constexpr int kSfB = F4 ? 8 : 4, kSf = 3 * kSfB;
   static constexpr int kSums = (512 - 2 * kSf) / 32 * 32;
   static constexpr int kOver = 2 * NT > kSums ? 2 * NT - kSums : 0;
-  static_assert(kCodes % 1024 == 0 && kOver % 32 == 0 && NT % 32 == 0 && NT <= 256, "whole chunks of columns");
+  static_assert(kCodes % 1024 == 0 && kOver % 32 == 0 && NT % 64 == 0 && NT <= 256 && kSmem <= 227 * 1024, "");
 };
 
-// 32 sums of row m from column n on.
-__device__ __forceinline__ void put32(const MmArgs& p, int64_t m, int64_t n, int64_t cols, uint32_t (&v)[32]) {
-  const bool whole = n + 32 <= cols;
-  if (p.add) {
-    const int64_t at = m * p.add_stride + n;
-    const char* src = static_cast<const char*>(p.add) + at * (p.fp32 ? 4 : 2);
-    if (whole && p.add_vector) {
+// 32 bytes of a row's scales, K blocks `first` on; 1 where there are none.
+__device__ __forceinline__ void load_scales32(const MmScales& s, int64_t row, int at, uint32_t (&g)[8]) {
+  if (row >= s.rows) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = 0x7F7F7F7Fu;
+    return;
+  }
+  const uint8_t* src = s.e8m0 + row * s.stride + at;
+  if (s.align == 32 && at + 32 <= s.bytes) {
+    // read once by this SM: not kept in L1, whose bandwidth the products' operands need
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(g[0]), "=r"(g[1]), "=r"(g[2]), "=r"(g[3]), "=r"(g[4]), "=r"(g[5]), "=r"(g[6]), "=r"(g[7])
+                 : "l"(src));
+  } else if (s.align >= 16 && at + 32 <= s.bytes) {
+    const uint4 x = *reinterpret_cast<const uint4*>(src), y = *reinterpret_cast<const uint4*>(src + 16);
+    g[0] = x.x, g[1] = x.y, g[2] = x.z, g[3] = x.w, g[4] = y.x, g[5] = y.y, g[6] = y.z, g[7] = y.w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = scale_word(src + 4 * k, s.bytes - at - 4 * k);
+  }
+}
+
+// add's 32 values of row m from column n on, onto v.
+__device__ __forceinline__ void add32(const MmArgs& p, int64_t m, int64_t n, int64_t cols, uint32_t (&v)[32]) {
+  const int64_t at = m * p.add_stride + n;
+  const char* src = static_cast<const char*>(p.add) + at * (p.fp32 ? 4 : 2);
+  if (n + 32 <= cols && p.add_vector) {
+    if (p.fp32) {
 #pragma unroll
       for (int k = 0; k < 32; k += 4) {
-        if (p.fp32) {
-          const float4 x = *reinterpret_cast<const float4*>(src + 4 * k);
-          v[k] = __float_as_uint(__uint_as_float(v[k]) + x.x);
-          v[k + 1] = __float_as_uint(__uint_as_float(v[k + 1]) + x.y);
-          v[k + 2] = __float_as_uint(__uint_as_float(v[k + 2]) + x.z);
-          v[k + 3] = __float_as_uint(__uint_as_float(v[k + 3]) + x.w);
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(src + 2 * k);
-          v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(x.x << 16));
-          v[k + 1] = __float_as_uint(__uint_as_float(v[k + 1]) + __uint_as_float(x.x & 0xFFFF0000u));
-          v[k + 2] = __float_as_uint(__uint_as_float(v[k + 2]) + __uint_as_float(x.y << 16));
-          v[k + 3] = __float_as_uint(__uint_as_float(v[k + 3]) + __uint_as_float(x.y & 0xFFFF0000u));
-        }
+        const float4 x = *reinterpret_cast<const float4*>(src + 4 * k);
+        v[k] = __float_as_uint(__uint_as_float(v[k]) + x.x);
+        v[k + 1] = __float_as_uint(__uint_as_float(v[k + 1]) + x.y);
+        v[k + 2] = __float_as_uint(__uint_as_float(v[k + 2]) + x.z);
+        v[k + 3] = __float_as_uint(__uint_as_float(v[k + 3]) + x.w);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (n + k < cols) v[k] = __float_as_uint(__uint_as_float(v[k]) + add_of(p, m, n + k));
-    }
-  }
-  const int64_t at = m * p.out_stride + n;
-  char* dst = static_cast<char*>(p.out) + at * (p.fp32 ? 4 : 2);
-  if (whole && p.out_vector) {
-    if (p.fp32) {
+      for (int k = 0; k < 32; k += 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(src + 2 * k);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int k = 0; k < 32; k += 8) store32(dst + 4 * k, v + k);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 32; k += 16) {
-        uint32_t h[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) h[x] = cvt_bf16x2(__uint_as_float(v[k + 2 * x]), __uint_as_float(v[k + 2 * x + 1]));
-        store32(dst + 2 * k, h);
+        for (int j = 0; j < 4; ++j) {
+          v[k + 2 * j] = __float_as_uint(__uint_as_float(v[k + 2 * j]) + __uint_as_float(w[j] << 16));
+          v[k + 2 * j + 1] = __float_as_uint(__uint_as_float(v[k + 2 * j + 1]) + __uint_as_float(w[j] & 0xFFFF0000u));
+        }
       }
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      if (n + k >= cols) break;
-      if (p.fp32) reinterpret_cast<uint32_t*>(dst)[k] = v[k];
-      else reinterpret_cast<uint16_t*>(dst)[k] = (uint16_t)cvt_bf16x2(__uint_as_float(v[k]), __uint_as_float(v[k]));
-    }
+    for (int k = 0; k < 32; ++k)
+      if (n + k < cols) v[k] = __float_as_uint(__uint_as_float(v[k]) + add_of(p, m, n + k));
   }
+}
+// 32 sums of row m from column n on, one by one.
+__device__ __forceinline__ void put32(const MmArgs& p, int64_t m, int64_t n, int64_t cols, const uint32_t (&v)[32]) {
+  char* dst = static_cast<char*>(p.out) + (m * p.out_stride + n) * (p.fp32 ? 4 : 2);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    if (n + k >= cols) break;
+    if (p.fp32) reinterpret_cast<uint32_t*>(dst)[k] = v[k];
+    else reinterpret_cast<uint16_t*>(dst)[k] = (uint16_t)cvt_bf16x2(__uint_as_float(v[k]), __uint_as_float(v[k]));
+  }
+}
+__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 template <bool F4, int NT>
@@ -440,13 +451,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
   __shared__ __align__(8) uint64_t full[ST], empty[ST], sums_full[2], sums_empty[2], shared_empty;
   __shared__ uint32_t s_tmem;
   const uint32_t smem = uniform(smem_addr(smem_raw) + (-smem_addr(smem_raw) & 1023u));
-  const uint32_t scales = smem + ST * C::kCodes;
+  const uint32_t staging = smem + ST * C::kCodes, scales = staging + 8 * C::kOut;
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], 1 + 8);          // the even CTA's: bytes of both, and both CTAs' scales
+      mbar_init(&full[i], 1 + 6);          // the even CTA's: bytes of both, and both CTAs' scales
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -457,6 +468,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     fence_barrier_init();
     prefetch_tensormap(&p.w);
     prefetch_tensormap(&p.t);
+    prefetch_tensormap(&p.o);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 1) tmem_alloc_pair(&s_tmem, 512);
@@ -478,21 +490,25 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
   bool ok = true;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int it = 0;
-      for (int tile = pair; tile < tiles && ok; tile += pairs) {
-        int tw, tt;
-        place(tile, &tw, &tt);
-        for (int i = 0; i < p.kblocks; ++i, ++it) {
-          const int st = it % ST;
-          if (it >= ST && !mbar_wait(&empty[st], (it / ST - 1) & 1)) {
-            ok = false;
-            break;
-          }
+    int st = 0, phase = 1;                 // a stage's first fill waits for nothing
+    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+      int tw, tt;
+      place(tile, &tw, &tt);
+      for (int i = 0; i < p.kblocks; ++i) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], phase))) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * C::kCodes);
           const uint32_t bar = lead_bar(&full[st]), at = smem + st * C::kCodes;
           tma_load_2d_pair(at, &p.w, bar, i * 128, tw * 256 + (int)rank * 128);
           tma_load_2d_pair(at + C::kB, &p.t, bar, i * 128, tt * NT + (int)rank * (NT / 2));
+        }
+        __syncwarp();
+        if (++st == ST) {
+          st = 0;
+          phase ^= 1;
         }
       }
     }
@@ -556,77 +572,126 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
   } else if (warp < 6) {
     const int q = warp & 3, row = 32 * q + lane;     // this warp's lanes of tensor memory
     const uint32_t lane_at = tmem + ((uint32_t)(32 * q) << 16);
-    int lt = 0;
+    const uint32_t stage = staging + (warp - 2) * 2 * C::kOut;
+    // 128 bytes of 32 rows at a time: through shared memory, in the swizzled
+    // order that conflicts with nothing, and out by TMA
+    const int step = p.fp32 ? 32 : 64;
+    int lt = 0, buf = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++lt) {
       int tw, tt;
       place(tile, &tw, &tt);
       const int b = lt & 1;
-      const bool got = mbar_wait(&sums_full[b], (lt / 2) & 1);
-      if (!__all_sync(0xFFFFFFFFu, got)) {
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sums_full[b], (lt / 2) & 1))) {
         ok = false;
         break;
       }
       tmem_fence_after();
-      const int64_t m = (int64_t)tw * 256 + rank * 128 + row, n0 = (int64_t)tt * NT;
+      const int64_t m0 = (int64_t)tw * 256 + rank * 128 + 32 * q, m = m0 + lane, n0 = (int64_t)tt * NT;
       const uint32_t from = lane_at + (b ? C::kSums - NT : 0);
 #pragma unroll 1
-      for (int x = 0; x < NT / 32; ++x) {
+      for (int x = 0; x < NT; x += step) {
         // the columns that the other buffer shares first: the last ones of the first, the first of the second
-        const int c = 32 * (C::kOver && !b ? NT / 32 - 1 - x : x);
-        uint32_t v[32];
-        tmem_ld32(v, from + c);
-        tmem_wait_ld(v);
-        if (C::kOver && x == C::kOver / 32 - 1) {
-          tmem_fence_before();
+        const int c0 = C::kOver && !b ? NT - step - x : x;
+        const uint32_t to = stage + buf * C::kOut + lane * 128;
+        if (p.tma_out) {
+          if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead_bar(&shared_empty));
         }
-        if (x == NT / 32 - 1) {
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead_bar(&sums_empty[b]));
-        }
-        if (m < p.ws.rows && n0 + c < p.ts.rows) put32(p, m, n0 + c, p.ts.rows, v);
-      }
-    }
-  } else {
-    const int r = threadIdx.x - 192;
-    int it = 0;
-    for (int tile = pair; tile < tiles && ok; tile += pairs) {
-      int tw, tt;
-      place(tile, &tw, &tt);
-      const int64_t ar = (int64_t)tw * 256 + rank * 128 + r;
-      const int64_t b0 = (int64_t)tt * NT + r, b1 = NT > 128 && r + 128 < NT ? b0 + 128 : (int64_t)p.ts.rows;
-      ScaleGroup<F4> a = load_scales<F4>(p.ws, ar, 0), u = load_scales<F4>(p.ts, b0, 0), v = load_scales<F4>(p.ts, b1, 0);
-      for (int i0 = 0; i0 < p.kblocks && ok; i0 += 4) {
-        // the next four blocks' are on their way meanwhile
-        const bool more = i0 + 4 < p.kblocks;
-        const ScaleGroup<F4> a2 = load_scales<F4>(p.ws, more ? ar : p.ws.rows, i0 + 4);
-        const ScaleGroup<F4> u2 = load_scales<F4>(p.ts, more ? b0 : p.ts.rows, i0 + 4);
-        const ScaleGroup<F4> v2 = load_scales<F4>(p.ts, more ? b1 : p.ts.rows, i0 + 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (i0 + j >= p.kblocks) break;
-          const int st = it % ST;
-          if (it >= ST) {
-            const bool got = mbar_wait(&empty[st], (it / ST - 1) & 1);
-            if (!__all_sync(0xFFFFFFFFu, got)) {
-              ok = false;
-              break;
+        for (int h = 0; h < 2; ++h) {
+          if (h && p.fp32) break;
+          const int c = c0 + 32 * h;
+          uint32_t v[32];
+          tmem_ld32(v, from + c);
+          tmem_wait_ld(v);
+          if (p.add && m < p.ws.rows && n0 + c < p.ts.rows) add32(p, m, n0 + c, p.ts.rows, v);
+          if (!p.tma_out) {
+            if (m < p.ws.rows) put32(p, m, n0 + c, p.ts.rows, v);
+          } else if (p.fp32) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              st_shared16(to + ((k ^ (lane & 7)) << 4), v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                w[y] = cvt_bf16x2(__uint_as_float(v[8 * k + 2 * y]), __uint_as_float(v[8 * k + 2 * y + 1]));
+              st_shared16(to + (((4 * h + k) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
             }
           }
-          const uint32_t at = scales + st * C::kScales;
-          store_scales<F4>(at, r, a, j);
-          store_scales<F4>(at + C::kScaleA, r, u, j, 1024);
-          store_scales<F4>(at + C::kScaleA + 512, r, v, j, 1024);
+        }
+        const bool shared_done = C::kOver && x < C::kOver && x + step >= C::kOver, done = x + step >= NT;
+        if (shared_done || done) {
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (shared_done) mbar_arrive_cluster(lead_bar(&shared_empty));
+            if (done) mbar_arrive_cluster(lead_bar(&sums_empty[b]));
+          }
+        }
+        if (p.tma_out) {
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            if (m0 < p.ws.rows && n0 + c0 < p.ts.rows) tma_store_2d_from(&p.o, stage + buf * C::kOut, (int)(n0 + c0), (int)m0);
+            bulk_commit();
+          }
+          buf ^= 1;
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  } else {
+    // Warp 6 has the scales of 128 rows of a, warps 7 and 8 of 128 rows of b
+    // each; a lane has four rows, 32 apart, whose bytes lie together in the
+    // order of the copies: a K block's go out as one or two 16-byte stores.
+    const int part = warp - 6;
+    const MmScales& sc = part == 0 ? p.ws : p.ts;
+    const uint32_t to = scales + (part == 0 ? 0 : C::kScaleA + (part - 1) * 512) + lane * 16;
+    const uint32_t pitch = part == 0 ? 512 : 1024;
+    int st = 0, phase = 1;
+    uint32_t g[4][8], next[4][8];
+    const auto load = [&](int tile, int i0, uint32_t (&v)[4][8]) {
+      int tw, tt;
+      place(min(tile, tiles - 1), &tw, &tt);
+      const int64_t row = part == 0 ? (int64_t)tw * 256 + rank * 128 + lane : (int64_t)tt * NT + (part - 1) * 128 + lane;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        load_scales32(sc, tile < tiles ? row + 32 * j : (int64_t)sc.rows, i0 * (32 / C::kGroup), v[j]);
+    };
+    load(pair, 0, g);
+    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+      for (int i0 = 0; i0 < p.kblocks && ok; i0 += C::kGroup) {
+        // the next group's are on their way meanwhile
+        const bool last = i0 + C::kGroup >= p.kblocks;
+        load(last ? tile + pairs : tile, last ? 0 : i0 + C::kGroup, next);
+#pragma unroll
+        for (int j = 0; j < C::kGroup; ++j) {
+          if (i0 + j >= p.kblocks) break;
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], phase))) {
+            ok = false;
+            break;
+          }
+          const uint32_t at = to + st * C::kScales;
+          constexpr int W = F4 ? 2 : 1;
+#pragma unroll
+          for (int c = 0; c < W; ++c)
+            st_shared16(at + c * pitch, g[0][W * j + c], g[1][W * j + c], g[2][W * j + c], g[3][W * j + c]);
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(lead_bar(&full[st]));
-          ++it;
+          if (++st == ST) {
+            st = 0;
+            phase ^= 1;
+          }
         }
-        a = a2;
-        u = u2;
-        v = v2;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) g[j][k] = next[j][k];
       }
     }
   }
@@ -659,6 +724,20 @@ static cudaError_t encode_codes(CUtensorMap* map, const MxView& m, int box) {
              ? cudaSuccess
              : cudaErrorInvalidValue;
 }
+// Tensor map of out: boxes of 32 rows x 128 bytes, 128-byte swizzle.
+static cudaError_t encode_out(CUtensorMap* map, const MxProduct& p) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const int size = p.fp32 ? 4 : 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)p.b.rows, (cuuint64_t)p.a.rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(p.out_stride * size)};
+  const cuuint32_t shape[2] = {128u / size, 32u}, step[2] = {1u, 1u};
+  return encode(map, p.fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out, dims, strides,
+                shape, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
 static MmScales scales_of(const MxView& m) {
   const uintptr_t starts = reinterpret_cast<uintptr_t>(m.e8m0) | (m.rows == 1 ? 0u : (uintptr_t)m.e_stride);
   MmScales s;
@@ -666,7 +745,7 @@ static MmScales scales_of(const MxView& m) {
   s.stride = m.e_stride;
   s.rows = (int32_t)m.rows;
   s.bytes = (int32_t)(m.cols / 32);
-  s.align = starts % 16 == 0 ? 16 : starts % 8 == 0 ? 8 : starts % 4 == 0 ? 4 : 1;
+  s.align = starts % 32 == 0 ? 32 : starts % 16 == 0 ? 16 : starts % 8 == 0 ? 8 : starts % 4 == 0 ? 4 : 1;
   return s;
 }
 
@@ -681,8 +760,8 @@ static cudaError_t set_args(MmArgs* a, const MxProduct& p, const MxView& w, cons
   a->out_stride = p.out_stride;
   a->add_stride = p.add_stride;
   a->fp32 = p.fp32;
+  a->tma_out = 0;
   const int size = p.fp32 ? 4 : 2;
-  a->out_vector = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size)) % 32) == 0;
   a->add_vector = ((reinterpret_cast<uintptr_t>(p.add) | (uintptr_t)(p.add_stride * size)) % 16) == 0;
   return e;
 }
@@ -739,6 +818,9 @@ static cudaError_t launch_pair(const MxProduct& p, cudaStream_t s, int* launches
   if (e != cudaSuccess) return e;
   MmArgs a;
   if ((e = set_args(&a, p, p.a, p.b, 128, NT / 2)) != cudaSuccess) return e;
+  const int size = p.fp32 ? 4 : 2;
+  a.tma_out = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size)) % 16) == 0;
+  if (a.tma_out && (e = encode_out(&a.o, p)) != cudaSuccess) return e;
   a.w_tiles = (int32_t)((p.a.rows + 255) / 256);
   a.t_tiles = (int32_t)((p.b.rows + NT - 1) / NT);
   const int64_t tiles = (int64_t)a.w_tiles * a.t_tiles;
