@@ -363,16 +363,17 @@ struct PairCfg {
   static constexpr int kB = 128 * 128;                             // codes of b within a stage
   static constexpr int kCodes = kB + NT / 2 * 128;
   static constexpr int kScaleA = F4 ? 1024 : 512, kScales = 3 * kScaleA;   // 128 rows of a, 256 of b
-  static constexpr int kStages = 5;
-  static constexpr int kOut = 4096;                                // 32 rows x 128 bytes of out
-  static constexpr int kSmem = kStages * (kCodes + kScales) + 4 * 2 * kOut + 2048;
+  static constexpr int kOut = 2048;                                // 32 rows x 64 bytes of out, two for each warp
+  static constexpr int kBars = 256;
+  static constexpr int kStages = (227 * 1024 - kBars - 8 * kOut) / (kCodes + kScales);
+  static constexpr int kSmem = kStages * (kCodes + kScales) + 8 * kOut + kBars;
   static constexpr int kGroup = F4 ? 4 : 8;                        // K blocks with 32 bytes of a row's scales
   // Tensor-memory columns of the scales of a K block, and of the sums: two
   // buffers of each.
   static constexpr int kSfB = F4 ? 8 : 4, kSf = 3 * kSfB;
   static constexpr int kSums = (512 - 2 * kSf) / 32 * 32;
   static constexpr int kOver = 2 * NT > kSums ? 2 * NT - kSums : 0;
-  static_assert(kCodes % 1024 == 0 && kOver % 32 == 0 && NT % 64 == 0 && NT <= 256 && kSmem <= 227 * 1024, "");
+  static_assert(kCodes % 1024 == 0 && kOver % 32 == 0 && NT % 32 == 0 && NT <= 256 && kOver < NT && kSmem <= 227 * 1024, "");
 };
 
 // 32 bytes of a row's scales, K blocks `first` on; 1 where there are none.
@@ -447,11 +448,19 @@ template <bool F4, int NT>
 __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_constant__ MmArgs p) {
   using C = PairCfg<F4, NT>;
   constexpr int ST = C::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[ST], empty[ST], sums_full[2], sums_empty[2], shared_empty;
-  __shared__ uint32_t s_tmem;
-  const uint32_t smem = uniform(smem_addr(smem_raw) + (-smem_addr(smem_raw) & 1023u));
+  // all of the SM's shared memory: no room to align within it, and nothing static
+  extern __shared__ __align__(1024) uint8_t pair_smem[];
+  const uint32_t smem = uniform(smem_addr(pair_smem));
   const uint32_t staging = smem + ST * C::kCodes, scales = staging + 8 * C::kOut;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(pair_smem + C::kSmem - C::kBars);
+  uint64_t *const empty = full + ST, *const sums_full = empty + ST, *const sums_empty = sums_full + 2,
+           *const shared_empty = sums_empty + 2;
+  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(shared_empty + 1);
+  static_assert(8 * (2 * ST + 5) + 4 <= C::kBars, "barriers");
+  if (smem & 1023u) {                      // the swizzle's tiles start at multiples of 1024; nothing has begun yet
+    if (threadIdx.x == 0) atomicAdd(&g_mm_wait_timeouts, 1u);
+    return;
+  }
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
 
@@ -464,21 +473,21 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
       mbar_init(&sums_full[i], 1);
       mbar_init(&sums_empty[i], 8);        // the even CTA's: both epilogues
     }
-    mbar_init(&shared_empty, 8);
+    mbar_init(shared_empty, 8);
     fence_barrier_init();
     prefetch_tensormap(&p.w);
     prefetch_tensormap(&p.t);
     prefetch_tensormap(&p.o);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp == 1) tmem_alloc_pair(&s_tmem, 512);
+  if (warp == 1) tmem_alloc_pair(s_tmem, 512);
   tmem_fence_before();
   __syncthreads();
   cluster_barrier();                       // the other CTA's barriers and tensor memory are there
   tmem_fence_after();
   // not before: the next grid's CTAs may take tensor memory once they come to the SM
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t tmem = uniform(s_tmem);
+  const uint32_t tmem = uniform(*s_tmem);
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int tiles = p.w_tiles * p.t_tiles;
   const auto place = [&](int tile, int* tw, int* tt) {
@@ -545,7 +554,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         const int b = lt & 1;
         const uint32_t d = tmem + (b ? C::kSums - NT : 0);
         if (lt >= 2 && !mbar_wait(&sums_empty[b], (lt / 2 - 1) & 1)) ok = false;
-        if (C::kOver && lt >= 1 && !mbar_wait(&shared_empty, (lt - 1) & 1)) ok = false;
+        if (C::kOver && lt >= 1 && !mbar_wait(shared_empty, (lt - 1) & 1)) ok = false;
         ok = __all_sync(0xFFFFFFFFu, ok);
         tmem_fence_after();
         for (int i = 0; i < p.kblocks && ok; ++i, ++it) {
@@ -573,9 +582,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     const int q = warp & 3, row = 32 * q + lane;     // this warp's lanes of tensor memory
     const uint32_t lane_at = tmem + ((uint32_t)(32 * q) << 16);
     const uint32_t stage = staging + (warp - 2) * 2 * C::kOut;
-    // 128 bytes of 32 rows at a time: through shared memory, in the swizzled
+    // 32 columns of 32 rows at a time: through shared memory, in the swizzled
     // order that conflicts with nothing, and out by TMA
-    const int step = p.fp32 ? 32 : 64;
     int lt = 0, buf = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++lt) {
       int tw, tt;
@@ -589,53 +597,44 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
       const int64_t m0 = (int64_t)tw * 256 + rank * 128 + 32 * q, m = m0 + lane, n0 = (int64_t)tt * NT;
       const uint32_t from = lane_at + (b ? C::kSums - NT : 0);
 #pragma unroll 1
-      for (int x = 0; x < NT; x += step) {
+      for (int x = 0; x < NT; x += 32) {
         // the columns that the other buffer shares first: the last ones of the first, the first of the second
-        const int c0 = C::kOver && !b ? NT - step - x : x;
-        const uint32_t to = stage + buf * C::kOut + lane * 128;
-        if (p.tma_out) {
-          if (lane == 0) bulk_wait_read<1>();
-          __syncwarp();
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h && p.fp32) break;
-          const int c = c0 + 32 * h;
-          uint32_t v[32];
-          tmem_ld32(v, from + c);
-          tmem_wait_ld(v);
-          if (p.add && m < p.ws.rows && n0 + c < p.ts.rows) add32(p, m, n0 + c, p.ts.rows, v);
-          if (!p.tma_out) {
-            if (m < p.ws.rows) put32(p, m, n0 + c, p.ts.rows, v);
-          } else if (p.fp32) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              st_shared16(to + ((k ^ (lane & 7)) << 4), v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                w[y] = cvt_bf16x2(__uint_as_float(v[8 * k + 2 * y]), __uint_as_float(v[8 * k + 2 * y + 1]));
-              st_shared16(to + (((4 * h + k) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
-            }
-          }
-        }
-        const bool shared_done = C::kOver && x < C::kOver && x + step >= C::kOver, done = x + step >= NT;
-        if (shared_done || done) {
+        const int c = C::kOver && !b ? NT - 32 - x : x;
+        uint32_t v[32];
+        tmem_ld32(v, from + c);
+        tmem_wait_ld(v);
+        if ((C::kOver && x + 32 == C::kOver) || x + 32 == NT) {
           tmem_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            if (shared_done) mbar_arrive_cluster(lead_bar(&shared_empty));
-            if (done) mbar_arrive_cluster(lead_bar(&sums_empty[b]));
-          }
+          if (lane == 0) mbar_arrive_cluster(lead_bar(x + 32 == NT ? &sums_empty[b] : shared_empty));
         }
-        if (p.tma_out) {
+        if (p.add && m < p.ws.rows && n0 + c < p.ts.rows) add32(p, m, n0 + c, p.ts.rows, v);
+        if (!p.tma_out) {
+          if (m < p.ws.rows) put32(p, m, n0 + c, p.ts.rows, v);
+          continue;
+        }
+        // 64 bytes of a row at a time: 32 columns of bf16, 16 of fp32
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          if (y && !p.fp32) break;
+          const uint32_t to = stage + buf * C::kOut, at = to + lane * 64;
+          const int sw = (lane >> 1) & 3;
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              w[z] = p.fp32 ? v[16 * y + 4 * k + z]
+                            : cvt_bf16x2(__uint_as_float(v[8 * k + 2 * z]), __uint_as_float(v[8 * k + 2 * z + 1]));
+            st_shared16(at + ((k ^ sw) << 4), w[0], w[1], w[2], w[3]);
+          }
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) {
-            if (m0 < p.ws.rows && n0 + c0 < p.ts.rows) tma_store_2d_from(&p.o, stage + buf * C::kOut, (int)(n0 + c0), (int)m0);
+            const int64_t n = n0 + c + 16 * y;
+            if (m0 < p.ws.rows && n < p.ts.rows) tma_store_2d_from(&p.o, to, (int)n, (int)m0);
             bulk_commit();
           }
           buf ^= 1;
@@ -724,16 +723,17 @@ static cudaError_t encode_codes(CUtensorMap* map, const MxView& m, int box) {
              ? cudaSuccess
              : cudaErrorInvalidValue;
 }
-// Tensor map of out: boxes of 32 rows x 128 bytes, 128-byte swizzle.
+// Tensor map of out: boxes of 32 rows x 64 bytes, 64-byte swizzle.
 static cudaError_t encode_out(CUtensorMap* map, const MxProduct& p) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
   const int size = p.fp32 ? 4 : 2;
   const cuuint64_t dims[2] = {(cuuint64_t)p.b.rows, (cuuint64_t)p.a.rows};
   const cuuint64_t strides[1] = {(cuuint64_t)(p.out_stride * size)};
-  const cuuint32_t shape[2] = {128u / size, 32u}, step[2] = {1u, 1u};
+  const cuuint32_t shape[2] = {64u / size, 32u}, step[2] = {1u, 1u};
   return encode(map, p.fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out, dims, strides,
-                shape, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                shape, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
@@ -835,7 +835,12 @@ static cudaError_t launch_pair(const MxProduct& p, cudaStream_t s, int* launches
 template <bool F4>
 static cudaError_t launch_format(const MxProduct& p, cudaStream_t s, int* launches) {
   const int64_t pair_tiles = ((p.a.rows + 255) / 256) * ((p.b.rows + 255) / 256);
-  if (pair_tiles >= 40) return launch_pair<F4, 256>(p, s, launches);
+  if (pair_tiles >= 40) {
+#ifdef FORCE_NT
+    return launch_pair<F4, FORCE_NT>(p, s, launches);
+#endif
+    return launch_pair<F4, 256>(p, s, launches);
+  }
   const bool w_is_a = p.a.rows > p.b.rows;           // the operand with more rows has the 128-row tiles
   const MxView &w = w_is_a ? p.a : p.b, &t = w_is_a ? p.b : p.a;
   if (t.rows <= 16) return launch_split<F4, 16>(p, w, t, w_is_a, s, launches);
