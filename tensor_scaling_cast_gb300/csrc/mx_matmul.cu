@@ -9,6 +9,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "mx_linear.cuh"
 #include "tcgen05.cuh"
 #include "tma.cuh"
@@ -42,7 +44,8 @@ struct MmArgs {
   int64_t out_stride, add_stride;
   int32_t fp32, w_is_a;      // out row: index in w (else in t)
   int32_t tma_out;           // out has a tensor map: rows start at multiples of 16 bytes
-  int32_t add_vector;        // so do add's
+  int32_t out_quads;         // rows of out start at multiples of four elements
+  int32_t add_vector;        // rows of add start at multiples of 16 bytes
 };
 
 // Up to four bytes from src on, `left` of them in the row; 1 (0x7F) for the
@@ -113,11 +116,30 @@ __device__ __forceinline__ float add_of(const MmArgs& p, int64_t m, int64_t n) {
   return p.fp32 ? static_cast<const float*>(p.add)[at]
                 : __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.add)[at] << 16);
 }
-__device__ __forceinline__ void put(const MmArgs& p, int64_t m, int64_t n, float v) {
-  if (p.add) v += add_of(p, m, n);
-  const int64_t at = m * p.out_stride + n;
-  if (p.fp32) static_cast<float*>(p.out)[at] = v;
-  else static_cast<uint16_t*>(p.out)[at] = (uint16_t)cvt_bf16x2(v, v);
+// Four sums of row m from column n on, the first of them inside.
+__device__ __forceinline__ void put4(const MmArgs& p, int64_t m, int64_t n, int64_t cols, const float4& sum) {
+  float v[4] = {sum.x, sum.y, sum.z, sum.w};
+  if (p.add) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (n + k < cols) v[k] += add_of(p, m, n + k);
+  }
+  char* dst = static_cast<char*>(p.out) + (m * p.out_stride + n) * (p.fp32 ? 4 : 2);
+  if (p.out_quads && n + 4 <= cols) {
+    if (p.fp32) *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+    else *reinterpret_cast<uint2*>(dst) = make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (n + k >= cols) break;
+    if (p.fp32) reinterpret_cast<float*>(dst)[k] = v[k];
+    else reinterpret_cast<uint16_t*>(dst)[k] = (uint16_t)cvt_bf16x2(v[k], v[k]);
+  }
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // The warp's index as a value that the compiler knows to be the warp's: the
@@ -134,6 +156,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float4 load_shared4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ float4 cluster_load4(uint32_t addr, uint32_t rank) {
   float4 v;
@@ -156,8 +183,9 @@ struct SplitCfg {
   static constexpr int kStages = 112 * 1024 / kStage;
   static constexpr int kSmem = kStages * kStage + 1024;
   static constexpr int kColumns = NT + 32 <= 64 ? 64 : NT + 32 <= 128 ? 128 : 256;    // sums, scales of two K blocks
-  static_assert(kStage % 1024 == 0 && 128 * NT * 4 <= kStages * kStage, "swizzled tiles; the parts of the sum");
+  static_assert(kStage % 1024 == 0 && 132 * NT * 4 <= kStages * kStage && 128 * (NT + 4) * 4 <= kStages * kStage, "swizzled tiles; the parts of the sum");
 };
+constexpr int kSplitLeast = 4;             // K blocks of a CTA that are worth a join
 constexpr int kSplitThreads = 192;         // TMA, products, and four warps of scales that end as the epilogue
 
 template <bool F4, int NT>
@@ -170,7 +198,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
   const uint32_t smem = uniform(smem_addr(smem_raw) + (-smem_addr(smem_raw) & 1023u));
   const int warp = warp_index(), lane = threadIdx.x & 31;
 
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1 + 4);
@@ -181,6 +208,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
     prefetch_tensormap(&p.w);
     prefetch_tensormap(&p.t);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 1) tmem_alloc(&s_tmem, C::kColumns);
   tmem_fence_before();
   __syncthreads();
@@ -285,60 +313,70 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
     __syncwarp();
     tmem_fence_after();
     const int q = warp & 3, row = 32 * q + lane;     // this warp's lanes of tensor memory
-    const int64_t wi = (int64_t)tw * 128 + row, t0 = (int64_t)tt * NT;
+    // this CTA's sums into shared memory, in rows of out with four words between
+    // them: [row of a][row of b], whichever of the two the 128 rows are
 #pragma unroll 1
     for (int c = 0; c < NT; c += 16) {
       uint32_t v[16];
       tmem_ld16(v, tmem + ((uint32_t)(32 * q) << 16) + c);
       tmem_wait_ld(v);
-      if (p.splits > 1) {
+      if (p.w_is_a) {
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) st_shared16(smem + (row * (NT + 4) + c + k) * 4, v[k], v[k + 1], v[k + 2], v[k + 3]);
+      } else {
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(smem + ((c + k) * 128 + row) * 4), "r"(v[k]) : "memory");
-      } else if (wi < p.ws.rows) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int64_t ti = t0 + c + k;
-          if (ti < p.ts.rows) put(p, p.w_is_a ? wi : ti, p.w_is_a ? ti : wi, __uint_as_float(v[k]));
-        }
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(smem + ((c + k) * 132 + row) * 4), "r"(v[k]) : "memory");
       }
     }
     tmem_fence_before();
   }
   if (!ok && lane == 0) atomicAdd(&g_mm_wait_timeouts, 1u);
   __syncwarp();
-  if (p.splits > 1) {
-    // each CTA of the cluster adds up its share of the columns, parts in order
-    cluster_barrier();
-    if (warp >= 2) {
-      // four rows of a column at a time, all parts' loads in flight together
-      const int c0 = NT * (int)rank / p.splits, c1 = NT * ((int)rank + 1) / p.splits;
-      for (int u = threadIdx.x - 64; u < (c1 - c0) * 32; u += 128) {
-        const int c = c0 + (u >> 5), row = (u & 31) * 4;
-        const int64_t ti = (int64_t)tt * NT + c, wi = (int64_t)tw * 128 + row;
-        if (ti >= p.ts.rows) break;
-        float4 part[8];
+  // Each CTA of the cluster adds up its share of the rows, parts in order, four
+  // neighbours of a row at a time and all parts' loads in flight together.
+  if (p.splits > 1) cluster_barrier();
+  else __syncthreads();
+  const int inner = p.w_is_a ? NT : 128, outer = p.w_is_a ? 128 : NT;
+  const int shift = p.w_is_a ? (NT == 16 ? 2 : NT == 32 ? 3 : NT == 64 ? 4 : 5) : 5, quads = 1 << shift;   // inner / 4
+  const int o0 = outer * (int)rank / p.splits, o1 = outer * ((int)rank + 1) / p.splits;
+  const int64_t m0 = p.w_is_a ? (int64_t)tw * 128 : (int64_t)tt * NT, n0 = p.w_is_a ? (int64_t)tt * NT : (int64_t)tw * 128;
+  const int rows = (int)min((int64_t)outer, (p.w_is_a ? p.ws.rows : p.ts.rows) - m0);
+  const int64_t cols = p.w_is_a ? p.ts.rows : p.ws.rows;
+  const auto join = [&](auto parts) {
+    constexpr int S = decltype(parts)::value, U = 8 / S;
+    const int units = (min(o1, rows) - o0) * quads;
+    for (int u0 = threadIdx.x; u0 < units; u0 += U * kSplitThreads) {
+      float4 part[U][S];
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-          part[s] = s < p.splits ? cluster_load4(smem + (c * 128 + row) * 4, s) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float4 sum = part[0];
+      for (int x = 0; x < U; ++x) {
+        const int u = min(u0 + x * kSplitThreads, units - 1);
+        const uint32_t at = smem + ((o0 + (u >> shift)) * (inner + 4) + (u & (quads - 1)) * 4) * 4;
 #pragma unroll
-        for (int s = 1; s < 8; ++s) {
-          sum.x += part[s].x;
-          sum.y += part[s].y;
-          sum.z += part[s].z;
-          sum.w += part[s].w;
+        for (int s = 0; s < S; ++s) part[x][s] = S == 1 ? load_shared4(at) : cluster_load4(at, s);
+      }
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        const int u = u0 + x * kSplitThreads;
+        const int64_t n = n0 + (u & (quads - 1)) * 4;
+        if (u >= units || n >= cols) continue;
+#pragma unroll
+        for (int s = 1; s < S; ++s) {
+          part[x][0].x += part[x][s].x;
+          part[x][0].y += part[x][s].y;
+          part[x][0].z += part[x][s].z;
+          part[x][0].w += part[x][s].w;
         }
-        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (wi + k < p.ws.rows) put(p, p.w_is_a ? wi + k : ti, p.w_is_a ? ti : wi + k, v[k]);
+        put4(p, m0 + o0 + (u >> shift), n, cols, part[x][0]);
       }
     }
-    cluster_barrier();                               // nobody leaves while its part is read
-  } else {
-    __syncthreads();
-  }
+  };
+  if (p.splits == 1) join(std::integral_constant<int, 1>());
+  else if (p.splits == 2) join(std::integral_constant<int, 2>());
+  else if (p.splits == 4) join(std::integral_constant<int, 4>());
+  else join(std::integral_constant<int, 8>());
+  if (p.splits > 1) cluster_barrier();               // nobody leaves while its part is read
+  else __syncthreads();
   if (warp == 1) {
     tmem_fence_after();
     tmem_free(tmem, C::kColumns);
@@ -439,9 +477,6 @@ __device__ __forceinline__ void put32(const MmArgs& p, int64_t m, int64_t n, int
     if (p.fp32) reinterpret_cast<uint32_t*>(dst)[k] = v[k];
     else reinterpret_cast<uint16_t*>(dst)[k] = (uint16_t)cvt_bf16x2(__uint_as_float(v[k]), __uint_as_float(v[k]));
   }
-}
-__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 template <bool F4, int NT>
@@ -762,6 +797,7 @@ static cudaError_t set_args(MmArgs* a, const MxProduct& p, const MxView& w, cons
   a->fp32 = p.fp32;
   a->tma_out = 0;
   const int size = p.fp32 ? 4 : 2;
+  a->out_quads = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size)) % (4 * size)) == 0;
   a->add_vector = ((reinterpret_cast<uintptr_t>(p.add) | (uintptr_t)(p.add_stride * size)) % 16) == 0;
   return e;
 }
@@ -802,7 +838,7 @@ static cudaError_t launch_split(const MxProduct& p, const MxView& w, const MxVie
   const int64_t tiles = (int64_t)a.w_tiles * a.t_tiles;
   const int sms = sm_count(device_of_current());
   int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= 2 * sms && a.kblocks / (splits * 2) >= 2) splits *= 2;
+  while (splits < 8 && tiles * splits * 2 <= sms && a.kblocks / (splits * 2) >= kSplitLeast) splits *= 2;
   a.splits = splits;
   a.idesc = mx_idesc(F4, w.format, t.format, 128, NT);
   a.w_is_a = w_is_a;
@@ -832,21 +868,40 @@ static cudaError_t launch_pair(const MxProduct& p, cudaStream_t s, int* launches
   return launch_clusters(kern, a, 2 * (tiles < pairs ? tiles : pairs), 2, kPairThreads, C::kSmem, s, launches);
 }
 
+// Cycles that the pair kernel's products take with NT columns a tile: whole
+// rounds of tiles, 2 NT a K block (4 products of NT / 2) and, measured on top,
+// 512 a tile where the buffers of sums share columns, 3% for 224 columns and
+// 30% for 128, which read more for each product.
+static int64_t pair_cycles(const MxProduct& p, int nt, int64_t kblocks, int64_t pairs) {
+  const int64_t tiles = ((p.a.rows + 255) / 256) * ((p.b.rows + nt - 1) / nt);
+  const int64_t block = nt == 256 ? 512 : nt == 224 ? 461 : 333;
+  return (tiles + pairs - 1) / pairs * (kblocks * block + (nt == 256 ? 512 : 100));
+}
+
 template <bool F4>
 static cudaError_t launch_format(const MxProduct& p, cudaStream_t s, int* launches) {
-  const int64_t pair_tiles = ((p.a.rows + 255) / 256) * ((p.b.rows + 255) / 256);
-  if (pair_tiles >= 40) {
-#ifdef FORCE_NT
-    return launch_pair<F4, FORCE_NT>(p, s, launches);
-#endif
-    return launch_pair<F4, 256>(p, s, launches);
+  const bool a_few = p.a.rows <= p.b.rows;
+  const MxView &few = a_few ? p.a : p.b, &many = a_few ? p.b : p.a;
+  const int64_t kblocks = (p.a.row_bytes() + 127) / 128, sms = sm_count(device_of_current());
+  // Few rows on one side, as when decoding: they are the columns of tiles of 128
+  // of the others.
+  if (few.rows <= 16) return launch_split<F4, 16>(p, many, few, !a_few, s, launches);
+  if (few.rows <= 32) return launch_split<F4, 32>(p, many, few, !a_few, s, launches);
+  // Up to 256: they are rows of tiles of 128 and all tiles run at once, with the
+  // sum split where there are few (4 bits, 64 x 2048 x 8192 7.4 us against 11.9
+  // in pairs; 256 x 8192 x 2048, where they do not all run at once, 8.1 against
+  // 6.8).  A short sum needs no split and takes narrower tiles (128 x 4096 x
+  // 1024 4.7 us against 5.4).
+  const int64_t bands = (few.rows + 127) / 128;
+  if (bands <= 2 && bands * ((many.rows + 63) / 64) <= sms) {
+    if (kblocks <= 2 * kSplitLeast && bands * ((many.rows + 31) / 32) <= sms)
+      return launch_split<F4, 32>(p, few, many, a_few, s, launches);
+    return launch_split<F4, 64>(p, few, many, a_few, s, launches);
   }
-  const bool w_is_a = p.a.rows > p.b.rows;           // the operand with more rows has the 128-row tiles
-  const MxView &w = w_is_a ? p.a : p.b, &t = w_is_a ? p.b : p.a;
-  if (t.rows <= 16) return launch_split<F4, 16>(p, w, t, w_is_a, s, launches);
-  if (t.rows <= 32) return launch_split<F4, 32>(p, w, t, w_is_a, s, launches);
-  if (t.rows <= 64) return launch_split<F4, 64>(p, w, t, w_is_a, s, launches);
-  return launch_split<F4, 128>(p, w, t, w_is_a, s, launches);
+  const int64_t c256 = pair_cycles(p, 256, kblocks, sms / 2), c224 = pair_cycles(p, 224, kblocks, sms / 2),
+                c128 = pair_cycles(p, 128, kblocks, sms / 2);
+  if (c128 < c224 && c128 < c256) return launch_pair<F4, 128>(p, s, launches);
+  return c224 < c256 ? launch_pair<F4, 224>(p, s, launches) : launch_pair<F4, 256>(p, s, launches);
 }
 
 cudaError_t launch_mx_matmul(const MxProduct& p, cudaStream_t s, int* launches) {
