@@ -31,11 +31,9 @@ struct MmScales {
   const uint8_t* e8m0;
   int64_t stride;
   int32_t rows, bytes;
-  int32_t align;             // every row starts at a multiple of 32, 16, 8 or 4 bytes, or 1
 };
 struct MmArgs {
   CUtensorMap w, t;          // codes of the operand with 128-row tiles, of the other
-  CUtensorMap o;             // out, where tma_out
   MmScales ws, ts;
   int32_t kblocks, w_tiles, t_tiles, splits;
   uint32_t idesc;
@@ -43,75 +41,125 @@ struct MmArgs {
   const void* add;
   int64_t out_stride, add_stride;
   int32_t fp32, w_is_a;      // out row: index in w (else in t)
-  int32_t tma_out;           // out has a tensor map: rows start at multiples of 16 bytes
-  int32_t out_quads;         // rows of out start at multiples of four elements
-  int32_t add_vector;        // rows of add start at multiples of 16 bytes
+  int32_t out_quads, add_quads;     // rows start at multiples of four elements
+  int32_t out_vector, add_vector;   // of 16 bytes
 };
 
-// Up to four bytes from src on, `left` of them in the row; 1 (0x7F) for the
-// others: the codes there are zeros.  Two aligned words hold them, each with a
-// byte of the row in it.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* src, int left) {
-  if (left <= 0) return 0x7F7F7F7Fu;
-  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(src) & 3u);
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(src - off);
-  const uint32_t v = __funnelshift_r(w[0], off && left > (int)(4 - off) ? w[1] : 0u, 8 * off);
-  const uint32_t mask = left >= 4 ? 0xFFFFFFFFu : (1u << (8 * left)) - 1u;
-  return (v & mask) | (0x7F7F7F7Fu & ~mask);
+__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-// E8M0 bytes of four K blocks of a row, kb, kb + 1, ..: two words each in 4
-// bits, one in 8.
-template <bool F4>
-struct ScaleGroup {
-  uint32_t w[F4 ? 8 : 4];
-};
-template <bool F4>
-__device__ __forceinline__ ScaleGroup<F4> load_scales(const MmScales& s, int64_t row, int kb) {
-  constexpr int W = F4 ? 8 : 4;
-  ScaleGroup<F4> g;
-  const int at = kb * W;
-  if (row >= s.rows) {
+
+// One warp brings the scales of 128 rows (`row0` on, up to `limit`) for K blocks
+// kb0 .. kb0 + n - 1; lane l has rows l, l + 32, l + 64 and l + 96, whose words
+// for the same 128 elements lie together in the order of the copies, so that a
+// K block's go out as one or two 16-byte stores without conflicts.  Rows are
+// read in whole sectors, 32 bytes at multiples of 32, past L1 (whose bandwidth
+// the operands need): a row that starts in the middle of one takes its bytes
+// from two neighbours, of which it reads one at a time.  A sector is read only
+// if some byte of it is the row's.  Bytes past the row's end are 1 (0x7F): the
+// codes there are zeros.
+// put(i, words): K block i's words of the four rows, [word][row]; false: stop.
+template <bool F4, int R, bool SHIFTED, class Put>
+__device__ __forceinline__ bool feed_groups(const uint8_t* const (&base)[R], const uint32_t (&off)[R], const int (&end)[R],
+                                            int bytes, int n, Put put) {
+  constexpr int W = F4 ? 2 : 1, G = 8 / W;           // words of a block, blocks of 32 bytes
+  const auto load = [&](int i, uint32_t (&v)[R][8]) {
 #pragma unroll
-    for (int k = 0; k < W; ++k) g.w[k] = 0x7F7F7F7Fu;
-    return g;
-  }
-  const uint8_t* src = s.e8m0 + row * s.stride + at;
-  if (s.align >= 16 && (kb & (F4 ? 1 : 3)) == 0 && at + 4 * W <= s.bytes) {
-#pragma unroll
-    for (int k = 0; k < W; k += 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(src + 4 * k);
-      g.w[k] = v.x;
-      g.w[k + 1] = v.y;
-      g.w[k + 2] = v.z;
-      g.w[k + 3] = v.w;
-    }
-  } else if (s.align >= (F4 ? 8 : 4) && at + 4 * W <= s.bytes) {
-#pragma unroll
-    for (int k = 0; k < W; k += F4 ? 2 : 1) {
-      if (F4) {
-        const uint2 v = *reinterpret_cast<const uint2*>(src + 4 * k);
-        g.w[k] = v.x;
-        g.w[k + (F4 ? 1 : 0)] = v.y;
+    for (int j = 0; j < R; ++j) {
+      if (32 * i < end[j]) {
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[j][0]), "=r"(v[j][1]), "=r"(v[j][2]), "=r"(v[j][3]), "=r"(v[j][4]), "=r"(v[j][5]),
+                       "=r"(v[j][6]), "=r"(v[j][7])
+                     : "l"(base[j] + 32 * (int64_t)i));
       } else {
-        g.w[k] = *reinterpret_cast<const uint32_t*>(src + 4 * k);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[j][k] = 0x7F7F7F7Fu;
       }
     }
-  } else {
+  };
+  const int groups = (n + G - 1) / G;
+  uint32_t held[R][8], next[R][8], then[SHIFTED ? R : 1][8];
+  load(0, held);
+  if constexpr (SHIFTED) load(1, next);
+#pragma unroll 1
+  for (int i = 0; i < groups; ++i) {
+    uint32_t g[R][8];
+    if constexpr (SHIFTED) {
+      load(i + 2, then);                             // on its way meanwhile
 #pragma unroll
-    for (int k = 0; k < W; ++k) g.w[k] = scale_word(src + 4 * k, s.bytes - at - 4 * k);
+      for (int j = 0; j < R; ++j) {
+        uint32_t x[16];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          x[k] = held[j][k];
+          x[k + 8] = next[j][k];
+        }
+#pragma unroll
+        for (int k = 0; k < 12; ++k) x[k] = off[j] & 16 ? x[k + 4] : x[k];
+#pragma unroll
+        for (int k = 0; k < 10; ++k) x[k] = off[j] & 8 ? x[k + 2] : x[k];
+#pragma unroll
+        for (int k = 0; k < 9; ++k) x[k] = off[j] & 4 ? x[k + 1] : x[k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[j][k] = __funnelshift_r(x[k], x[k + 1], 8 * (off[j] & 3));
+      }
+    } else {
+      load(i + 1, next);
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[j][k] = held[j][k];
+    }
+    if (32 * i + 32 > bytes) {                       // the rows end in this group
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int in = bytes - 32 * i - 4 * k;
+        const uint32_t mask = in >= 4 ? 0xFFFFFFFFu : in <= 0 ? 0u : (1u << (8 * in)) - 1u;
+#pragma unroll
+        for (int j = 0; j < R; ++j) g[j][k] = (g[j][k] & mask) | (0x7F7F7F7Fu & ~mask);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < G; ++b) {
+      if (i * G + b >= n) break;
+      uint32_t words[W][4];
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) words[w][j] = j < R ? g[j < R ? j : 0][W * b + w] : 0x7F7F7F7Fu;
+      if (!put(i * G + b, words)) return false;
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        held[j][k] = next[j][k];
+        if constexpr (SHIFTED) next[j][k] = then[j][k];
+      }
   }
-  return g;
+  return true;
 }
-// Block j's into the place of row r of 128: 512 bytes for each 128 elements.
-template <bool F4>
-__device__ __forceinline__ void store_scales(uint32_t smem, int r, const ScaleGroup<F4>& g, int j, int pitch = 512) {
-  const uint32_t at = smem + (r & 31) * 16 + (r >> 5) * 4;
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(g.w[F4 ? 2 * j : j]) : "memory");
-  if (F4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + pitch), "r"(g.w[F4 ? 2 * j + 1 : j]) : "memory");
+template <bool F4, int ROWS, class Put>
+__device__ __forceinline__ bool feed_scales(const MmScales& sc, int64_t row0, int64_t limit, int kb0, int n, Put put) {
+  constexpr int R = (ROWS + 31) / 32;                // rows of a lane
+  const int lane = threadIdx.x & 31, at = kb0 * (F4 ? 8 : 4), bytes = sc.bytes - at;
+  const uint8_t* base[R];
+  uint32_t off[R], any = 0;
+  int end[R];                                        // bytes from base to the row's end; 0 for no row
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const int64_t row = row0 + lane + 32 * j;
+    const uint8_t* src = sc.e8m0 + row * sc.stride + at;
+    off[j] = (uint32_t)(reinterpret_cast<uintptr_t>(src) & 31u);
+    base[j] = src - off[j];
+    end[j] = row < limit ? (int)off[j] + bytes : 0;
+    any |= off[j];
+  }
+  return __any_sync(0xFFFFFFFFu, any != 0) ? feed_groups<F4, R, true>(base, off, end, bytes, n, put)
+                                           : feed_groups<F4, R, false>(base, off, end, bytes, n, put);
 }
 
 __device__ __forceinline__ float add_of(const MmArgs& p, int64_t m, int64_t n) {
-  if (!p.add) return 0.0f;
   const int64_t at = m * p.add_stride + n;
   return p.fp32 ? static_cast<const float*>(p.add)[at]
                 : __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.add)[at] << 16);
@@ -119,7 +167,17 @@ __device__ __forceinline__ float add_of(const MmArgs& p, int64_t m, int64_t n) {
 // Four sums of row m from column n on, the first of them inside.
 __device__ __forceinline__ void put4(const MmArgs& p, int64_t m, int64_t n, int64_t cols, const float4& sum) {
   float v[4] = {sum.x, sum.y, sum.z, sum.w};
-  if (p.add) {
+  if (p.add && p.add_quads && n + 4 <= cols) {
+    const char* src = static_cast<const char*>(p.add) + (m * p.add_stride + n) * (p.fp32 ? 4 : 2);
+    if (p.fp32) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(src);
+      v[0] += __uint_as_float(x.x << 16), v[1] += __uint_as_float(x.x & 0xFFFF0000u);
+      v[2] += __uint_as_float(x.y << 16), v[3] += __uint_as_float(x.y & 0xFFFF0000u);
+    }
+  } else if (p.add) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (n + k < cols) v[k] += add_of(p, m, n + k);
@@ -136,10 +194,6 @@ __device__ __forceinline__ void put4(const MmArgs& p, int64_t m, int64_t n, int6
     if (p.fp32) reinterpret_cast<float*>(dst)[k] = v[k];
     else reinterpret_cast<uint16_t*>(dst)[k] = (uint16_t)cvt_bf16x2(v[k], v[k]);
   }
-}
-
-__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // The warp's index as a value that the compiler knows to be the warp's: the
@@ -186,7 +240,7 @@ struct SplitCfg {
   static_assert(kStage % 1024 == 0 && 132 * NT * 4 <= kStages * kStage && 128 * (NT + 4) * 4 <= kStages * kStage, "swizzled tiles; the parts of the sum");
 };
 constexpr int kSplitLeast = 4;             // K blocks of a CTA that are worth a join
-constexpr int kSplitThreads = 192;         // TMA, products, and four warps of scales that end as the epilogue
+constexpr int kSplitThreads = 192;         // TMA, products, and four warps of the epilogue, the first two of which bring scales
 
 template <bool F4, int NT>
 __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid_constant__ MmArgs p) {
@@ -200,7 +254,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], 1 + 4);
+      mbar_init(&full[i], 1 + 2);
       mbar_init(&empty[i], 1);
     }
     mbar_init(&done, 1);
@@ -281,33 +335,24 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
     if (elect_one()) mma_commit(&done);
     __syncwarp();
   } else {
-    const int r = threadIdx.x - 64;
-    const int64_t wr = (int64_t)tw * 128 + r, tr = r < NT ? (int64_t)tt * NT + r : p.ts.rows;
-    ScaleGroup<F4> w = load_scales<F4>(p.ws, wr, kb0), t = load_scales<F4>(p.ts, tr, kb0);
-    for (int b = 0; b < n && ok; b += 4) {
-      // the next four blocks' are on their way meanwhile
-      const ScaleGroup<F4> w2 = load_scales<F4>(p.ws, b + 4 < n ? wr : p.ws.rows, kb0 + b + 4);
-      const ScaleGroup<F4> t2 = load_scales<F4>(p.ts, b + 4 < n ? tr : p.ts.rows, kb0 + b + 4);
+    if (warp < 4) {
+      const auto put = [&](uint32_t at, int i, const auto& w) {
+        const int st = i % ST;
+        if (i >= ST && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], (i / ST - 1) & 1))) return false;
+        const uint32_t to = smem + st * C::kStage + at + lane * 16;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = b + j, st = i % ST;
-        if (i >= n) break;
-        if (i >= ST) {
-          const bool got = mbar_wait(&empty[st], (i / ST - 1) & 1);
-          if (!__all_sync(0xFFFFFFFFu, got)) {
-            ok = false;
-            break;
-          }
-        }
-        const uint32_t at = smem + st * C::kStage;
-        store_scales<F4>(at + C::kWs, r, w, j);
-        if (r < NT) store_scales<F4>(at + C::kTs, r, t, j);
+        for (int c = 0; c < (F4 ? 2 : 1); ++c) st_shared16(to + 512 * c, w[c][0], w[c][1], w[c][2], w[c][3]);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
-      }
-      w = w2;
-      t = t2;
+        return true;
+      };
+      if (warp == 2)
+        ok = feed_scales<F4, 128>(p.ws, (int64_t)tw * 128, p.ws.rows, kb0, n,
+                                  [&](int i, const auto& w) { return put(C::kWs, i, w); });
+      else
+        ok = feed_scales<F4, NT>(p.ts, (int64_t)tt * NT, min((int64_t)p.ts.rows, (int64_t)(tt + 1) * NT), kb0, n,
+                                 [&](int i, const auto& w) { return put(C::kTs, i, w); });
     }
     if (!mbar_wait(&done, 0)) ok = false;
     __syncwarp();
@@ -401,11 +446,10 @@ struct PairCfg {
   static constexpr int kB = 128 * 128;                             // codes of b within a stage
   static constexpr int kCodes = kB + NT / 2 * 128;
   static constexpr int kScaleA = F4 ? 1024 : 512, kScales = 3 * kScaleA;   // 128 rows of a, 256 of b
-  static constexpr int kOut = 2048;                                // 32 rows x 64 bytes of out, two for each warp
+  static constexpr int kOut = 4096;                                // 32 rows x 128 bytes of out
   static constexpr int kBars = 256;
-  static constexpr int kStages = (227 * 1024 - kBars - 8 * kOut) / (kCodes + kScales);
-  static constexpr int kSmem = kStages * (kCodes + kScales) + 8 * kOut + kBars;
-  static constexpr int kGroup = F4 ? 4 : 8;                        // K blocks with 32 bytes of a row's scales
+  static constexpr int kStages = (227 * 1024 - kBars - 4 * kOut) / (kCodes + kScales);
+  static constexpr int kSmem = kStages * (kCodes + kScales) + 4 * kOut + kBars;
   // Tensor-memory columns of the scales of a K block, and of the sums: two
   // buffers of each.
   static constexpr int kSfB = F4 ? 8 : 4, kSf = 3 * kSfB;
@@ -414,68 +458,30 @@ struct PairCfg {
   static_assert(kCodes % 1024 == 0 && kOver % 32 == 0 && NT % 32 == 0 && NT <= 256 && kOver < NT && kSmem <= 227 * 1024, "");
 };
 
-// 32 bytes of a row's scales, K blocks `first` on; 1 where there are none.
-__device__ __forceinline__ void load_scales32(const MmScales& s, int64_t row, int at, uint32_t (&g)[8]) {
-  if (row >= s.rows) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) g[k] = 0x7F7F7F7Fu;
+// What mm_pair_kernel does with the staged w columns of `rows` rows at the edges
+// of out, or where rows of out or add start anywhere.
+__device__ __noinline__ void store_part(const MmArgs& p, uint32_t stage, int64_t m0, int64_t n0, int rows, int w, bool wide) {
+  const int lane = threadIdx.x & 31;
+  const int64_t cols = p.ts.rows;
+  if (wide) {
+    const int k = lane & 7;
+#pragma unroll 4
+    for (int r = lane >> 3; r < rows; r += 4)
+      if (n0 + 4 * k < cols) put4(p, m0 + r, n0 + 4 * k, cols, load_shared4(stage + r * 128 + ((k ^ (r & 7)) << 4)));
     return;
   }
-  const uint8_t* src = s.e8m0 + row * s.stride + at;
-  if (s.align == 32 && at + 32 <= s.bytes) {
-    // read once by this SM: not kept in L1, whose bandwidth the products' operands need
-    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(g[0]), "=r"(g[1]), "=r"(g[2]), "=r"(g[3]), "=r"(g[4]), "=r"(g[5]), "=r"(g[6]), "=r"(g[7])
-                 : "l"(src));
-  } else if (s.align >= 16 && at + 32 <= s.bytes) {
-    const uint4 x = *reinterpret_cast<const uint4*>(src), y = *reinterpret_cast<const uint4*>(src + 16);
-    g[0] = x.x, g[1] = x.y, g[2] = x.z, g[3] = x.w, g[4] = y.x, g[5] = y.y, g[6] = y.z, g[7] = y.w;
-  } else {
+  // a row's columns side by side
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r) {
+    uint16_t* dst = static_cast<uint16_t*>(p.out) + (m0 + r) * p.out_stride + n0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) g[k] = scale_word(src + 4 * k, s.bytes - at - 4 * k);
-  }
-}
-
-// add's 32 values of row m from column n on, onto v.
-__device__ __forceinline__ void add32(const MmArgs& p, int64_t m, int64_t n, int64_t cols, uint32_t (&v)[32]) {
-  const int64_t at = m * p.add_stride + n;
-  const char* src = static_cast<const char*>(p.add) + at * (p.fp32 ? 4 : 2);
-  if (n + 32 <= cols && p.add_vector) {
-    if (p.fp32) {
-#pragma unroll
-      for (int k = 0; k < 32; k += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src + 4 * k);
-        v[k] = __float_as_uint(__uint_as_float(v[k]) + x.x);
-        v[k + 1] = __float_as_uint(__uint_as_float(v[k + 1]) + x.y);
-        v[k + 2] = __float_as_uint(__uint_as_float(v[k + 2]) + x.z);
-        v[k + 3] = __float_as_uint(__uint_as_float(v[k + 3]) + x.w);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 32; k += 8) {
-        const uint4 x = *reinterpret_cast<const uint4*>(src + 2 * k);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[k + 2 * j] = __float_as_uint(__uint_as_float(v[k + 2 * j]) + __uint_as_float(w[j] << 16));
-          v[k + 2 * j + 1] = __float_as_uint(__uint_as_float(v[k + 2 * j + 1]) + __uint_as_float(w[j] & 0xFFFF0000u));
-        }
-      }
+    for (int y = 0; y < 64; y += 32) {
+      const int at = y + lane;
+      uint16_t h;
+      asm volatile("ld.shared.u16 %0, [%1];"
+                   : "=h"(h) : "r"(stage + r * 128 + (((at >> 3) ^ (r & 7)) << 4) + (at & 7) * 2) : "memory");
+      if (at < w && n0 + at < cols) dst[at] = h;
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 32; ++k)
-      if (n + k < cols) v[k] = __float_as_uint(__uint_as_float(v[k]) + add_of(p, m, n + k));
-  }
-}
-// 32 sums of row m from column n on, one by one.
-__device__ __forceinline__ void put32(const MmArgs& p, int64_t m, int64_t n, int64_t cols, const uint32_t (&v)[32]) {
-  char* dst = static_cast<char*>(p.out) + (m * p.out_stride + n) * (p.fp32 ? 4 : 2);
-#pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    if (n + k >= cols) break;
-    if (p.fp32) reinterpret_cast<uint32_t*>(dst)[k] = v[k];
-    else reinterpret_cast<uint16_t*>(dst)[k] = (uint16_t)cvt_bf16x2(__uint_as_float(v[k]), __uint_as_float(v[k]));
   }
 }
 
@@ -486,7 +492,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
   // all of the SM's shared memory: no room to align within it, and nothing static
   extern __shared__ __align__(1024) uint8_t pair_smem[];
   const uint32_t smem = uniform(smem_addr(pair_smem));
-  const uint32_t staging = smem + ST * C::kCodes, scales = staging + 8 * C::kOut;
+  const uint32_t staging = smem + ST * C::kCodes, scales = staging + 4 * C::kOut;
   uint64_t* const full = reinterpret_cast<uint64_t*>(pair_smem + C::kSmem - C::kBars);
   uint64_t *const empty = full + ST, *const sums_full = empty + ST, *const sums_empty = sums_full + 2,
            *const shared_empty = sums_empty + 2;
@@ -512,7 +518,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     fence_barrier_init();
     prefetch_tensormap(&p.w);
     prefetch_tensormap(&p.t);
-    prefetch_tensormap(&p.o);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 1) tmem_alloc_pair(s_tmem, 512);
@@ -616,10 +621,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
   } else if (warp < 6) {
     const int q = warp & 3, row = 32 * q + lane;     // this warp's lanes of tensor memory
     const uint32_t lane_at = tmem + ((uint32_t)(32 * q) << 16);
-    const uint32_t stage = staging + (warp - 2) * 2 * C::kOut;
-    // 32 columns of 32 rows at a time: through shared memory, in the swizzled
-    // order that conflicts with nothing, and out by TMA
-    int lt = 0, buf = 0;
+    const uint32_t stage = staging + (warp - 2) * C::kOut;
+    // 32 rows of 128 bytes at a time pass through shared memory, swizzled, so
+    // that they leave in whole lines: 64 columns of bf16, or 32 of fp32 sums
+    // where out is fp32 or something is added.
+    const bool wide = p.fp32 || p.add;
+    const int64_t cols = p.ts.rows;
+    // chunk k of row `lane`; chunk lane % 8 of rows 4 i + lane / 8, i even or odd
+    uint32_t mine[8], theirs[2];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mine[k] = stage + lane * 128 + ((k ^ (lane & 7)) << 4);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) theirs[k] = stage + (lane >> 3) * 128 + (((lane & 7) ^ (4 * k + (lane >> 3))) << 4);
+    int lt = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++lt) {
       int tw, tt;
       place(tile, &tw, &tt);
@@ -629,104 +643,131 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         break;
       }
       tmem_fence_after();
-      const int64_t m0 = (int64_t)tw * 256 + rank * 128 + 32 * q, m = m0 + lane, n0 = (int64_t)tt * NT;
+      const int64_t m0 = (int64_t)tw * 256 + rank * 128 + 32 * q, n0 = (int64_t)tt * NT;
+      const int rows = (int)min((int64_t)32, p.ws.rows - m0);      // may be none
       const uint32_t from = lane_at + (b ? C::kSums - NT : 0);
 #pragma unroll 1
-      for (int x = 0; x < NT; x += 32) {
+      for (int x = 0; x < NT;) {
+        const int w = wide ? 32 : min(64, NT - x);
         // the columns that the other buffer shares first: the last ones of the first, the first of the second
-        const int c = C::kOver && !b ? NT - 32 - x : x;
-        uint32_t v[32];
+        const int c = C::kOver && !b ? NT - w - x : x;
+        uint32_t v[32], u[32];
         tmem_ld32(v, from + c);
+        if (w == 64) tmem_ld32(u, from + c + 32);
         tmem_wait_ld(v);
-        if ((C::kOver && x + 32 == C::kOver) || x + 32 == NT) {
+        tmem_wait_ld(u);
+        const bool shared_done = C::kOver && x < C::kOver && x + w >= C::kOver;
+        x += w;
+        if (shared_done || x == NT) {
           tmem_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead_bar(x + 32 == NT ? &sums_empty[b] : shared_empty));
+          if (lane == 0) mbar_arrive_cluster_relaxed(lead_bar(x == NT ? &sums_empty[b] : shared_empty));
         }
-        if (p.add && m < p.ws.rows && n0 + c < p.ts.rows) add32(p, m, n0 + c, p.ts.rows, v);
-        if (!p.tma_out) {
-          if (m < p.ws.rows) put32(p, m, n0 + c, p.ts.rows, v);
-          continue;
-        }
-        // 64 bytes of a row at a time: 32 columns of bf16, 16 of fp32
+        if (wide) {
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          if (y && !p.fp32) break;
-          const uint32_t to = stage + buf * C::kOut, at = to + lane * 64;
-          const int sw = (lane >> 1) & 3;
-          if (lane == 0) bulk_wait_read<1>();
-          __syncwarp();
+          for (int k = 0; k < 8; ++k) st_shared16(mine[k], v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
+            uint32_t h[4], g[4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z)
-              w[z] = p.fp32 ? v[16 * y + 4 * k + z]
-                            : cvt_bf16x2(__uint_as_float(v[8 * k + 2 * z]), __uint_as_float(v[8 * k + 2 * z + 1]));
-            st_shared16(at + ((k ^ sw) << 4), w[0], w[1], w[2], w[3]);
+            for (int z = 0; z < 4; ++z) {
+              h[z] = cvt_bf16x2(__uint_as_float(v[8 * k + 2 * z]), __uint_as_float(v[8 * k + 2 * z + 1]));
+              g[z] = cvt_bf16x2(__uint_as_float(u[8 * k + 2 * z]), __uint_as_float(u[8 * k + 2 * z + 1]));
+            }
+            st_shared16(mine[k], h[0], h[1], h[2], h[3]);
+            st_shared16(mine[k + 4], g[0], g[1], g[2], g[3]);      // not read where there are 32 columns
           }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            const int64_t n = n0 + c + 16 * y;
-            if (m0 < p.ws.rows && n < p.ts.rows) tma_store_2d_from(&p.o, to, (int)n, (int)m0);
-            bulk_commit();
-          }
-          buf ^= 1;
         }
+        __syncwarp();
+        if (rows == 32 && n0 + c + w <= cols && p.out_vector && (!p.add || p.add_vector)) {
+          const int size = p.fp32 ? 4 : 2;
+          if (p.add) {
+            // four sums of row 4 i + lane / 8 at a time
+            const int64_t n = n0 + c + 4 * (lane & 7), m = m0 + (lane >> 3);
+            const char* src = static_cast<const char*>(p.add) + (m * p.add_stride + n) * size;
+            char* dst = static_cast<char*>(p.out) + (m * p.out_stride + n) * size;
+            uint4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const char* at = src + i * (4 * size) * p.add_stride;
+              if (p.fp32) {
+                x[i] = *reinterpret_cast<const uint4*>(at);
+              } else {
+                const uint2 y = *reinterpret_cast<const uint2*>(at);
+                x[i] = make_uint4(y.x << 16, y.x & 0xFFFF0000u, y.y << 16, y.y & 0xFFFF0000u);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float4 t = load_shared4(theirs[i & 1] + 512 * i);
+              t.x += __uint_as_float(x[i].x);
+              t.y += __uint_as_float(x[i].y);
+              t.z += __uint_as_float(x[i].z);
+              t.w += __uint_as_float(x[i].w);
+              char* at = dst + i * (4 * size) * p.out_stride;
+              if (p.fp32) *reinterpret_cast<float4*>(at) = t;
+              else *reinterpret_cast<uint2*>(at) = make_uint2(cvt_bf16x2(t.x, t.y), cvt_bf16x2(t.z, t.w));
+            }
+          } else if (wide || w == 64) {
+            // whole lines: 16 bytes of row 4 i + lane / 8 at a time
+            char* dst = static_cast<char*>(p.out) + ((m0 + (lane >> 3)) * p.out_stride + n0 + c) * size + (lane & 7) * 16;
+            const int64_t step = 4 * p.out_stride * size;
+            float4 t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = load_shared4(theirs[i & 1] + 512 * i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              *reinterpret_cast<float4*>(dst) = t[i];
+              dst += step;
+            }
+          } else {
+            // half lines: of row 8 i + lane / 4
+            char* dst = static_cast<char*>(p.out) + ((m0 + (lane >> 2)) * p.out_stride + n0 + c) * 2 + (lane & 3) * 16;
+            const int64_t step = 16 * p.out_stride;
+            float4 t[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              t[i] = load_shared4(stage + (8 * i + (lane >> 2)) * 128 + (((lane & 3) ^ (lane >> 2)) << 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              *reinterpret_cast<float4*>(dst) = t[i];
+              dst += step;
+            }
+          }
+        } else {
+          store_part(p, stage, m0, n0 + c, rows, w, wide);
+        }
+        __syncwarp();
       }
     }
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
   } else {
-    // Warp 6 has the scales of 128 rows of a, warps 7 and 8 of 128 rows of b
-    // each; a lane has four rows, 32 apart, whose bytes lie together in the
-    // order of the copies: a K block's go out as one or two 16-byte stores.
+    // warp 6 brings the scales of 128 rows of a, warps 7 and 8 of 128 rows of b each
     const int part = warp - 6;
-    const MmScales& sc = part == 0 ? p.ws : p.ts;
     const uint32_t to = scales + (part == 0 ? 0 : C::kScaleA + (part - 1) * 512) + lane * 16;
     const uint32_t pitch = part == 0 ? 512 : 1024;
     int st = 0, phase = 1;
-    uint32_t g[4][8], next[4][8];
-    const auto load = [&](int tile, int i0, uint32_t (&v)[4][8]) {
-      int tw, tt;
-      place(min(tile, tiles - 1), &tw, &tt);
-      const int64_t row = part == 0 ? (int64_t)tw * 256 + rank * 128 + lane : (int64_t)tt * NT + (part - 1) * 128 + lane;
+    const auto put = [&](int, const auto& w) {
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], phase))) return false;
+      const uint32_t at = to + st * C::kScales;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        load_scales32(sc, tile < tiles ? row + 32 * j : (int64_t)sc.rows, i0 * (32 / C::kGroup), v[j]);
-    };
-    load(pair, 0, g);
-    for (int tile = pair; tile < tiles && ok; tile += pairs) {
-      for (int i0 = 0; i0 < p.kblocks && ok; i0 += C::kGroup) {
-        // the next group's are on their way meanwhile
-        const bool last = i0 + C::kGroup >= p.kblocks;
-        load(last ? tile + pairs : tile, last ? 0 : i0 + C::kGroup, next);
-#pragma unroll
-        for (int j = 0; j < C::kGroup; ++j) {
-          if (i0 + j >= p.kblocks) break;
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], phase))) {
-            ok = false;
-            break;
-          }
-          const uint32_t at = to + st * C::kScales;
-          constexpr int W = F4 ? 2 : 1;
-#pragma unroll
-          for (int c = 0; c < W; ++c)
-            st_shared16(at + c * pitch, g[0][W * j + c], g[1][W * j + c], g[2][W * j + c], g[3][W * j + c]);
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead_bar(&full[st]));
-          if (++st == ST) {
-            st = 0;
-            phase ^= 1;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) g[j][k] = next[j][k];
+      for (int c = 0; c < (F4 ? 2 : 1); ++c) st_shared16(at + c * pitch, w[c][0], w[c][1], w[c][2], w[c][3]);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(lead_bar(&full[st]));
+      if (++st == ST) {
+        st = 0;
+        phase ^= 1;
       }
+      return true;
+    };
+    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+      int tw, tt;
+      place(tile, &tw, &tt);
+      const int64_t row0 = part == 0 ? (int64_t)tw * 256 + rank * 128 : (int64_t)tt * NT + (part - 1) * 128;
+      const MmScales& sc = part == 0 ? p.ws : p.ts;
+      ok = feed_scales<F4, 128>(sc, row0, part == 0 ? (int64_t)sc.rows : min((int64_t)sc.rows, (int64_t)(tt + 1) * NT), 0,
+                                p.kblocks, put);
     }
   }
   if (!ok) {
@@ -758,29 +799,12 @@ static cudaError_t encode_codes(CUtensorMap* map, const MxView& m, int box) {
              ? cudaSuccess
              : cudaErrorInvalidValue;
 }
-// Tensor map of out: boxes of 32 rows x 64 bytes, 64-byte swizzle.
-static cudaError_t encode_out(CUtensorMap* map, const MxProduct& p) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-  if (!encode) return cudaErrorNotSupported;
-  const int size = p.fp32 ? 4 : 2;
-  const cuuint64_t dims[2] = {(cuuint64_t)p.b.rows, (cuuint64_t)p.a.rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)(p.out_stride * size)};
-  const cuuint32_t shape[2] = {64u / size, 32u}, step[2] = {1u, 1u};
-  return encode(map, p.fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out, dims, strides,
-                shape, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? cudaSuccess
-             : cudaErrorInvalidValue;
-}
 static MmScales scales_of(const MxView& m) {
-  const uintptr_t starts = reinterpret_cast<uintptr_t>(m.e8m0) | (m.rows == 1 ? 0u : (uintptr_t)m.e_stride);
   MmScales s;
   s.e8m0 = m.e8m0;
   s.stride = m.e_stride;
   s.rows = (int32_t)m.rows;
   s.bytes = (int32_t)(m.cols / 32);
-  s.align = starts % 32 == 0 ? 32 : starts % 16 == 0 ? 16 : starts % 8 == 0 ? 8 : starts % 4 == 0 ? 4 : 1;
   return s;
 }
 
@@ -795,10 +819,13 @@ static cudaError_t set_args(MmArgs* a, const MxProduct& p, const MxView& w, cons
   a->out_stride = p.out_stride;
   a->add_stride = p.add_stride;
   a->fp32 = p.fp32;
-  a->tma_out = 0;
   const int size = p.fp32 ? 4 : 2;
-  a->out_quads = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size)) % (4 * size)) == 0;
-  a->add_vector = ((reinterpret_cast<uintptr_t>(p.add) | (uintptr_t)(p.add_stride * size)) % 16) == 0;
+  const uintptr_t out = reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size);
+  const uintptr_t add = reinterpret_cast<uintptr_t>(p.add) | (uintptr_t)(p.add_stride * size);
+  a->out_quads = out % (4 * size) == 0;
+  a->add_quads = add % (4 * size) == 0;
+  a->out_vector = out % 16 == 0;
+  a->add_vector = add % 16 == 0;
   return e;
 }
 static cudaError_t launch_clusters(const void* kern, MmArgs& a, int64_t ctas, int cluster, int threads, int smem,
@@ -854,9 +881,6 @@ static cudaError_t launch_pair(const MxProduct& p, cudaStream_t s, int* launches
   if (e != cudaSuccess) return e;
   MmArgs a;
   if ((e = set_args(&a, p, p.a, p.b, 128, NT / 2)) != cudaSuccess) return e;
-  const int size = p.fp32 ? 4 : 2;
-  a.tma_out = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size)) % 16) == 0;
-  if (a.tma_out && (e = encode_out(&a.o, p)) != cudaSuccess) return e;
   a.w_tiles = (int32_t)((p.a.rows + 255) / 256);
   a.t_tiles = (int32_t)((p.b.rows + NT - 1) / NT);
   const int64_t tiles = (int64_t)a.w_tiles * a.t_tiles;

@@ -197,6 +197,12 @@ __device__ __forceinline__ uint32_t lead_bar(const uint64_t* bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same where all that has to come before are tensor-memory loads, which the
+// thread has waited for: without a release, which would wait for its stores to
+// global memory as well.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // Tile into this CTA's shared memory, its bytes counted on a barrier of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
   asm volatile(
