@@ -31,9 +31,11 @@ struct MmScales {
   const uint8_t* e8m0;
   int64_t stride;
   int32_t rows, bytes;
+  int32_t sectors;           // every row is a number of whole 32-byte sectors
 };
 struct MmArgs {
   CUtensorMap w, t;          // codes of the operand with 128-row tiles, of the other
+  CUtensorMap o;             // out, where tma_out
   MmScales ws, ts;
   int32_t kblocks, w_tiles, t_tiles, splits;
   uint32_t idesc;
@@ -41,12 +43,25 @@ struct MmArgs {
   const void* add;
   int64_t out_stride, add_stride;
   int32_t fp32, w_is_a;      // out row: index in w (else in t)
+  int32_t tma_out;                  // out leaves by TMA
   int32_t out_quads, add_quads;     // rows start at multiples of four elements
   int32_t out_vector, add_vector;   // of 16 bytes
 };
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// 32 bytes at a multiple of 32, past L1; all 1 (0x7F) from nowhere.
+__device__ __forceinline__ void load_sector(const uint8_t* src, uint32_t (&v)[8]) {
+  if (src) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(src));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0x7F7F7F7Fu;
+  }
 }
 
 // One warp brings the scales of 128 rows (`row0` on, up to `limit`) for K blocks
@@ -65,17 +80,7 @@ __device__ __forceinline__ bool feed_groups(const uint8_t* const (&base)[R], con
   constexpr int W = F4 ? 2 : 1, G = 8 / W;           // words of a block, blocks of 32 bytes
   const auto load = [&](int i, uint32_t (&v)[R][8]) {
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (32 * i < end[j]) {
-        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(v[j][0]), "=r"(v[j][1]), "=r"(v[j][2]), "=r"(v[j][3]), "=r"(v[j][4]), "=r"(v[j][5]),
-                       "=r"(v[j][6]), "=r"(v[j][7])
-                     : "l"(base[j] + 32 * (int64_t)i));
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[j][k] = 0x7F7F7F7Fu;
-      }
-    }
+    for (int j = 0; j < R; ++j) load_sector(32 * i < end[j] ? base[j] + 32 * (int64_t)i : nullptr, v[j]);
   };
   const int groups = (n + G - 1) / G;
   uint32_t held[R][8], next[R][8], then[SHIFTED ? R : 1][8];
@@ -633,7 +638,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     for (int k = 0; k < 8; ++k) mine[k] = stage + lane * 128 + ((k ^ (lane & 7)) << 4);
 #pragma unroll
     for (int k = 0; k < 2; ++k) theirs[k] = stage + (lane >> 3) * 128 + (((lane & 7) ^ (4 * k + (lane >> 3))) << 4);
-    int lt = 0;
+    int lt = 0, buf = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++lt) {
       int tw, tt;
       place(tile, &tw, &tt);
@@ -646,6 +651,53 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
       const int64_t m0 = (int64_t)tw * 256 + rank * 128 + 32 * q, n0 = (int64_t)tt * NT;
       const int rows = (int)min((int64_t)32, p.ws.rows - m0);      // may be none
       const uint32_t from = lane_at + (b ? C::kSums - NT : 0);
+      if (p.tma_out) {
+        // 32 columns at a time; the next ones leave tensor memory meanwhile
+        uint32_t v[32];
+        tmem_ld32(v, from + (C::kOver && !b ? NT - 32 : 0));
+        tmem_wait_ld(v);
+#pragma unroll 1
+        for (int x = 0; x < NT; x += 32) {
+          // the columns that the other buffer shares first: the last ones of the first, the first of the second
+          const int c = C::kOver && !b ? NT - 32 - x : x;
+          if ((C::kOver && x + 32 == C::kOver) || x + 32 == NT) {
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(lead_bar(x + 32 == NT ? &sums_empty[b] : shared_empty));
+          }
+          uint32_t next[32];
+          if (x + 32 < NT) tmem_ld32(next, from + (C::kOver && !b ? c - 32 : c + 32));
+          // 64 bytes of a row at a time: 32 columns of bf16, 16 of fp32
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            if (y && !p.fp32) break;
+            const uint32_t to = stage + buf * (C::kOut / 2), at = to + lane * 64;
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                w[z] = p.fp32 ? v[16 * y + 4 * k + z]
+                              : cvt_bf16x2(__uint_as_float(v[8 * k + 2 * z]), __uint_as_float(v[8 * k + 2 * z + 1]));
+              st_shared16(at + ((k ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              const int64_t n = n0 + c + 16 * y;
+              if (rows > 0 && n < cols) tma_store_2d_from(&p.o, to, (int)n, (int)m0);
+              bulk_commit();
+            }
+            buf ^= 1;
+          }
+          tmem_wait_ld(next);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = next[k];
+        }
+        continue;
+      }
 #pragma unroll 1
       for (int x = 0; x < NT;) {
         const int w = wide ? 32 : min(64, NT - x);
@@ -741,6 +793,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         __syncwarp();
       }
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   } else {
     // warp 6 brings the scales of 128 rows of a, warps 7 and 8 of 128 rows of b each
     const int part = warp - 6;
@@ -761,13 +815,54 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
       }
       return true;
     };
-    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+    const MmScales& sc = part == 0 ? p.ws : p.ts;
+    const auto first_row = [&](int tile) {
       int tw, tt;
       place(tile, &tw, &tt);
-      const int64_t row0 = part == 0 ? (int64_t)tw * 256 + rank * 128 : (int64_t)tt * NT + (part - 1) * 128;
-      const MmScales& sc = part == 0 ? p.ws : p.ts;
-      ok = feed_scales<F4, 128>(sc, row0, part == 0 ? (int64_t)sc.rows : min((int64_t)sc.rows, (int64_t)(tt + 1) * NT), 0,
-                                p.kblocks, put);
+      return part == 0 ? (int64_t)tw * 256 + rank * 128 : (int64_t)tt * NT + (part - 1) * 128;
+    };
+    if (sc.sectors) {
+      // rows of whole sectors: the next group's are on their way meanwhile, the next tile's too
+      constexpr int W = F4 ? 2 : 1, G = 8 / W;
+      const uint8_t* base[4];
+      uint32_t g[4][8], next[4][8];
+      const auto open = [&](int tile) {
+        const int64_t row = first_row(min(tile, tiles - 1)) + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          base[j] = tile < tiles && row + 32 * j < sc.rows ? sc.e8m0 + (row + 32 * j) * sc.stride : nullptr;
+      };
+      const auto load = [&](int at, uint32_t (&v)[4][8]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_sector(base[j] && at < sc.bytes ? base[j] + at : nullptr, v[j]);
+      };
+      open(pair);
+      load(0, g);
+      for (int tile = pair; tile < tiles && ok; tile += pairs) {
+#pragma unroll 1
+        for (int i = 0; i < p.kblocks && ok; i += G) {
+          if (i + G >= p.kblocks) open(tile + pairs);
+          load(i + G >= p.kblocks ? 0 : (i + G) * 4 * W, next);
+#pragma unroll
+          for (int b = 0; b < G; ++b) {
+            if (i + b >= p.kblocks) break;
+            uint32_t words[W][4];
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) words[w][j] = g[j][W * b + w];
+            ok = put(i + b, words);
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) g[j][k] = next[j][k];
+        }
+      }
+    } else {
+      for (int tile = pair; tile < tiles && ok; tile += pairs)
+        ok = feed_scales<F4, 128>(sc, first_row(tile), sc.rows, 0, p.kblocks, put);
     }
   }
   if (!ok) {
@@ -799,12 +894,27 @@ static cudaError_t encode_codes(CUtensorMap* map, const MxView& m, int box) {
              ? cudaSuccess
              : cudaErrorInvalidValue;
 }
+// Tensor map of out: boxes of 32 rows x 64 bytes, 64-byte swizzle.
+static cudaError_t encode_out(CUtensorMap* map, const MxProduct& p) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const int size = p.fp32 ? 4 : 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)p.b.rows, (cuuint64_t)p.a.rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(p.out_stride * size)};
+  const cuuint32_t shape[2] = {64u / size, 32u}, step[2] = {1u, 1u};
+  return encode(map, p.fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out, dims, strides,
+                shape, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
 static MmScales scales_of(const MxView& m) {
   MmScales s;
   s.e8m0 = m.e8m0;
   s.stride = m.e_stride;
   s.rows = (int32_t)m.rows;
   s.bytes = (int32_t)(m.cols / 32);
+  s.sectors = (reinterpret_cast<uintptr_t>(m.e8m0) | (uintptr_t)m.e_stride | (uintptr_t)s.bytes) % 32 == 0;
   return s;
 }
 
@@ -822,6 +932,7 @@ static cudaError_t set_args(MmArgs* a, const MxProduct& p, const MxView& w, cons
   const int size = p.fp32 ? 4 : 2;
   const uintptr_t out = reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size);
   const uintptr_t add = reinterpret_cast<uintptr_t>(p.add) | (uintptr_t)(p.add_stride * size);
+  a->tma_out = 0;
   a->out_quads = out % (4 * size) == 0;
   a->add_quads = add % (4 * size) == 0;
   a->out_vector = out % 16 == 0;
@@ -873,7 +984,7 @@ static cudaError_t launch_split(const MxProduct& p, const MxView& w, const MxVie
 }
 
 template <bool F4, int NT>
-static cudaError_t launch_pair(const MxProduct& p, cudaStream_t s, int* launches) {
+static cudaError_t launch_pair(const MxProduct& p, bool by_tma, cudaStream_t s, int* launches) {
   using C = PairCfg<F4, NT>;
   const void* kern = reinterpret_cast<const void*>(mm_pair_kernel<F4, NT>);
   int occ = 1;
@@ -889,17 +1000,37 @@ static cudaError_t launch_pair(const MxProduct& p, cudaStream_t s, int* launches
   a.idesc = mx_idesc(F4, p.a.format, p.b.format, 256, NT);
   a.w_is_a = 1;
   const int64_t pairs = sm_count(device_of_current()) / 2;
+  a.tma_out = by_tma;
+  if (a.tma_out && (e = encode_out(&a.o, p)) != cudaSuccess) return e;
   return launch_clusters(kern, a, 2 * (tiles < pairs ? tiles : pairs), 2, kPairThreads, C::kSmem, s, launches);
 }
 
-// Cycles that the pair kernel's products take with NT columns a tile: whole
-// rounds of tiles, 2 NT a K block (4 products of NT / 2) and, measured on top,
-// 512 a tile where the buffers of sums share columns, 3% for 224 columns and
-// 30% for 128, which read more for each product.
-static int64_t pair_cycles(const MxProduct& p, int nt, int64_t kblocks, int64_t pairs) {
+// How the pair kernel would take a product with NT columns a tile, and the
+// cycles of its products: whole rounds of tiles, 2 NT a K block (4 products of
+// NT / 2) and, fitted to measurements, 512 a tile where the buffers of sums share
+// columns, 3% for 224 columns and 30% and 300 a tile for 128, which read more for
+// each product and have more tiles to start.
+struct PairPlan {
+  int64_t cycles;
+  bool by_tma;
+};
+static PairPlan plan_pair(const MxProduct& p, int nt, int64_t kblocks, int64_t pairs) {
   const int64_t tiles = ((p.a.rows + 255) / 256) * ((p.b.rows + nt - 1) / nt);
+  const int64_t size = p.fp32 ? 4 : 2;
+  const bool lines = (reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size)) % 16 == 0;
+  // Out leaves by TMA, a few boxes at a time, where the products of the next
+  // tile take about as long: stores from registers hold up the warps that bring
+  // scales (4 bits, 16384 x 8192 x 2048 96 us against 102).  Under shorter
+  // products stores from registers are done sooner (4096 x 4096 x 1024 12.5 us
+  // against 16.5; one round of tiles, 512 x 8192 x 2048, 7.7 against 8.7), and
+  // under long ones they hardly matter (8192 x 8192 x 8192 158 against 162).
+  const int64_t products = kblocks * 2 * nt;
+  const bool by_tma = lines && !p.add && tiles > pairs && products >= 3000 && products < 12000;
   const int64_t block = nt == 256 ? 512 : nt == 224 ? 461 : 333;
-  return (tiles + pairs - 1) / pairs * (kblocks * block + (nt == 256 ? 512 : 100));
+  int64_t cycles = (tiles + pairs - 1) / pairs * (kblocks * block + (nt == 256 ? 512 : nt == 224 ? 100 : 300));
+  // 448 bytes of bf16 a row are no whole lines: only by TMA
+  if (nt == 224 && !by_tma && !p.fp32 && !p.add) cycles *= 2;
+  return {cycles, by_tma};
 }
 
 template <bool F4>
@@ -922,10 +1053,11 @@ static cudaError_t launch_format(const MxProduct& p, cudaStream_t s, int* launch
       return launch_split<F4, 32>(p, few, many, a_few, s, launches);
     return launch_split<F4, 64>(p, few, many, a_few, s, launches);
   }
-  const int64_t c256 = pair_cycles(p, 256, kblocks, sms / 2), c224 = pair_cycles(p, 224, kblocks, sms / 2),
-                c128 = pair_cycles(p, 128, kblocks, sms / 2);
-  if (c128 < c224 && c128 < c256) return launch_pair<F4, 128>(p, s, launches);
-  return c224 < c256 ? launch_pair<F4, 224>(p, s, launches) : launch_pair<F4, 256>(p, s, launches);
+  const PairPlan c256 = plan_pair(p, 256, kblocks, sms / 2), c224 = plan_pair(p, 224, kblocks, sms / 2),
+                 c128 = plan_pair(p, 128, kblocks, sms / 2);
+  if (c128.cycles < c224.cycles && c128.cycles < c256.cycles) return launch_pair<F4, 128>(p, c128.by_tma, s, launches);
+  return c224.cycles < c256.cycles ? launch_pair<F4, 224>(p, c224.by_tma, s, launches)
+                                   : launch_pair<F4, 256>(p, c256.by_tma, s, launches);
 }
 
 cudaError_t launch_mx_matmul(const MxProduct& p, cudaStream_t s, int* launches) {
