@@ -93,6 +93,9 @@ cudaError_t launch_mx4_rows(const void* x, int dtype, int64_t nelem, int headroo
 // into 32-byte rows before they go out.
 
 using Mx4DualCfg = TpCfg<3, 1, 4, true, 4096, 1, true, 12, true>;
+// Few sub-tiles: chunks of two row tiles and CTAs of two warps, so that every SM
+// has some (see tp_small).
+using Mx4DualSmallCfg = TpCfg<2, 1, 2, true, 4096, 0, true, 2, true>;
 
 static __device__ unsigned int g_mx4_wait_timeouts;   // see fp8q_pipeline_status
 
@@ -284,6 +287,10 @@ static cudaError_t launch_dual(const void* x, int64_t rows, int64_t cols, int ru
 cudaError_t launch_mx4_dual(const void* x, int dtype, int64_t rows, int64_t cols, int rule, int headroom,
                             uint8_t* q_row, uint8_t* e8_row, uint8_t* q_colt, uint8_t* e8_colt,
                             unsigned long long* cr, unsigned long long* cc, cudaStream_t s, int* launches) {
+  if (tp_small(rows, cols, dtype))
+    return dtype == FP8Q_BF16
+               ? launch_dual<FP8Q_BF16, Mx4DualSmallCfg>(x, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s, launches)
+               : launch_dual<FP8Q_F32, Mx4DualSmallCfg>(x, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s, launches);
   return dtype == FP8Q_BF16
              ? launch_dual<FP8Q_BF16, Mx4DualCfg>(x, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s, launches)
              : launch_dual<FP8Q_F32, Mx4DualCfg>(x, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s, launches);

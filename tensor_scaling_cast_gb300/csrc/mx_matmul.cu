@@ -267,7 +267,24 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
     prefetch_tensormap(&p.w);
     prefetch_tensormap(&p.t);
   }
+  const uint32_t rank = p.splits > 1 ? cluster_rank() : 0u;
+  const int tile = blockIdx.x / p.splits;
+  const int tt = tile / p.w_tiles, tw = tile - tt * p.w_tiles;
+  const int kb0 = (int)((int64_t)p.kblocks * rank / p.splits);
+  const int n = (int)((int64_t)p.kblocks * (rank + 1) / p.splits) - kb0;
+  bool ok = true;
+  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const auto load = [&](int i) {
+    const int st = i % ST;
+    const uint32_t at = smem + st * C::kStage;
+    mbar_arrive_expect_tx(&full[st], C::kWs);
+    tma_load_2d_at(at, &p.w, &full[st], (kb0 + i) * 128, tw * 128);
+    tma_load_2d_at(at + C::kT, &p.t, &full[st], (kb0 + i) * 128, tt * NT);
+  };
+  // the first codes are on their way before there is tensor memory
+  if (warp == 0 && lane == 0)
+    for (int i = 0; i < min(n, ST); ++i) load(i);
   if (warp == 1) tmem_alloc(&s_tmem, C::kColumns);
   tmem_fence_before();
   __syncthreads();
@@ -275,26 +292,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
   // not before: the next grid's CTAs may take tensor memory once they come to the SM
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = uniform(s_tmem);
-  const uint32_t rank = p.splits > 1 ? cluster_rank() : 0u;
-  const int tile = blockIdx.x / p.splits;
-  const int tt = tile / p.w_tiles, tw = tile - tt * p.w_tiles;
-  const int kb0 = (int)((int64_t)p.kblocks * rank / p.splits);
-  const int n = (int)((int64_t)p.kblocks * (rank + 1) / p.splits) - kb0;
-  bool ok = true;
 
   if (warp == 0) {
     if (lane == 0) {
-      int i = 0;
+      int i = ST;
       for (; i < n; ++i) {
-        const int st = i % ST;
-        if (i >= ST && !mbar_wait(&empty[st], (i / ST - 1) & 1)) {
+        if (!mbar_wait(&empty[i % ST], (i / ST - 1) & 1)) {
           ok = false;
           break;
         }
-        const uint32_t at = smem + st * C::kStage;
-        mbar_arrive_expect_tx(&full[st], C::kWs);
-        tma_load_2d_at(at, &p.w, &full[st], (kb0 + i) * 128, tw * 128);
-        tma_load_2d_at(at + C::kT, &p.t, &full[st], (kb0 + i) * 128, tt * NT);
+        load(i);
       }
       if (!ok)                                       // loads in flight land before the CTA leaves
         for (int k = max(0, i - ST); k < i; ++k) mbar_wait(&full[k % ST], (k / ST) & 1);
@@ -524,15 +531,22 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     prefetch_tensormap(&p.w);
     prefetch_tensormap(&p.t);
   }
+  __syncwarp();
+  cluster_barrier();                       // the other CTA's barriers are there
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 1) tmem_alloc_pair(s_tmem, 512);
-  tmem_fence_before();
-  __syncthreads();
-  cluster_barrier();                       // the other CTA's barriers and tensor memory are there
-  tmem_fence_after();
   // not before: the next grid's CTAs may take tensor memory once they come to the SM
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t tmem = uniform(*s_tmem);
+  tmem_fence_before();
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  // both CTAs have their tensor memory; the loads of codes do not wait for it
+  const auto wait_for_tmem = [&] {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    tmem_fence_after();
+    return uniform(*s_tmem);
+  };
+  uint32_t tmem = 0;
+  if (warp != 0) tmem = wait_for_tmem();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int tiles = p.w_tiles * p.t_tiles;
   const auto place = [&](int tile, int* tw, int* tt) {
@@ -872,6 +886,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     while (clock64() < until) __nanosleep(1000);
   }
   __syncwarp();
+  if (warp == 0) tmem = wait_for_tmem();
   tmem_fence_before();
   cluster_barrier();                       // barriers and shared memory are no longer used by the other CTA
   if (warp == 1) {

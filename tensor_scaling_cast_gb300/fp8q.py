@@ -508,24 +508,23 @@ class MXMatrix:
                    torch.empty(rows, cols // 32, dtype=torch.uint8, device=device), fmt)
 
 
-def _mx(m):
-    return None if m is None else m._ref
-
-
+# As with the cache, small calls are bound by the host: each shape and stride
+# is read once.
 def _plain(what, t, shape, dtype):
-    """(pointer, row stride) of a plain matrix, or of one left out."""
-    if t is None:
-        return None, 0
-    if t.dtype is not dtype or t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
+    """(pointer, row stride) of a plain matrix."""
+    strides = t.stride()
+    if t.dtype is not dtype or t.shape != shape or (strides[1] != 1 and shape[1] > 1):
         raise TypeError(f"{what}: {dtype} {tuple(shape)} with consecutive elements in a row: got {t.dtype} "
-                        f"{tuple(t.shape)} with strides {t.stride()}")
-    return t.data_ptr(), t.stride(0)
+                        f"{tuple(t.shape)} with strides {strides}")
+    return t.data_ptr(), strides[0]
 
 
 def mx_decode(m: MXMatrix, out: torch.Tensor, stream=None):
     """The values that m's codes stand for, into out [rows, cols] (bf16 or fp32)."""
-    ptr, stride = _plain("mx_decode: out", out, m.shape, out.dtype)
-    st = (_lib or load()).mx_decode(m._ref, ptr, _dtype(out), stride, _stream(stream))
+    dtype = out.dtype
+    ptr, stride = _plain("mx_decode: out", out, m.shape, dtype)
+    st = (_lib or load()).mx_decode(m._ref, ptr, BF16 if dtype is torch.bfloat16 else _dtype(out), stride,
+                                    _stream(stream))
     if st:
         _check(st, "mx_decode")
 
@@ -535,7 +534,7 @@ def mx_matmul(a: MXMatrix, b: MXMatrix, out: torch.Tensor, add=None, stream=None
     shape (out itself, to accumulate).  Both E2M1, or each E4M3 or E5M2."""
     shape, dtype = (a.shape[0], b.shape[0]), out.dtype
     ptr, stride = _plain("mx_matmul: out", out, shape, dtype)
-    add_ptr, add_stride = _plain("mx_matmul: add", add, shape, dtype)
+    add_ptr, add_stride = (None, 0) if add is None else _plain("mx_matmul: add", add, shape, dtype)
     st = (_lib or load()).mx_matmul(a._ref, b._ref, ptr, BF16 if dtype is torch.bfloat16 else _dtype(out), stride,
                                     add_ptr, add_stride, _stream(stream))
     if st:
@@ -551,10 +550,12 @@ def mx_act_forward(act: int, z: torch.Tensor, u=None, z_saved=None, u_saved=None
     if len(shape) != 2:
         raise TypeError(f"mx_act_forward: z is [rows, cols]: got {tuple(shape)}")
     zp, zs = _plain("mx_act_forward: z", z, shape, dtype)
-    up, us = _plain("mx_act_forward: u", u, shape, dtype)
-    hp, hs = _plain("mx_act_forward: h", h, shape, dtype)
-    st = (_lib or load()).mx_act_forward(act, zp, zs, up, us, _dtype(z), shape[0], shape[1], _mx(z_saved),
-                                         _mx(u_saved), rule, hp, hs, _mx(h_mx), _stream(stream))
+    up, us = (None, 0) if u is None else _plain("mx_act_forward: u", u, shape, dtype)
+    hp, hs = (None, 0) if h is None else _plain("mx_act_forward: h", h, shape, dtype)
+    st = (_lib or load()).mx_act_forward(
+        act, zp, zs, up, us, BF16 if dtype is torch.bfloat16 else _dtype(z), shape[0], shape[1],
+        None if z_saved is None else z_saved._ref, None if u_saved is None else u_saved._ref, rule, hp, hs,
+        None if h_mx is None else h_mx._ref, _stream(stream))
     if st:
         _check(st, "mx_act_forward")
 
@@ -567,10 +568,11 @@ def mx_act_backward(act: int, z_saved: MXMatrix, u_saved, dh: torch.Tensor, dz: 
     shape, dtype = z_saved.shape, dh.dtype
     gp, gs = _plain("mx_act_backward: dh", dh, shape, dtype)
     zp, zs = _plain("mx_act_backward: dz", dz, shape, dtype)
-    up, us = _plain("mx_act_backward: du", du, shape, dtype)
-    hp, hs = _plain("mx_act_backward: h", h, shape, dtype)
-    st = (_lib or load()).mx_act_backward(act, z_saved._ref, _mx(u_saved), gp, gs, _dtype(dh), zp, zs, up, us, hp, hs,
-                                          _stream(stream))
+    up, us = (None, 0) if du is None else _plain("mx_act_backward: du", du, shape, dtype)
+    hp, hs = (None, 0) if h is None else _plain("mx_act_backward: h", h, shape, dtype)
+    st = (_lib or load()).mx_act_backward(
+        act, z_saved._ref, None if u_saved is None else u_saved._ref, gp, gs,
+        BF16 if dtype is torch.bfloat16 else _dtype(dh), zp, zs, up, us, hp, hs, _stream(stream))
     if st:
         _check(st, "mx_act_backward")
 
