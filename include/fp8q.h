@@ -540,8 +540,8 @@ FP8Q_API int mx_matmul(const mx_matrix* a, const mx_matrix* b, void* out, int dt
  *   MX_ACT_GELU_TANH  f(z) = z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2
  * Forward: h = f(z) * u, or f(z) where u is NULL, from z and u [rows, cols] of
  * dtype.
- *   z_saved, u_saved  MX(z) and MX(u) under `rule`, E4M3 or E5M2, or NULL (not
- *                     kept; with u, both or neither)
+ *   z_saved, u_saved  MX(z) and MX(u) under `rule`, both E4M3 or both E5M2, or
+ *                     NULL (not kept; with u, both or neither)
  *   h                 [rows, cols] of dtype, or NULL
  *   h_mx              MX(h) under `rule` in any format, of h before its
  *                     rounding to dtype, or NULL

@@ -92,10 +92,10 @@ cudaError_t launch_mx4_rows(const void* x, int dtype, int64_t nelem, int headroo
 // sector, so two row tiles' transposed blocks are gathered in shared memory
 // into 32-byte rows before they go out.
 
-using Mx4DualCfg = TpCfg<3, 1, 4, true, 4096, 1, true, 12, true>;
+using Mx4DualCfg = TpCfg<3, 1, 4, true, 3072, 1, true, 14, true>;
 // Few sub-tiles: chunks of two row tiles and CTAs of two warps, so that every SM
 // has some (see tp_small).
-using Mx4DualSmallCfg = TpCfg<2, 1, 2, true, 4096, 0, true, 2, true>;
+using Mx4DualSmallCfg = TpCfg<2, 1, 2, true, 3072, 0, true, 2, true>;
 
 static __device__ unsigned int g_mx4_wait_timeouts;   // see fp8q_pipeline_status
 
@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) mx4_dual_kernel(
       ebytes |= mx4_block([&](int k) { return elem_bits<DT>(v[k / EPL], k % EPL); }, mag_bits<DT>(pm), rule, headroom,
                           clip_r, o)
                 << (8 * b);
-      if (G::BPR == 2) stage16<32>(ob, lane, b, o[0], o[1], o[2], o[3]);
-      else *reinterpret_cast<uint4*>(ob + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (G::BPR == 2) stage16<32>(ob + 2048, lane, b, o[0], o[1], o[2], o[3]);
+      else *reinterpret_cast<uint4*>(ob + 2048 + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
     }
     {
       uint8_t* e8 = e8_row + (r0 + lane) * cb + (c0 >> 5);
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) mx4_dual_kernel(
     uint32_t w[32], o[4];
     const auto put = [&](int c, const uint32_t (&p)[4]) {
       if (single) *reinterpret_cast<uint4*>(q_colt + (c0 + c) * (rows / 2) + r0 / 2) = make_uint4(p[0], p[1], p[2], p[3]);
-      else stage16<32>(ob + 2048, c, ci & 1, p[0], p[1], p[2], p[3]);
+      else stage16<32>(ob, c, ci & 1, p[0], p[1], p[2], p[3]);
     };
     if (DT == FP8Q_BF16) {
       const int64_t c = c0 + 2 * lane;
@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) mx4_dual_kernel(
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(&qmap, ob, (int)(c0 / 2), (int)r0);
-      if (ci & 1) tma_store_2d(&qtmap, ob + 2048, (int)((r0 - 32) / 2), (int)c0);
+      tma_store_2d(&qmap, ob + 2048, (int)(c0 / 2), (int)r0);
+      if (ci & 1) tma_store_2d(&qtmap, ob, (int)((r0 - 32) / 2), (int)c0);
       bulk_commit();
     }
     pipe.release();

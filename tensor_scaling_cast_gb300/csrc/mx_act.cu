@@ -70,25 +70,58 @@ cudaError_t launch_mx_decode(const MxView& m, void* out, int dtype, int64_t out_
 
 // ---- activations ------------------------------------------------------------------
 
-// f(z) and f'(z).  Where the tensors are bf16 (FAST) the exponential, the
-// reciprocal and the division are the approximate instructions, good to 2^-21
-// of the value next to the result's 2^-8; in 32 bits the exact functions.
+// f(z) and f'(z).  Where the tensors are bf16 (FAST) exponentials and
+// reciprocals are the approximate instructions, good to 2^-22 of the value and
+// 2^-24 of the exponent's argument next to the result's 2^-8 (a reciprocal
+// below 2^-126 is 0); in 32 bits the exact functions.
 template <bool FAST>
-__device__ __forceinline__ float exp_of(float x) { return FAST ? __expf(x) : expf(x); }
+__device__ __forceinline__ float exp_of(float x) {
+  if (!FAST) return expf(x);
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
 template <bool FAST>
-__device__ __forceinline__ float over(float a, float b) { return FAST ? __fdividef(a, b) : a / b; }
+__device__ __forceinline__ float reciprocal(float x) {
+  if (!FAST) return 1.0f / x;
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 template <bool FAST>
 __device__ __forceinline__ float sigmoid(float x) {
-  // __fdividef gives 0 for divisors past 2^126, as the quotient is here
-  return over<FAST>(1.0f, 1.0f + exp_of<FAST>(-x));
+  return reciprocal<FAST>(1.0f + exp_of<FAST>(-x));
+}
+
+// (1 + erf(z / sqrt 2)) / 2 and e = e^(-z z / 2).  Approximate: with x =
+// |z| / sqrt 2 and t = 1 / (1 + 0.425 x), erfc(x) = e t P(t), P the polynomial of
+// degree 7 that is nearest in relative error for x up to 10 (a least-squares fit
+// at Chebyshev points, weights moved towards the largest error: 1.5e-7, and
+// 4.5e-7 as evaluated here); further out e is below 2^-126.
+template <bool FAST>
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  e = exp_of<FAST>(-0.5f * z * z);
+  if (!FAST) return 0.5f * erfcf(-0.70710678118654752f * z);
+  const float t = reciprocal<FAST>(fmaf(0.425f * 0.70710678118654752f, fabsf(z), 1.0f));
+  float p = 0.07147661596536636f;
+  p = fmaf(p, t, -0.3131510317325592f);
+  p = fmaf(p, t, 0.40760907530784607f);
+  p = fmaf(p, t, -0.1032443568110466f);
+  p = fmaf(p, t, 0.2550836503505707f);
+  p = fmaf(p, t, 0.20070675015449524f);
+  p = fmaf(p, t, 0.24184052646160126f);
+  p = fmaf(p, t, 0.23967863619327545f);
+  const float half = 0.5f * t * p * e;
+  return z < 0.0f ? half : 1.0f - half;
 }
 
 template <int ACT, bool FAST, bool WITH_D>
 __device__ __forceinline__ void activation(float z, float& f, float& d) {
   if (ACT == MX_ACT_GELU) {
-    const float p = 0.5f * erfcf(-0.70710678118654752f * z);
+    float e;
+    const float p = normal_cdf<FAST>(z, e);
     f = z * p;
-    if (WITH_D) d = fmaf(z * 0.39894228040143268f, exp_of<FAST>(-0.5f * z * z), p);
+    if (WITH_D) d = fmaf(z * 0.39894228040143268f, e, p);
   } else {
     constexpr float C = 1.5957691216057308f;             // 2 sqrt(2 / pi)
     const float z2 = z * z;
@@ -148,7 +181,7 @@ __device__ __forceinline__ uint32_t absmax_of(const float (&f)[8]) {
 
 constexpr int kActAhead = 2;
 
-template <int ACT, int DT, bool GATED>
+template <int ACT, int DT, bool GATED, int FMT>
 __global__ void __launch_bounds__(kUnitThreads) mx_act_forward_kernel(const __grid_constant__ MxActForward a,
                                                                       const __grid_constant__ Units u) {
   constexpr int U = kActAhead;
@@ -178,8 +211,8 @@ __global__ void __launch_bounds__(kUnitThreads) mx_act_forward_kernel(const __gr
       if (GATED) y[k] = __uint_as_float(bits8<DT>(g[j], k));
     }
     if (a.z_saved.q) {
-      write_block_any(a.z_saved, row[j], col[j], on, x, absmax8<DT>(z[j]), a.rule);
-      if (GATED) write_block_any(a.u_saved, row[j], col[j], on, y, absmax8<DT>(g[j]), a.rule);
+      write_block<FMT>(a.z_saved, row[j], col[j], on, x, absmax8<DT>(z[j]), a.rule);
+      if (GATED) write_block<FMT>(a.u_saved, row[j], col[j], on, y, absmax8<DT>(g[j]), a.rule);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -236,13 +269,16 @@ __global__ void __launch_bounds__(kUnitThreads) mx_act_backward_kernel(const __g
   }
 }
 
+template <int ACT, int DT, bool GATED>
+static const void* forward_of(int format) {
+  return format == FP8Q_E5M2 ? reinterpret_cast<const void*>(mx_act_forward_kernel<ACT, DT, GATED, FP8Q_E5M2>)
+                             : reinterpret_cast<const void*>(mx_act_forward_kernel<ACT, DT, GATED, FP8Q_E4M3>);
+}
 template <int ACT>
-static const void* forward_kernel(int dtype, bool gated) {
+static const void* forward_kernel(int dtype, bool gated, int format) {
   if (dtype == FP8Q_BF16)
-    return gated ? reinterpret_cast<const void*>(mx_act_forward_kernel<ACT, FP8Q_BF16, true>)
-                 : reinterpret_cast<const void*>(mx_act_forward_kernel<ACT, FP8Q_BF16, false>);
-  return gated ? reinterpret_cast<const void*>(mx_act_forward_kernel<ACT, FP8Q_F32, true>)
-               : reinterpret_cast<const void*>(mx_act_forward_kernel<ACT, FP8Q_F32, false>);
+    return gated ? forward_of<ACT, FP8Q_BF16, true>(format) : forward_of<ACT, FP8Q_BF16, false>(format);
+  return gated ? forward_of<ACT, FP8Q_F32, true>(format) : forward_of<ACT, FP8Q_F32, false>(format);
 }
 template <int ACT, int DT, bool GATED>
 static const void* backward_of(int format) {
@@ -264,9 +300,9 @@ cudaError_t launch_mx_act_forward(const MxActForward& a, int act, int dtype, int
   MxActForward args_a = a;
   void* args[] = {&args_a, &u};
   const bool gated = a.u != nullptr;
-  const void* k = act == MX_ACT_SILU   ? forward_kernel<MX_ACT_SILU>(dtype, gated)
-                  : act == MX_ACT_GELU ? forward_kernel<MX_ACT_GELU>(dtype, gated)
-                                       : forward_kernel<MX_ACT_GELU_TANH>(dtype, gated);
+  const void* k = act == MX_ACT_SILU   ? forward_kernel<MX_ACT_SILU>(dtype, gated, a.z_saved.format)
+                  : act == MX_ACT_GELU ? forward_kernel<MX_ACT_GELU>(dtype, gated, a.z_saved.format)
+                                       : forward_kernel<MX_ACT_GELU_TANH>(dtype, gated, a.z_saved.format);
   return launch_dependent(k, dim3((unsigned)grid), kUnitThreads, 0, args, s, launches);
 }
 

@@ -117,6 +117,7 @@ FP8Q_API int mx_act_forward(int act, const void* z, int64_t z_stride, const void
   int st = check_kept(z_saved, rows, cols, true, &a.z_saved);
   if (st == FP8Q_OK) st = check_kept(u_saved, rows, cols, true, &a.u_saved);
   if (st == FP8Q_OK) st = check_kept(h_mx, rows, cols, false, &a.h_mx);
+  if (st == FP8Q_OK && u_saved && u_saved->format != z_saved->format) st = FP8Q_EDTYPE;
   if (st != FP8Q_OK) return st;
   if (rows == 0) return FP8Q_OK;
   st = check_plain(z, dtype, rows, cols, z_stride, 16);

@@ -120,6 +120,7 @@ def test_activation_refusals(lib):
     assert forward(lib, z_saved=eight) == -1                       # u would be lost
     assert forward(lib, u=None, z_saved=eight, u_saved=matrix()) == -1
     assert forward(lib, z_saved=four, u_saved=matrix()) == -3
+    assert forward(lib, z_saved=eight, u_saved=matrix(fmt=E5M2)) == -3
     assert forward(lib, z_saved=matrix(rows=63), u_saved=matrix()) == -1
     assert forward(lib, h_mx=matrix(cols=160)) == -1
     assert forward(lib, rows=0, z=None, u=None, h=0x50000) == 0
