@@ -517,18 +517,21 @@ FP8Q_API int mx_decode(const mx_matrix* m, void* out, int dtype, int64_t out_str
  * training": the products whose operands are cast).  With row-wise casts of x
  * [tokens, in] and w [out, in] it is the linear layer x w^T; with the dual
  * casts' transposes it is both of its gradients.
- *   a, b    cols alike (K); both E2M1, or each E4M3 or E5M2 (else FP8Q_EDTYPE)
+ *   a, b    cols alike (K, up to MX_MATMUL_MAX_K); both E2M1, or each E4M3 or
+ *           E5M2 (else FP8Q_EDTYPE)
  *   out     device [a.rows, b.rows] of dtype, rows out_stride elements apart
  *   add     device, of the same type and shape, rows add_stride elements
- *           apart, or NULL; it may be out itself
+ *           apart, or NULL; it may be out itself (same base and stride), and
+ *           may not overlap it otherwise; out may not overlap a or b
  *   out and add aligned to their elements; strides >= b.rows
  * Roundings: products are exact, sums are held in 32 bits by the tensor cores
  * (K / 64 or K / 32 additions of a tile's partial sums, each cut to 24 bits or
  * more), add is added in 32 bits, and the result is rounded once to dtype.
- * NaN and Inf (codes, blocks with E8M0 0xFF) go where the products take them.
- * Products of scales below 2^-126 may be taken as zero.  The order of the sums
+ * NaN and Inf (codes, blocks with E8M0 0xFF) go where the products take them;
+ * sums below 2^-126 may be taken as zero.  The order of the sums
  * is fixed by the sizes: results repeat from call to call.
  * One launch, no workspace; capturable. */
+#define MX_MATMUL_MAX_K (1LL << 26)
 FP8Q_API int mx_matmul(const mx_matrix* a, const mx_matrix* b, void* out, int dtype, int64_t out_stride,
                        const void* add, int64_t add_stride, void* stream);
 

@@ -92,10 +92,12 @@ cudaError_t launch_mx4_rows(const void* x, int dtype, int64_t nelem, int headroo
 // sector, so two row tiles' transposed blocks are gathered in shared memory
 // into 32-byte rows before they go out.
 
-using Mx4DualCfg = TpCfg<3, 1, 4, true, 3072, 1, true, 14, true>;
+template <bool COUNT>
+using Mx4DualCfg = TpCfg<2, 1, 4, true, 3072, 1, COUNT, 16, COUNT>;
 // Few sub-tiles: chunks of two row tiles and CTAs of two warps, so that every SM
 // has some (see tp_small).
-using Mx4DualSmallCfg = TpCfg<2, 1, 2, true, 3072, 0, true, 2, true>;
+template <bool COUNT>
+using Mx4DualSmallCfg = TpCfg<2, 1, 2, true, 3072, 0, COUNT, 2, COUNT>;
 
 static __device__ unsigned int g_mx4_wait_timeouts;   // see fp8q_pipeline_status
 
@@ -108,7 +110,7 @@ cudaError_t read_mx4_wait_timeouts(unsigned int* count) {
 
 // One block from the fp32 bits of its 32 elements: its codes into o, returns
 // its E8M0 byte and adds its clipped elements to clip.
-template <class Bits>
+template <bool COUNT, class Bits>
 __device__ __forceinline__ uint32_t mx4_block(Bits bits, uint32_t m, int rule, int headroom, uint32_t& clip,
                                               uint32_t (&o)[4]) {
   if (m >= 0x7F800000u) {
@@ -123,7 +125,7 @@ __device__ __forceinline__ uint32_t mx4_block(Bits bits, uint32_t m, int rule, i
   }
   const int E = block_exp<FP8Q_E2M1>(m, rule, headroom);
   const float s = block_inv_scale<FP8Q_E2M1>(E);
-  const bool count = mx_block_may_clip<FP8Q_E2M1>(m, E);
+  const bool count = COUNT && mx_block_may_clip<FP8Q_E2M1>(m, E);
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     float f[8];
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) mx4_dual_kernel(
 #pragma unroll
       for (int k = 1; k < NG; ++k) pm = mag_max<DT>(pm, mag_load<DT>(v[k]));
       uint32_t o[4];
-      ebytes |= mx4_block([&](int k) { return elem_bits<DT>(v[k / EPL], k % EPL); }, mag_bits<DT>(pm), rule, headroom,
+      ebytes |= mx4_block<C::kClipCount>([&](int k) { return elem_bits<DT>(v[k / EPL], k % EPL); }, mag_bits<DT>(pm), rule, headroom,
                           clip_r, o)
                 << (8 * b);
       if (G::BPR == 2) stage16<32>(ob + 2048, lane, b, o[0], o[1], o[2], o[3]);
@@ -216,10 +218,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) mx4_dual_kernel(
       if (c < cols) {
         load_column_words(tile, lane, w);
         const uint32_t pm = tree_absmax32<true>(w);
-        e8c0 |= (E8Acc<C::kChunk>)mx4_block([&](int k) { return half_bits<0>(w[k]); }, pm << 16, rule, headroom, clip_c, o)
+        e8c0 |= (E8Acc<C::kChunk>)mx4_block<C::kClipCount>([&](int k) { return half_bits<0>(w[k]); }, pm << 16, rule, headroom, clip_c, o)
                 << (8 * ci);
         put(2 * lane, o);
-        e8c1 |= (E8Acc<C::kChunk>)mx4_block([&](int k) { return half_bits<1>(w[k]); }, pm & 0xFFFF0000u, rule, headroom,
+        e8c1 |= (E8Acc<C::kChunk>)mx4_block<C::kClipCount>([&](int k) { return half_bits<1>(w[k]); }, pm & 0xFFFF0000u, rule, headroom,
                                             clip_c, o)
                 << (8 * ci);
         put(2 * lane + 1, o);
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kMinBlocks) mx4_dual_kernel(
       const int64_t c = c0 + lane;
       if (c < cols) {
         load_column_words(tile, lane, w);
-        e8c0 |= (E8Acc<C::kChunk>)mx4_block([&](int k) { return w[k]; }, tree_absmax32<false>(w), rule, headroom, clip_c, o)
+        e8c0 |= (E8Acc<C::kChunk>)mx4_block<C::kClipCount>([&](int k) { return w[k]; }, tree_absmax32<false>(w), rule, headroom, clip_c, o)
                 << (8 * ci);
         put(lane, o);
         if (flush) store_e8_run<C::kChunk>(e8_colt + c * rb + rt0, e8c0, ci + 1);
@@ -284,16 +286,24 @@ static cudaError_t launch_dual(const void* x, int64_t rows, int64_t cols, int ru
   return cudaGetLastError();
 }
 
+template <bool COUNT>
+static cudaError_t launch_dual_counting(const void* x, int dtype, int64_t rows, int64_t cols, int rule, int headroom,
+                                        uint8_t* q_row, uint8_t* e8_row, uint8_t* q_colt, uint8_t* e8_colt,
+                                        unsigned long long* cr, unsigned long long* cc, cudaStream_t s, int* launches) {
+  const bool b = dtype == FP8Q_BF16;
+  const auto launch = tp_small(rows, cols, dtype)
+                          ? (b ? launch_dual<FP8Q_BF16, Mx4DualSmallCfg<COUNT>> : launch_dual<FP8Q_F32, Mx4DualSmallCfg<COUNT>>)
+                          : (b ? launch_dual<FP8Q_BF16, Mx4DualCfg<COUNT>> : launch_dual<FP8Q_F32, Mx4DualCfg<COUNT>>);
+  return launch(x, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s, launches);
+}
+
 cudaError_t launch_mx4_dual(const void* x, int dtype, int64_t rows, int64_t cols, int rule, int headroom,
                             uint8_t* q_row, uint8_t* e8_row, uint8_t* q_colt, uint8_t* e8_colt,
                             unsigned long long* cr, unsigned long long* cc, cudaStream_t s, int* launches) {
-  if (tp_small(rows, cols, dtype))
-    return dtype == FP8Q_BF16
-               ? launch_dual<FP8Q_BF16, Mx4DualSmallCfg>(x, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s, launches)
-               : launch_dual<FP8Q_F32, Mx4DualSmallCfg>(x, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s, launches);
-  return dtype == FP8Q_BF16
-             ? launch_dual<FP8Q_BF16, Mx4DualCfg>(x, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s, launches)
-             : launch_dual<FP8Q_F32, Mx4DualCfg>(x, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s, launches);
+  // nothing to count where nobody asks or nothing can clip
+  return (cr || cc) && !mx_clip_free(rule, headroom)
+             ? launch_dual_counting<true>(x, dtype, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s, launches)
+             : launch_dual_counting<false>(x, dtype, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s, launches);
 }
 
 }  // namespace fp8q

@@ -84,7 +84,7 @@ FP8Q_API int mx_matmul(const mx_matrix* a, const mx_matrix* b, void* out, int dt
   if (st == FP8Q_OK) st = check_matrix(b, &p.b);
   if (st != FP8Q_OK) return st;
   if (!known_dtype(dtype) || (a->format == FP8Q_E2M1) != (b->format == FP8Q_E2M1)) return FP8Q_EDTYPE;
-  if (a->cols != b->cols) return FP8Q_EINVAL;
+  if (a->cols != b->cols || a->cols > MX_MATMUL_MAX_K) return FP8Q_EINVAL;
   if (a->rows == 0 || b->rows == 0) return FP8Q_OK;
   const int size = dtype == FP8Q_F32 ? 4 : 2;
   st = check_plain(out, dtype, a->rows, b->rows, out_stride, size);

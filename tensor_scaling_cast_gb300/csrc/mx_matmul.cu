@@ -470,31 +470,62 @@ struct PairCfg {
   static_assert(kCodes % 1024 == 0 && kOver % 32 == 0 && NT % 32 == 0 && NT <= 256 && kOver < NT && kSmem <= 227 * 1024, "");
 };
 
-// What mm_pair_kernel does with the staged w columns of `rows` rows at the edges
-// of out, or where rows of out or add start anywhere.
-__device__ __noinline__ void store_part(const MmArgs& p, uint32_t stage, int64_t m0, int64_t n0, int rows, int w, bool wide) {
-  const int lane = threadIdx.x & 31;
+// What mm_pair_kernel does with 32 staged columns of fp32 sums at the edges of
+// out, or where rows of out or add start anywhere.
+__device__ __forceinline__ void store_wide(const MmArgs& p, uint32_t stage, int64_t m0, int64_t n0, int rows) {
+  const int lane = threadIdx.x & 31, k = lane & 7;
   const int64_t cols = p.ts.rows;
-  if (wide) {
-    const int k = lane & 7;
 #pragma unroll 4
-    for (int r = lane >> 3; r < rows; r += 4)
-      if (n0 + 4 * k < cols) put4(p, m0 + r, n0 + 4 * k, cols, load_shared4(stage + r * 128 + ((k ^ (r & 7)) << 4)));
-    return;
+  for (int r = lane >> 3; r < rows; r += 4)
+    if (n0 + 4 * k < cols) put4(p, m0 + r, n0 + 4 * k, cols, load_shared4(stage + r * 128 + ((k ^ (r & 7)) << 4)));
+}
+// 32 columns of bf16 whose rows start anywhere, or at the edges of out: row
+// `lane` goes to shared memory as far past a multiple of 16 bytes as it lies in
+// out, and its 16-byte pieces leave whole but for the first and the last.  The
+// columns come from tensor memory at `from`; bar, where not 0, is told then.
+__device__ __noinline__ void store_anywhere(uint32_t from, uint32_t bar, uint32_t stage, uint16_t* out, int64_t stride,
+                                            int rows, int width) {
+  const int lane = threadIdx.x & 31;
+  uint32_t v[32];
+  tmem_ld32(v, from);
+  tmem_wait_ld(v);
+  if (bar) {
+    tmem_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster_relaxed(bar);
   }
-  // a row's columns side by side
-#pragma unroll 4
-  for (int r = 0; r < rows; ++r) {
-    uint16_t* dst = static_cast<uint16_t*>(p.out) + (m0 + r) * p.out_stride + n0;
+  if (rows <= 0 || width <= 0) return;
+  // in elements, and only the low bits count
+  const uint32_t start = (uint32_t)(reinterpret_cast<uintptr_t>(out) >> 1), step = (uint32_t)stride;
+  const auto phase = [&](int r) { return (int)((start + r * step) & 7u); };
+  const int mine = phase(lane);
+  const uint32_t to = stage + lane * 80 + (mine >> 1) * 4;
+  uint32_t before = 0;
 #pragma unroll
-    for (int y = 0; y < 64; y += 32) {
-      const int at = y + lane;
-      uint16_t h;
-      asm volatile("ld.shared.u16 %0, [%1];"
-                   : "=h"(h) : "r"(stage + r * 128 + (((at >> 3) ^ (r & 7)) << 4) + (at & 7) * 2) : "memory");
-      if (at < w && n0 + at < cols) dst[at] = h;
+  for (int k = 0; k < 17; ++k) {
+    const uint32_t h = k < 16 ? cvt_bf16x2(__uint_as_float(v[2 * (k & 15)]), __uint_as_float(v[2 * (k & 15) + 1])) : 0u;
+    const uint32_t word = mine & 1 ? __funnelshift_l(before, h, 16) : h;
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * k), "r"(word) : "memory");
+    before = h;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const int u = 32 * i + lane, r = u / 5, j = u - 5 * r;
+    const float4 t = load_shared4(stage + r * 80 + j * 16);
+    if (r >= rows) continue;
+    const int first = phase(r), lo = max(8 * j, first) - 8 * j, hi = min(8 * j + 8, first + width) - 8 * j;
+    uint16_t* dst = out + r * stride - first + 8 * j;
+    if (lo == 0 && hi == 8) {
+      *reinterpret_cast<float4*>(dst) = t;
+    } else {
+      const uint32_t h[4] = {__float_as_uint(t.x), __float_as_uint(t.y), __float_as_uint(t.z), __float_as_uint(t.w)};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e >= lo && e < hi) dst[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
     }
   }
+  __syncwarp();
 }
 
 template <bool F4, int NT>
@@ -712,6 +743,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         }
         continue;
       }
+      if (!wide && !(p.out_vector && rows == 32 && n0 + NT <= cols)) {
+#pragma unroll 1
+        for (int x = 0; x < NT; x += 32) {
+          const int c = C::kOver && !b ? NT - 32 - x : x;
+          const uint32_t bar = x + 32 == NT ? lead_bar(&sums_empty[b]) : C::kOver && x + 32 == C::kOver ? lead_bar(shared_empty) : 0u;
+          store_anywhere(from + c, bar, stage, static_cast<uint16_t*>(p.out) + m0 * p.out_stride + n0 + c, p.out_stride,
+                         rows, (int)max((int64_t)0, min((int64_t)32, cols - n0 - c)));
+        }
+        continue;
+      }
 #pragma unroll 1
       for (int x = 0; x < NT;) {
         const int w = wide ? 32 : min(64, NT - x);
@@ -746,7 +787,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
           }
         }
         __syncwarp();
-        if (rows == 32 && n0 + c + w <= cols && p.out_vector && (!p.add || p.add_vector)) {
+        if (!wide || (rows == 32 && n0 + c + 32 <= cols && p.out_vector && (!p.add || p.add_vector))) {
           const int size = p.fp32 ? 4 : 2;
           if (p.add) {
             // four sums of row 4 i + lane / 8 at a time
@@ -802,7 +843,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
             }
           }
         } else {
-          store_part(p, stage, m0, n0 + c, rows, w, wide);
+          store_wide(p, stage, m0, n0 + c, rows);
         }
         __syncwarp();
       }

@@ -148,6 +148,22 @@ def test_decode_of_slices(rows, cols, fmt):
     assert (out[:, :32] == 5).all() and (out[:, 32 + cols:] == 5).all()
 
 
+def test_more_units_than_31_bits():
+    """Past 2^31 units of eight elements: every row of a tall matrix lands in its place."""
+    rows, cols = (1 << 29) + 5, 32
+    if torch.cuda.mem_get_info()[0] < 70 << 30:
+        pytest.skip("70 GB of free memory")
+    q = torch.zeros(rows, 16, dtype=torch.uint8, device="cuda")
+    e = torch.full((rows, 1), 127, dtype=torch.uint8, device="cuda")
+    at = torch.tensor([0, 1, 1 << 20, (1 << 29) - 1, 1 << 29, rows - 1], device="cuda")
+    q[at] = torch.arange(1, 7, dtype=torch.uint8, device="cuda")[:, None]
+    out = torch.empty(rows, cols, dtype=BF, device="cuda")
+    F.mx_decode(F.MXMatrix(q, e, kv.E2M1), out)
+    want = torch.from_numpy(kv.decode(q[at].cpu().numpy(), e[at].cpu().numpy(), kv.E2M1)).to(BF)
+    assert torch.equal(out[at].cpu(), want)
+    assert int(out.view(torch.int32).count_nonzero()) == int(want.view(torch.int32).count_nonzero())
+
+
 # ---- products --------------------------------------------------------------------
 
 def random_mx(rows, cols, fmt, seed, lo=110, hi=135, wide=0):
@@ -253,6 +269,37 @@ def test_one_scale_and_one_element_at_a_time():
             out = G.empty((x.shape[0], y.shape[0]), F32)
             F.mx_matmul(x, y, out)
             assert torch.equal(out.double(), values(x) @ values(y).T)
+
+
+@pytest.mark.parametrize("fmt", [kv.E2M1, kv.E4M3])
+@pytest.mark.parametrize("m,n", [(3, 130), (70, 200), (2100, 2300)])
+def test_products_over_the_range_of_scales(fmt, m, n):
+    """Scales from 2^-126 to 2^127 on one side and their reciprocals on the
+    other, block by block; and sums up to 2^120."""
+    k = 512
+    a, b = random_mx(m, k, fmt, 1), random_mx(n, k, fmt, 2)
+    e = torch.randint(1, 254, (k // 32,), generator=torch.Generator().manual_seed(3))
+    a.e8m0.copy_(e.to(torch.uint8).expand(m, -1))
+    b.e8m0.copy_((254 - e).to(torch.uint8).expand(n, -1))
+    out = G.empty((m, n), F32)
+    F.mx_matmul(a, b, out)
+    check_product(a, b, out)
+    a.e8m0.fill_(127 + 50)
+    b.e8m0.fill_(127 + 50)
+    F.mx_matmul(a, b, out)
+    check_product(a, b, out)
+
+
+def test_products_of_infinities():
+    """E5M2's Inf: against positive values Inf, against zeros NaN, in its row alone."""
+    a, b = random_mx(5, 64, kv.E5M2, 1), random_mx(200, 64, kv.E5M2, 2)
+    a.q[2, 7] = 0x7C
+    b.q[:, 7] = 0x3C
+    b.q[11, 7] = 0
+    out = G.empty((5, 200), F32)
+    F.mx_matmul(a, b, out)
+    assert out[2, 11].isnan() and (out[2, :11] == math.inf).all() and (out[2, 12:] == math.inf).all()
+    assert torch.isfinite(out[[0, 1, 3, 4]]).all()
 
 
 @pytest.mark.parametrize("m,n", [(3, 200), (300, 500), (1200, 1400), (2300, 2400)])

@@ -90,6 +90,7 @@ def test_matmul_refusals(lib):
     assert matmul(lib, None, b) == -1
     assert matmul(lib, a, None) == -1
     assert matmul(lib, a, matrix(cols=160)) == -1
+    assert matmul(lib, matrix(cols=(1 << 26) + 32), matrix(cols=(1 << 26) + 32)) == -1
     assert matmul(lib, a, matrix(fmt=E2M1)) == -3
     assert matmul(lib, matrix(fmt=E2M1), b) == -3
     assert matmul(lib, a, b, dtype=2) == -3
