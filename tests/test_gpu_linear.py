@@ -582,3 +582,17 @@ def test_half_an_mlp_step(tokens, ffn, hidden, gated, h_fmt):
     for t, k in zip((y, dh, dz, du, dw), kept):
         if t is not du or gated:
             assert torch.equal(t, k)
+
+
+def test_the_example_runs_and_its_gradients_are_near():
+    """Against the step in 32 bits without casts: what the formats keep of a
+    block's largest element (E2M1 2^-2, E4M3 2^-4, E5M2 2^-3), for two operands."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "mx_mlp_step.py")
+    spec = importlib.util.spec_from_file_location("mx_mlp_step", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    off = m.main(tokens=160, ffn=576, hidden=224, quiet=True)
+    assert off["y"] < 2 * 2.0 ** -2
+    assert all(off[k] < 2.0 ** -3 + 3 * 2.0 ** -4 for k in ("dz", "du", "dw"))
