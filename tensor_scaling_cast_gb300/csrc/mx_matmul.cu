@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     for (int k = 0; k < 8; ++k) mine[k] = stage + lane * 128 + ((k ^ (lane & 7)) << 4);
 #pragma unroll
     for (int k = 0; k < 2; ++k) theirs[k] = stage + (lane >> 3) * 128 + (((lane & 7) ^ (4 * k + (lane >> 3))) << 4);
-    int lt = 0, buf = 0;
+    int lt = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++lt) {
       int tw, tt;
       place(tile, &tw, &tt);
@@ -697,49 +697,68 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
       const int rows = (int)min((int64_t)32, p.ws.rows - m0);      // may be none
       const uint32_t from = lane_at + (b ? C::kSums - NT : 0);
       if (p.tma_out) {
-        // 32 columns at a time; the next ones leave tensor memory meanwhile
-        uint32_t v[32];
-        tmem_ld32(v, from + (C::kOver && !b ? NT - 32 : 0));
+        // 64 columns of bf16, or 32 of fp32, at a time: two boxes of 64 bytes a
+        // row; the columns after them leave tensor memory meanwhile.  One fence
+        // and one wait for both boxes: each costs the warp hundreds of cycles.
+        const bool down = C::kOver && !b;      // shared columns first: the last ones of the first buffer
+        const int sw = (lane >> 1) & 3;
+        const auto box = [&](uint32_t to, const uint32_t (&w)[16]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            st_shared16(to + lane * 64 + ((k ^ sw) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        };
+        const auto pack = [](const uint32_t (&v)[32], uint32_t (&w)[16]) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = cvt_bf16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+        };
+        const int most = p.fp32 ? 32 : 64;
+        uint32_t v[32], u[32], w[16];
+        int c = down ? NT - 32 : 0;
+        tmem_ld32(v, from + c);
         tmem_wait_ld(v);
 #pragma unroll 1
-        for (int x = 0; x < NT; x += 32) {
-          // the columns that the other buffer shares first: the last ones of the first, the first of the second
-          const int c = C::kOver && !b ? NT - 32 - x : x;
-          if ((C::kOver && x + 32 == C::kOver) || x + 32 == NT) {
+        for (int x = 0; x < NT;) {
+          // v: columns c .. c + 31; u: the next 32, up or down
+          const int width = min(most, NT - x), c2 = down ? c - 32 : c + 32;
+          if (width == 64) tmem_ld32(u, from + c2);
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          if (p.fp32) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = v[k];
+            box(stage, w);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = v[16 + k];
+            box(stage + C::kOut / 2, w);
+          } else {
+            pack(v, w);
+            box(stage, w);
+          }
+          if (width == 64) tmem_wait_ld(u);
+          const bool shared_done = C::kOver && x < C::kOver && x + width >= C::kOver;
+          x += width;
+          if (shared_done || x == NT) {
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(lead_bar(x + 32 == NT ? &sums_empty[b] : shared_empty));
+            if (lane == 0) mbar_arrive_cluster_relaxed(lead_bar(x == NT ? &sums_empty[b] : shared_empty));
           }
-          uint32_t next[32];
-          if (x + 32 < NT) tmem_ld32(next, from + (C::kOver && !b ? c - 32 : c + 32));
-          // 64 bytes of a row at a time: 32 columns of bf16, 16 of fp32
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            if (y && !p.fp32) break;
-            const uint32_t to = stage + buf * (C::kOut / 2), at = to + lane * 64;
-            if (lane == 0) bulk_wait_read<1>();
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z)
-                w[z] = p.fp32 ? v[16 * y + 4 * k + z]
-                              : cvt_bf16x2(__uint_as_float(v[8 * k + 2 * z]), __uint_as_float(v[8 * k + 2 * z + 1]));
-              st_shared16(at + ((k ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-              const int64_t n = n0 + c + 16 * y;
-              if (rows > 0 && n < cols) tma_store_2d_from(&p.o, to, (int)n, (int)m0);
-              bulk_commit();
-            }
-            buf ^= 1;
+          const int c_next = down ? c - width : c + width;
+          if (x < NT) tmem_ld32(v, from + c_next);
+          if (width == 64) {
+            pack(u, w);
+            box(stage + C::kOut / 2, w);
           }
-          tmem_wait_ld(next);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = next[k];
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            const int64_t n = n0 + c, n2 = p.fp32 ? n + 16 : n0 + c2;
+            if (rows > 0 && n < cols) tma_store_2d_from(&p.o, stage, (int)n, (int)m0);
+            if (rows > 0 && n2 < cols && (p.fp32 || width == 64))
+              tma_store_2d_from(&p.o, stage + C::kOut / 2, (int)n2, (int)m0);
+            bulk_commit();
+          }
+          if (x < NT) tmem_wait_ld(v);
+          c = c_next;
         }
         continue;
       }

@@ -268,8 +268,10 @@ def mx_cast_ex(x: torch.Tensor, fmt: int, rule: int, headroom: int, axis: int, q
     """axis MX_ROWWISE: e8m0 [rows, cols/32]; MX_COLWISE: e8m0 [rows/32, cols].
     E2M1 (row-wise): q [rows, cols/2]."""
     rows, cols = x.shape
-    _check(load().mx_cast_ex(_ptr(x), _dtype(x), rows, cols, fmt, rule, headroom, axis, _ptr(q),
-                             _ptr(e8m0), _ptr(clipped), _stream(stream)), "mx_cast_ex")
+    st = (_lib or load()).mx_cast_ex(_ptr(x), _dtype(x), rows, cols, fmt, rule, headroom, axis, _ptr(q), _ptr(e8m0),
+                                     None if clipped is None else clipped.data_ptr(), _stream(stream))
+    if st:
+        _check(st, "mx_cast_ex")
 
 
 def mx_cast_dual(x: torch.Tensor, fmt: int, rule: int, headroom: int, q_row, e8_row, q_colt, e8_colt,
@@ -279,9 +281,11 @@ def mx_cast_dual(x: torch.Tensor, fmt: int, rule: int, headroom: int, q_row, e8_
     q_colt [cols, rows], e8_colt [cols, rows/32] (E2M1: q_row [rows, cols/2],
     q_colt [cols, rows/2])."""
     rows, cols = x.shape
-    _check(load().mx_cast_dual(_ptr(x), _dtype(x), rows, cols, fmt, rule, headroom, _ptr(q_row),
-                               _ptr(e8_row), _ptr(q_colt), _ptr(e8_colt), _ptr(clipped_row),
-                               _ptr(clipped_col), _stream(stream)), "mx_cast_dual")
+    st = (_lib or load()).mx_cast_dual(_ptr(x), _dtype(x), rows, cols, fmt, rule, headroom, _ptr(q_row),
+                                       _ptr(e8_row), _ptr(q_colt), _ptr(e8_colt), _ptr(clipped_row),
+                                       _ptr(clipped_col), _stream(stream))
+    if st:
+        _check(st, "mx_cast_dual")
 
 
 def fp8q_cast_transpose(h: int, x: torch.Tensor, q, qt, scale_inv=None, amax=None, clipped=None,
