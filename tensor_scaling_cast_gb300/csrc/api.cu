@@ -203,13 +203,14 @@ FP8Q_API int fp8q_pipeline_selftest(void* stream) {
 FP8Q_API int fp8q_pipeline_status(unsigned int* timed_out_waits) {
   FP8Q_TRACE_CALL();
   if (!timed_out_waits) return FP8Q_EINVAL;
-  unsigned int a = 0, b = 0, c = 0, d = 0, f = 0;
+  unsigned int a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
   cudaError_t e = read_wait_timeouts(&a);
   if (e == cudaSuccess) e = read_tp_wait_timeouts(&b);
   if (e == cudaSuccess) e = read_kv_wait_timeouts(&c);
   if (e == cudaSuccess) e = read_mx4_wait_timeouts(&d);
-  if (e == cudaSuccess) e = read_mm_wait_timeouts(&f);
-  *timed_out_waits = a + b + c + d + f;
+  if (e == cudaSuccess) e = read_mm4_wait_timeouts(&f);
+  if (e == cudaSuccess) e = read_mm8_wait_timeouts(&g);
+  *timed_out_waits = a + b + c + d + f + g;
   return e == cudaSuccess ? FP8Q_OK : fail_cuda(e);
 }
 

@@ -1,6 +1,6 @@
 // Matrices in MX blocks as the kernels of linear layers see them: the 4-bit
 // casts (mx4.cu), decoding and the activations kept in 8 bits (mx_act.cu) and
-// products (mx_matmul.cu).
+// products (mx_matmul.cuh).
 #pragma once
 
 #include <stdint.h>
@@ -171,7 +171,7 @@ struct MxActBackward {
   int64_t dz_stride, du_stride, h_stride;
 };
 cudaError_t launch_mx_act_backward(const MxActBackward& a, int act, int dtype, cudaStream_t s, int* launches);
-// mx_matmul.cu
+// mx_matmul_4.cu, mx_matmul_8.cu
 struct MxProduct {
   MxView a, b;                 // [m, k] and [n, k]
   void* out;                   // [m, n]
@@ -179,7 +179,9 @@ struct MxProduct {
   int64_t out_stride, add_stride;
   int32_t fp32;                // type of out and add
 };
-cudaError_t launch_mx_matmul(const MxProduct& p, cudaStream_t s, int* launches);
-cudaError_t read_mm_wait_timeouts(unsigned int* count);       // and reset to 0
+cudaError_t launch_mx_matmul_4(const MxProduct& p, cudaStream_t s, int* launches);
+cudaError_t launch_mx_matmul_8(const MxProduct& p, cudaStream_t s, int* launches);
+cudaError_t read_mm4_wait_timeouts(unsigned int* count);      // and reset to 0
+cudaError_t read_mm8_wait_timeouts(unsigned int* count);
 
 }  // namespace fp8q

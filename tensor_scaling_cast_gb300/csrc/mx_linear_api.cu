@@ -98,7 +98,8 @@ FP8Q_API int mx_matmul(const mx_matrix* a, const mx_matrix* b, void* out, int dt
   int launches = 0;
   cudaError_t e;
   try {                            // the occupancy cache allocates
-    e = launch_mx_matmul(p, reinterpret_cast<cudaStream_t>(stream), &launches);
+    const auto launch = a->format == FP8Q_E2M1 ? launch_mx_matmul_4 : launch_mx_matmul_8;
+    e = launch(p, reinterpret_cast<cudaStream_t>(stream), &launches);
   } catch (...) {
     return FP8Q_ENOMEM;
   }

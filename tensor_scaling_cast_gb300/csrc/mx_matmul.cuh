@@ -6,6 +6,8 @@
 // (zeros outside the matrices); its scales, rows of E8M0 bytes in memory, are
 // read by four warps that write them in the order that the tensor core takes
 // them in (tcgen05.cuh), one thread a row.
+#pragma once
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -17,9 +19,9 @@
 
 namespace fp8q {
 
-static __device__ unsigned int g_mm_wait_timeouts;   // see fp8q_pipeline_status
+static __device__ unsigned int g_mm_wait_timeouts;   // of this translation unit; see fp8q_pipeline_status
 
-cudaError_t read_mm_wait_timeouts(unsigned int* count) {
+static cudaError_t read_timeouts(unsigned int* count) {
   unsigned int zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(count, g_mm_wait_timeouts, sizeof(unsigned int));
   if (e == cudaSuccess && *count) e = cudaMemcpyToSymbol(g_mm_wait_timeouts, &zero, sizeof(unsigned int));
@@ -35,7 +37,7 @@ struct MmScales {
 };
 struct MmArgs {
   CUtensorMap w, t;          // codes of the operand with 128-row tiles, of the other
-  CUtensorMap o;             // out, where tma_out
+  CUtensorMap o;             // out, where it leaves by TMA
   MmScales ws, ts;
   int32_t kblocks, w_tiles, t_tiles, splits;
   uint32_t idesc;
@@ -43,7 +45,6 @@ struct MmArgs {
   const void* add;
   int64_t out_stride, add_stride;
   int32_t fp32, w_is_a;      // out row: index in w (else in t)
-  int32_t tma_out;                  // out leaves by TMA
   int32_t out_quads, add_quads;     // rows start at multiples of four elements
   int32_t out_vector, add_vector;   // of 16 bytes
 };
@@ -169,24 +170,24 @@ __device__ __forceinline__ float add_of(const MmArgs& p, int64_t m, int64_t n) {
   return p.fp32 ? static_cast<const float*>(p.add)[at]
                 : __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.add)[at] << 16);
 }
-// Four sums of row m from column n on, the first of them inside.
-__device__ __forceinline__ void put4(const MmArgs& p, int64_t m, int64_t n, int64_t cols, const float4& sum) {
-  float v[4] = {sum.x, sum.y, sum.z, sum.w};
-  if (p.add && p.add_quads && n + 4 <= cols) {
+// add's four values of row m from column n on, the first of them inside.
+__device__ __forceinline__ float4 add4(const MmArgs& p, int64_t m, int64_t n, int64_t cols) {
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (p.add_quads && n + 4 <= cols) {
     const char* src = static_cast<const char*>(p.add) + (m * p.add_stride + n) * (p.fp32 ? 4 : 2);
-    if (p.fp32) {
-      const float4 x = *reinterpret_cast<const float4*>(src);
-      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-    } else {
-      const uint2 x = *reinterpret_cast<const uint2*>(src);
-      v[0] += __uint_as_float(x.x << 16), v[1] += __uint_as_float(x.x & 0xFFFF0000u);
-      v[2] += __uint_as_float(x.y << 16), v[3] += __uint_as_float(x.y & 0xFFFF0000u);
-    }
-  } else if (p.add) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (n + k < cols) v[k] += add_of(p, m, n + k);
+    if (p.fp32) return *reinterpret_cast<const float4*>(src);
+    const uint2 x = *reinterpret_cast<const uint2*>(src);
+    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u), __uint_as_float(x.y << 16),
+                       __uint_as_float(x.y & 0xFFFF0000u));
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (n + k < cols) v[k] = add_of(p, m, n + k);
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+// Four values of row m of out from column n on, the first of them inside.
+__device__ __forceinline__ void put4(const MmArgs& p, int64_t m, int64_t n, int64_t cols, const float4& sum) {
+  const float v[4] = {sum.x, sum.y, sum.z, sum.w};
   char* dst = static_cast<char*>(p.out) + (m * p.out_stride + n) * (p.fp32 ? 4 : 2);
   if (p.out_quads && n + 4 <= cols) {
     if (p.fp32) *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
@@ -412,6 +413,15 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
 #pragma unroll
         for (int s = 0; s < S; ++s) part[x][s] = S == 1 ? load_shared4(at) : cluster_load4(at, s);
       }
+      float4 extra[U];                               // add may be out: before the first store
+      if (p.add) {
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+          const int u = u0 + x * kSplitThreads;
+          const int64_t n = n0 + (u & (quads - 1)) * 4;
+          if (u < units && n < cols) extra[x] = add4(p, m0 + o0 + (u >> shift), n, cols);
+        }
+      }
 #pragma unroll
       for (int x = 0; x < U; ++x) {
         const int u = u0 + x * kSplitThreads;
@@ -423,6 +433,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
           part[x][0].y += part[x][s].y;
           part[x][0].z += part[x][s].z;
           part[x][0].w += part[x][s].w;
+        }
+        if (p.add) {
+          part[x][0].x += extra[x].x;
+          part[x][0].y += extra[x].y;
+          part[x][0].z += extra[x].z;
+          part[x][0].w += extra[x].w;
         }
         put4(p, m0 + o0 + (u >> shift), n, cols, part[x][0]);
       }
@@ -453,6 +469,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
 constexpr int kPairThreads = 288;          // TMA, products, four warps of epilogue, three of scales
 constexpr int kPairBand = 8;               // tiles of a in a band: pairs in flight cover a compact block
 
+// How out leaves: by TMA, or from registers as bf16 or fp32, or as one of them
+// after something is added.  Kernels of their own: one with all of them needs
+// more registers than there are.
+enum class Out { kTma, kBf16, kF32, kAddBf16, kAddF32 };
+
 template <bool F4, int NT>
 struct PairCfg {
   static constexpr int kB = 128 * 128;                             // codes of b within a stage
@@ -470,65 +491,182 @@ struct PairCfg {
   static_assert(kCodes % 1024 == 0 && kOver % 32 == 0 && NT % 32 == 0 && NT <= 256 && kOver < NT && kSmem <= 227 * 1024, "");
 };
 
-// What mm_pair_kernel does with 32 staged columns of fp32 sums at the edges of
-// out, or where rows of out or add start anywhere.
-__device__ __forceinline__ void store_wide(const MmArgs& p, uint32_t stage, int64_t m0, int64_t n0, int rows) {
-  const int lane = threadIdx.x & 31, k = lane & 7;
-  const int64_t cols = p.ts.rows;
-#pragma unroll 4
-  for (int r = lane >> 3; r < rows; r += 4)
-    if (n0 + 4 * k < cols) put4(p, m0 + r, n0 + 4 * k, cols, load_shared4(stage + r * 128 + ((k ^ (r & 7)) << 4)));
-}
-// 32 columns of bf16 whose rows start anywhere, or at the edges of out: row
-// `lane` goes to shared memory as far past a multiple of 16 bytes as it lies in
-// out, and its 16-byte pieces leave whole but for the first and the last.  The
-// columns come from tensor memory at `from`; bar, where not 0, is told then.
-__device__ __noinline__ void store_anywhere(uint32_t from, uint32_t bar, uint32_t stage, uint16_t* out, int64_t stride,
-                                            int rows, int width) {
+// `chunks` times 32 columns of sums of 32 rows (row `lane` of the warp's lanes
+// of tensor memory, at `from` on) into out, in fp32 or with ADD added; bar, where
+// not 0, is told once they have left tensor memory.  LINES: all of it lies inside
+// and its rows start at multiples of 16 bytes; the sums then pass through shared
+// memory so that they leave in whole lines, four of a row at a time.  Otherwise
+// a row's columns leave side by side.  add may be out: a chunk's values are read
+// before any of it is stored, while its sums go to shared memory.
+template <class T, bool ADD, bool LINES>
+__device__ __forceinline__ void store_sums(uint32_t from, int chunks, uint32_t bar, uint32_t stage, T* out, int64_t stride,
+                                           const T* add, int64_t add_stride, int rows, int width) {
   const int lane = threadIdx.x & 31;
-  uint32_t v[32];
-  tmem_ld32(v, from);
-  tmem_wait_ld(v);
-  if (bar) {
-    tmem_fence_before();
+  uint32_t mine[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) mine[k] = stage + lane * 128 + ((k ^ (lane & 7)) << 4);
+  out += LINES ? (lane >> 3) * stride + 4 * (lane & 7) : lane;
+  if (ADD) add += LINES ? (lane >> 3) * add_stride + 4 * (lane & 7) : lane;
+  uint32_t x[32];
+  const auto fetch = [&](int i, uint32_t (&to)[32]) {
+    if (LINES) {
+      const T* at = add + 32 * i;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (sizeof(T) == 4) {
+          const uint4 t = *reinterpret_cast<const uint4*>(at);
+          to[4 * k] = t.x, to[4 * k + 1] = t.y, to[4 * k + 2] = t.z, to[4 * k + 3] = t.w;
+        } else {
+          const uint2 t = *reinterpret_cast<const uint2*>(at);
+          to[4 * k] = t.x << 16, to[4 * k + 1] = t.x & 0xFFFF0000u;
+          to[4 * k + 2] = t.y << 16, to[4 * k + 3] = t.y & 0xFFFF0000u;
+        }
+        at += 4 * add_stride;
+      }
+    } else if (32 * i + lane < width && rows > 0) {
+      const T* at = add + 32 * i;
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        to[r] = sizeof(T) == 4 ? (uint32_t)*at : (uint32_t)*at << 16;
+        at += r + 1 < rows ? add_stride : 0;         // past the last row: that one again
+      }
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; i < chunks; ++i) {
+    if (ADD) fetch(i, x);
+    {
+      uint32_t v[32];
+      tmem_ld32(v, from + 32 * i);
+      tmem_wait_ld(v);
+      if (i + 1 == chunks && bar) {
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(bar);
+      }
+      __syncwarp();                        // the chunk before has left shared memory
+#pragma unroll
+      for (int k = 0; k < 8; ++k) st_shared16(mine[k], v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
     __syncwarp();
-    if (lane == 0) mbar_arrive_cluster_relaxed(bar);
-  }
-  if (rows <= 0 || width <= 0) return;
-  // in elements, and only the low bits count
-  const uint32_t start = (uint32_t)(reinterpret_cast<uintptr_t>(out) >> 1), step = (uint32_t)stride;
-  const auto phase = [&](int r) { return (int)((start + r * step) & 7u); };
-  const int mine = phase(lane);
-  const uint32_t to = stage + lane * 80 + (mine >> 1) * 4;
-  uint32_t before = 0;
+    T* dst = out + 32 * i;
+    if (LINES) {
+      float4 t[8];
 #pragma unroll
-  for (int k = 0; k < 17; ++k) {
-    const uint32_t h = k < 16 ? cvt_bf16x2(__uint_as_float(v[2 * (k & 15)]), __uint_as_float(v[2 * (k & 15) + 1])) : 0u;
-    const uint32_t word = mine & 1 ? __funnelshift_l(before, h, 16) : h;
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * k), "r"(word) : "memory");
-    before = h;
-  }
-  __syncwarp();
+      for (int k = 0; k < 8; ++k) {
+        const int r = 4 * k + (lane >> 3);
+        t[k] = load_shared4(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+      }
 #pragma unroll
-  for (int i = 0; i < 5; ++i) {
-    const int u = 32 * i + lane, r = u / 5, j = u - 5 * r;
-    const float4 t = load_shared4(stage + r * 80 + j * 16);
-    if (r >= rows) continue;
-    const int first = phase(r), lo = max(8 * j, first) - 8 * j, hi = min(8 * j + 8, first + width) - 8 * j;
-    uint16_t* dst = out + r * stride - first + 8 * j;
-    if (lo == 0 && hi == 8) {
-      *reinterpret_cast<float4*>(dst) = t;
-    } else {
-      const uint32_t h[4] = {__float_as_uint(t.x), __float_as_uint(t.y), __float_as_uint(t.z), __float_as_uint(t.w)};
+      for (int k = 0; k < 8; ++k) {
+        if (ADD) {
+          t[k].x += __uint_as_float(x[4 * k]);
+          t[k].y += __uint_as_float(x[4 * k + 1]);
+          t[k].z += __uint_as_float(x[4 * k + 2]);
+          t[k].w += __uint_as_float(x[4 * k + 3]);
+        }
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(dst) = t[k];
+        else *reinterpret_cast<uint2*>(dst) = make_uint2(cvt_bf16x2(t[k].x, t[k].y), cvt_bf16x2(t[k].z, t[k].w));
+        dst += 4 * stride;
+      }
+    } else if (32 * i + lane < width) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e >= lo && e < hi) dst[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
+      for (int h = 0; h < 32; h += 16) {
+        float v[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          asm volatile("ld.shared.f32 %0, [%1];"
+                       : "=f"(v[r]) : "r"(stage + (h + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) : "memory");
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          if (ADD) v[r] += __uint_as_float(x[h + r]);
+          if (h + r < rows) {
+            if constexpr (sizeof(T) == 4) *dst = __float_as_uint(v[r]);
+            else *dst = (uint16_t)cvt_bf16x2(v[r], v[r]);
+          }
+          dst += stride;
+        }
+      }
     }
   }
   __syncwarp();
 }
 
-template <bool F4, int NT>
+// The form for anywhere as a function of its own, with registers of its own.
+template <class T, bool ADD>
+static __device__ __noinline__ void store_sums_anywhere(uint32_t from, int chunks, uint32_t bar, uint32_t stage, T* out,
+                                                        int64_t stride, const T* add, int64_t add_stride, int rows,
+                                                        int width) {
+  store_sums<T, ADD, false>(from, chunks, bar, stage, out, stride, add, add_stride, rows, width);
+}
+
+// `chunks` times 32 columns of bf16 whose rows start anywhere, or at the edges
+// of out, from tensor memory at `from` on; bar, where not 0, is told once they
+// have left it.  Row `lane` passes through shared memory as far past a multiple
+// of 16 bytes as it lies in out, so that its 16-byte pieces leave whole, what is
+// left of a chunk with the next one, but for the first and the last.
+static __device__ __noinline__ void store_anywhere(uint32_t from, int chunks, uint32_t bar, uint32_t stage, uint16_t* out,
+                                            int64_t stride, int rows, int width) {
+  const int lane = threadIdx.x & 31;
+  // in elements, and only the low bits count
+  const uint32_t start = (uint32_t)(reinterpret_cast<uintptr_t>(out) >> 1), step = (uint32_t)stride;
+  const uint32_t phase = (start + lane * step) & 7u, odd = 16 * (phase & 1);
+  const uint32_t row = stage + lane * 80, to = row + (phase >> 1) * 4;
+  uint32_t before = 0;
+#pragma unroll 1
+  for (int i = 0; i < chunks; ++i) {
+    uint32_t v[32];
+    tmem_ld32(v, from + 32 * i);
+    tmem_wait_ld(v);
+    if (i + 1 == chunks && bar) {
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(bar);
+    }
+    if (rows <= 0 || 32 * i >= width) continue;
+    __syncwarp();
+    if (i) {                               // what the chunk before left
+      const float4 left = load_shared4(row + 64);
+      st_shared16(row, __float_as_uint(left.x), __float_as_uint(left.y), __float_as_uint(left.z), __float_as_uint(left.w));
+    }
+#pragma unroll
+    for (int k = 0; k < 17; ++k) {
+      const uint32_t h = k < 16 ? cvt_bf16x2(__uint_as_float(v[2 * (k & 15)]), __uint_as_float(v[2 * (k & 15) + 1])) : 0u;
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * k), "r"(__funnelshift_l(before, h, odd)) : "memory");
+      if (k < 16) before = h;
+    }
+    __syncwarp();
+    const bool inside = i > 0 && 32 * i + 32 <= width, last = i + 1 == chunks || 32 * i + 32 >= width;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int r = 8 * x + (lane >> 2), j = lane & 3;
+      const float4 t = load_shared4(stage + r * 80 + j * 16);
+      if (r >= rows) continue;
+      const int at = 32 * i + 8 * j - (int)((start + r * step) & 7u);      // of the piece's first element
+      uint16_t* dst = out + r * stride + at;
+      if (inside || (at >= 0 && at + 8 <= width)) {
+        *reinterpret_cast<float4*>(dst) = t;
+      } else {
+        const uint32_t h[4] = {__float_as_uint(t.x), __float_as_uint(t.y), __float_as_uint(t.z), __float_as_uint(t.w)};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (at + e >= 0 && at + e < width) dst[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
+      }
+    }
+    if (last && lane < rows) {             // and what is left at the end
+      const float4 t = load_shared4(row + 64);
+      const int at = 32 * i + 32 - (int)phase;
+      uint16_t* dst = out + lane * stride + at;
+      const uint32_t h[4] = {__float_as_uint(t.x), __float_as_uint(t.y), __float_as_uint(t.z), __float_as_uint(t.w)};
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < (int)phase && at + e < width) dst[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+  __syncwarp();
+}
+
+template <bool F4, int NT, Out OUT>
 __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_constant__ MmArgs p) {
   using C = PairCfg<F4, NT>;
   constexpr int ST = C::kStages;
@@ -561,6 +699,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     fence_barrier_init();
     prefetch_tensormap(&p.w);
     prefetch_tensormap(&p.t);
+    if (OUT == Out::kTma) prefetch_tensormap(&p.o);
   }
   __syncwarp();
   cluster_barrier();                       // the other CTA's barriers are there
@@ -672,17 +811,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     const int q = warp & 3, row = 32 * q + lane;     // this warp's lanes of tensor memory
     const uint32_t lane_at = tmem + ((uint32_t)(32 * q) << 16);
     const uint32_t stage = staging + (warp - 2) * C::kOut;
-    // 32 rows of 128 bytes at a time pass through shared memory, swizzled, so
-    // that they leave in whole lines: 64 columns of bf16, or 32 of fp32 sums
-    // where out is fp32 or something is added.
-    const bool wide = p.fp32 || p.add;
     const int64_t cols = p.ts.rows;
-    // chunk k of row `lane`; chunk lane % 8 of rows 4 i + lane / 8, i even or odd
-    uint32_t mine[8], theirs[2];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) mine[k] = stage + lane * 128 + ((k ^ (lane & 7)) << 4);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) theirs[k] = stage + (lane >> 3) * 128 + (((lane & 7) ^ (4 * k + (lane >> 3))) << 4);
     int lt = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++lt) {
       int tw, tt;
@@ -696,7 +825,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
       const int64_t m0 = (int64_t)tw * 256 + rank * 128 + 32 * q, n0 = (int64_t)tt * NT;
       const int rows = (int)min((int64_t)32, p.ws.rows - m0);      // may be none
       const uint32_t from = lane_at + (b ? C::kSums - NT : 0);
-      if (p.tma_out) {
+      if constexpr (OUT == Out::kTma) {
         // 64 columns of bf16, or 32 of fp32, at a time: two boxes of 64 bytes a
         // row; the columns after them leave tensor memory meanwhile.  One fence
         // and one wait for both boxes: each costs the warp hundreds of cycles.
@@ -762,19 +891,40 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         }
         continue;
       }
-      if (!wide && !(p.out_vector && rows == 32 && n0 + NT <= cols)) {
+      // inside, and rows of whole 16-byte pieces
+      const bool lines = rows == 32 && n0 + NT <= cols && p.out_vector && (!p.add || p.add_vector);
+      if (OUT != Out::kBf16 || !lines) {
+        // two parts: the columns that the other buffer shares first
 #pragma unroll 1
-        for (int x = 0; x < NT; x += 32) {
-          const int c = C::kOver && !b ? NT - 32 - x : x;
-          const uint32_t bar = x + 32 == NT ? lead_bar(&sums_empty[b]) : C::kOver && x + 32 == C::kOver ? lead_bar(shared_empty) : 0u;
-          store_anywhere(from + c, bar, stage, static_cast<uint16_t*>(p.out) + m0 * p.out_stride + n0 + c, p.out_stride,
-                         rows, (int)max((int64_t)0, min((int64_t)32, cols - n0 - c)));
+        for (int part = C::kOver ? 0 : 1; part < 2; ++part) {
+          const int c = (part == 0) == (b != 0) ? 0 : b ? C::kOver : part ? 0 : NT - C::kOver;
+          const int n = part ? NT - C::kOver : C::kOver;
+          const uint32_t bar = lead_bar(part ? &sums_empty[b] : shared_empty);
+          const int64_t at = m0 * p.out_stride + n0 + c, add_at = m0 * p.add_stride + n0 + c;
+          const int width = (int)max((int64_t)0, min((int64_t)n, cols - n0 - c));
+          if constexpr (OUT == Out::kBf16)
+            store_anywhere(from + c, n / 32, bar, stage, static_cast<uint16_t*>(p.out) + at, p.out_stride, rows, width);
+          else if constexpr (OUT != Out::kTma) {
+            using T = std::conditional_t<OUT == Out::kAddBf16, uint16_t, uint32_t>;
+            constexpr bool ADD = OUT != Out::kF32;
+            T* const out = static_cast<T*>(p.out) + at;
+            const T* const add = ADD ? static_cast<const T*>(p.add) + add_at : nullptr;
+            if (lines) store_sums<T, ADD, true>(from + c, n / 32, bar, stage, out, p.out_stride, add, p.add_stride, rows, width);
+            else store_sums_anywhere<T, ADD>(from + c, n / 32, bar, stage, out, p.out_stride, add, p.add_stride, rows, width);
+          }
         }
         continue;
       }
+      // 128 bytes of 32 rows pass through shared memory, swizzled: chunk k of row
+      // `lane`; chunk lane % 8 of rows 4 i + lane / 8, i even or odd
+      uint32_t mine[8], theirs[2];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mine[k] = stage + lane * 128 + ((k ^ (lane & 7)) << 4);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) theirs[k] = stage + (lane >> 3) * 128 + (((lane & 7) ^ (4 * k + (lane >> 3))) << 4);
 #pragma unroll 1
       for (int x = 0; x < NT;) {
-        const int w = wide ? 32 : min(64, NT - x);
+        const int w = min(64, NT - x);
         // the columns that the other buffer shares first: the last ones of the first, the first of the second
         const int c = C::kOver && !b ? NT - w - x : x;
         uint32_t v[32], u[32];
@@ -789,85 +939,47 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(lead_bar(x == NT ? &sums_empty[b] : shared_empty));
         }
-        if (wide) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) st_shared16(mine[k], v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        } else {
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h[4], g[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t h[4], g[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              h[z] = cvt_bf16x2(__uint_as_float(v[8 * k + 2 * z]), __uint_as_float(v[8 * k + 2 * z + 1]));
-              g[z] = cvt_bf16x2(__uint_as_float(u[8 * k + 2 * z]), __uint_as_float(u[8 * k + 2 * z + 1]));
-            }
-            st_shared16(mine[k], h[0], h[1], h[2], h[3]);
-            st_shared16(mine[k + 4], g[0], g[1], g[2], g[3]);      // not read where there are 32 columns
+          for (int z = 0; z < 4; ++z) {
+            h[z] = cvt_bf16x2(__uint_as_float(v[8 * k + 2 * z]), __uint_as_float(v[8 * k + 2 * z + 1]));
+            g[z] = cvt_bf16x2(__uint_as_float(u[8 * k + 2 * z]), __uint_as_float(u[8 * k + 2 * z + 1]));
           }
+          st_shared16(mine[k], h[0], h[1], h[2], h[3]);
+          st_shared16(mine[k + 4], g[0], g[1], g[2], g[3]);        // not read where there are 32 columns
         }
         __syncwarp();
-        if (!wide || (rows == 32 && n0 + c + 32 <= cols && p.out_vector && (!p.add || p.add_vector))) {
-          const int size = p.fp32 ? 4 : 2;
-          if (p.add) {
-            // four sums of row 4 i + lane / 8 at a time
-            const int64_t n = n0 + c + 4 * (lane & 7), m = m0 + (lane >> 3);
-            const char* src = static_cast<const char*>(p.add) + (m * p.add_stride + n) * size;
-            char* dst = static_cast<char*>(p.out) + (m * p.out_stride + n) * size;
-            uint4 x[8];
+        uint16_t* const dst = static_cast<uint16_t*>(p.out) + m0 * p.out_stride + n0 + c;
+        if (w == 64) {
+          // whole lines: 16 bytes of row 4 i + lane / 8 at a time
+          uint16_t* at = dst + (lane >> 3) * p.out_stride + (lane & 7) * 8;
+          float4 t[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const char* at = src + i * (4 * size) * p.add_stride;
-              if (p.fp32) {
-                x[i] = *reinterpret_cast<const uint4*>(at);
-              } else {
-                const uint2 y = *reinterpret_cast<const uint2*>(at);
-                x[i] = make_uint4(y.x << 16, y.x & 0xFFFF0000u, y.y << 16, y.y & 0xFFFF0000u);
-              }
-            }
+          for (int i = 0; i < 8; ++i) t[i] = load_shared4(theirs[i & 1] + 512 * i);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float4 t = load_shared4(theirs[i & 1] + 512 * i);
-              t.x += __uint_as_float(x[i].x);
-              t.y += __uint_as_float(x[i].y);
-              t.z += __uint_as_float(x[i].z);
-              t.w += __uint_as_float(x[i].w);
-              char* at = dst + i * (4 * size) * p.out_stride;
-              if (p.fp32) *reinterpret_cast<float4*>(at) = t;
-              else *reinterpret_cast<uint2*>(at) = make_uint2(cvt_bf16x2(t.x, t.y), cvt_bf16x2(t.z, t.w));
-            }
-          } else if (wide || w == 64) {
-            // whole lines: 16 bytes of row 4 i + lane / 8 at a time
-            char* dst = static_cast<char*>(p.out) + ((m0 + (lane >> 3)) * p.out_stride + n0 + c) * size + (lane & 7) * 16;
-            const int64_t step = 4 * p.out_stride * size;
-            float4 t[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = load_shared4(theirs[i & 1] + 512 * i);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              *reinterpret_cast<float4*>(dst) = t[i];
-              dst += step;
-            }
-          } else {
-            // half lines: of row 8 i + lane / 4
-            char* dst = static_cast<char*>(p.out) + ((m0 + (lane >> 2)) * p.out_stride + n0 + c) * 2 + (lane & 3) * 16;
-            const int64_t step = 16 * p.out_stride;
-            float4 t[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              t[i] = load_shared4(stage + (8 * i + (lane >> 2)) * 128 + (((lane & 3) ^ (lane >> 2)) << 4));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              *reinterpret_cast<float4*>(dst) = t[i];
-              dst += step;
-            }
+          for (int i = 0; i < 8; ++i) {
+            *reinterpret_cast<float4*>(at) = t[i];
+            at += 4 * p.out_stride;
           }
         } else {
-          store_wide(p, stage, m0, n0 + c, rows);
+          // half lines: of row 8 i + lane / 4
+          uint16_t* at = dst + (lane >> 2) * p.out_stride + (lane & 3) * 8;
+          float4 t[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            t[i] = load_shared4(stage + (8 * i + (lane >> 2)) * 128 + (((lane & 3) ^ (lane >> 2)) << 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<float4*>(at) = t[i];
+            at += 8 * p.out_stride;
+          }
         }
         __syncwarp();
       }
     }
-    if (lane == 0) bulk_wait_all();
+    if (OUT == Out::kTma && lane == 0) bulk_wait_all();
     __syncwarp();
   } else {
     // warp 6 brings the scales of 128 rows of a, warps 7 and 8 of 128 rows of b each
@@ -1007,7 +1119,6 @@ static cudaError_t set_args(MmArgs* a, const MxProduct& p, const MxView& w, cons
   const int size = p.fp32 ? 4 : 2;
   const uintptr_t out = reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size);
   const uintptr_t add = reinterpret_cast<uintptr_t>(p.add) | (uintptr_t)(p.add_stride * size);
-  a->tma_out = 0;
   a->out_quads = out % (4 * size) == 0;
   a->add_quads = add % (4 * size) == 0;
   a->out_vector = out % 16 == 0;
@@ -1058,10 +1169,10 @@ static cudaError_t launch_split(const MxProduct& p, const MxView& w, const MxVie
   return launch_clusters(kern, a, tiles * splits, splits, kSplitThreads, C::kSmem, s, launches);
 }
 
-template <bool F4, int NT>
-static cudaError_t launch_pair(const MxProduct& p, bool by_tma, cudaStream_t s, int* launches) {
+template <bool F4, int NT, Out OUT>
+static cudaError_t launch_pair(const MxProduct& p, cudaStream_t s, int* launches) {
   using C = PairCfg<F4, NT>;
-  const void* kern = reinterpret_cast<const void*>(mm_pair_kernel<F4, NT>);
+  const void* kern = reinterpret_cast<const void*>(mm_pair_kernel<F4, NT, OUT>);
   int occ = 1;
   cudaError_t e = kernel_occupancy(kern, kPairThreads, C::kSmem, &occ);
   if (e != cudaSuccess) return e;
@@ -1075,8 +1186,7 @@ static cudaError_t launch_pair(const MxProduct& p, bool by_tma, cudaStream_t s, 
   a.idesc = mx_idesc(F4, p.a.format, p.b.format, 256, NT);
   a.w_is_a = 1;
   const int64_t pairs = sm_count(device_of_current()) / 2;
-  a.tma_out = by_tma;
-  if (a.tma_out && (e = encode_out(&a.o, p)) != cudaSuccess) return e;
+  if (OUT == Out::kTma && (e = encode_out(&a.o, p)) != cudaSuccess) return e;
   return launch_clusters(kern, a, 2 * (tiles < pairs ? tiles : pairs), 2, kPairThreads, C::kSmem, s, launches);
 }
 
@@ -1100,11 +1210,11 @@ static PairPlan plan_pair(const MxProduct& p, int nt, int64_t kblocks, int64_t p
   // against 16.5; one round of tiles, 512 x 8192 x 2048, 7.7 against 8.7), and
   // under long ones they hardly matter (8192 x 8192 x 8192 158 against 162).
   const int64_t products = kblocks * 2 * nt;
-  const bool by_tma = lines && !p.add && tiles > pairs && products >= 3000 && products < 12000;
+  const bool by_tma = lines && !p.add && (nt == 224 || (tiles > pairs && products >= 3000 && products < 12000));
   const int64_t block = nt == 256 ? 512 : nt == 224 ? 461 : 333;
   int64_t cycles = (tiles + pairs - 1) / pairs * (kblocks * block + (nt == 256 ? 512 : nt == 224 ? 100 : 300));
-  // 448 bytes of bf16 a row are no whole lines: only by TMA
-  if (nt == 224 && !by_tma && !p.fp32 && !p.add) cycles *= 2;
+  // 448 bytes of bf16 a row are no whole lines: by TMA, or for fp32 sums that are added to
+  if (nt == 224 && !by_tma && !(p.fp32 && p.add)) cycles *= 2;
   return {cycles, by_tma};
 }
 
@@ -1130,13 +1240,19 @@ static cudaError_t launch_format(const MxProduct& p, cudaStream_t s, int* launch
   }
   const PairPlan c256 = plan_pair(p, 256, kblocks, sms / 2), c224 = plan_pair(p, 224, kblocks, sms / 2),
                  c128 = plan_pair(p, 128, kblocks, sms / 2);
-  if (c128.cycles < c224.cycles && c128.cycles < c256.cycles) return launch_pair<F4, 128>(p, c128.by_tma, s, launches);
-  return c224.cycles < c256.cycles ? launch_pair<F4, 224>(p, c224.by_tma, s, launches)
-                                   : launch_pair<F4, 256>(p, c256.by_tma, s, launches);
-}
-
-cudaError_t launch_mx_matmul(const MxProduct& p, cudaStream_t s, int* launches) {
-  return p.a.format == FP8Q_E2M1 ? launch_format<true>(p, s, launches) : launch_format<false>(p, s, launches);
+  if (c128.cycles < c224.cycles && c128.cycles < c256.cycles)
+    return c128.by_tma ? launch_pair<F4, 128, Out::kTma>(p, s, launches)
+           : p.add     ? (p.fp32 ? launch_pair<F4, 128, Out::kAddF32>(p, s, launches)
+                                 : launch_pair<F4, 128, Out::kAddBf16>(p, s, launches))
+           : p.fp32    ? launch_pair<F4, 128, Out::kF32>(p, s, launches)
+                       : launch_pair<F4, 128, Out::kBf16>(p, s, launches);
+  if (c224.cycles < c256.cycles)
+    return c224.by_tma ? launch_pair<F4, 224, Out::kTma>(p, s, launches) : launch_pair<F4, 224, Out::kAddF32>(p, s, launches);
+  return c256.by_tma ? launch_pair<F4, 256, Out::kTma>(p, s, launches)
+         : p.add     ? (p.fp32 ? launch_pair<F4, 256, Out::kAddF32>(p, s, launches)
+                               : launch_pair<F4, 256, Out::kAddBf16>(p, s, launches))
+         : p.fp32    ? launch_pair<F4, 256, Out::kF32>(p, s, launches)
+                     : launch_pair<F4, 256, Out::kBf16>(p, s, launches);
 }
 
 }  // namespace fp8q
