@@ -11,6 +11,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "mx_linear.cuh"
@@ -411,7 +412,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
         const int u = min(u0 + x * kSplitThreads, units - 1);
         const uint32_t at = smem + ((o0 + (u >> shift)) * (inner + 4) + (u & (quads - 1)) * 4) * 4;
 #pragma unroll
-        for (int s = 0; s < S; ++s) part[x][s] = S == 1 ? load_shared4(at) : cluster_load4(at, s);
+        for (int s = 0; s < S; ++s)
+          part[x][s] = S == 1                       ? load_shared4(at)
+                       : S < 8 || s < p.splits ? cluster_load4(at, s)
+                                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
       float4 extra[U];                               // add may be out: before the first store
       if (p.add) {
@@ -444,6 +448,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
       }
     }
   };
+  // (forms for one, two, four and up to eight: a form for each costs small calls
+  // 2 to 5%, for the code that they fetch)
   if (p.splits == 1) join(std::integral_constant<int, 1>());
   else if (p.splits == 2) join(std::integral_constant<int, 2>());
   else if (p.splits == 4) join(std::integral_constant<int, 4>());
@@ -1147,6 +1153,15 @@ static cudaError_t launch_clusters(const void* kern, MmArgs& a, int64_t ctas, in
   return e;
 }
 
+// CTAs that share a tile's sum: as many as run at once, up to a portable
+// cluster, with at least kSplitLeast K blocks each (1 x 8192 x 2048 in 4 bits:
+// two of four blocks 4.5 us, four of two 5.1, one of eight 5.1; more CTAs than
+// SMs cost 64 x 8192 x 2048 3 us).
+static int splits_of(int64_t tiles, int64_t kblocks, int64_t sms) {
+  const int64_t n = std::min(std::min<int64_t>(8, sms / tiles), kblocks / kSplitLeast);
+  return n < 1 ? 1 : (int)n;
+}
+
 template <bool F4, int NT>
 static cudaError_t launch_split(const MxProduct& p, const MxView& w, const MxView& t, bool w_is_a, cudaStream_t s,
                                 int* launches) {
@@ -1160,9 +1175,7 @@ static cudaError_t launch_split(const MxProduct& p, const MxView& w, const MxVie
   a.w_tiles = (int32_t)((w.rows + 127) / 128);
   a.t_tiles = (int32_t)((t.rows + NT - 1) / NT);
   const int64_t tiles = (int64_t)a.w_tiles * a.t_tiles;
-  const int sms = sm_count(device_of_current());
-  int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= sms && a.kblocks / (splits * 2) >= kSplitLeast) splits *= 2;
+  const int splits = splits_of(tiles, a.kblocks, sm_count(device_of_current()));
   a.splits = splits;
   a.idesc = mx_idesc(F4, w.format, t.format, 128, NT);
   a.w_is_a = w_is_a;
@@ -1227,19 +1240,22 @@ static cudaError_t launch_format(const MxProduct& p, cudaStream_t s, int* launch
   // of the others.
   if (few.rows <= 16) return launch_split<F4, 16>(p, many, few, !a_few, s, launches);
   if (few.rows <= 32) return launch_split<F4, 32>(p, many, few, !a_few, s, launches);
-  // Up to 256: they are rows of tiles of 128 and all tiles run at once, with the
-  // sum split where there are few (4 bits, 64 x 2048 x 8192 7.4 us against 11.9
-  // in pairs; 256 x 8192 x 2048, where they do not all run at once, 8.1 against
-  // 6.8).  A short sum needs no split and takes narrower tiles (128 x 4096 x
-  // 1024 4.7 us against 5.4).
-  const int64_t bands = (few.rows + 127) / 128;
-  if (bands <= 2 && bands * ((many.rows + 63) / 64) <= sms) {
-    if (kblocks <= 2 * kSplitLeast && bands * ((many.rows + 31) / 32) <= sms)
-      return launch_split<F4, 32>(p, few, many, a_few, s, launches);
-    return launch_split<F4, 64>(p, few, many, a_few, s, launches);
-  }
   const PairPlan c256 = plan_pair(p, 256, kblocks, sms / 2), c224 = plan_pair(p, 224, kblocks, sms / 2),
                  c128 = plan_pair(p, 128, kblocks, sms / 2);
+  // Where all tiles of 128 x 64 run at once, the few rows being those of 128, the
+  // sum can be split: up to 256 rows always (4 bits, 64 x 2048 x 8192 7.4 us
+  // against 11.9 in pairs; 256 x 8192 x 2048, where they do not all run at once,
+  // 8.1 against 6.8), for more by the K blocks that a CTA then has, 330 cycles
+  // each and 2500 for the join.  A short sum needs no split and takes narrower
+  // tiles (128 x 4096 x 1024 4.7 us against 5.4).
+  const int64_t bands = (few.rows + 127) / 128, tiles = bands * ((many.rows + 63) / 64);
+  if (tiles <= sms) {
+    if (bands <= 2 && kblocks <= 2 * kSplitLeast && bands * ((many.rows + 31) / 32) <= sms)
+      return launch_split<F4, 32>(p, few, many, a_few, s, launches);
+    const int64_t blocks = kblocks / splits_of(tiles, kblocks, sms);
+    if (bands <= 2 || blocks * 330 + 2500 < std::min(c128.cycles, std::min(c224.cycles, c256.cycles)))
+      return launch_split<F4, 64>(p, few, many, a_few, s, launches);
+  }
   if (c128.cycles < c224.cycles && c128.cycles < c256.cycles)
     return c128.by_tma ? launch_pair<F4, 128, Out::kTma>(p, s, launches)
            : p.add     ? (p.fp32 ? launch_pair<F4, 128, Out::kAddF32>(p, s, launches)
