@@ -243,7 +243,8 @@ struct SplitCfg {
   // two CTAs per SM, so that one's loads run while the other starts or ends
   static constexpr int kStages = 112 * 1024 / kStage;
   static constexpr int kSmem = kStages * kStage + 1024;
-  static constexpr int kColumns = NT + 32 <= 64 ? 64 : NT + 32 <= 128 ? 128 : 256;    // sums, scales of two K blocks
+  static constexpr int kColumns = NT + 16 * kStages <= 128 ? 128 : 256;   // sums, scales of each stage
+  static_assert(NT + 16 * kStages <= kColumns, "two CTAs per SM have 256 columns each");
   static_assert(kStage % 1024 == 0 && 132 * NT * 4 <= kStages * kStage && 128 * (NT + 4) * 4 <= kStages * kStage, "swizzled tiles; the parts of the sum");
 };
 constexpr int kSplitLeast = 4;             // K blocks of a CTA that are worth a join
@@ -310,12 +311,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
     }
   } else if (warp == 1) {
     const uint32_t hi = desc_hi(1024);
-    // a block's scales are copied before the block before it is multiplied (see mm_pair_kernel)
+    // scales are copied ahead of the block before, to their stage's place (see mm_pair_kernel)
     const auto copy = [&](int i) {
       const int st = i % ST;
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (i / ST) & 1))) return false;
       tmem_fence_after();
-      const uint32_t at = smem + st * C::kStage, to = tmem + NT + (i & 1) * 16;
+      const uint32_t at = smem + st * C::kStage, to = tmem + NT + st * 16;
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < (F4 ? 2 : 1); ++c) {
@@ -328,12 +329,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
     };
     ok = copy(0);
     for (int i = 0; i < n && ok; ++i) {
-      if (i + 1 < n && !copy(i + 1)) {
-        ok = false;
-        break;
-      }
+      if (i + 1 < n) ok = copy(i + 1);
+      if (!ok) break;
       const int st = i % ST;
-      const uint32_t at = smem + st * C::kStage, sf = tmem + NT + (i & 1) * 16;
+      const uint32_t at = smem + st * C::kStage, sf = tmem + NT + st * 16;
       const uint32_t w_lo = desc_lo(at, 16), t_lo = desc_lo(at + C::kT, 16);
       if (elect_one()) {
 #pragma unroll
@@ -343,11 +342,14 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
                         sf + 8 + col, i > 0 || s > 0);
         }
         mma_commit(&empty[st]);
+        if (i + 1 == n) mma_commit(&done);
       }
       __syncwarp();
     }
-    if (elect_one()) mma_commit(&done);
-    __syncwarp();
+    if (!ok) {                             // for the epilogue, which waits
+      if (elect_one()) mma_commit(&done);
+      __syncwarp();
+    }
   } else {
     if (warp < 4) {
       const auto put = [&](uint32_t at, int i, const auto& w) {
@@ -489,12 +491,12 @@ struct PairCfg {
   static constexpr int kBars = 256;
   static constexpr int kStages = (227 * 1024 - kBars - 4 * kOut) / (kCodes + kScales);
   static constexpr int kSmem = kStages * (kCodes + kScales) + 4 * kOut + kBars;
-  // Tensor-memory columns of the scales of a K block, and of the sums: two
-  // buffers of each.
-  static constexpr int kSfB = F4 ? 8 : 4, kSf = 3 * kSfB;
-  static constexpr int kSums = (512 - 2 * kSf) / 32 * 32;
+  // Tensor-memory columns of the scales of a K block, a buffer of them for each
+  // stage or (where there is no room) two, and two buffers of sums.
+  static constexpr int kSfB = F4 ? 8 : 4, kSf = 3 * kSfB, kSfBufs = NT <= 128 ? kStages : 2;
+  static constexpr int kSums = NT <= 128 ? 256 : (512 - kSfBufs * kSf) / 32 * 32;
   static constexpr int kOver = 2 * NT > kSums ? 2 * NT - kSums : 0;
-  static_assert(kCodes % 1024 == 0 && kOver % 32 == 0 && NT % 32 == 0 && NT <= 256 && kOver < NT && kSmem <= 227 * 1024, "");
+  static_assert(kSums + kSfBufs * kSf <= 512 && kCodes % 1024 == 0 && kOver % 32 == 0 && NT % 32 == 0 && NT <= 256 && kOver < NT && kSmem <= 227 * 1024, "");
 };
 
 // `chunks` times 32 columns of sums of 32 rows (row `lane` of the warp's lanes
@@ -760,14 +762,27 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     if (rank == 0) {
       const uint32_t hi = desc_hi(1024);
       const int own = tiles > pair ? (tiles - pair - 1) / pairs + 1 : 0, total = own * p.kblocks;
-      // A block's scales are copied before the block before it is multiplied:
-      // copies and products are carried out in the order of their issue, and a
-      // product waits for its copies to arrive.
-      int cst = 0, cphase = 0;
+      // A block's scales are copied into the buffer of an earlier block, whose
+      // products have to be done: products wait for the copies issued before
+      // them, but a copy need not wait for products that still read its buffer.
+      // With a buffer for each stage the stage's new contents tell that, and they
+      // are copied ahead of the block before.  With two the products are waited
+      // for, and the copies follow the block before (ahead of it the tensor cores
+      // run dry: 8192 x 8192 x 8192 in 4 bits 167 -> 239 us); for the short
+      // blocks of 128 columns the wait alone cost 512 x 2048 x 8192 12.0 -> 13.7.
+      constexpr int NB = C::kSfBufs;
+      int cst = 0, cphase = 0, dst = 0, dphase = 0;
       const auto copy = [&](int it) {
+        if (NB < ST && it >= NB) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[dst], dphase))) return false;
+          if (++dst == ST) {
+            dst = 0;
+            dphase ^= 1;
+          }
+        }
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[cst], cphase))) return false;
         tmem_fence_after();
-        const uint32_t from = scales + cst * C::kScales, to = tmem + C::kSums + (it & 1) * C::kSf;
+        const uint32_t from = scales + cst * C::kScales, to = tmem + C::kSums + (NB == ST ? cst : it & 1) * C::kSf;
         if (elect_one()) {
 #pragma unroll
           for (int c = 0; c < (F4 ? 2 : 1); ++c) {
@@ -793,11 +808,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         ok = __all_sync(0xFFFFFFFFu, ok);
         tmem_fence_after();
         for (int i = 0; i < p.kblocks && ok; ++i, ++it) {
-          if (it + 1 < total && !copy(it + 1)) {
-            ok = false;
-            break;
-          }
-          const uint32_t at = smem + st * C::kCodes, sf = tmem + C::kSums + (it & 1) * C::kSf;
+          if (NB == ST && it + 1 < total) ok = copy(it + 1);
+          if (!ok) break;
+          const uint32_t at = smem + st * C::kCodes, sf = tmem + C::kSums + (NB == ST ? st : it & 1) * C::kSf;
           const uint32_t a_lo = desc_lo(at, 16), b_lo = desc_lo(at + C::kB, 16);
           if (elect_one()) {
 #pragma unroll
@@ -805,16 +818,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
               mma_mx<F4, 2>(d, a_lo + 2 * s, b_lo + 2 * s, hi, mx_idesc_step<F4>(p.idesc, F4 ? s & 1 : s),
                             sf + (F4 ? 4 * (s >> 1) : 0), sf + C::kSfB + (F4 ? 8 * (s >> 1) : 0), i > 0 || s > 0);
             mma_commit_pair(&empty[st]);
+            if (i + 1 == p.kblocks) mma_commit_pair(&sums_full[b]);
           }
           __syncwarp();
           if (++st == ST) st = 0;
+          if (NB < ST && it + 1 < total) ok = copy(it + 1);
         }
-        if (elect_one()) mma_commit_pair(&sums_full[b]);
-        __syncwarp();
+        if (!ok) {                         // for the epilogue, which waits
+          if (elect_one()) mma_commit_pair(&sums_full[b]);
+          __syncwarp();
+        }
       }
     }
   } else if (warp < 6) {
-    const int q = warp & 3, row = 32 * q + lane;     // this warp's lanes of tensor memory
+    const int q = warp & 3;                          // this warp's lanes of tensor memory: 32 q on
     const uint32_t lane_at = tmem + ((uint32_t)(32 * q) << 16);
     const uint32_t stage = staging + (warp - 2) * C::kOut;
     const int64_t cols = p.ts.rows;
@@ -921,68 +938,70 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         }
         continue;
       }
-      // 128 bytes of 32 rows pass through shared memory, swizzled: chunk k of row
-      // `lane`; chunk lane % 8 of rows 4 i + lane / 8, i even or odd
-      uint32_t mine[8], theirs[2];
+      if constexpr (OUT == Out::kBf16) {
+        // 128 bytes of 32 rows pass through shared memory, swizzled: chunk k of row
+        // `lane`; chunk lane % 8 of rows 4 i + lane / 8, i even or odd
+        uint32_t mine[8], theirs[2];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) mine[k] = stage + lane * 128 + ((k ^ (lane & 7)) << 4);
+        for (int k = 0; k < 8; ++k) mine[k] = stage + lane * 128 + ((k ^ (lane & 7)) << 4);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) theirs[k] = stage + (lane >> 3) * 128 + (((lane & 7) ^ (4 * k + (lane >> 3))) << 4);
+        for (int k = 0; k < 2; ++k) theirs[k] = stage + (lane >> 3) * 128 + (((lane & 7) ^ (4 * k + (lane >> 3))) << 4);
 #pragma unroll 1
-      for (int x = 0; x < NT;) {
-        const int w = min(64, NT - x);
-        // the columns that the other buffer shares first: the last ones of the first, the first of the second
-        const int c = C::kOver && !b ? NT - w - x : x;
-        uint32_t v[32], u[32];
-        tmem_ld32(v, from + c);
-        if (w == 64) tmem_ld32(u, from + c + 32);
-        tmem_wait_ld(v);
-        tmem_wait_ld(u);
-        const bool shared_done = C::kOver && x < C::kOver && x + w >= C::kOver;
-        x += w;
-        if (shared_done || x == NT) {
-          tmem_fence_before();
+        for (int x = 0; x < NT;) {
+          const int w = min(64, NT - x);
+          // the columns that the other buffer shares first: the last ones of the first, the first of the second
+          const int c = C::kOver && !b ? NT - w - x : x;
+          uint32_t v[32], u[32];
+          tmem_ld32(v, from + c);
+          if (w == 64) tmem_ld32(u, from + c + 32);
+          tmem_wait_ld(v);
+          tmem_wait_ld(u);
+          const bool shared_done = C::kOver && x < C::kOver && x + w >= C::kOver;
+          x += w;
+          if (shared_done || x == NT) {
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(lead_bar(x == NT ? &sums_empty[b] : shared_empty));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h[4], g[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              h[z] = cvt_bf16x2(__uint_as_float(v[8 * k + 2 * z]), __uint_as_float(v[8 * k + 2 * z + 1]));
+              g[z] = cvt_bf16x2(__uint_as_float(u[8 * k + 2 * z]), __uint_as_float(u[8 * k + 2 * z + 1]));
+            }
+            st_shared16(mine[k], h[0], h[1], h[2], h[3]);
+            st_shared16(mine[k + 4], g[0], g[1], g[2], g[3]);        // not read where there are 32 columns
+          }
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_relaxed(lead_bar(x == NT ? &sums_empty[b] : shared_empty));
-        }
+          uint16_t* const dst = static_cast<uint16_t*>(p.out) + m0 * p.out_stride + n0 + c;
+          if (w == 64) {
+            // whole lines: 16 bytes of row 4 i + lane / 8 at a time
+            uint16_t* at = dst + (lane >> 3) * p.out_stride + (lane & 7) * 8;
+            float4 t[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t h[4], g[4];
+            for (int i = 0; i < 8; ++i) t[i] = load_shared4(theirs[i & 1] + 512 * i);
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            h[z] = cvt_bf16x2(__uint_as_float(v[8 * k + 2 * z]), __uint_as_float(v[8 * k + 2 * z + 1]));
-            g[z] = cvt_bf16x2(__uint_as_float(u[8 * k + 2 * z]), __uint_as_float(u[8 * k + 2 * z + 1]));
+            for (int i = 0; i < 8; ++i) {
+              *reinterpret_cast<float4*>(at) = t[i];
+              at += 4 * p.out_stride;
+            }
+          } else {
+            // half lines: of row 8 i + lane / 4
+            uint16_t* at = dst + (lane >> 2) * p.out_stride + (lane & 3) * 8;
+            float4 t[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              t[i] = load_shared4(stage + (8 * i + (lane >> 2)) * 128 + (((lane & 3) ^ (lane >> 2)) << 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              *reinterpret_cast<float4*>(at) = t[i];
+              at += 8 * p.out_stride;
+            }
           }
-          st_shared16(mine[k], h[0], h[1], h[2], h[3]);
-          st_shared16(mine[k + 4], g[0], g[1], g[2], g[3]);        // not read where there are 32 columns
+          __syncwarp();
         }
-        __syncwarp();
-        uint16_t* const dst = static_cast<uint16_t*>(p.out) + m0 * p.out_stride + n0 + c;
-        if (w == 64) {
-          // whole lines: 16 bytes of row 4 i + lane / 8 at a time
-          uint16_t* at = dst + (lane >> 3) * p.out_stride + (lane & 7) * 8;
-          float4 t[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] = load_shared4(theirs[i & 1] + 512 * i);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            *reinterpret_cast<float4*>(at) = t[i];
-            at += 4 * p.out_stride;
-          }
-        } else {
-          // half lines: of row 8 i + lane / 4
-          uint16_t* at = dst + (lane >> 2) * p.out_stride + (lane & 3) * 8;
-          float4 t[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            t[i] = load_shared4(stage + (8 * i + (lane >> 2)) * 128 + (((lane & 3) ^ (lane >> 2)) << 4));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<float4*>(at) = t[i];
-            at += 8 * p.out_stride;
-          }
-        }
-        __syncwarp();
       }
     }
     if (OUT == Out::kTma && lane == 0) bulk_wait_all();

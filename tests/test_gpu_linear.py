@@ -237,6 +237,21 @@ def test_products_of_slices_with_add(m, n, k, fmts):
         check_product(a, b, base[:, 7:7 + n], held)
 
 
+@pytest.mark.parametrize("m,n,k,fmt,kind,with_add", [
+    (5120, 4096, 2048, kv.E2M1, BF, False), (2048, 8192, 2048, kv.E4M3, F32, True), (2048, 8192, 2048, kv.E4M3, BF, True),
+    (9001, 2048, 512, kv.E2M1, F32, False), (5120, 4096, 2048, kv.E5M2, F32, False), (1000, 2050, 256, kv.E2M1, F32, True),
+    (1000, 2048, 4096, kv.E2M1, F32, True), (258, 696, 13408, kv.E2M1, BF, True), (205, 1394, 9984, kv.E4M3, F32, True)])
+def test_products_of_every_way_out(m, n, k, fmt, kind, with_add):
+    """Tiles of each width, out by TMA and from registers, added to and not, sums
+    split over three, five and more CTAs."""
+    a, b = random_mx(m, k, fmt, 1), random_mx(n, k, fmt, 2)
+    add = torch.randn(m, n, generator=torch.Generator().manual_seed(1)).to(kind).cuda() * 2.0 ** 12 if with_add else None
+    out = G.empty((m, n), kind)
+    F.mx_matmul(a, b, out, add=add)
+    G.check("after mx_matmul")
+    check_product(a, b, out, add)
+
+
 @pytest.mark.parametrize("fmt", [kv.E2M1, kv.E4M3])
 @pytest.mark.parametrize("m,n,k", [(1, 200, 1024), (40, 300, 2048), (150, 140, 1024), (600, 1100, 544), (2100, 2300, 1024)])
 def test_products_of_whole_numbers_are_exact(fmt, m, n, k):
@@ -360,6 +375,40 @@ def test_two_products_at_once():
     for (a, b), o in zip(pairs, outs):
         check_product(a, b, o[0])
         assert all(torch.equal(o[0], x) for x in o[1:])
+
+
+def test_both_kernels_and_attention_at_once():
+    """Large and split products, an activation and attention over a cache on four
+    streams: they share tensor memory and shared memory of the same SMs, and nothing else."""
+    a, b = random_mx(2300, 1024, kv.E4M3, 1), random_mx(2500, 1024, kv.E4M3, 2)
+    c, d = random_mx(9, 4096, kv.E2M1, 3), random_mx(2000, 4096, kv.E2M1, 4)
+    big, small = G.empty((2300, 2500), BF), G.empty((9, 2000), BF)
+    z = torch.randn(500, 2048, device="cuda").bfloat16()
+    h, want_h = torch.empty_like(z), torch.empty_like(z)
+    cache = F.MXKVCache.allocate(64, 16, 4, 128)
+    for t in (cache.k_q, cache.v_q):
+        t.copy_(torch.randint(0, 256, t.shape, dtype=torch.uint8))
+    cache.k_e8m0.fill_(120), cache.v_e8m0.fill_(120)
+    table = torch.arange(64, dtype=torch.int32, device="cuda")[None]
+    lens, cu = torch.tensor([1000], dtype=torch.int32, device="cuda"), torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+    q = torch.randn(300, 8, 128, device="cuda").bfloat16()
+    out, want_out = torch.empty_like(q), torch.empty_like(q)
+    ws = F.mx_kv_attention_workspace(cache, q, table, max_q=300)
+
+    def calls(o, hh):
+        return (lambda: F.mx_matmul(a, b, big), lambda: F.mx_matmul(c, d, small), lambda: F.mx_act_forward(1, z, h=hh),
+                lambda: F.mx_kv_attention(cache, q, o, table, lens, cu_q=cu, max_q=300, workspace=ws))
+    for f in calls(want_out, want_h):
+        f()
+    want = big.clone(), small.clone()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for f, s in zip(calls(out, h), streams):
+            with torch.cuda.stream(s):
+                f()
+    torch.cuda.synchronize()
+    assert torch.equal(big, want[0]) and torch.equal(small, want[1]) and torch.equal(h, want_h) and torch.equal(out, want_out)
 
 
 # ---- activations -------------------------------------------------------------------
@@ -487,6 +536,33 @@ def test_h_in_blocks(fmt, dtype, gated, rule):
         v = kv.decode(hm.q.cpu().numpy(), got_e, fmt)
         mid = (g + v) / 2
         assert (np.abs(h - mid)[wrong] <= (400 * 2.0 ** -24 * np.abs(h))[wrong]).all()
+
+
+def test_activation_into_slices():
+    """z and u kept in the two halves of one matrix, h's blocks within a wider one
+    whose other bytes stay."""
+    rows, cols = 70, 160
+    z, u, dh = act_inputs(rows, cols, BF, True)
+    both, wide = guarded(rows, 2 * cols, kv.E4M3), guarded(rows, cols + 128, kv.E2M1)
+    before = wide.q.clone(), wide.e8m0.clone()
+    zs, us = (F.MXMatrix(both.q[:, i * cols:(i + 1) * cols], both.e8m0[:, i * 5:(i + 1) * 5], kv.E4M3) for i in (0, 1))
+    hm = F.MXMatrix(wide.q[:, 32:32 + cols // 2], wide.e8m0[:, 2:7], kv.E2M1)
+    F.mx_act_forward(0, z, u, z_saved=zs, u_saved=us, h_mx=hm, rule=1)
+    G.check("after mx_act_forward")
+    alone = F.MXMatrix.allocate(rows, cols, kv.E2M1)
+    F.mx_act_forward(0, z, u, h_mx=alone, rule=1)
+    assert torch.equal(hm.q, alone.q) and torch.equal(hm.e8m0, alone.e8m0)
+    hm.q.copy_(before[0][:, 32:32 + cols // 2]), hm.e8m0.copy_(before[1][:, 2:7])
+    assert torch.equal(wide.q, before[0]) and torch.equal(wide.e8m0, before[1])
+    for m, x in ((zs, z), (us, u)):
+        code, e8 = kv.encode(x.float().cpu().numpy(), kv.E4M3, 1)
+        assert np.array_equal(m.q.cpu().numpy(), code) and np.array_equal(m.e8m0.cpu().numpy(), e8)
+    dz, du = G.empty((rows, cols), BF), G.empty((rows, cols), BF)
+    F.mx_act_backward(0, zs, us, dh, dz, du)
+    f, d, terms = activation64(0, values(zs))
+    g, gate = dh.double(), values(us)
+    check_close(dz, g * gate * d, (g * gate).abs() * terms, values(zs), 0, g * gate)
+    check_close(du, g * f, (g * f).abs(), values(zs), 0, g)
 
 
 def test_activation_of_nan_and_inf():
