@@ -1172,13 +1172,17 @@ static cudaError_t launch_clusters(const void* kern, MmArgs& a, int64_t ctas, in
   return e;
 }
 
-// CTAs that share a tile's sum: as many as run at once, up to a portable
-// cluster, with at least kSplitLeast K blocks each (1 x 8192 x 2048 in 4 bits:
-// two of four blocks 4.5 us, four of two 5.1, one of eight 5.1; more CTAs than
-// SMs cost 64 x 8192 x 2048 3 us).
-static int splits_of(int64_t tiles, int64_t kblocks, int64_t sms) {
-  const int64_t n = std::min(std::min<int64_t>(8, sms / tiles), kblocks / kSplitLeast);
-  return n < 1 ? 1 : (int)n;
+// CTAs that share a tile's sum, up to a portable cluster.  One per SM, with at
+// least kSplitLeast K blocks each (1 x 8192 x 2048 in 4 bits: two of four blocks
+// 4.5 us, four of two 5.1, one of eight 5.1); two per SM where each still has
+// `twice` blocks (0: never): their loads overlap more (1 x 8192 x 8192 9.9 -> 8.7
+// us, in 8 bits 128 x 4096 x 8192 16.9 -> 13.2), but with shorter sums their
+// starts and ends cost more than that gains (64 x 8192 x 2048 in 8 bits, eight
+// blocks each, 7.4 -> 9.3).
+static int splits_of(int64_t tiles, int64_t kblocks, int64_t sms, int64_t twice) {
+  const int64_t one = std::min(sms / tiles, kblocks / kSplitLeast);
+  const int64_t two = twice ? std::min(2 * sms / tiles, kblocks / twice) : 0;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(8, std::max(one, two)));
 }
 
 template <bool F4, int NT>
@@ -1194,7 +1198,7 @@ static cudaError_t launch_split(const MxProduct& p, const MxView& w, const MxVie
   a.w_tiles = (int32_t)((w.rows + 127) / 128);
   a.t_tiles = (int32_t)((t.rows + NT - 1) / NT);
   const int64_t tiles = (int64_t)a.w_tiles * a.t_tiles;
-  const int splits = splits_of(tiles, a.kblocks, sm_count(device_of_current()));
+  const int splits = splits_of(tiles, a.kblocks, sm_count(device_of_current()), NT <= 32 ? 8 : w.rows <= 256 ? 16 : 0);
   a.splits = splits;
   a.idesc = mx_idesc(F4, w.format, t.format, 128, NT);
   a.w_is_a = w_is_a;
@@ -1271,7 +1275,7 @@ static cudaError_t launch_format(const MxProduct& p, cudaStream_t s, int* launch
   if (tiles <= sms) {
     if (bands <= 2 && kblocks <= 2 * kSplitLeast && bands * ((many.rows + 31) / 32) <= sms)
       return launch_split<F4, 32>(p, few, many, a_few, s, launches);
-    const int64_t blocks = kblocks / splits_of(tiles, kblocks, sms);
+    const int64_t blocks = kblocks / splits_of(tiles, kblocks, sms, 0);
     if (bands <= 2 || blocks * 330 + 2500 < std::min(c128.cycles, std::min(c224.cycles, c256.cycles)))
       return launch_split<F4, 64>(p, few, many, a_few, s, launches);
   }
