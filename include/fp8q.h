@@ -508,7 +508,8 @@ typedef struct mx_matrix {
  * low precision training": a block's elements share one power of two), into out
  * [rows, cols] of dtype (rows out_stride elements apart), rounded to nearest
  * even where it is bf16 (exact there unless subnormal).  A block with E8M0 0xFF
- * reads as NaN.  out and its stride in bytes: multiples of 16.  One launch. */
+ * reads as NaN.  out and its stride in bytes: multiples of 16; out may not
+ * overlap m.  One launch. */
 FP8Q_API int mx_decode(const mx_matrix* m, void* out, int dtype, int64_t out_stride, void* stream);
 
 /* out[i, j] = sum_k a[i, k] b[j, k] (+ add[i, j]) of two matrices in MX blocks

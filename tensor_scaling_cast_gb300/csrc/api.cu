@@ -87,7 +87,10 @@ cudaError_t kernel_occupancy(const void* kernel, int threads, int smem, int* occ
   int v = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kernel, threads, (size_t)smem) != cudaSuccess || v < 1)
     v = 1;
-  cache.push_back({kernel, threads, smem, device, ctx, v});
+  try {
+    cache.push_back({kernel, threads, smem, device, ctx, v});
+  } catch (...) {                          // no memory for the entry: looked up again next time
+  }
   *occ = v;
   return cudaSuccess;
 }

@@ -12,7 +12,12 @@
 //              y = 2 sqrt(2 / pi) (z + 0.044715 z^3): (1 + tanh(y / 2)) / 2 is s
 //
 // All three are streaming passes bound by HBM.  A unit is eight elements of a
-// row; four neighbouring lanes hold one block.
+// row; four neighbouring lanes hold one block.  16384 x 8192 bf16: decoding 4
+// bits 51.0 us (6.66 TB/s); forward, gated, with both inputs kept, 170 us (SILU,
+// 6.3 TB/s), 178 (GELU_TANH), 206 (GELU); backward 158, 182, 200.  GELU's are
+// bound by issue slots, 76% of which forward SILU already uses; two units a
+// thread in flight (with four the registers cost more than the loads gain: 1.25
+// times as long).
 #include <cuda_runtime.h>
 
 #include "mx_linear.cuh"

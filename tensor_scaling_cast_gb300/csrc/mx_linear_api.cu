@@ -38,7 +38,7 @@ static int check_plain(const void* x, int dtype, int64_t rows, int64_t cols, int
   const int64_t size = dtype == FP8Q_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(x) % align != 0) return FP8Q_EALIGN;
   if (rows <= 1) return FP8Q_OK;
-  if (stride * size % align != 0) return FP8Q_EALIGN;
+  if (stride % (align / size) != 0) return FP8Q_EALIGN;
   return stride < cols || stride >= (int64_t(1) << 40) ? FP8Q_EINVAL : FP8Q_OK;
 }
 
@@ -96,13 +96,8 @@ FP8Q_API int mx_matmul(const mx_matrix* a, const mx_matrix* b, void* out, int dt
   p.add_stride = add_stride;
   p.fp32 = dtype == FP8Q_F32;
   int launches = 0;
-  cudaError_t e;
-  try {                            // the occupancy cache allocates
-    const auto launch = a->format == FP8Q_E2M1 ? launch_mx_matmul_4 : launch_mx_matmul_8;
-    e = launch(p, reinterpret_cast<cudaStream_t>(stream), &launches);
-  } catch (...) {
-    return FP8Q_ENOMEM;
-  }
+  const auto launch = a->format == FP8Q_E2M1 ? launch_mx_matmul_4 : launch_mx_matmul_8;
+  const cudaError_t e = launch(p, reinterpret_cast<cudaStream_t>(stream), &launches);
   return finish(e, launches);
 }
 

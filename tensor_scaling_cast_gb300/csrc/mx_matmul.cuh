@@ -6,6 +6,14 @@
 // (zeros outside the matrices); its scales, rows of E8M0 bytes in memory, are
 // read by four warps that write them in the order that the tensor core takes
 // them in (tcgen05.cuh), one thread a row.
+//
+// Few rows are bound by the latency of a launch, a first load and a join, then
+// by HBM: 1 x 8192 x 2048 in 4 bits 4.7 us, 1 x 8192 x 8192 8.7 us (36 MB, 4.1
+// TB/s), 64 x 2048 x 8192 7.4 us.  Large ones are bound by the tensor cores,
+// 75% of whose cycles in 4 bits and 85% in 8 have a product (8192 x 8192 x 8192:
+// 165 us = 6.7 PFLOP/s and 340 us = 3.2, there with the clock at 1.56 GHz for
+// the power); short sums by storing them (16384 x 8192 x 2048 in 4 bits 91 us
+// for 268 MB of bf16).
 #pragma once
 
 #include <cuda.h>
@@ -234,6 +242,10 @@ __device__ __forceinline__ float4 cluster_load4(uint32_t addr, uint32_t rank) {
 }
 
 // ---- tiles of 128 x NT, the sum split over a cluster -----------------------------
+//
+// The matrix of more rows has the 128 lanes of tensor memory, the other NT
+// columns.  A CTA sums a range of K; parts meet in the cluster's shared memory
+// and are added in the order of K.
 
 template <bool F4, int NT>
 struct SplitCfg {
@@ -475,7 +487,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
 // epilogue reads first, so that the next tile's products start while the others
 // are still being stored.
 constexpr int kPairThreads = 288;          // TMA, products, four warps of epilogue, three of scales
-constexpr int kPairBand = 8;               // tiles of a in a band: pairs in flight cover a compact block
+constexpr int kPairBand = 8;               // tiles of a in a band: pairs in flight cover a compact block (4 and 16 no faster)
 
 // How out leaves: by TMA, or from registers as bf16 or fp32, or as one of them
 // after something is added.  Kernels of their own: one with all of them needs
@@ -1172,6 +1184,9 @@ static cudaError_t launch_clusters(const void* kern, MmArgs& a, int64_t ctas, in
   return e;
 }
 
+// SMs of the current device; without a GPU, where the launch will say so, a pair.
+static int64_t sms_or_a_pair() { return std::max(2, sm_count(device_of_current())); }
+
 // CTAs that share a tile's sum, up to a portable cluster.  One per SM, with at
 // least kSplitLeast K blocks each (1 x 8192 x 2048 in 4 bits: two of four blocks
 // 4.5 us, four of two 5.1, one of eight 5.1); two per SM where each still has
@@ -1198,7 +1213,7 @@ static cudaError_t launch_split(const MxProduct& p, const MxView& w, const MxVie
   a.w_tiles = (int32_t)((w.rows + 127) / 128);
   a.t_tiles = (int32_t)((t.rows + NT - 1) / NT);
   const int64_t tiles = (int64_t)a.w_tiles * a.t_tiles;
-  const int splits = splits_of(tiles, a.kblocks, sm_count(device_of_current()), NT <= 32 ? 8 : w.rows <= 256 ? 16 : 0);
+  const int splits = splits_of(tiles, a.kblocks, sms_or_a_pair(), NT <= 32 ? 8 : w.rows <= 256 ? 16 : 0);
   a.splits = splits;
   a.idesc = mx_idesc(F4, w.format, t.format, 128, NT);
   a.w_is_a = w_is_a;
@@ -1221,7 +1236,7 @@ static cudaError_t launch_pair(const MxProduct& p, cudaStream_t s, int* launches
   a.splits = 1;
   a.idesc = mx_idesc(F4, p.a.format, p.b.format, 256, NT);
   a.w_is_a = 1;
-  const int64_t pairs = sm_count(device_of_current()) / 2;
+  const int64_t pairs = sms_or_a_pair() / 2;
   if (OUT == Out::kTma && (e = encode_out(&a.o, p)) != cudaSuccess) return e;
   return launch_clusters(kern, a, 2 * (tiles < pairs ? tiles : pairs), 2, kPairThreads, C::kSmem, s, launches);
 }
@@ -1258,7 +1273,7 @@ template <bool F4>
 static cudaError_t launch_format(const MxProduct& p, cudaStream_t s, int* launches) {
   const bool a_few = p.a.rows <= p.b.rows;
   const MxView &few = a_few ? p.a : p.b, &many = a_few ? p.b : p.a;
-  const int64_t kblocks = (p.a.row_bytes() + 127) / 128, sms = sm_count(device_of_current());
+  const int64_t kblocks = (p.a.row_bytes() + 127) / 128, sms = sms_or_a_pair();
   // Few rows on one side, as when decoding: they are the columns of tiles of 128
   // of the others.
   if (few.rows <= 16) return launch_split<F4, 16>(p, many, few, !a_few, s, launches);

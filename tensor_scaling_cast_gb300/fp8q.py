@@ -500,7 +500,10 @@ class MXMatrix:
             raise TypeError(f"an MX matrix is uint8 codes [rows, cols] (E2M1: [rows, cols / 2]) and uint8 E8M0 bytes "
                             f"[rows, cols / 32] with consecutive elements: got {q.dtype} {tuple(q.shape)}, "
                             f"{e8m0.dtype} {tuple(e8m0.shape)}")
+        if e8m0.get_device() != q.get_device():
+            raise TypeError(f"an MX matrix is on one device: got {q.device} and {e8m0.device}")
         self.q, self.e8m0, self.fmt = q, e8m0, fmt
+        self._device = q.get_device()
         self.shape = (e8m0.shape[0], 32 * e8m0.shape[1])
         self._struct = _MXMatrixStruct(q.data_ptr(), e8m0.data_ptr(), *self.shape, q.stride(0), e8m0.stride(0), fmt)
         self._ref = ctypes.addressof(self._struct)
@@ -514,21 +517,39 @@ class MXMatrix:
 
 # As with the cache, small calls are bound by the host: each shape and stride
 # is read once.
-def _plain(what, t, shape, dtype):
+def _plain(what, t, shape, dtype, device):
     """(pointer, row stride) of a plain matrix."""
     strides = t.stride()
+    if t.get_device() != device:
+        raise TypeError(f"{what}: all tensors of a call are on one device: got {t.device}")
     if t.dtype is not dtype or t.shape != shape or (strides[1] != 1 and shape[1] > 1):
         raise TypeError(f"{what}: {dtype} {tuple(shape)} with consecutive elements in a row: got {t.dtype} "
                         f"{tuple(t.shape)} with strides {strides}")
     return t.data_ptr(), strides[0]
 
 
+def _same_device(what, m, device):
+    """m's description (None: no matrix)."""
+    if m is None:
+        return None
+    if m._device != device:
+        raise TypeError(f"{what}: all tensors of a call are on one device: got {m.q.device}")
+    return m._ref
+
+
+def _stream_on(what, stream, device):
+    """The stream's handle, for tensors on the current device."""
+    if device < 0 or device != torch.cuda.current_device():
+        raise TypeError(f"{what}: tensors are on the current GPU: got {f'cuda:{device}' if device >= 0 else 'cpu'}")
+    return _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
+
+
 def mx_decode(m: MXMatrix, out: torch.Tensor, stream=None):
     """The values that m's codes stand for, into out [rows, cols] (bf16 or fp32)."""
-    dtype = out.dtype
-    ptr, stride = _plain("mx_decode: out", out, m.shape, dtype)
+    dtype, device = out.dtype, m._device
+    ptr, stride = _plain("mx_decode: out", out, m.shape, dtype, device)
     st = (_lib or load()).mx_decode(m._ref, ptr, BF16 if dtype is torch.bfloat16 else _dtype(out), stride,
-                                    _stream(stream))
+                                    _stream_on("mx_decode", stream, device))
     if st:
         _check(st, "mx_decode")
 
@@ -536,11 +557,11 @@ def mx_decode(m: MXMatrix, out: torch.Tensor, stream=None):
 def mx_matmul(a: MXMatrix, b: MXMatrix, out: torch.Tensor, add=None, stream=None):
     """out [a rows, b rows] (bf16 or fp32) = a b^T, + add of out's type and
     shape (out itself, to accumulate).  Both E2M1, or each E4M3 or E5M2."""
-    shape, dtype = (a.shape[0], b.shape[0]), out.dtype
-    ptr, stride = _plain("mx_matmul: out", out, shape, dtype)
-    add_ptr, add_stride = (None, 0) if add is None else _plain("mx_matmul: add", add, shape, dtype)
-    st = (_lib or load()).mx_matmul(a._ref, b._ref, ptr, BF16 if dtype is torch.bfloat16 else _dtype(out), stride,
-                                    add_ptr, add_stride, _stream(stream))
+    shape, dtype, device = (a.shape[0], b.shape[0]), out.dtype, a._device
+    ptr, stride = _plain("mx_matmul: out", out, shape, dtype, device)
+    add_ptr, add_stride = (None, 0) if add is None else _plain("mx_matmul: add", add, shape, dtype, device)
+    st = (_lib or load()).mx_matmul(a._ref, _same_device("mx_matmul: b", b, device), ptr, BF16 if dtype is torch.bfloat16 else _dtype(out), stride,
+                                    add_ptr, add_stride, _stream_on("mx_matmul", stream, device))
     if st:
         _check(st, "mx_matmul")
 
@@ -550,16 +571,16 @@ def mx_act_forward(act: int, z: torch.Tensor, u=None, z_saved=None, u_saved=None
     """h = f(z) * u (u None: f(z)) of z, u [rows, cols] (bf16 or fp32), into the
     plain h and / or the MXMatrix h_mx; MX(z), MX(u) into the 8-bit MXMatrix
     z_saved, u_saved for mx_act_backward."""
-    shape, dtype = z.shape, z.dtype
+    shape, dtype, device = z.shape, z.dtype, z.get_device()
     if len(shape) != 2:
         raise TypeError(f"mx_act_forward: z is [rows, cols]: got {tuple(shape)}")
-    zp, zs = _plain("mx_act_forward: z", z, shape, dtype)
-    up, us = (None, 0) if u is None else _plain("mx_act_forward: u", u, shape, dtype)
-    hp, hs = (None, 0) if h is None else _plain("mx_act_forward: h", h, shape, dtype)
+    zp, zs = _plain("mx_act_forward: z", z, shape, dtype, device)
+    up, us = (None, 0) if u is None else _plain("mx_act_forward: u", u, shape, dtype, device)
+    hp, hs = (None, 0) if h is None else _plain("mx_act_forward: h", h, shape, dtype, device)
     st = (_lib or load()).mx_act_forward(
         act, zp, zs, up, us, BF16 if dtype is torch.bfloat16 else _dtype(z), shape[0], shape[1],
-        None if z_saved is None else z_saved._ref, None if u_saved is None else u_saved._ref, rule, hp, hs,
-        None if h_mx is None else h_mx._ref, _stream(stream))
+        _same_device("mx_act_forward: z_saved", z_saved, device), _same_device("mx_act_forward: u_saved", u_saved, device),
+        rule, hp, hs, _same_device("mx_act_forward: h_mx", h_mx, device), _stream_on("mx_act_forward", stream, device))
     if st:
         _check(st, "mx_act_forward")
 
@@ -569,14 +590,15 @@ def mx_act_backward(act: int, z_saved: MXMatrix, u_saved, dh: torch.Tensor, dz: 
     """dz = dh u f'(z) and du = dh f(z) (u_saved and du None: dz = dh f'(z)) from
     the saved blocks, and h = f(z) u again where it is given; dh, dz, du and h
     [rows, cols], all bf16 or all fp32."""
-    shape, dtype = z_saved.shape, dh.dtype
-    gp, gs = _plain("mx_act_backward: dh", dh, shape, dtype)
-    zp, zs = _plain("mx_act_backward: dz", dz, shape, dtype)
-    up, us = (None, 0) if du is None else _plain("mx_act_backward: du", du, shape, dtype)
-    hp, hs = (None, 0) if h is None else _plain("mx_act_backward: h", h, shape, dtype)
+    shape, dtype, device = z_saved.shape, dh.dtype, z_saved._device
+    gp, gs = _plain("mx_act_backward: dh", dh, shape, dtype, device)
+    zp, zs = _plain("mx_act_backward: dz", dz, shape, dtype, device)
+    up, us = (None, 0) if du is None else _plain("mx_act_backward: du", du, shape, dtype, device)
+    hp, hs = (None, 0) if h is None else _plain("mx_act_backward: h", h, shape, dtype, device)
     st = (_lib or load()).mx_act_backward(
-        act, z_saved._ref, None if u_saved is None else u_saved._ref, gp, gs,
-        BF16 if dtype is torch.bfloat16 else _dtype(dh), zp, zs, up, us, hp, hs, _stream(stream))
+        act, z_saved._ref, _same_device("mx_act_backward: u_saved", u_saved, device), gp, gs,
+        BF16 if dtype is torch.bfloat16 else _dtype(dh), zp, zs, up, us, hp, hs,
+        _stream_on("mx_act_backward", stream, device))
     if st:
         _check(st, "mx_act_backward")
 

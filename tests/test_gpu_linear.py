@@ -672,3 +672,20 @@ def test_the_example_runs_and_its_gradients_are_near():
     off = m.main(tokens=160, ffn=576, hidden=224, quiet=True)
     assert off["y"] < 2 * 2.0 ** -2
     assert all(off[k] < 2.0 ** -3 + 3 * 2.0 ** -4 for k in ("dz", "du", "dw"))
+
+
+def test_tensors_of_a_call_are_on_the_current_gpu():
+    m = F.MXMatrix.allocate(8, 64, F.E4M3)
+    cpu = F.MXMatrix.allocate(8, 64, F.E4M3, device="cpu")
+    x = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(8, 8, device="cuda")
+    with pytest.raises(TypeError, match="cpu"):
+        F.MXMatrix(m.q, cpu.e8m0, F.E4M3)
+    for call in (lambda: F.mx_decode(m, x.cpu()), lambda: F.mx_decode(cpu, x), lambda: F.mx_matmul(m, m, out.cpu()),
+                 lambda: F.mx_matmul(m, cpu, out), lambda: F.mx_matmul(m, m, out, add=out.cpu()),
+                 lambda: F.mx_act_forward(0, x, h=x.cpu()), lambda: F.mx_act_forward(0, x, x.cpu(), h=x),
+                 lambda: F.mx_act_forward(0, x, z_saved=cpu), lambda: F.mx_act_forward(0, x, h_mx=cpu),
+                 lambda: F.mx_act_backward(0, m, None, x, x.cpu()), lambda: F.mx_act_backward(0, m, cpu, x, x, x),
+                 lambda: F.mx_act_backward(0, cpu, None, x, x)):
+        with pytest.raises(TypeError, match="cpu"):
+            call()

@@ -174,6 +174,30 @@ def test_binding_refuses_wrong_tensors():
             call()
 
 
+def test_binding_refuses_tensors_off_the_gpu():
+    from tensor_scaling_cast_gb300 import fp8q as F
+    m = F.MXMatrix.allocate(8, 64, E4M3, device="cpu")
+    x = torch.zeros(8, 64, dtype=torch.bfloat16)
+    for call in (lambda: F.mx_decode(m, x), lambda: F.mx_matmul(m, m, torch.zeros(8, 8)),
+                 lambda: F.mx_act_forward(0, x, h=x), lambda: F.mx_act_backward(0, m, None, x, x)):
+        with pytest.raises(TypeError, match="cpu"):
+            call()
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU answer")
+@pytest.mark.parametrize("fmt", [E2M1, E4M3])
+def test_no_gpu_is_an_error(lib, fmt):
+    for m, n, k in ((1, 64, 64), (20, 300, 2048), (40, 64, 64), (64, 8192, 8192), (300, 300, 2048), (1024, 1024, 64)):
+        assert matmul(lib, matrix(m, k, fmt), matrix(n, k, fmt), stride=n) == -4          # FP8Q_ECUDA
+        assert matmul(lib, matrix(m, k, fmt), matrix(n, k, fmt), dtype=F32, stride=n, add=0x30000, add_stride=n) == -4
+    assert decode(lib, matrix(fmt=fmt)) == -4
+    assert forward(lib, z_saved=matrix(), u_saved=matrix()) == -4
+    assert backward(lib, matrix(), matrix()) == -4
+    for rows, cols in ((32, 32), (8192, 8192)):
+        assert lib.mx_cast_dual(0x10000, BF16, rows, cols, fmt, 0, 0, 0x20000, 0x30000, 0x40000, 0x50000, None, None,
+                                None) == -4
+
+
 def test_reference_with_headroom_agrees_with_the_c_oracle(orc):
     x = (np.random.default_rng(3).standard_normal((16, 64)) * 100).astype(np.float32)
     x[3, :32] = 0
