@@ -515,13 +515,17 @@ class MXMatrix:
                    torch.empty(rows, cols // 32, dtype=torch.uint8, device=device), fmt)
 
 
+def _device_name(index):
+    return f"cuda:{index}" if index >= 0 else "cpu"
+
+
 # As with the cache, small calls are bound by the host: each shape and stride
 # is read once.
 def _plain(what, t, shape, dtype, device):
     """(pointer, row stride) of a plain matrix."""
     strides = t.stride()
     if t.get_device() != device:
-        raise TypeError(f"{what}: all tensors of a call are on one device: got {t.device}")
+        raise TypeError(f"{what}: all tensors of a call are on one device: got {_device_name(device)} and {t.device}")
     if t.dtype is not dtype or t.shape != shape or (strides[1] != 1 and shape[1] > 1):
         raise TypeError(f"{what}: {dtype} {tuple(shape)} with consecutive elements in a row: got {t.dtype} "
                         f"{tuple(t.shape)} with strides {strides}")
@@ -533,14 +537,14 @@ def _same_device(what, m, device):
     if m is None:
         return None
     if m._device != device:
-        raise TypeError(f"{what}: all tensors of a call are on one device: got {m.q.device}")
+        raise TypeError(f"{what}: all tensors of a call are on one device: got {_device_name(device)} and {m.q.device}")
     return m._ref
 
 
 def _stream_on(what, stream, device):
     """The stream's handle, for tensors on the current device."""
     if device < 0 or device != torch.cuda.current_device():
-        raise TypeError(f"{what}: tensors are on the current GPU: got {f'cuda:{device}' if device >= 0 else 'cpu'}")
+        raise TypeError(f"{what}: tensors are on the current GPU: got {_device_name(device)}")
     return _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
 
 
