@@ -100,6 +100,7 @@ cudaError_t launch_mx4_rows(const void* x, int dtype, int64_t nelem, int headroo
 constexpr int kMx4OutBytes = 64 * 32 + 32 * 32;
 template <bool COUNT>
 using Mx4DualCfg = TpCfg<2, 1, 4, true, kMx4OutBytes, 1, COUNT, 16, COUNT>;
+constexpr int kMx4SmallMore = 27;          // percent a sub-tile, see tp_small
 // Few sub-tiles: chunks of two row tiles and CTAs of two warps, so that every SM
 // has some (see tp_small).
 template <bool COUNT>
@@ -297,7 +298,7 @@ static cudaError_t launch_dual_counting(const void* x, int dtype, int64_t rows, 
                                         uint8_t* q_row, uint8_t* e8_row, uint8_t* q_colt, uint8_t* e8_colt,
                                         unsigned long long* cr, unsigned long long* cc, cudaStream_t s, int* launches) {
   const bool b = dtype == FP8Q_BF16;
-  const auto launch = tp_small(rows, cols, dtype)
+  const auto launch = tp_small(rows, cols, dtype, Mx4DualCfg<COUNT>::kWarps, kMx4SmallMore)
                           ? (b ? launch_dual<FP8Q_BF16, Mx4DualSmallCfg<COUNT>> : launch_dual<FP8Q_F32, Mx4DualSmallCfg<COUNT>>)
                           : (b ? launch_dual<FP8Q_BF16, Mx4DualCfg<COUNT>> : launch_dual<FP8Q_F32, Mx4DualCfg<COUNT>>);
   return launch(x, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s, launches);

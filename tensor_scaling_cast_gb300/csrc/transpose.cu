@@ -55,6 +55,7 @@ using DualCfg = TpCfg<3, 1, 4, true, 4096, 1, true, 12, true>;
 using CtCfg = TpCfg<6, 1, 4, true, 4096, 1>;
 // The MX dual of few sub-tiles (see tp_small): single row tiles, two warps per
 // CTA.
+constexpr int kDualSmallMore = 12;         // percent a sub-tile, see tp_small
 using DualSmallCfg = TpCfg<2, 1, 1, true, 4096, 0, true, 2, true>;
 constexpr int kTpL2Promotion = 128;      // bytes the L2 fetches per input-tile request
 
@@ -388,7 +389,7 @@ static cudaError_t launch_dual_t(const void* x, int64_t rows, int64_t cols, int 
                                  uint8_t* q_row, uint8_t* e8_row, uint8_t* q_colt, uint8_t* e8_colt,
                                  unsigned long long* cr, unsigned long long* cc, cudaStream_t s,
                                  int* launches) {
-  if (tp_small(rows, cols, DT))
+  if (tp_small(rows, cols, DT, DualCfg::kWarps, kDualSmallMore))
     return launch_dual_c<DT, FMT, DualSmallCfg>(x, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc,
                                                 s, launches);
   return launch_dual_c<DT, FMT, DualCfg>(x, rows, cols, rule, headroom, q_row, e8_row, q_colt, e8_colt, cr, cc, s,

@@ -65,12 +65,20 @@ struct TpCfg {
 // do not depend on the shape.
 inline bool mx_clip_free(int rule, int headroom) { return rule == FP8Q_MX_CEIL || headroom >= 1; }
 
-// Fewer sub-tiles than give every warp of the dual casts' full grid (twelve per
-// SM) a chunk of four: a smaller shape spreads them over the SMs (416 x 4096 to 8
-// bits 12.6 -> 3.8 us).
-inline bool tp_small(int64_t rows, int64_t cols, int dtype) {
-  const int64_t tile_c = dtype == FP8Q_BF16 ? 64 : 32;
-  return rows / 32 * ((cols + tile_c - 1) / tile_c) < (int64_t)sm_count(device_of_current()) * 12 * 4;
+// Whether the dual casts' small shape, which spreads single sub-tiles (8 bits) or
+// pairs of them (4 bits) over CTAs of two warps, is done before the full one,
+// whose `warps` warps per SM go over chunks of four in whole rounds.  The small
+// one takes `more` percent longer a sub-tile, and falls behind with more rounds,
+// where the full one's wide bands count.  bf16 to 8 bits: 416 x 4096 12.5 -> 3.9
+// us, 2048 x 8192 (1.1 rounds) 24.3 -> 16.9, 4096 x 8192 (2.2) 34.0 -> 29.1, but
+// 8192 x 8192 (4.5) 53.7 -> 58.7 and 16384 x 8192 93 -> 125; to 4 bits 416 x 4096
+// 12.4 -> 4.7, 2560 x 8192 (1.05) 22.4 -> 17.6, but 2048 x 8192 (0.84) 13.5 ->
+// 15.7 and 4096 x 8192 (1.7) 22.6 -> 25.0.
+inline bool tp_small(int64_t rows, int64_t cols, int dtype, int warps, int more) {
+  const int64_t tile_c = dtype == FP8Q_BF16 ? 64 : 32, ctiles = (cols + tile_c - 1) / tile_c;
+  const int64_t tiles = rows / 32 * ctiles, chunks = (rows / 32 + 3) / 4 * ctiles;
+  const int64_t grid = (int64_t)sm_count(device_of_current()) * warps, rounds = (chunks + grid - 1) / grid;
+  return rounds <= 4 && tiles * (100 + more) < rounds * grid * 4 * 100;
 }
 
 template <int DT>
