@@ -104,6 +104,27 @@ def test_4_bit_dual_is_exact(rows, cols, dtype, rule, headroom):
         assert int(counts[k]) == clipped(v, e8)
 
 
+@pytest.mark.parametrize("fmt", [kv.E2M1, kv.E4M3, kv.E5M2])
+@pytest.mark.parametrize("rows,cols,dtype", [(2080, 8320, BF), (4128, 8224, BF), (2592, 8192, BF), (16416, 4160, BF),
+                                             (2080, 4128, F32), (8224, 4160, F32)])
+@pytest.mark.parametrize("rule,counted", [(0, True), (0, False), (1, True)])
+def test_dual_of_every_shape_is_both_row_wise_casts(rows, cols, dtype, fmt, rule, counted):
+    """From part of a round of the kernels' grids to several: the same bytes as
+    the row-wise casts of x and of its transpose."""
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols)
+    x = torch.randn(rows, cols, generator=gen, device="cuda")
+    x = (x * torch.exp(6 * torch.randn(1, cols, generator=gen, device="cuda"))).to(dtype)
+    r, c = guarded(rows, cols, fmt), guarded(cols, rows, fmt)
+    counts = G.full((4,), -1, torch.int64)
+    F.mx_cast_dual(x, fmt, rule, 0, r.q, r.e8m0, c.q, c.e8m0, *((counts[:1], counts[1:2]) if counted else (None, None)))
+    G.check("after mx_cast_dual")
+    for k, (m, v) in enumerate(((r, x), (c, x.t().contiguous()))):
+        want = F.MXMatrix.allocate(*v.shape, fmt)
+        F.mx_cast_ex(v, fmt, rule, 0, F.MX_ROWWISE, want.q, want.e8m0, counts[2 + k:3 + k])
+        assert torch.equal(m.e8m0, want.e8m0) and torch.equal(m.q, want.q)
+        assert int(counts[k]) == (int(counts[2 + k]) if counted else -1)
+
+
 def test_4_bit_largest_exponent_under_headroom():
     """E = 127 takes its factor 2^-127 as a subnormal number."""
     x = torch.full((1, 32), 3e38)
