@@ -624,64 +624,86 @@ static __device__ __noinline__ void store_sums_anywhere(uint32_t from, int chunk
 // of out, from tensor memory at `from` on; bar, where not 0, is told once they
 // have left it.  Row `lane` passes through shared memory as far past a multiple
 // of 16 bytes as it lies in out, so that its 16-byte pieces leave whole, what is
-// left of a chunk with the next one, but for the first and the last.
+// left of a chunk with the next one; the elements before the first piece and
+// behind the last leave in two or three stores: 8192 x 8190 x 512 in 4 bits 56 us
+// (66 with the ends element by element and each chunk waited for), 8192 columns,
+// whole lines, 31.  (One warp per scheduler: its
+// instructions count.  Moving rows in registers instead, without conflicts in
+// shared memory, takes twice the selects that this takes stores; multiples of 32
+// bytes, for whole sectors, three times.)
 static __device__ __noinline__ void store_anywhere(uint32_t from, int chunks, uint32_t bar, uint32_t stage, uint16_t* out,
-                                            int64_t stride, int rows, int width) {
+                                                   int64_t stride, int rows, int width) {
   const int lane = threadIdx.x & 31;
   // in elements, and only the low bits count
   const uint32_t start = (uint32_t)(reinterpret_cast<uintptr_t>(out) >> 1), step = (uint32_t)stride;
   const uint32_t phase = (start + lane * step) & 7u, odd = 16 * (phase & 1);
   const uint32_t row = stage + lane * 80, to = row + (phase >> 1) * 4;
+  uint16_t* const mine = out + lane * stride - (int)phase;           // piece 0 of the first chunk
   uint32_t before = 0;
+  uint32_t v[32];
+  tmem_ld32(v, from);
+  tmem_wait_ld(v);
 #pragma unroll 1
   for (int i = 0; i < chunks; ++i) {
-    uint32_t v[32];
-    tmem_ld32(v, from + 32 * i);
-    tmem_wait_ld(v);
-    if (i + 1 == chunks && bar) {
+    uint32_t h[17];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) h[k] = cvt_bf16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+    h[16] = 0;
+    if (i + 1 < chunks) {
+      tmem_ld32(v, from + 32 * (i + 1));                             // on its way meanwhile
+    } else if (bar) {
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(bar);
     }
-    if (rows <= 0 || 32 * i >= width) continue;
-    __syncwarp();
-    if (i) {                               // what the chunk before left
-      const float4 left = load_shared4(row + 64);
-      st_shared16(row, __float_as_uint(left.x), __float_as_uint(left.y), __float_as_uint(left.z), __float_as_uint(left.w));
-    }
+    if (rows > 0 && 32 * i < width) {
+      __syncwarp();
+      if (i) {                             // what the chunk before left
+        const float4 left = load_shared4(row + 64);
+        st_shared16(row, __float_as_uint(left.x), __float_as_uint(left.y), __float_as_uint(left.z), __float_as_uint(left.w));
+      }
 #pragma unroll
-    for (int k = 0; k < 17; ++k) {
-      const uint32_t h = k < 16 ? cvt_bf16x2(__uint_as_float(v[2 * (k & 15)]), __uint_as_float(v[2 * (k & 15) + 1])) : 0u;
-      asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * k), "r"(__funnelshift_l(before, h, odd)) : "memory");
-      if (k < 16) before = h;
-    }
-    __syncwarp();
-    const bool inside = i > 0 && 32 * i + 32 <= width, last = i + 1 == chunks || 32 * i + 32 >= width;
+      for (int k = 0; k < 17; ++k)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * k), "r"(__funnelshift_l(k ? h[k ? k - 1 : 0] : before, h[k], odd))
+                     : "memory");
+      before = h[15];
+      __syncwarp();
+      const int held = min(32, width - 32 * i);      // columns of this chunk
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int r = 8 * x + (lane >> 2), j = lane & 3;
-      const float4 t = load_shared4(stage + r * 80 + j * 16);
-      if (r >= rows) continue;
-      const int at = 32 * i + 8 * j - (int)((start + r * step) & 7u);      // of the piece's first element
-      uint16_t* dst = out + r * stride + at;
-      if (inside || (at >= 0 && at + 8 <= width)) {
-        *reinterpret_cast<float4*>(dst) = t;
-      } else {
-        const uint32_t h[4] = {__float_as_uint(t.x), __float_as_uint(t.y), __float_as_uint(t.z), __float_as_uint(t.w)};
+      for (int x = 0; x < 4; ++x) {
+        const int r = 8 * x + (lane >> 2), j = lane & 3;
+        const float4 t = load_shared4(stage + r * 80 + j * 16);
+        const int moved = (int)((start + r * step) & 7u);
+        if (r < rows && (i > 0 || j > 0 || moved == 0) && 8 * j + 8 <= moved + held)
+          *reinterpret_cast<float4*>(out + r * stride + 32 * i + 8 * j - moved) = t;
+      }
+      const int end = (int)phase + held;             // of what the row holds
+      const bool within = i == 0 && phase && end < 8;
+      if (i == 0 && phase && lane < rows) {          // before the first whole piece
+        const float4 t = load_shared4(row);
+        const uint32_t w[4] = {__float_as_uint(t.x), __float_as_uint(t.y), __float_as_uint(t.z), __float_as_uint(t.w)};
+        if (within) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (at + e >= 0 && at + e < width) dst[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
+          for (int e = 1; e < 7; ++e)
+            if (e >= (int)phase && e < end) mine[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        } else {
+          const int two = (phase + 1) & ~1, four = (two + 2) & ~3;   // where 4 bytes start, and 8
+          if (phase & 1) mine[phase] = (uint16_t)((phase < 4 ? phase < 2 ? w[0] : w[1] : phase < 6 ? w[2] : w[3]) >> 16);
+          if (two & 2) *reinterpret_cast<uint32_t*>(mine + two) = two == 2 ? w[1] : w[3];
+          if (four == 4) *reinterpret_cast<uint2*>(mine + 4) = make_uint2(w[2], w[3]);
+        }
+      }
+      if ((i + 1 == chunks || held < 32 || 32 * i + 32 == width) && lane < rows && !within) {     // behind the last one
+        const int k = end >> 3, n = end & 7;
+        const float4 t = load_shared4(row + 16 * k);
+        const uint32_t w[4] = {__float_as_uint(t.x), __float_as_uint(t.y), __float_as_uint(t.z), __float_as_uint(t.w)};
+        uint16_t* const at = mine + 32 * i + 8 * k;
+        if (n & 4) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+        if (n & 2) *reinterpret_cast<uint32_t*>(at + (n & 4)) = n & 4 ? w[2] : w[0];
+        if (n & 1) at[n - 1] = (uint16_t)(n & 4 ? n & 2 ? w[3] : w[2] : n & 2 ? w[1] : w[0]);
       }
     }
-    if (last && lane < rows) {             // and what is left at the end
-      const float4 t = load_shared4(row + 64);
-      const int at = 32 * i + 32 - (int)phase;
-      uint16_t* dst = out + lane * stride + at;
-      const uint32_t h[4] = {__float_as_uint(t.x), __float_as_uint(t.y), __float_as_uint(t.z), __float_as_uint(t.w)};
-#pragma unroll
-      for (int e = 0; e < 7; ++e)
-        if (e < (int)phase && at + e < width) dst[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
-    }
+    if (i + 1 < chunks) tmem_wait_ld(v);
   }
   __syncwarp();
 }

@@ -291,6 +291,31 @@ def test_products_of_whole_numbers_are_exact(fmt, m, n, k):
     assert torch.equal(out.double(), want)
 
 
+@pytest.mark.parametrize("kind", [BF, F32])
+@pytest.mark.parametrize("start", [0, 1, 3, 6])
+def test_out_starts_and_ends_anywhere(kind, start):
+    """Tiles of the larger kernel whose rows start at any multiple of an element
+    and whose last columns are any number: whole numbers up to 2^8, exactly."""
+    m, k = 2100, 64
+    gen = torch.Generator().manual_seed(start)
+    a = torch.randint(-2, 3, (m, k), generator=gen).float()
+    b = torch.randint(-1, 2, (1200, k), generator=gen).float()
+    a[:, 32:] = 0                                    # at most 64 in magnitude
+    am, bm = guarded(m, k, F.E2M1), guarded(1200, k, F.E2M1)
+    for x, q in ((a, am), (b, bm)):
+        F.mx_cast_ex(x.cuda(), F.E2M1, 0, 0, F.MX_ROWWISE, q.q, q.e8m0)
+    want = (a @ b.t()).to(kind).cuda()
+    for n in [1024 + c for c in range(1, 41)] + [1119, 1136, 1199]:
+        flat = G.empty((m * (n + start) + 16,), kind)
+        flat.fill_(-7)
+        out = flat[start:start + m * (n + start)].view(m, n + start)[:, :n]
+        F.mx_matmul(am, F.MXMatrix(bm.q[:n], bm.e8m0[:n], F.E2M1), out)
+        G.check(f"{n} columns")
+        assert torch.equal(out, want[:, :n]), n
+        assert bool((flat[:start] == -7).all()) and bool((flat[start:start + m * (n + start)].view(m, n + start)[:, n:] == -7).all())
+        assert bool((flat[start + m * (n + start):] == -7).all())
+
+
 def test_one_scale_and_one_element_at_a_time():
     """Each block and each element of K reaches the sum with its own scale: a
     single one is not zero."""
