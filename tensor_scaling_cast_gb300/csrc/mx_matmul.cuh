@@ -630,7 +630,8 @@ static __device__ __noinline__ void store_sums_anywhere(uint32_t from, int chunk
 // whole lines, 31.  (One warp per scheduler: its
 // instructions count.  Moving rows in registers instead, without conflicts in
 // shared memory, takes twice the selects that this takes stores; multiples of 32
-// bytes, for whole sectors, three times.)
+// bytes, for whole sectors, three times.  fp32 is done sooner column by column,
+// in store_sums: 3830 x 11557 x 128 in 8 bits 55 us, by pieces 60 to 74.)
 static __device__ __noinline__ void store_anywhere(uint32_t from, int chunks, uint32_t bar, uint32_t stage, uint16_t* out,
                                                    int64_t stride, int rows, int width) {
   const int lane = threadIdx.x & 31;
