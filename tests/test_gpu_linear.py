@@ -125,6 +125,48 @@ def test_dual_of_every_shape_is_both_row_wise_casts(rows, cols, dtype, fmt, rule
         assert int(counts[k]) == (int(counts[2 + k]) if counted else -1)
 
 
+@pytest.mark.parametrize("fmt", [kv.E2M1, kv.E4M3])
+@pytest.mark.parametrize("rows,cols", [(64, 96), (2080, 4160)])
+def test_calls_one_after_the_other_in_a_graph(rows, cols, fmt):
+    """An activation, the dual cast of what it wrote (with its counts cleared
+    before), decoding of both, and the buffer written anew by the next round:
+    replayed with new inputs each gives what the calls by themselves give."""
+    z = torch.empty(rows, cols, dtype=BF, device="cuda")
+    h = torch.empty_like(z)
+    r, c = guarded(rows, cols, fmt), guarded(cols, rows, fmt)
+    counts = G.full((2,), -1, torch.int64)
+    out, out_t = torch.empty_like(h), torch.empty(cols, rows, dtype=BF, device="cuda")
+    twice = torch.empty_like(h)
+
+    def calls(wait=lambda: None):
+        for act, dst in ((0, out), (2, twice)):
+            F.mx_act_forward(act, z, h=h)
+            wait()
+            F.mx_cast_dual(h, fmt, 0, 0, r.q, r.e8m0, c.q, c.e8m0, counts[:1], counts[1:])
+            wait()
+            F.mx_decode(r, dst)
+            wait()
+        F.mx_decode(c, out_t)
+        wait()
+
+    z.normal_()
+    calls(torch.cuda.synchronize)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for seed in range(4):
+        z.copy_(torch.randn(rows, cols, generator=torch.Generator().manual_seed(seed)) * 8)
+        calls(torch.cuda.synchronize)
+        want = [t.clone() for t in (out, out_t, twice, counts, r.q, c.q, r.e8m0, c.e8m0)]
+        for t in (out, out_t, twice):
+            t.zero_()
+        counts.fill_(-1)
+        graph.replay()
+        G.check("after the replay")
+        for t, w in zip((out, out_t, twice, counts, r.q, c.q, r.e8m0, c.e8m0), want):
+            assert torch.equal(t, w)
+
+
 def test_4_bit_largest_exponent_under_headroom():
     """E = 127 takes its factor 2^-127 as a subnormal number."""
     x = torch.full((1, 32), 3e38)
