@@ -130,6 +130,8 @@ def _dtype(t: torch.Tensor) -> int:
 # torch's raw getter of the current stream (the public path builds a Stream
 # object per call); falls back to the public path where it is absent.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# likewise for the current device, once there are tensors on one
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
@@ -256,20 +258,60 @@ def fp8q_loss_scaler_read(h: int):
     return sc.value, g.value
 
 
+# The MX casts' C calls take bare pointers: a slice would be taken as if its rows
+# were consecutive, and too short a tensor past its end.  Small casts are bound
+# by the host: the usual ones are seen to fit in one expression.
+def _fits(q, e8m0, n, fmt, row, device):
+    """Whether q and e8m0, both on the device (a GPU) and contiguous, have room for
+    n elements; 4-bit codes in rows of `row` elements (None: any), as they are read
+    back."""
+    return (q is not None and e8m0 is not None and q.is_contiguous() and e8m0.is_contiguous()
+            and q.get_device() == device >= 0 and e8m0.get_device() == device and e8m0.nbytes >= n >> 5
+            and (q.nbytes >= n if fmt != E2M1 else q.nbytes >= n >> 1 and (row is None or 2 * q.size(-1) == row)))
+
+
+def _name_misfit(what, x, fmt, *buffers):
+    """Raises for what is wrong with x or one of (codes, E8M0 bytes, row); passes what
+    _fits is too short to tell: flat tensors, page-locked host memory, and pointers
+    left out, which the C call refuses."""
+    tensors = [(x, 0, None)]
+    for q, e8m0, row in buffers:
+        tensors += (q, 4 if fmt == E2M1 else 8, row if fmt == E2M1 else None), (e8m0, 0.25, None)
+    tensors = [t for t in tensors if t[0] is not None]
+    for t, bits, row in tensors:
+        if (not t.is_contiguous() or 8 * t.nbytes < bits * x.numel()
+                or row is not None and t.dim() == 2 and 2 * t.shape[1] != row):
+            raise TypeError(f"{what}: x, codes and E8M0 bytes (of 32 elements each) are contiguous tensors that hold "
+                            f"{x.numel()} elements{f' in rows of {row}' if row else ''}: got {t.dtype} {tuple(t.shape)} "
+                            f"with strides {t.stride()}")
+    for t, _, _ in tensors:
+        if not (t.is_pinned() if t.get_device() < 0 else t.get_device() == torch.cuda.current_device()):
+            raise TypeError(f"{what}: tensors are on the current GPU: got {_device_name(t.get_device())}")
+
+
 def mx_cast(x: torch.Tensor, fmt: int, headroom: int, q: torch.Tensor, e8m0: torch.Tensor,
             clipped=None, stream=None):
-    rows, cols = x.shape
+    (rows, cols), device = x.shape, x.get_device()
+    if not (x.is_contiguous() and _fits(q, e8m0, rows * cols, fmt, cols, device)):
+        _name_misfit("mx_cast", x, fmt, (q, e8m0, cols))
     _check(load().mx_cast(_ptr(x), _dtype(x), rows, cols, fmt, headroom, _ptr(q), _ptr(e8m0),
-                          _ptr(clipped), _stream(stream)), "mx_cast")
+                          _ptr(clipped), _stream(stream) if device < 0 else _stream_on("mx_cast", stream, device)), "mx_cast")
 
 
 def mx_cast_ex(x: torch.Tensor, fmt: int, rule: int, headroom: int, axis: int, q: torch.Tensor,
                e8m0: torch.Tensor, clipped=None, stream=None):
     """axis MX_ROWWISE: e8m0 [rows, cols/32]; MX_COLWISE: e8m0 [rows/32, cols].
-    E2M1 (row-wise): q [rows, cols/2]."""
-    rows, cols = x.shape
-    st = (_lib or load()).mx_cast_ex(_ptr(x), _dtype(x), rows, cols, fmt, rule, headroom, axis, _ptr(q), _ptr(e8m0),
-                                     None if clipped is None else clipped.data_ptr(), _stream(stream))
+    E2M1 (row-wise): q [rows, cols/2].  x, q and e8m0 contiguous."""
+    (rows, cols), device = x.shape, x.get_device()
+    row = cols if axis == MX_ROWWISE else None
+    if not (x.is_contiguous() and _fits(q, e8m0, rows * cols, fmt, row, device)):
+        _name_misfit("mx_cast_ex", x, fmt, (q, e8m0, row))
+    dtype = x.dtype
+    st = (_lib or load()).mx_cast_ex(x.data_ptr(), BF16 if dtype is torch.bfloat16 else _dtype(x), rows, cols, fmt, rule,
+                                     headroom, axis, None if q is None else q.data_ptr(),
+                                     None if e8m0 is None else e8m0.data_ptr(),
+                                     None if clipped is None else clipped.data_ptr(),
+                                     _stream(stream) if device < 0 else _stream_on("mx_cast_ex", stream, device))
     if st:
         _check(st, "mx_cast_ex")
 
@@ -279,11 +321,15 @@ def mx_cast_dual(x: torch.Tensor, fmt: int, rule: int, headroom: int, q_row, e8_
     """Row-wise MX of x and row-wise MX of x^T (column-wise blocks written
     transposed) from one read: q_row [rows, cols], e8_row [rows, cols/32],
     q_colt [cols, rows], e8_colt [cols, rows/32] (E2M1: q_row [rows, cols/2],
-    q_colt [cols, rows/2])."""
-    rows, cols = x.shape
+    q_colt [cols, rows/2]), all contiguous."""
+    (rows, cols), device = x.shape, x.get_device()
+    n = rows * cols
+    if not (x.is_contiguous() and _fits(q_row, e8_row, n, fmt, cols, device)
+            and _fits(q_colt, e8_colt, n, fmt, rows, device)):
+        _name_misfit("mx_cast_dual", x, fmt, (q_row, e8_row, cols), (q_colt, e8_colt, rows))
     st = (_lib or load()).mx_cast_dual(_ptr(x), _dtype(x), rows, cols, fmt, rule, headroom, _ptr(q_row),
                                        _ptr(e8_row), _ptr(q_colt), _ptr(e8_colt), _ptr(clipped_row),
-                                       _ptr(clipped_col), _stream(stream))
+                                       _ptr(clipped_col), _stream(stream) if device < 0 else _stream_on("mx_cast_dual", stream, device))
     if st:
         _check(st, "mx_cast_dual")
 
@@ -343,6 +389,8 @@ def fp8q_error_stats_noalloc(x: torch.Tensor, q: torch.Tensor, fmt: int, scale_i
 def mx_error_stats(x: torch.Tensor, q: torch.Tensor, e8m0: torch.Tensor, fmt: int,
                    out: torch.Tensor, stream=None):
     rows, cols = x.shape
+    if not (x.is_contiguous() and _fits(q, e8m0, rows * cols, fmt, cols, x.get_device())):
+        _name_misfit("mx_error_stats", x, fmt, (q, e8m0, cols))
     _check(load().mx_error_stats(_ptr(x), _dtype(x), rows, cols, _ptr(q), _ptr(e8m0), fmt,
                                  _ptr(out), _stream(stream)), "mx_error_stats")
 
@@ -543,7 +591,7 @@ def _same_device(what, m, device):
 
 def _stream_on(what, stream, device):
     """The stream's handle, for tensors on the current device."""
-    if device < 0 or device != torch.cuda.current_device():
+    if device < 0 or device != _raw_device():
         raise TypeError(f"{what}: tensors are on the current GPU: got {_device_name(device)}")
     return _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
 
