@@ -190,10 +190,18 @@ __device__ __forceinline__ uint32_t lead_bar(const uint64_t* bar) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_addr(bar)));
   return a;
 }
-// Shared memory that the arriving thread wrote for the pair's products is
-// ordered by its own proxy fence before.  (With a release of cluster scope each
-// arrival waits for the thread's loads of the next scales: 8192 x 8192 x 8192 in
-// 4 bits 417 us against 250.)
+// One arrival on a barrier of the pair for shared memory that the arriving warp
+// wrote for the pair's products, after a proxy fence of each lane.  The arrival
+// releases at CTA scope, the default.  From the odd CTA to the even one, whose
+// thread issues the products, PTX's memory model promises the order of writes only
+// for a release (and an acquire) of cluster scope: that the products see the odd
+// CTA's scales is what the hardware does, whose proxy fence is over when the
+// writes are in shared memory, and not what the model says.  The acquire would
+// cost nothing, but a release of cluster scope waits for a round trip to L2 and for
+// the thread's loads in flight.  8192 x 8192 x 8192 in 4 bits 157 us (8 bits 325);
+// with such a release by the warps that bring scales 2.6 times that, by a warp
+// that they tell 342 (880), by four such warps in turn 181 (368), and with scales'
+// stages free again as soon as they are copied 174 (351).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
