@@ -199,9 +199,9 @@ __device__ __forceinline__ uint32_t lead_bar(const uint64_t* bar) {
 // writes are in shared memory, and not what the model says.  The acquire would
 // cost nothing, but a release of cluster scope waits for a round trip to L2 and for
 // the thread's loads in flight.  8192 x 8192 x 8192 in 4 bits 157 us (8 bits 325);
-// with such a release by the warps that bring scales 2.6 times that, by a warp
-// that they tell 342 (880), by four such warps in turn 181 (368), and with scales'
-// stages free again as soon as they are copied 174 (351).
+// with such a release by the warps that bring scales 1.7 times as long as without,
+// by one warp that they tell 342 (880), by four in turn 181 (368), by three in turn
+// for two blocks at a time, scales' stages free again once they are copied, 168 (332).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
