@@ -536,6 +536,22 @@ FP8Q_API int mx_decode(const mx_matrix* m, void* out, int dtype, int64_t out_str
 FP8Q_API int mx_matmul(const mx_matrix* a, const mx_matrix* b, void* out, int dtype, int64_t out_stride,
                        const void* add, int64_t add_stride, void* stream);
 
+/* How mx_matmul takes a call, as a diagnostic: the arguments as above (checked
+ * alike; no pointer is followed and no CUDA call made) on a GPU of `sms` SMs (two
+ * at least).
+ *   pair      1: tiles of 256 rows of a x `columns` of b on pairs of SMs;  0: tiles
+ *             of 128 rows of one matrix x `columns` of the other
+ *   way_out   pair 1: 0 through TMA; from registers 1 bf16, 2 fp32, and after
+ *             something is added 3 bf16, 4 fp32
+ *   splits    CTAs that share a tile's sum
+ *   tiles     of out (0: nothing to do, nor is the rest set) */
+typedef struct mx_matmul_form {
+  int32_t pair, columns, way_out, splits;
+  int64_t tiles;
+} mx_matmul_form;
+FP8Q_API int mx_matmul_plan(const mx_matrix* a, const mx_matrix* b, const void* out, int dtype, int64_t out_stride,
+                            const void* add, int64_t add_stride, int sms, mx_matmul_form* form);
+
 /* Activation of an MLP with its inputs kept in 8 bits for the backward pass
  * ("Mixed Precision FP16/BF16/FP8": activations in E4M3; "what actually breaks
  * low precision training": casts after the fact do not diverge).

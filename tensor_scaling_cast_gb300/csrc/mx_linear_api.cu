@@ -4,6 +4,7 @@
 
 #include "fp8q.h"
 #include "mx_linear.cuh"
+#include "mx_matmul_plan.cuh"
 
 using namespace fp8q;
 
@@ -60,6 +61,26 @@ static int check_kept(const mx_matrix* m, int64_t rows, int64_t cols, bool eight
   return m->rows == rows && m->cols == cols ? FP8Q_OK : FP8Q_EINVAL;
 }
 
+// A product's arguments; rows of a or b may be none, and the rest is then not looked at.
+static int check_product(const mx_matrix* a, const mx_matrix* b, void* out, int dtype, int64_t out_stride,
+                         const void* add, int64_t add_stride, MxProduct* p) {
+  int st = check_matrix(a, &p->a);
+  if (st == FP8Q_OK) st = check_matrix(b, &p->b);
+  if (st != FP8Q_OK) return st;
+  if (!known_dtype(dtype) || (a->format == FP8Q_E2M1) != (b->format == FP8Q_E2M1)) return FP8Q_EDTYPE;
+  if (a->cols != b->cols || a->cols > MX_MATMUL_MAX_K) return FP8Q_EINVAL;
+  if (a->rows == 0 || b->rows == 0) return FP8Q_OK;
+  const int size = dtype == FP8Q_F32 ? 4 : 2;
+  st = check_plain(out, dtype, a->rows, b->rows, out_stride, size);
+  if (st == FP8Q_OK && add) st = check_plain(add, dtype, a->rows, b->rows, add_stride, size);
+  p->out = out;
+  p->add = add;
+  p->out_stride = out_stride;
+  p->add_stride = add_stride;
+  p->fp32 = dtype == FP8Q_F32;
+  return st;
+}
+
 extern "C" {
 
 FP8Q_API int mx_decode(const mx_matrix* m, void* out, int dtype, int64_t out_stride, void* stream) {
@@ -80,25 +101,31 @@ FP8Q_API int mx_matmul(const mx_matrix* a, const mx_matrix* b, void* out, int dt
                        const void* add, int64_t add_stride, void* stream) {
   FP8Q_TRACE_CALL();
   MxProduct p;
-  int st = check_matrix(a, &p.a);
-  if (st == FP8Q_OK) st = check_matrix(b, &p.b);
+  const int st = check_product(a, b, out, dtype, out_stride, add, add_stride, &p);
   if (st != FP8Q_OK) return st;
-  if (!known_dtype(dtype) || (a->format == FP8Q_E2M1) != (b->format == FP8Q_E2M1)) return FP8Q_EDTYPE;
-  if (a->cols != b->cols || a->cols > MX_MATMUL_MAX_K) return FP8Q_EINVAL;
-  if (a->rows == 0 || b->rows == 0) return FP8Q_OK;
-  const int size = dtype == FP8Q_F32 ? 4 : 2;
-  st = check_plain(out, dtype, a->rows, b->rows, out_stride, size);
-  if (st == FP8Q_OK && add) st = check_plain(add, dtype, a->rows, b->rows, add_stride, size);
-  if (st != FP8Q_OK) return st;
-  p.out = out;
-  p.add = add;
-  p.out_stride = out_stride;
-  p.add_stride = add_stride;
-  p.fp32 = dtype == FP8Q_F32;
+  if (p.a.rows == 0 || p.b.rows == 0) return FP8Q_OK;
   int launches = 0;
   const auto launch = a->format == FP8Q_E2M1 ? launch_mx_matmul_4 : launch_mx_matmul_8;
   const cudaError_t e = launch(p, reinterpret_cast<cudaStream_t>(stream), &launches);
   return finish(e, launches);
+}
+
+FP8Q_API int mx_matmul_plan(const mx_matrix* a, const mx_matrix* b, const void* out, int dtype, int64_t out_stride,
+                            const void* add, int64_t add_stride, int sms, mx_matmul_form* form) {
+  FP8Q_TRACE_CALL();
+  if (!form || sms < 2) return FP8Q_EINVAL;
+  MxProduct p;
+  const int st = check_product(a, b, const_cast<void*>(out), dtype, out_stride, add, add_stride, &p);
+  if (st != FP8Q_OK) return st;
+  *form = mx_matmul_form{};
+  if (p.a.rows == 0 || p.b.rows == 0) return FP8Q_OK;
+  const MmPlan plan = plan_product(p, sms);
+  form->pair = plan.pair;
+  form->columns = plan.columns;
+  form->way_out = plan.pair ? static_cast<int32_t>(plan.out) : 0;
+  form->splits = plan.splits;
+  form->tiles = plan.tiles;
+  return FP8Q_OK;
 }
 
 FP8Q_API int mx_act_forward(int act, const void* z, int64_t z_stride, const void* u, int64_t u_stride, int dtype,

@@ -19,10 +19,10 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <algorithm>
 #include <type_traits>
 
 #include "mx_linear.cuh"
+#include "mx_matmul_plan.cuh"
 #include "tcgen05.cuh"
 #include "tma.cuh"
 
@@ -259,7 +259,6 @@ struct SplitCfg {
   static_assert(NT + 16 * kStages <= kColumns, "two CTAs per SM have 256 columns each");
   static_assert(kStage % 1024 == 0 && 132 * NT * 4 <= kStages * kStage && 128 * (NT + 4) * 4 <= kStages * kStage, "swizzled tiles; the parts of the sum");
 };
-constexpr int kSplitLeast = 4;             // K blocks of a CTA that are worth a join
 constexpr int kSplitThreads = 192;         // TMA, products, and four warps of the epilogue, the first two of which bring scales
 
 template <bool F4, int NT>
@@ -489,11 +488,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mm_split_kernel(const __grid
 constexpr int kPairThreads = 288;          // TMA, products, four warps of epilogue, three of scales
 constexpr int kPairBand = 8;               // tiles of a in a band: pairs in flight cover a compact block (4 and 16 no faster)
 
-// How out leaves: by TMA, or from registers as bf16 or fp32, or as one of them
-// after something is added.  Kernels of their own: one with all of them needs
-// more registers than there are.
-enum class Out { kTma, kBf16, kF32, kAddBf16, kAddF32 };
-
 template <bool F4, int NT>
 struct PairCfg {
   static constexpr int kB = 128 * 128;                             // codes of b within a stage
@@ -709,7 +703,7 @@ static __device__ __noinline__ void store_anywhere(uint32_t from, int chunks, ui
   __syncwarp();
 }
 
-template <bool F4, int NT, Out OUT>
+template <bool F4, int NT, MmOut OUT>
 __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_constant__ MmArgs p) {
   using C = PairCfg<F4, NT>;
   constexpr int ST = C::kStages;
@@ -742,7 +736,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
     fence_barrier_init();
     prefetch_tensormap(&p.w);
     prefetch_tensormap(&p.t);
-    if (OUT == Out::kTma) prefetch_tensormap(&p.o);
+    if (OUT == MmOut::kTma) prefetch_tensormap(&p.o);
   }
   __syncwarp();
   cluster_barrier();                       // the other CTA's barriers are there
@@ -883,7 +877,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
       const int64_t m0 = (int64_t)tw * 256 + rank * 128 + 32 * q, n0 = (int64_t)tt * NT;
       const int rows = (int)min((int64_t)32, p.ws.rows - m0);      // may be none
       const uint32_t from = lane_at + (b ? C::kSums - NT : 0);
-      if constexpr (OUT == Out::kTma) {
+      if constexpr (OUT == MmOut::kTma) {
         // 64 columns of bf16, or 32 of fp32, at a time: two boxes of 64 bytes a
         // row; the columns after them leave tensor memory meanwhile.  One fence
         // and one wait for both boxes: each costs the warp hundreds of cycles.
@@ -951,7 +945,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
       }
       // inside, and rows of whole 16-byte pieces
       const bool lines = rows == 32 && n0 + NT <= cols && p.out_vector && (!p.add || p.add_vector);
-      if (OUT != Out::kBf16 || !lines) {
+      if (OUT != MmOut::kBf16 || !lines) {
         // two parts: the columns that the other buffer shares first
 #pragma unroll 1
         for (int part = C::kOver ? 0 : 1; part < 2; ++part) {
@@ -960,11 +954,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
           const uint32_t bar = lead_bar(part ? &sums_empty[b] : shared_empty);
           const int64_t at = m0 * p.out_stride + n0 + c, add_at = m0 * p.add_stride + n0 + c;
           const int width = (int)max((int64_t)0, min((int64_t)n, cols - n0 - c));
-          if constexpr (OUT == Out::kBf16)
+          if constexpr (OUT == MmOut::kBf16)
             store_anywhere(from + c, n / 32, bar, stage, static_cast<uint16_t*>(p.out) + at, p.out_stride, rows, width);
-          else if constexpr (OUT != Out::kTma) {
-            using T = std::conditional_t<OUT == Out::kAddBf16, uint16_t, uint32_t>;
-            constexpr bool ADD = OUT != Out::kF32;
+          else if constexpr (OUT != MmOut::kTma) {
+            using T = std::conditional_t<OUT == MmOut::kAddBf16, uint16_t, uint32_t>;
+            constexpr bool ADD = OUT != MmOut::kF32;
             T* const out = static_cast<T*>(p.out) + at;
             const T* const add = ADD ? static_cast<const T*>(p.add) + add_at : nullptr;
             if (lines) store_sums<T, ADD, true>(from + c, n / 32, bar, stage, out, p.out_stride, add, p.add_stride, rows, width);
@@ -973,7 +967,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         }
         continue;
       }
-      if constexpr (OUT == Out::kBf16) {
+      if constexpr (OUT == MmOut::kBf16) {
         // 128 bytes of 32 rows pass through shared memory, swizzled: chunk k of row
         // `lane`; chunk lane % 8 of rows 4 i + lane / 8, i even or odd
         uint32_t mine[8], theirs[2];
@@ -1039,7 +1033,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
         }
       }
     }
-    if (OUT == Out::kTma && lane == 0) bulk_wait_all();
+    if (OUT == MmOut::kTma && lane == 0) bulk_wait_all();
     __syncwarp();
   } else {
     // warp 6 brings the scales of 128 rows of a, warps 7 and 8 of 128 rows of b each
@@ -1210,23 +1204,10 @@ static cudaError_t launch_clusters(const void* kern, MmArgs& a, int64_t ctas, in
 // SMs of the current device; without a GPU, where the launch will say so, a pair.
 static int64_t sms_or_a_pair() { return std::max(2, sm_count(device_of_current())); }
 
-// CTAs that share a tile's sum, up to a portable cluster.  One per SM, with at
-// least kSplitLeast K blocks each (1 x 8192 x 2048 in 4 bits: two of four blocks
-// 4.5 us, four of two 5.1, one of eight 5.1); two per SM where each still has
-// `twice` blocks (0: never): their loads overlap more (1 x 8192 x 8192 9.9 -> 8.7
-// us, in 8 bits 128 x 4096 x 8192 16.9 -> 13.2), but with shorter sums their
-// starts and ends cost more than that gains (64 x 8192 x 2048 in 8 bits, eight
-// blocks each, 7.4 -> 9.3).
-static int splits_of(int64_t tiles, int64_t kblocks, int64_t sms, int64_t twice) {
-  const int64_t one = std::min(sms / tiles, kblocks / kSplitLeast);
-  const int64_t two = twice ? std::min(2 * sms / tiles, kblocks / twice) : 0;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(8, std::max(one, two)));
-}
-
 template <bool F4, int NT>
-static cudaError_t launch_split(const MxProduct& p, const MxView& w, const MxView& t, bool w_is_a, cudaStream_t s,
-                                int* launches) {
+static cudaError_t launch_split(const MxProduct& p, const MmPlan& plan, cudaStream_t s, int* launches) {
   using C = SplitCfg<F4, NT>;
+  const MxView &w = plan.w_is_a ? p.a : p.b, &t = plan.w_is_a ? p.b : p.a;
   const void* kern = reinterpret_cast<const void*>(mm_split_kernel<F4, NT>);
   int occ = 1;
   cudaError_t e = kernel_occupancy(kern, kSplitThreads, C::kSmem, &occ);
@@ -1235,16 +1216,14 @@ static cudaError_t launch_split(const MxProduct& p, const MxView& w, const MxVie
   if ((e = set_args(&a, p, w, t, 128, NT)) != cudaSuccess) return e;
   a.w_tiles = (int32_t)((w.rows + 127) / 128);
   a.t_tiles = (int32_t)((t.rows + NT - 1) / NT);
-  const int64_t tiles = (int64_t)a.w_tiles * a.t_tiles;
-  const int splits = splits_of(tiles, a.kblocks, sms_or_a_pair(), NT <= 32 ? 8 : w.rows <= 256 ? 16 : 0);
-  a.splits = splits;
+  a.splits = plan.splits;
   a.idesc = mx_idesc(F4, w.format, t.format, 128, NT);
-  a.w_is_a = w_is_a;
-  return launch_clusters(kern, a, tiles * splits, splits, kSplitThreads, C::kSmem, s, launches);
+  a.w_is_a = plan.w_is_a;
+  return launch_clusters(kern, a, plan.tiles * plan.splits, plan.splits, kSplitThreads, C::kSmem, s, launches);
 }
 
-template <bool F4, int NT, Out OUT>
-static cudaError_t launch_pair(const MxProduct& p, cudaStream_t s, int* launches) {
+template <bool F4, int NT, MmOut OUT>
+static cudaError_t launch_pair(const MxProduct& p, const MmPlan& plan, cudaStream_t s, int* launches) {
   using C = PairCfg<F4, NT>;
   const void* kern = reinterpret_cast<const void*>(mm_pair_kernel<F4, NT, OUT>);
   int occ = 1;
@@ -1254,82 +1233,40 @@ static cudaError_t launch_pair(const MxProduct& p, cudaStream_t s, int* launches
   if ((e = set_args(&a, p, p.a, p.b, 128, NT / 2)) != cudaSuccess) return e;
   a.w_tiles = (int32_t)((p.a.rows + 255) / 256);
   a.t_tiles = (int32_t)((p.b.rows + NT - 1) / NT);
-  const int64_t tiles = (int64_t)a.w_tiles * a.t_tiles;
+  const int64_t tiles = plan.tiles;
   if (tiles > (1 << 27)) return cudaErrorInvalidValue;          // 32-bit tile counts
   a.splits = 1;
   a.idesc = mx_idesc(F4, p.a.format, p.b.format, 256, NT);
   a.w_is_a = 1;
   const int64_t pairs = sms_or_a_pair() / 2;
-  if (OUT == Out::kTma && (e = encode_out(&a.o, p)) != cudaSuccess) return e;
+  if (OUT == MmOut::kTma && (e = encode_out(&a.o, p)) != cudaSuccess) return e;
   return launch_clusters(kern, a, 2 * (tiles < pairs ? tiles : pairs), 2, kPairThreads, C::kSmem, s, launches);
 }
 
-// How the pair kernel would take a product with NT columns a tile, and the
-// cycles of its products: whole rounds of tiles, 2 NT a K block (4 products of
-// NT / 2) and, fitted to measurements, 512 a tile where the buffers of sums share
-// columns, 3% for 224 columns and 30% and 300 a tile for 128, which read more for
-// each product and have more tiles to start.
-struct PairPlan {
-  int64_t cycles;
-  bool by_tma;
-};
-static PairPlan plan_pair(const MxProduct& p, int nt, int64_t kblocks, int64_t pairs) {
-  const int64_t tiles = ((p.a.rows + 255) / 256) * ((p.b.rows + nt - 1) / nt);
-  const int64_t size = p.fp32 ? 4 : 2;
-  const bool lines = (reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size)) % 16 == 0;
-  // Out leaves by TMA, a few boxes at a time, where the products of the next
-  // tile take about as long: stores from registers hold up the warps that bring
-  // scales (4 bits, 16384 x 8192 x 2048 96 us against 102).  Under shorter
-  // products stores from registers are done sooner (4096 x 4096 x 1024 12.5 us
-  // against 16.5; one round of tiles, 512 x 8192 x 2048, 7.7 against 8.7), and
-  // under long ones they hardly matter (8192 x 8192 x 8192 158 against 162).
-  const int64_t products = kblocks * 2 * nt;
-  const bool by_tma = lines && !p.add && (nt == 224 || (tiles > pairs && products >= 3000 && products < 12000));
-  const int64_t block = nt == 256 ? 512 : nt == 224 ? 461 : 333;
-  int64_t cycles = (tiles + pairs - 1) / pairs * (kblocks * block + (nt == 256 ? 512 : nt == 224 ? 100 : 300));
-  // 448 bytes of bf16 a row are no whole lines: by TMA, or for fp32 sums that are added to
-  if (nt == 224 && !by_tma && !(p.fp32 && p.add)) cycles *= 2;
-  return {cycles, by_tma};
+template <bool F4, int NT>
+static cudaError_t launch_pair_out(const MxProduct& p, const MmPlan& plan, cudaStream_t s, int* launches) {
+  switch (plan.out) {
+    case MmOut::kTma: return launch_pair<F4, NT, MmOut::kTma>(p, plan, s, launches);
+    case MmOut::kBf16: return launch_pair<F4, NT, MmOut::kBf16>(p, plan, s, launches);
+    case MmOut::kF32: return launch_pair<F4, NT, MmOut::kF32>(p, plan, s, launches);
+    case MmOut::kAddBf16: return launch_pair<F4, NT, MmOut::kAddBf16>(p, plan, s, launches);
+    default: return launch_pair<F4, NT, MmOut::kAddF32>(p, plan, s, launches);
+  }
 }
 
 template <bool F4>
 static cudaError_t launch_format(const MxProduct& p, cudaStream_t s, int* launches) {
-  const bool a_few = p.a.rows <= p.b.rows;
-  const MxView &few = a_few ? p.a : p.b, &many = a_few ? p.b : p.a;
-  const int64_t kblocks = (p.a.row_bytes() + 127) / 128, sms = sms_or_a_pair();
-  // Few rows on one side, as when decoding: they are the columns of tiles of 128
-  // of the others.
-  if (few.rows <= 16) return launch_split<F4, 16>(p, many, few, !a_few, s, launches);
-  if (few.rows <= 32) return launch_split<F4, 32>(p, many, few, !a_few, s, launches);
-  const PairPlan c256 = plan_pair(p, 256, kblocks, sms / 2), c224 = plan_pair(p, 224, kblocks, sms / 2),
-                 c128 = plan_pair(p, 128, kblocks, sms / 2);
-  // Where all tiles of 128 x 64 run at once, the few rows being those of 128, the
-  // sum can be split: up to 256 rows always (4 bits, 64 x 2048 x 8192 7.4 us
-  // against 11.9 in pairs; 256 x 8192 x 2048, where they do not all run at once,
-  // 8.1 against 6.8), for more by the K blocks that a CTA then has, 330 cycles
-  // each and 2500 for the join.  A short sum needs no split and takes narrower
-  // tiles (128 x 4096 x 1024 4.7 us against 5.4).
-  const int64_t bands = (few.rows + 127) / 128, tiles = bands * ((many.rows + 63) / 64);
-  if (tiles <= sms) {
-    if (bands <= 2 && kblocks <= 2 * kSplitLeast && bands * ((many.rows + 31) / 32) <= sms)
-      return launch_split<F4, 32>(p, few, many, a_few, s, launches);
-    const int64_t blocks = kblocks / splits_of(tiles, kblocks, sms, 0);
-    if (bands <= 2 || blocks * 330 + 2500 < std::min(c128.cycles, std::min(c224.cycles, c256.cycles)))
-      return launch_split<F4, 64>(p, few, many, a_few, s, launches);
-  }
-  if (c128.cycles < c224.cycles && c128.cycles < c256.cycles)
-    return c128.by_tma ? launch_pair<F4, 128, Out::kTma>(p, s, launches)
-           : p.add     ? (p.fp32 ? launch_pair<F4, 128, Out::kAddF32>(p, s, launches)
-                                 : launch_pair<F4, 128, Out::kAddBf16>(p, s, launches))
-           : p.fp32    ? launch_pair<F4, 128, Out::kF32>(p, s, launches)
-                       : launch_pair<F4, 128, Out::kBf16>(p, s, launches);
-  if (c224.cycles < c256.cycles)
-    return c224.by_tma ? launch_pair<F4, 224, Out::kTma>(p, s, launches) : launch_pair<F4, 224, Out::kAddF32>(p, s, launches);
-  return c256.by_tma ? launch_pair<F4, 256, Out::kTma>(p, s, launches)
-         : p.add     ? (p.fp32 ? launch_pair<F4, 256, Out::kAddF32>(p, s, launches)
-                               : launch_pair<F4, 256, Out::kAddBf16>(p, s, launches))
-         : p.fp32    ? launch_pair<F4, 256, Out::kF32>(p, s, launches)
-                     : launch_pair<F4, 256, Out::kBf16>(p, s, launches);
+  const MmPlan plan = plan_product(p, sms_or_a_pair());
+  if (!plan.pair)
+    return plan.columns == 16   ? launch_split<F4, 16>(p, plan, s, launches)
+           : plan.columns == 32 ? launch_split<F4, 32>(p, plan, s, launches)
+                                : launch_split<F4, 64>(p, plan, s, launches);
+  if (plan.columns == 128) return launch_pair_out<F4, 128>(p, plan, s, launches);
+  // 224 columns leave in two ways (see plan_pair)
+  if (plan.columns == 224)
+    return plan.out == MmOut::kTma ? launch_pair<F4, 224, MmOut::kTma>(p, plan, s, launches)
+                                   : launch_pair<F4, 224, MmOut::kAddF32>(p, plan, s, launches);
+  return launch_pair_out<F4, 256>(p, plan, s, launches);
 }
 
 }  // namespace fp8q

@@ -82,6 +82,7 @@ def load() -> ctypes.CDLL:
     L.mx_kv_attention_workspace.restype = i64
     L.mx_decode.argtypes = [p, p, i, i64, p]
     L.mx_matmul.argtypes = [p, p, p, i, i64, p, i64, p]
+    L.mx_matmul_plan.argtypes = [p, p, p, i, i64, p, i64, i, p]
     L.mx_act_forward.argtypes = [i, p, i64, p, i64, i, i64, i64, p, p, i, p, i64, p, p]
     L.mx_act_backward.argtypes = [i, p, p, p, i64, i, p, i64, p, i64, p, i64, p]
     L.fp8q_pipeline_status.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -99,7 +100,7 @@ def load() -> ctypes.CDLL:
                  "fp8q_amax_history", "fp8q_scale_state", "fp8q_set_history", "fp8q_reset",
                  "fp8q_error_stats", "mx_error_stats", "fp8q_error_stats_noalloc",
                  "mx_kv_write", "mx_kv_read", "mx_kv_attention",
-                 "mx_decode", "mx_matmul", "mx_act_forward", "mx_act_backward"):
+                 "mx_decode", "mx_matmul", "mx_matmul_plan", "mx_act_forward", "mx_act_backward"):
         getattr(L, name).restype = i
     _lib = L
     return L
@@ -616,6 +617,22 @@ def mx_matmul(a: MXMatrix, b: MXMatrix, out: torch.Tensor, add=None, stream=None
                                     add_ptr, add_stride, _stream_on("mx_matmul", stream, device))
     if st:
         _check(st, "mx_matmul")
+
+
+class MXMatmulForm(ctypes.Structure):
+    """How mx_matmul takes a call (see the C header)."""
+    _fields_ = [("pair", ctypes.c_int32), ("columns", ctypes.c_int32), ("way_out", ctypes.c_int32),
+                ("splits", ctypes.c_int32), ("tiles", ctypes.c_int64)]
+
+
+def mx_matmul_plan(a: MXMatrix, b: MXMatrix, out: torch.Tensor, add=None, sms=None) -> MXMatmulForm:
+    """The form that mx_matmul(a, b, out, add) takes on a GPU of `sms` SMs (None: out's)."""
+    if sms is None:
+        sms = torch.cuda.get_device_properties(out.device).multi_processor_count
+    form = MXMatmulForm()
+    _check(load().mx_matmul_plan(a._ref, b._ref, out.data_ptr(), _dtype(out), out.stride(0), _ptr(add),
+                                 0 if add is None else add.stride(0), sms, ctypes.addressof(form)), "mx_matmul_plan")
+    return form
 
 
 def mx_act_forward(act: int, z: torch.Tensor, u=None, z_saved=None, u_saved=None, h=None, h_mx=None,
