@@ -574,8 +574,16 @@ FP8Q_API int mx_matmul_plan(const mx_matrix* a, const mx_matrix* b, const void* 
  * strides in bytes are multiples of 16.  The outputs may not overlap the inputs, but for
  * dz or du on dh and h on z or u, exactly (same base and stride).  A z or u block with NaN
  * or Inf gives NaN gradients for its 32 elements.
- * Computed in 32 bits; where dtype is bf16 with approximate exponentials and
- * reciprocals, off by less than 2^-18 of the value for |z| up to 80.
+ * Computed in 32 bits and rounded once, to dtype or to a block's codes; where
+ * dtype is bf16 with approximate exponentials, reciprocals and (GELU) normal
+ * integral, for h_mx as well: codes next to a border between two may differ from
+ * those of the exact h.  Before that rounding, with w the magnitude of the
+ * exponential's argument, |z| (SILU), z^2 / 2 (GELU) or 2 sqrt(2 / pi) |z +
+ * 0.044715 z^3| (GELU_TANH), h and du are off by at most (24 + 8 w) 2^-24 of
+ * their size, and dz by (24 + 17 w) 2^-24 of |dh u| (s + |z s'|) where f = z s(z):
+ * f' = s + z s' has a zero, near which no part of itself bounds it.  Past w = 87,
+ * where the exponential or its reciprocal leaves the normal numbers, results
+ * below 2^-118 of the factor u, dh or dh u may be 0.
  * One launch each; capturable. */
 enum { MX_ACT_SILU = 0, MX_ACT_GELU = 1, MX_ACT_GELU_TANH = 2 };
 FP8Q_API int mx_act_forward(int act, const void* z, int64_t z_stride, const void* u, int64_t u_stride, int dtype,
