@@ -506,8 +506,11 @@ typedef struct mx_matrix {
 
 /* The values that a matrix's codes stand for, code * 2^E ("what actually breaks
  * low precision training": a block's elements share one power of two), into out
- * [rows, cols] of dtype (rows out_stride elements apart), rounded to nearest
- * even where it is bf16 (exact there unless subnormal).  A block with E8M0 0xFF
+ * [rows, cols] of dtype (rows out_stride elements apart).  They are exact, but for
+ * subnormal numbers of bf16, which are rounded to nearest even, and for values
+ * past dtype's largest, which are Inf: codes under E8M0 bytes near 254 can be, and
+ * E2M1 casts with headroom write such bytes themselves, 3e38 under headroom 4 as
+ * 2 * 2^127.  A block with E8M0 0xFF
  * reads as NaN.  out and its stride in bytes: multiples of 16; out may not
  * overlap m.  One launch. */
 FP8Q_API int mx_decode(const mx_matrix* m, void* out, int dtype, int64_t out_stride, void* stream);
