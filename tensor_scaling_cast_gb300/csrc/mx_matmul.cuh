@@ -742,7 +742,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) mm_pair_kernel(const __grid_c
   cluster_barrier();                       // the other CTA's barriers are there
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 1) tmem_alloc_pair(s_tmem, 512);
-  // not before: the next grid's CTAs may take tensor memory once they come to the SM
+  // The next grid may be set up from here on, whether or not there is tensor memory
+  // yet: no CTA finds room in shared memory beside one of this kernel, and the
+  // kernels here that take tensor memory wait for the grid before them first.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tmem_fence_before();
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
