@@ -495,7 +495,11 @@ FP8Q_API int64_t mx_kv_attention_workspace(const mx_kv_cache* c, int64_t total_q
  *   q          16-byte aligned, q_stride a multiple of 16 (else FP8Q_EALIGN)
  *   strides    not below a row's bytes (FP8Q_EINVAL); a slice of a wider
  *              matrix is one with that matrix's strides.  A single row's are
- *              not used. */
+ *              not used.
+ * mx_matmul reads E8M0 rows in whole 32-byte sectors of memory: up to 31 bytes
+ * before and behind a row are read with it, and not used.  They lie in memory that
+ * the row's own bytes make accessible, and may hold anything; a tool that tracks
+ * which bytes are initialised, or who writes them meanwhile, will see the reads. */
 typedef struct mx_matrix {
   uint8_t* q;
   uint8_t* e8m0;
