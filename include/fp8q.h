@@ -580,7 +580,8 @@ FP8Q_API int mx_matmul_plan(const mx_matrix* a, const mx_matrix* b, const void* 
  *   h                 [rows, cols] of dtype, or NULL
  *   h_mx              MX(h) under `rule` in any format, of h before its
  *                     rounding to dtype, or NULL
- * One of h, h_mx, z_saved at least.
+ * One of h, h_mx, z_saved at least (with no rows there is nothing to do, whichever
+ * pointers are NULL).
  * Backward: z and u as the saved blocks hold them,
  *   dz = dh * u * f'(z) (dh * f'(z) without u),  du = dh * f(z),
  * and h = f(z) * u again where h is not NULL (the operand of the weight

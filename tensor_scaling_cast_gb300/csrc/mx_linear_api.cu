@@ -135,12 +135,13 @@ FP8Q_API int mx_act_forward(int act, const void* z, int64_t z_stride, const void
   if (!known_act(act) || rule < FP8Q_MX_FLOOR || rule > FP8Q_MX_NEAREST) return FP8Q_EINVAL;
   if (!known_dtype(dtype)) return FP8Q_EDTYPE;
   if (rows < 0 || rows > 0x7FFFFFFF || cols <= 0 || cols % 32 != 0 || cols > (int64_t(1) << 31)) return FP8Q_EINVAL;
-  if ((!h && !h_mx && !z_saved) || (u_saved && !u) || (u && !u_saved != !z_saved)) return FP8Q_EINVAL;
+  // without rows a tensor that is there may have no address either
+  if (rows && ((!h && !h_mx && !z_saved) || (u_saved && !u) || (u && !u_saved != !z_saved))) return FP8Q_EINVAL;
   MxActForward a;
   int st = check_kept(z_saved, rows, cols, true, &a.z_saved);
   if (st == FP8Q_OK) st = check_kept(u_saved, rows, cols, true, &a.u_saved);
   if (st == FP8Q_OK) st = check_kept(h_mx, rows, cols, false, &a.h_mx);
-  if (st == FP8Q_OK && u_saved && u_saved->format != z_saved->format) st = FP8Q_EDTYPE;
+  if (st == FP8Q_OK && u_saved && z_saved && u_saved->format != z_saved->format) st = FP8Q_EDTYPE;
   if (st != FP8Q_OK) return st;
   if (rows == 0) return FP8Q_OK;
   st = check_plain(z, dtype, rows, cols, z_stride, 16);
@@ -163,9 +164,10 @@ FP8Q_API int mx_act_backward(int act, const mx_matrix* z_saved, const mx_matrix*
                              int64_t dh_stride, int dtype, void* dz, int64_t dz_stride, void* du, int64_t du_stride,
                              void* h, int64_t h_stride, void* stream) {
   FP8Q_TRACE_CALL();
-  if (!known_act(act) || !z_saved || !u_saved != !du) return FP8Q_EINVAL;
-  if (!known_dtype(dtype)) return FP8Q_EDTYPE;
+  if (!known_act(act) || !z_saved) return FP8Q_EINVAL;
   const int64_t rows = z_saved->rows, cols = z_saved->cols;
+  if (rows && !u_saved != !du) return FP8Q_EINVAL;
+  if (!known_dtype(dtype)) return FP8Q_EDTYPE;
   MxActBackward a;
   int st = check_kept(z_saved, rows, cols, true, &a.z);
   if (st == FP8Q_OK) st = check_kept(u_saved, rows, cols, true, &a.u);
