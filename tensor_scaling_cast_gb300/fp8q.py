@@ -540,7 +540,8 @@ class MXMatrix:
     """A matrix in MX blocks along its rows and its description for the C
     calls: q uint8 [rows, cols] (E2M1: [rows, cols / 2]) and e8m0 uint8
     [rows, cols / 32], as the row-wise casts write them.  Both may be slices of
-    wider ones (consecutive elements within a row)."""
+    wider ones (consecutive elements within a row), but for the casts, which
+    write into contiguous ones."""
 
     def __init__(self, q: torch.Tensor, e8m0: torch.Tensor, fmt: int = E4M3):
         if (q.dtype is not torch.uint8 or e8m0.dtype is not torch.uint8 or q.dim() != 2 or e8m0.dim() != 2
